@@ -1,7 +1,7 @@
 """GB300-native selected-block (block-sparse) attention.
 
 The compute path is libbsa.so (hand-written sm_103a CUDA behind a C ABI,
-include/bsa.h); this package only builds it and marshals torch tensors into
+include/bsa.h and include/bsa_paged.h); this package only builds it and marshals torch tensors into
 its calls.
 """
 
@@ -23,5 +23,14 @@ from .api import (  # noqa: F401
     bsa_select_workspace_size,
     bsa_validate_indices,
     bsa_version,
+)
+from .paged import (  # noqa: F401
+    PAGE_SIZES_SUPPORTED,
+    bsa_axis_frequencies,
+    bsa_cache_append,
+    bsa_forward_paged,
+    bsa_forward_paged_workspace_size,
+    bsa_rope_axes,
+    bsa_rope_axes_backward,
 )
 from .build import build  # noqa: F401

@@ -1,4 +1,4 @@
-"""ctypes declarations of the libbsa C ABI (include/bsa.h)."""
+"""ctypes declarations of the libbsa C ABI (include/bsa.h, include/bsa_paged.h)."""
 
 from __future__ import annotations
 
@@ -22,6 +22,25 @@ class BsaTensor(ctypes.Structure):
         ("stride_b", ctypes.c_int64),
         ("stride_s", ctypes.c_int64),
         ("stride_h", ctypes.c_int64),
+    ]
+
+
+class BsapRope(ctypes.Structure):
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("axes", ctypes.c_void_p),
+        ("pairs", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+class BsapPositions(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64),
+        ("stride_s", ctypes.c_int64),
+        ("stride_a", ctypes.c_int64),
     ]
 
 
@@ -61,6 +80,18 @@ SIGNATURES = {
     "bsa_debug_wait_probe": (_I, [_I32, ctypes.c_uint64, _P]),
 }
 
+# the calls of include/bsa_paged.h
+_I64 = ctypes.c_int64
+_RP = ctypes.POINTER(BsapRope)
+_PP = ctypes.POINTER(BsapPositions)
+PAGED_SIGNATURES = {
+    "bsap_rope_axes": (_I, [_TP, _TP, _PP, _PP, _RP, _I32, _P, _P, _P]),
+    "bsap_cache_append": (_I, [_TP, _TP, _TP, _TP, _P, _I64, _I32, _P, _P, _RP, _PP, _TP, _P, _P]),
+    "bsap_forward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "bsap_forward": (_I, [_TP, _TP, _TP, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ,
+                          _P]),
+}
+
 
 def lib_path() -> str:
     return LIB
@@ -78,7 +109,7 @@ def load(path: str | None = None):
                 f"libbsa.so not found at {p}: build it first "
                 "(python -m block_sparse_attention_bsa_gb300.build); there is no fallback path")
         lib = ctypes.CDLL(p)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in (*SIGNATURES.items(), *PAGED_SIGNATURES.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsa.so")
-SOURCES = ("bsa_api.cu", "bsa_select.cu", "bsa_fmha.cu", "bsa_bwd.cu")
+SOURCES = ("bsa_api.cu", "bsa_select.cu", "bsa_fmha.cu", "bsa_bwd.cu", "bsa_rope.cu", "bsa_paged.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,6 +49,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "bsa.h"),
+                                                                 os.path.join(ROOT, "include", "bsa_paged.h"),
                                                                  os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 

@@ -12,6 +12,7 @@
 #include <string>
 
 #include "bsa_internal.h"
+#include "bsa_paged.h"
 
 namespace bsa {
 
@@ -505,7 +506,10 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
   // the forward kernels' and the backward kernels' error words (each read and cleared)
   const unsigned int ef = read_and_clear_fwd_error();
   const unsigned int eb = read_and_clear_bwd_error();
-  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu)
+  // and those of the cache append and the paged attention
+  const unsigned int er = read_and_clear_rope_error();
+  const unsigned int ep = read_and_clear_paged_error();
+  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || er == 0xFFFFFFFFu || ep == 0xFFFFFFFFu)
     return set_error(BSA_ERR_CUDA, "bsa_device_status: cannot read the device error word");
   int bad = 0;
   const int zero = 0;
@@ -520,8 +524,18 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
                      std::to_string(bad) + " malformed index-list rows reached bsa_forward / bsa_backward "
                      "(BSA_DEBUG validation: indices in range of the request's real key blocks and strictly "
                      "ascending, count 0 for query blocks without real rows)" +
-                         (((ef | eb) & 1u) ? "; a bounded device wait also gave up" : ""));
+                         (((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : ""));
   }
+  if ((er | ep) & kErrPage)
+    return set_error(BSA_ERR_INVALID_INDICES,
+                     std::string("a page table entry outside the cache, or a length without pages, reached ") +
+                         ((er & kErrPage) ? ((ep & kErrPage) ? "bsap_cache_append and bsap_forward" : "bsap_cache_append")
+                                          : "bsap_forward") +
+                         (((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : ""));
+  if (ep & 1u)
+    return set_error(BSA_ERR_TIMEOUT, std::string("a bounded device wait gave up in the ") +
+                                          (((ef | eb) & 1u) ? "paged attention and other" : "paged attention") +
+                                          " kernels (the kernel aborted its tiles)");
   if ((ef | eb) & 1u)
     return set_error(BSA_ERR_TIMEOUT, std::string("a bounded device wait gave up in the ") +
                                           (ef & 1u ? (eb & 1u ? "forward and backward" : "forward") : "backward") +

@@ -1,0 +1,34 @@
+// Host-side declarations of the position, cache and paged-attention calls.
+#pragma once
+
+#include <string>
+
+#include "../../include/bsa_paged.h"
+#include "bsa_internal.h"
+
+namespace bsa {
+
+// Bit of the device error words of bsa_rope.cu and bsa_paged.cu: a page table
+// entry that names no page, or a length without pages (bit 0: a bounded wait
+// gave up).
+constexpr unsigned int kErrPage = 2u;
+unsigned int read_and_clear_rope_error();
+unsigned int read_and_clear_paged_error();
+
+constexpr int kMaxPagedBatch = 4096;
+
+// [B, S, H, D] bf16 input of the calls of bsa_paged.h.  Strides of axes of
+// length 1 are replaced by 0; `cache`: strides of longer axes must be positive.
+bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, bool cache, bsa_tensor* view);
+
+// The paged cache and its tables, checked.
+struct PagedArgs {
+  bsa_tensor k, v;
+  const int32_t* page_table; int64_t table_stride; int max_pages;
+  const int32_t* kv_lens; const int32_t* new_lens;
+};
+bsa_status check_paged(const char* fn, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
+                       const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
+                       const int32_t* new_lens, int64_t B, PagedArgs* a);
+
+}  // namespace bsa

@@ -1,0 +1,337 @@
+"""Python binding of the calls of include/bsa_paged.h: rotary positions with
+several axes, the paged key/value cache, attention of new tokens over it.
+
+Argument checks and marshalling only, as in ``api``.  The names carry the
+package's ``bsa_`` prefix; the C entry points are ``bsap_rope_axes``,
+``bsap_cache_append`` and ``bsap_forward``.  ``stream`` is a torch stream or a
+raw stream handle (default: the current stream of the tensors' device);
+outputs and workspaces that a call makes itself are allocated on that stream.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from . import _lib
+from .api import _check, _check_buffer
+
+PAGE_SIZES_SUPPORTED = (16, 32, 64, 128, 256)
+
+
+def _tensor(t, name: str, device=None) -> _lib.BsaTensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16 (got {t.dtype})")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be 4-D [B, S, H, d] (got {tuple(t.shape)})")
+    sb, ss, sh, sd = t.stride()
+    B, S, H, D = t.shape
+    if sd != 1 and D != 1:
+        raise ValueError(f"{name} must have a contiguous last dim")
+    return _lib.BsaTensor(t.data_ptr(), B, S, H, D, sb, ss, sh)
+
+
+def _ints(t, name: str, device, shape) -> Optional[int]:
+    """Pointer of an int32 vector on the call's device (None passes as NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of shape {shape} on {device} "
+                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+    return t.data_ptr()
+
+
+def _positions(t, name: str, device, B: int, S: int):
+    """Descriptor of int32 positions [B, S, A] or [S, A] (shared by the batch)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"{name} must be a torch.int32 tensor on {device} (got {t.dtype}, {t.device})")
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    if t.dim() != 3 or t.shape[0] not in (1, B) or t.shape[1] != S:
+        raise ValueError(f"{name} must be [B, S, axes] or [S, axes] with B = {B}, S = {S} (got {tuple(t.shape)})")
+    sb, ss, sa = t.stride()
+    return _lib.BsapPositions(t.data_ptr(), sb if t.shape[0] > 1 else 0, ss if S > 1 else 0, sa), t.shape[2]
+
+
+def _rope(inv_freq, axes, n_axes: int, interleaved: bool, device) -> _lib.BsapRope:
+    for name, t, dtype in (("inv_freq", inv_freq, torch.float64), ("axes", axes, torch.int32)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on {device} "
+                             f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+    if inv_freq.numel() != axes.numel():
+        raise ValueError(f"inv_freq has {inv_freq.numel()} pairs, axes {axes.numel()}")
+    return _lib.BsapRope(inv_freq.data_ptr(), axes.data_ptr(), axes.numel(), n_axes, 1 if interleaved else 0)
+
+
+def _extent(t: torch.Tensor):
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
+def _check_overlap(name: str, out: torch.Tensor, inputs, in_place) -> None:
+    """Refuses an output that shares memory with an input, but for ``in_place``
+    itself when it is contiguous and starts where the output does."""
+    lo, hi = _extent(out)
+    for t in inputs:
+        a, z = _extent(t)
+        if lo < z and a < hi and not (t is in_place and a == lo and t.is_contiguous()):
+            raise ValueError(f"{name} overlaps an input (in place takes the whole contiguous input)")
+
+
+@contextlib.contextmanager
+def _elsewhere(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device)
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _on(device, stream):
+    """Makes the tensors' device and the call's stream current."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _elsewhere(device, stream)
+
+
+def _current():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def bsa_axis_frequencies(sections: Sequence[int], theta: float = 10000.0, layout: str = "sections", device="cuda"):
+    """``(inv_freq, axes)`` device tensors for ``bsa_rope_axes``: pair counts
+    per axis in ``sections`` (e.g. time, height, width), n pairs in all.
+
+    ``layout``: ``"sections"`` cuts one spectrum theta^(-p/n) into consecutive
+    sections; ``"per_axis"`` gives each axis a spectrum theta^(-i/sections[a])
+    of its own; ``"cycled"`` deals the one spectrum's pairs to the axes in
+    turn, until an axis has its share.
+    """
+    sections = [int(x) for x in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) == 0:
+        raise ValueError(f"sections must be 1 to 4 non-negative pair counts (got {sections})")
+    n = sum(sections)
+    if layout == "cycled":
+        left, axes = list(sections), []
+        while len(axes) < n:
+            for a in range(len(left)):
+                if left[a]:
+                    left[a] -= 1
+                    axes.append(a)
+    elif layout in ("sections", "per_axis"):
+        axes = [a for a, m in enumerate(sections) for _ in range(m)]
+    else:
+        raise ValueError(f"layout must be 'sections', 'per_axis' or 'cycled' (got {layout!r})")
+    if layout == "per_axis":
+        inv = [float(theta) ** (-i / m) for m in sections for i in range(m)]
+    else:
+        inv = [float(theta) ** (-p / n) for p in range(n)]
+    return (torch.tensor(inv, dtype=torch.float64, device=device),
+            torch.tensor(axes, dtype=torch.int32, device=device))
+
+
+def _rope_call(q, k, pos_q, pos_k, inv_freq, axes, interleaved, backward, q_out, k_out, stream, names):
+    qd = _tensor(q, names[0])
+    dev = q.device
+    B, S, Hq, d = q.shape
+    pq, n_axes = _positions(pos_q, "pos_q", dev, B, S)
+    rope = _rope(inv_freq, axes, n_axes, interleaved, dev)
+    kd = pk = None
+    if k is not None:
+        kd = _tensor(k, names[1], dev)
+        pk, nk = _positions(pos_k, "pos_k", dev, k.shape[0], k.shape[1])
+        if nk != n_axes:
+            raise ValueError(f"pos_q has {n_axes} axes, pos_k {nk}")
+    elif k_out is not None:
+        raise ValueError(f"{names[3]} is given without {names[1]}")
+    inputs = [t for t in (q, k) if t is not None]
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _check_buffer(names[2], q_out, q.shape, torch.bfloat16, dev)
+            _check_overlap(names[2], q_out, inputs, q)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+            else:
+                _check_buffer(names[3], k_out, k.shape, torch.bfloat16, dev)
+                _check_overlap(names[3], k_out, [*inputs, q_out], k)
+        _check(_lib.load().bsap_rope_axes(ctypes.byref(qd), ctypes.byref(kd) if kd is not None else None,
+                                          ctypes.byref(pq), ctypes.byref(pk) if pk is not None else None,
+                                          ctypes.byref(rope), 1 if backward else 0, q_out.data_ptr(),
+                                          k_out.data_ptr() if k is not None else None, _current()))
+    return q_out, k_out
+
+
+def bsa_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos_q: torch.Tensor, pos_k: Optional[torch.Tensor],
+                  inv_freq: torch.Tensor, axes: torch.Tensor, *, interleaved: bool = False,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions with several axes: pair p of a head's channels is turned
+    by ``position[axes[p]] * inv_freq[p]``.
+
+    q ``[B, S, Hq, d]``, k ``[B2, S2, Hkv, d]`` or None; positions int32 ``[B,
+    S, A]`` or ``[S, A]`` (A = 1..4, any strides: a permuted ``[A, B, S]`` is
+    fine); ``inv_freq`` fp64 and ``axes`` int32 ``[pairs]`` on the GPU (see
+    ``bsa_axis_frequencies``), pairs a multiple of 8, at most d/2.  Pairs are
+    channels (p, p + pairs), or (2p, 2p + 1) with ``interleaved``; channels from
+    2 * pairs on pass through.  Returns ``(q_out, k_out)``, contiguous, to pass
+    to ``bsa_select`` and ``bsa_forward``; in place with ``q_out=q`` when q is
+    contiguous.
+    """
+    return _rope_call(q, k, pos_q, pos_k, inv_freq, axes, interleaved, False, q_out, k_out, stream,
+                      ("q", "k", "q_out", "k_out"))
+
+
+def bsa_rope_axes_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], pos_q: torch.Tensor,
+                           pos_k: Optional[torch.Tensor], inv_freq: torch.Tensor, axes: torch.Tensor, *,
+                           interleaved: bool = False, dq_out: Optional[torch.Tensor] = None,
+                           dk_out: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of ``bsa_rope_axes`` with respect to q and k, given those of
+    its outputs (as ``bsa_backward`` returns them): the rotation turned back."""
+    return _rope_call(dq, dk, pos_q, pos_k, inv_freq, axes, interleaved, True, dq_out, dk_out, stream,
+                      ("dq", "dk", "dq_out", "dk_out"))
+
+
+def _table(page_table, B: int, device):
+    if not isinstance(page_table, torch.Tensor):
+        raise TypeError("page_table must be a torch.Tensor")
+    if page_table.dtype != torch.int32 or page_table.device != device:
+        raise ValueError(f"page_table must be a torch.int32 tensor on {device} (got {page_table.dtype}, "
+                         f"{page_table.device})")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [B, max_pages] with B = {B} (got {tuple(page_table.shape)})")
+    n = page_table.shape[1]
+    if n > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have a contiguous last dim")
+    return page_table.data_ptr(), page_table.stride(0) if B > 1 else n, n
+
+
+def bsa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     page_table: torch.Tensor, kv_lens: torch.Tensor, *, new_lens: Optional[torch.Tensor] = None,
+                     q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, axes: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, q_out: Optional[torch.Tensor] = None, stream=None):
+    """Writes new keys and values ``[B, T, Hkv, d]`` into a paged cache
+    ``[pages, page_size, Hkv, d]``, K rotated on the way.
+
+    Token t of request b goes to key position ``kv_lens[b] - n + t``, where
+    ``kv_lens`` (int32 ``[B]``) counts the request's keys INCLUDING its n =
+    ``new_lens[b]`` (default T) new ones; tokens from n on are not written, and
+    nothing else of the cache changes.  ``page_table`` int32 ``[B, max_pages]``:
+    request b's pages in order (entries behind its length are not read).
+    With ``positions`` (int32 ``[B, T, A]``), ``inv_freq`` and ``axes`` k is
+    rotated as by ``bsa_rope_axes``, and so is ``q`` when given (all T rows);
+    without them k is copied.  Returns the rotated q, or None.
+    """
+    kd = _tensor(k, "k")
+    dev = k.device
+    vd, kc, vc = _tensor(v, "v", dev), _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
+    B, T = k.shape[:2]
+    table, stride, n = _table(page_table, B, dev)
+    lens = _ints(kv_lens, "kv_lens", dev, (B,))
+    new = _ints(new_lens, "new_lens", dev, (B,))
+    rope = pos = qd = None
+    if positions is not None:
+        pos, n_axes = _positions(positions, "positions", dev, B, T)
+        rope = _rope(inv_freq, axes, n_axes, interleaved, dev)
+    elif inv_freq is not None or axes is not None or q is not None:
+        raise ValueError("inv_freq, axes and q are given without positions")
+    if q is not None:
+        qd = _tensor(q, "q", dev)
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    with _on(dev, stream):
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            else:
+                _check_buffer("q_out", q_out, q.shape, torch.bfloat16, dev)
+                _check_overlap("q_out", q_out, (q, k, v, k_cache, v_cache), q)
+        _check(_lib.load().bsap_cache_append(
+            ctypes.byref(kd), ctypes.byref(vd), ctypes.byref(kc), ctypes.byref(vc), table, stride, n, lens, new,
+            ctypes.byref(rope) if rope is not None else None, ctypes.byref(pos) if pos is not None else None,
+            ctypes.byref(qd) if qd is not None else None, q_out.data_ptr() if q is not None else None, _current()))
+    return q_out
+
+
+def bsa_forward_paged_workspace_size(B, T, Hq, Hkv, d, has_prefix, num_sms=0) -> int:
+    return int(_lib.load().bsap_forward_workspace_size(B, T, Hq, Hkv, d, 1 if has_prefix else 0, num_sms))
+
+
+def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                      kv_lens: torch.Tensor, *, new_lens: Optional[torch.Tensor] = None,
+                      prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0, causal: bool = True,
+                      softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                      workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of T new tokens per request over a paged cache, the form of
+    ``bsa_forward_causal`` for tokens that come later (T = 1: one decoding step).
+
+    q ``[B, T, Hq, d]``; cache, ``page_table``, ``kv_lens`` and ``new_lens`` as
+    in ``bsa_cache_append`` (which is called first: ``kv_lens`` includes the new
+    tokens).  Row i < n of request b sees the first ``prefix_len`` keys of the
+    pages ``prefix_table`` (int32 ``[pages]``), which all requests share and
+    which are read once for the batch, and its request's own keys, with
+    ``causal`` only those up to position ``kv_lens[b] - n + i``.  Rows from n
+    on, and rows without a key, get output 0 and LSE -inf.
+
+    Returns ``(out [B, T, Hq, d] bf16, lse [B, Hq, T] fp32 or None)``.
+    """
+    qd = _tensor(q, "q")
+    dev = q.device
+    kc, vc = _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
+    B, T, Hq, d = q.shape
+    table, stride, n = _table(page_table, B, dev)
+    lens = _ints(kv_lens, "kv_lens", dev, (B,))
+    new = _ints(new_lens, "new_lens", dev, (B,))
+    prefix_len = int(prefix_len)
+    shared = None
+    if prefix_len > 0:
+        if prefix_table is None:
+            raise ValueError(f"prefix_len is {prefix_len}, prefix_table is None")
+        shared = _ints(prefix_table, "prefix_table", dev, (prefix_table.numel(),))
+        if prefix_table.numel() * k_cache.shape[1] < prefix_len:
+            raise ValueError(f"prefix_table has {prefix_table.numel()} pages of {k_cache.shape[1]}, prefix_len is "
+                             f"{prefix_len}")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_buffer("out", out, (B, T, Hq, d), torch.bfloat16, dev)
+            _check_overlap("out", out, (q, k_cache, v_cache), None)
+        if lse is not None:
+            _check_buffer("lse", lse, (B, Hq, T), torch.float32, dev)
+        elif return_lse:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        lib = _lib.load()
+        if workspace is None:
+            need = lib.bsap_forward_workspace_size(B, T, Hq, k_cache.shape[2], d, 1 if prefix_len > 0 else 0, 0)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _check_buffer("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        _check(lib.bsap_forward(ctypes.byref(qd), ctypes.byref(kc), ctypes.byref(vc), table, stride, n, lens, new,
+                                shared, prefix_len, 1 if causal else 0, float(softmax_scale), out.data_ptr(),
+                                lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                                workspace.numel(), _current()))
+    return out, lse

@@ -1,0 +1,134 @@
+/*
+ * bsa_paged.h -- C ABI of libbsa, second part: rotary positions with several
+ * axes, a paged key/value cache, and attention of new tokens over it.
+ *
+ * These calls stand around the ones of bsa.h.  bsap_rope_axes turns Q and K
+ * before bsa_select / bsa_forward (and bsap_rope_axes with `backward` turns
+ * the gradients bsa_backward returns); bsap_cache_append keeps the keys and
+ * values of the understanding stream, or of any token stream, in pages;
+ * bsap_forward is the form of bsa_forward_causal for tokens that come later:
+ * one new token per request, a few, or a chunk, over the pages, with a prefix
+ * that every request of the batch shares.
+ *
+ * The conventions of bsa.h hold: device memory is the caller's, nothing is
+ * allocated, no call synchronises, all work is enqueued on the caller's
+ * stream, arguments are checked on the host before anything is launched, the
+ * message of a refusal comes from bsa_get_last_error(), and every call can be
+ * captured in a CUDA graph.  Head dim 64 or 128, bf16.  The symbols carry the
+ * prefix bsap_.
+ *
+ * Lengths and tables that change from step to step (kv_lens, new_lens, the
+ * page tables, positions, frequencies) are DEVICE arrays that the kernels read
+ * when they run, so that a captured step follows them.  The host cannot check
+ * their values.  The kernels do: they never read or write outside the given
+ * buffers, and a table entry that names no page, or a length that the table
+ * has no pages for, sets an error word that the next bsa_device_status()
+ * returns as BSA_ERR_INVALID_INDICES (results of the requests concerned are
+ * then unspecified).
+ */
+#ifndef BSA_PAGED_H_
+#define BSA_PAGED_H_
+
+#include "bsa.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------- rotation ---
+ * Pair p of `pairs` (a multiple of 8, at most D / 2) is the channels
+ * (p, p + pairs), or with interleaved != 0 (2p, 2p + 1).  Its angle at a token
+ * is position[axes[p]] * inv_freq[p], and
+ *     y_lo = x_lo cos - x_hi sin,    y_hi = x_hi cos + x_lo sin.
+ * Channels from 2 * pairs on, and pairs whose axis is outside [0, n_axes),
+ * are passed through.  Angles are formed in 64-bit fixed point (turns modulo
+ * one), so that they are as exact at position 2^30 as at position 1; products
+ * are fp32, rounded to bf16 once.
+ * inv_freq: device double [pairs], finite, |inv_freq| < 2^10 (radians per
+ *   position).  axes: device int32 [pairs].  n_axes: 1 to 4. */
+typedef struct bsap_rope {
+  const double* inv_freq;
+  const int32_t* axes;
+  int32_t pairs, n_axes, interleaved;
+} bsap_rope;
+
+/* int32 positions [B, S, n_axes] in device memory; strides in elements, a
+ * stride of 0 shares positions along that axis. */
+typedef struct bsap_positions {
+  const int32_t* ptr;
+  int64_t stride_b, stride_s, stride_a;
+} bsap_positions;
+
+/* Rotates q, and k too unless it is NULL, in one launch.
+ * q [B, S, Hq, D], k [B2, S2, Hk, D]: inputs as bsa_tensor; here a stride may
+ *   be 0 (a broadcast input), and strides of axes of length 1 are not looked at.
+ * q_out, k_out: bf16 contiguous, 16-byte aligned, of the input's shape; may be
+ *   the input's own storage when the input is contiguous, and may otherwise
+ *   not overlap any input.
+ * backward != 0: the transposed rotation, which takes the gradients of q_out
+ *   and k_out to those of q and k. */
+BSA_API bsa_status bsap_rope_axes(const bsa_tensor* q, const bsa_tensor* k, const bsap_positions* pos_q,
+                                  const bsap_positions* pos_k, const bsap_rope* rope, int32_t backward,
+                                  void* q_out, void* k_out, bsa_stream_t stream);
+
+/* ---------------------------------------------------------- paged cache ---
+ * k_cache, v_cache: bsa_tensor with B = number of pages, S = page size (16,
+ *   32, 64, 128 or 256 slots), H = Hkv, D; same shape, any strides that keep
+ *   rows 16-byte aligned and slots apart.
+ * page_table: device int32, request b's pages at page_table[b * table_stride
+ *   + 0 .. max_pages).  Key j of request b lies in page table[b][j / S], slot
+ *   j % S.  Entries behind a request's length are not read.
+ * kv_lens: device int32 [B], keys of request b INCLUDING the call's new tokens.
+ * new_lens: device int32 [B], the request's real new tokens, or NULL = all T;
+ *   clamped to [0, T].
+ *
+ * Append: token t < new_lens[b] of k and v [B, T, Hkv, D] is written to key
+ *   position kv_lens[b] - new_lens[b] + t of request b; a token whose position
+ *   is negative or behind the table, or whose page does not exist, is dropped
+ *   and reported.  Nothing else of the cache changes.  With `rope`, k is
+ *   rotated on the way at pos [B, T, n_axes], and so are the queries q [B, T,
+ *   Hq, D] into q_out (contiguous, all T rows, also behind new_lens; in place
+ *   when q is contiguous); q may be NULL, and rope NULL copies k (q must then
+ *   be NULL).  Two tokens with the same page and slot are the caller's
+ *   mistake: which of them stays, K and V each, is unspecified. */
+BSA_API bsa_status bsap_cache_append(const bsa_tensor* k, const bsa_tensor* v, const bsa_tensor* k_cache,
+                                     const bsa_tensor* v_cache, const int32_t* page_table, int64_t table_stride,
+                                     int32_t max_pages, const int32_t* kv_lens, const int32_t* new_lens,
+                                     const bsap_rope* rope, const bsap_positions* pos, const bsa_tensor* q,
+                                     void* q_out, bsa_stream_t stream);
+
+/* ------------------------------------------------------------ attention ---
+ * Workspace bytes of bsap_forward for B requests of T new tokens on a device
+ * with num_sms SMs (0: the current device): partial sums of the key ranges
+ * that the thread blocks split the keys into.  0 for sizes that bsap_forward refuses. */
+BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has_prefix, int num_sms);
+
+/* Row i < n = new_lens[b] of request b (q [B, T, Hq, D]) attends, with query
+ * head h reading KV head h / (Hq / Hkv),
+ *   - the prefix_len first keys of the pages prefix_table[0 .. ceil(prefix_len
+ *     / S)), the same for every request, read once for the whole batch, and
+ *   - its request's own keys j < kv_lens[b]; with causal != 0 only
+ *     j <= kv_lens[b] - n + i.
+ * out_i = sum_j softmax(z)_j v_j (bf16), z_j = softmax_scale q_i . k_j;
+ * lse_i = ln sum_j exp(z_j).  Rows i >= n and rows without a key: out 0, lse
+ * -inf.  Slots behind a request's keys are never read into a result, whatever
+ * they hold; the values of real keys have to be finite.
+ * out: bf16 [B, T, Hq, D] contiguous; lse: fp32 [B, Hq, T] contiguous or NULL.
+ * softmax_scale <= 0 selects D^-1/2.  prefix_len 0: prefix_table may be NULL.
+ * max_pages 0: no own keys (page_table and kv_lens may be NULL).
+ * Results do not depend on scheduling (no atomics), but the split of the keys
+ * depends on the lengths of the whole batch and on the number of SMs.
+ * B <= 4096, Hq <= 256.  workspace: device, 256-byte aligned; every byte that
+ * is read was written by the same call, so calls that follow one another on a
+ * stream, captured or not, may share one; calls that overlap may not. */
+BSA_API bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
+                                const int32_t* page_table, int64_t table_stride, int32_t max_pages,
+                                const int32_t* kv_lens, const int32_t* new_lens, const int32_t* prefix_table,
+                                int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
+                                void* workspace, size_t ws_bytes, bsa_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* BSA_PAGED_H_ */
