@@ -1,14 +1,41 @@
 // Attention of new tokens over a paged key/value cache whose first prefix_len
-// keys all requests share.
+// keys all requests share (tcgen05 + TMEM + TMA).
 //
 // Mathematics: row i of request b and query head h sees the prefix keys and
 // its request's own keys up to a limit; out = sum_j e^{z_j} v_j / sum_j
 // e^{z_j}, computed over any split of the keys as partial (max, sum, sum of
 // v) triples that are joined by rescaling to the common maximum.
+//
+// What bounds it: for one token per request, reading K and V once (each 64 KB
+// of a 128-key tile of K and V at head dim 128 takes an SM 1.5 us at its share
+// of the memory rate, while its two products and its softmax take 0.7 us);
+// with hundreds of rows on one prefix, the exponentials (16 a clock and SM).
+//
+// Layout of the work:
+//  * A segment is up to 128 query rows that read the same keys: for the prefix
+//    any 128 rows (b, i, g) of the whole batch under one KV head, so that the
+//    prefix is read once for all; for a request's own keys the rows (i, g) of
+//    that request under one KV head.  A GQA group's heads are rows of one tile.
+//  * All segments' 128-key tiles are put in one row and cut into equal pieces,
+//    one for each CTA, whatever the lengths are (they are read from the device,
+//    so a captured graph follows them).  A cut segment leaves one partial
+//    result per CTA; the pair (segment, CTA) only ever steps forward along the
+//    row, so segment + CTA numbers the partial results without gaps of meaning
+//    and without a table.
+//  * One CTA per SM: warp 0 gathers K and V tiles page by page with TMA into
+//    one ring in the order the products use them (K_0, K_1, V_0, K_2, V_1 ..),
+//    warp 1 issues the MMAs (S = Q K^T of tile q + 1 before O += P V of tile
+//    q), warps 2 and 3 load the next segment's Q rows, warps 4-7 do the online
+//    softmax with one row per thread, P staying in TMEM, and write the result.
+//    S and O each have two buffers in TMEM, so neither the next tile nor the
+//    next segment waits for the softmax or for the results' way out.
+//  * paged_join_kernel adds up the partial results (launched with programmatic
+//    dependence, so that it is resident when the first kernel ends).
 #include <cuda_bf16.h>
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 #include "bsa_paged.h"
@@ -17,94 +44,792 @@
 namespace bsa {
 namespace {
 
+constexpr int kTileKeys = 128;
+constexpr int kRowTile = 128;
+constexpr int kPagedThreads = 256;
+constexpr int kMaxBlocks = kMaxPagedBatch / 32;     // blocks of 32 requests in the schedule
+
+template <int D>
+struct PagedCfg {
+  static constexpr int kChunks = D / 64;                      // 128-byte chunks per row
+  static constexpr int kQBytes = kRowTile * 128 * kChunks;
+  static constexpr int kTileBytes = kTileKeys * 128 * kChunks;
+  static constexpr int kBarBytes = 1024;
+  static constexpr int kSmemMax = 232448;                     // 227 KB per CTA
+  static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - 2 * kQBytes) / kTileBytes;
+  static constexpr int kStages = kFit > 10 ? 10 : kFit;       // 5 of 32 KB, 10 of 16 KB
+  static constexpr int kSmemBytes = 1024 + kBarBytes + 2 * kQBytes + kStages * kTileBytes;
+};
+
 struct PagedParams {
+  CUtensorMap tk, tv;             // [pages, Hkv, slots, D] of the whole cache
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
-  const __nv_bfloat16* k; int64_t k_sp, k_ss, k_sh;
-  const __nv_bfloat16* v; int64_t v_sp, v_ss, v_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
+  int TG;                         // rows of a request under one KV head
+  int own_rt;                     // row tiles of a request
+  int pre_rt;                     // row tiles of the whole batch (prefix)
+  int pre_tiles;                  // key tiles of the prefix
+  int pre_slot_rows, own_slot_rows;   // rows of a partial result's slot
+  int ctas;
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
+  int32_t* cum;                   // workspace: [B + 1] tiles of own keys before request b
+  float* pre_ml; float* pre_o;    // workspace: partial (max, sum) and rows, prefix
+  float* own_ml; float* own_o;    // the same, own keys
 };
 
 // Request b's own keys and new tokens, clamped to what the tables hold.
 __device__ __forceinline__ int own_keys(const PagedParams& p, int b) {
   if (p.max_pages == 0) return 0;
-  const int kv = __ldg(p.kv_lens + b), most = p.max_pages << p.page_shift;
-  return min(max(kv, 0), most);
+  return min(max(__ldg(p.kv_lens + b), 0), p.max_pages << p.page_shift);
 }
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
   return p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.T) : p.T;
 }
+// Own keys that row i of a request with kv keys and n new tokens sees.
+__device__ __forceinline__ int seen_keys(const PagedParams& p, int kv, int n, int i) {
+  return p.causal ? max(kv - n + i + 1, 0) : kv;
+}
+// Key tiles of row tile rt of such a request.
+__device__ __forceinline__ int own_tiles(const PagedParams& p, int kv, int n, int rt) {
+  const int first = rt * kRowTile / p.G;
+  if (first >= n) return 0;
+  const int last = min(n - 1, (rt * kRowTile + kRowTile - 1) / p.G);
+  return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
+}
+// Key tiles of request b under one KV head.
+__device__ __forceinline__ int request_tiles(const PagedParams& p, int b) {
+  const int kv = own_keys(p, b), n = new_tokens(p, b);
+  int sum = 0;
+  for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles(p, kv, n, rt);
+  return sum;
+}
 
-// One block of four warps per output row; each warp takes every fourth key.
+__device__ __forceinline__ int warp_inclusive_sum(int v) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+// Among W tiles, the CTAs that get some (every one of them at least one),
+// the first tile of CTA c of n, and the CTA of tile t.
+__device__ __forceinline__ int cta_count(const PagedParams& p, int W) { return min(p.ctas, W); }
+__device__ __forceinline__ int cta_begin(int c, int n, int W) { return (int)((int64_t)c * W / n); }
+__device__ __forceinline__ int cta_of(int t, int n, int W) { return (int)((((int64_t)t + 1) * n - 1) / W); }
+
+// A segment's part that one CTA works on.
+struct Segment {
+  int b;               // request, -1: prefix
+  int hk;
+  int row0, rows;      // first flat row (b * T + i) * G + g, and how many
+  int tile0, tiles;    // first key tile and how many
+  int slot;            // number of the partial result (segment + CTA)
+  int whole;           // this CTA has all tiles of the segment
+  int keys;            // keys that stand in the source
+  int kv, n;           // of the request
+};
+
+// The segment that holds tile t and its part before tile `end` (all lanes of
+// a warp call it; the CTA's tiles are [begin, end); block_sum[i] = tiles of own
+// keys before request 32 i).
+__device__ __forceinline__ Segment find_segment(const PagedParams& p, const int* block_sum, int cta, int begin, int t,
+                                                int end) {
+  Segment s;
+  const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+  int t0, t1;
+  if (t < pre) {
+    const int seg = t / p.pre_tiles;
+    t0 = seg * p.pre_tiles;
+    t1 = t0 + p.pre_tiles;
+    s.b = -1;
+    s.hk = seg / p.pre_rt;
+    s.row0 = (seg % p.pre_rt) * kRowTile;
+    s.rows = min(kRowTile, p.B * p.TG - s.row0);
+    s.slot = seg + cta;
+    s.keys = p.prefix_len;
+    s.kv = s.n = 0;
+  } else {
+    const int u = t - pre, lane = threadIdx.x % 32;
+    int blk = 0;
+    for (int i = 32; i < p.B && block_sum[i / 32] <= u; i += 32) ++blk;
+    const int b0 = blk * 32 + lane;
+    const int mine = b0 < p.B ? request_tiles(p, b0) * p.Hkv : 0;
+    const int upto = warp_inclusive_sum(mine) + block_sum[blk];
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > u);
+    const int src = __ffs(past) - 1;               // there is one: u < W - pre
+    s.b = blk * 32 + src;
+    const int all = __shfl_sync(0xffffffffu, mine, src), before = __shfl_sync(0xffffffffu, upto, src) - all;
+    const int per_head = all / p.Hkv;
+    s.hk = (u - before) / per_head;
+    s.kv = own_keys(p, s.b);
+    s.n = new_tokens(p, s.b);
+    t0 = pre + before + s.hk * per_head;
+    int rt = 0, m = own_tiles(p, s.kv, s.n, 0);
+    while (t >= t0 + m) {
+      t0 += m;
+      m = own_tiles(p, s.kv, s.n, ++rt);
+    }
+    t1 = t0 + m;
+    s.row0 = s.b * p.TG + rt * kRowTile;
+    s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
+    s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
+    s.keys = s.kv;
+  }
+  s.tile0 = t - t0;
+  s.tiles = min(t1, end) - t;
+  s.whole = begin <= t0 && t1 <= end;
+  return s;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// Orders this thread's shared-memory writes before later reads by the async
+// proxy (the MMAs read Q and V through it).
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// mbar_wait by all lanes of a warp, with one answer for all of them (what
+// follows uses warp-wide instructions).
+__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort));
+}
+
+template <int N>
+__device__ __forceinline__ void advance(uint32_t& stage, uint32_t& phase) {
+  if (++stage == N) { stage = 0; phase ^= 1u; }
+}
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_rows_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kPer = D / 32;
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
+  using C = PagedCfg<D>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* q_smem = smem;                                  // [2] Q buffers
+  uint8_t* ring = smem + 2 * C::kQBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kStages * C::kTileBytes);
+  uint64_t* q_full = bars;              // [2] 64 loader threads
+  uint64_t* q_empty = bars + 2;         // [2] commit
+  uint64_t* s_full = bars + 4;          // [2] commit
+  uint64_t* p_full = bars + 6;          // [2] 4 softmax warps
+  uint64_t* o_empty = bars + 8;         // [2] 4 softmax warps
+  uint64_t* pv_done = bars + 10;        // commit
+  uint64_t* mma_end = bars + 11;        // commit
+  uint64_t* full = bars + 12;           // [kStages] transaction bytes
+  uint64_t* empty = full + kStages;     // [kStages] commit
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + kStages);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* total_slot = reinterpret_cast<int*>(tmem_slot + 2);
+  int* block_sum = total_slot + 1;      // [kMaxBlocks]
+  static_assert((12 + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes, "barrier block");
+
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t row = blockIdx.x;                 // (b * T + i) * Hq + h
-  const int h = (int)(row % p.Hq);
-  const int64_t bt = row / p.Hq;
-  const int b = (int)(bt / p.T), i = (int)(bt % p.T), hk = h / p.G;
-  const int n = new_tokens(p, b), kv = own_keys(p, b);
-  if (threadIdx.x == 0 && i == 0 && p.max_pages > 0 && (p.kv_lens[b] < 0 || p.kv_lens[b] > p.max_pages << p.page_shift))
-    atomicOr(&g_bsa_error, kErrPage);
-  const int own = i >= n ? 0 : (p.causal ? max(min(kv - n + i + 1, kv), 0) : kv);
-  const int total = i >= n ? 0 : p.prefix_len + own;
-  float q[kPer], acc[kPer], m = -INFINITY, l = 0.f;
-  const __nv_bfloat16* qr = p.q + b * p.q_sb + i * p.q_ss + h * p.q_sh + lane * kPer;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    q[e] = __bfloat162float(qr[e]);
-    acc[e] = 0.f;
-  }
-  for (int j = warp; j < total; j += 4) {
-    const int32_t* table = j < p.prefix_len ? p.prefix_table : p.page_table + b * p.table_stride;
-    const int jj = j < p.prefix_len ? j : j - p.prefix_len;
-    const int page = __ldg(table + (jj >> p.page_shift)), slot = jj & ((1 << p.page_shift) - 1);
-    const bool there = page >= 0 && page < p.num_pages;
-    if (!there && lane == 0) atomicOr(&g_bsa_error, kErrPage);
-    const __nv_bfloat16* kr = p.k + page * p.k_sp + slot * p.k_ss + hk * p.k_sh + lane * kPer;
-    const __nv_bfloat16* vr = p.v + page * p.v_sp + slot * p.v_ss + hk * p.v_sh + lane * kPer;
-    float z = 0.f, vv[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      z = fmaf(q[e], there ? __bfloat162float(kr[e]) : 0.f, z);
-      vv[e] = there ? __bfloat162float(vr[e]) : 0.f;
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(q_full + i), 64);
+      mbar_init(smem_u32(q_empty + i), 1);
+      mbar_init(smem_u32(s_full + i), 1);
+      mbar_init(smem_u32(p_full + i), 4);
+      mbar_init(smem_u32(o_empty + i), 4);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    z *= p.scale_log2;
-    const float m2 = fmaxf(m, z), a = exp2f(m - m2), w = exp2f(z - m2);
-    m = m2;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * a + w * vv[e];
+    mbar_init(smem_u32(pv_done), 1);
+    mbar_init(smem_u32(mma_end), 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
   }
-  __shared__ float sm[4], sl[4], so[4][D];
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = acc[e];
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // the schedule: tiles of own keys per block of 32 requests, then their sums
+  const int nblk = (p.B + 31) / 32;
+  for (int blk = warp; blk < nblk; blk += kPagedThreads / 32) {
+    const int b = blk * 32 + lane;
+    const int sum = warp_inclusive_sum(b < p.B ? request_tiles(p, b) * p.Hkv : 0);
+    if (lane == 31) block_sum[blk] = sum;
+    if (cta == 0 && b < p.B && p.max_pages > 0) {
+      const int kv = __ldg(p.kv_lens + b);
+      if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+    }
+  }
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x < D) {
-    const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float o = 0.f, ll = 0.f;
-    for (int w = 0; w < 4; ++w) {
-      const float a = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - mm);
-      o += a * so[w][threadIdx.x];
-      ll += a * sl[w];
+  tc_fence_after();
+  if (warp == 0) {
+    int before = 0;
+    for (int i = 0; i < nblk; i += 32) {
+      const int v = i + lane < nblk ? block_sum[i + lane] : 0;
+      const int incl = warp_inclusive_sum(v) + before;
+      if (i + lane < nblk) block_sum[i + lane] = incl - v;
+      before = __shfl_sync(0xffffffffu, incl, 31);
     }
-    p.out[row * D + threadIdx.x] = __float2bfloat16_rn(ll > 0.f ? o / ll : 0.f);
-    if (threadIdx.x == 0 && p.lse)
-      p.lse[((int64_t)b * p.Hq + h) * p.T + i] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) *total_slot = before;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  const int W = *total_slot + p.pre_tiles * p.pre_rt * p.Hkv;
+  if (cta == 0) {                       // the join finds each request's tiles here
+    for (int blk = warp; blk < nblk; blk += kPagedThreads / 32) {
+      const int b = blk * 32 + lane;
+      const int mine = b < p.B ? request_tiles(p, b) * p.Hkv : 0;
+      const int incl = warp_inclusive_sum(mine) + block_sum[blk];
+      if (b < p.B) p.cum[b] = incl - mine;
+    }
+    if (threadIdx.x == 0) p.cum[p.B] = *total_slot;
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int ctas = cta_count(p, W);
+  const int begin = cta < ctas ? cta_begin(cta, ctas, W) : 0, end = cta < ctas ? cta_begin(cta + 1, ctas, W) : 0;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer ---
+    // K of tile q, then V of tile q - 1, for every tile of the CTA's row.
+    const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;   // pages per tile
+    const int box_rows = kTileKeys / per_tile;
+    const uint32_t ring_base = smem_u32(ring);
+    uint32_t stage = 0, phase = 0;
+    int v_page = 0, v_slot = 0, v_hk = 0;          // of the tile whose V is still to come
+    auto load = [&](const CUtensorMap* map, int page, int slot, int hk) -> bool {
+      bool go = true;
+      if (lane == 0) {
+        go = mbar_wait(smem_u32(empty + stage), phase ^ 1u, abort_flag);
+        if (go) mbar_arrive_expect_tx(smem_u32(full + stage), C::kTileBytes);
+      }
+      go = __shfl_sync(0xffffffffu, go, 0);
+      if (go && lane < per_tile) {
+        const uint32_t dst = ring_base + stage * C::kTileBytes + lane * box_rows * 128;
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_load_4d(dst + c * (kTileKeys * 128), map, smem_u32(full + stage), c * 64, slot, hk, page);
+      }
+      __syncwarp();
+      if (go) advance<kStages>(stage, phase);
+      return go;
+    };
+    for (int t = begin; t < end && ok;) {
+      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+      auto page_of = [&](int j) {                  // lane's page of key tile j (a page past the end reads zeros)
+        const int key = j * kTileKeys + lane * box_rows;
+        int page = p.num_pages;
+        if (lane < per_tile && key < s.keys) {
+          page = __ldg(table + (key >> p.page_shift));
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_bsa_error, kErrPage);
+            page = p.num_pages;
+          }
+        }
+        return page;
+      };
+      int page = page_of(s.tile0);
+      for (int j = s.tile0; j < s.tile0 + s.tiles && ok; ++j) {
+        const int next = j + 1 < s.tile0 + s.tiles ? page_of(j + 1) : 0;
+        const int slot = (j * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
+        ok = load(&p.tk, page, slot, s.hk);
+        if (ok && (j > s.tile0 || t > begin)) ok = load(&p.tv, v_page, v_slot, v_hk);
+        v_page = page; v_slot = slot; v_hk = s.hk;
+        page = next;
+      }
+      t += s.tiles;
+    }
+    if (ok && begin < end) load(&p.tv, v_page, v_slot, v_hk);
+    // the copies in flight land before the CTA may leave
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_drain(smem_u32(full + stage), phase ^ 1u);
+        advance<kStages>(stage, phase);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer ---
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, true);
+    const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_smem), 16, 1024);
+    const uint64_t kdesc0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t vdesc0 = sdesc_sw128(smem_u32(ring), kTileKeys * 128, 1024);
+    uint32_t stage = 0, phase = 0, q = 0, seg = 0;
+    bool v_first = false;               // of the tile whose P V is still to come
+    uint32_t v_seg = 0;
+    auto product = [&]() -> bool {      // O (+)= P V of tile q - 1
+      const uint32_t tile = q - 1, sb = tile & 1u, ob = v_seg & 1u;
+      if (v_first && !mbar_wait(smem_u32(o_empty + ob), ((v_seg >> 1) & 1u) ^ 1u, abort_flag)) return false;
+      if (!mbar_wait(smem_u32(p_full + sb), (tile >> 1) & 1u, abort_flag)) return false;
+      if (!mbar_wait(smem_u32(full + stage), phase, abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t bs = vdesc0 + (uint64_t)((stage * C::kTileBytes) >> 4);
+      const uint32_t d_t = tmem + 256 + ob * 128, a_t = tmem + sb * 128;
+#pragma unroll
+      for (int kk = 0; kk < kTileKeys / 16; ++kk)
+        mma_ts(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o, kk > 0 || !v_first);
+      mma_commit(smem_u32(empty + stage));
+      mma_commit(smem_u32(pv_done));
+      advance<kStages>(stage, phase);
+      return true;
+    };
+    for (int t = begin; t < end && ok;) {
+      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      if (lane == 0) {
+        ok = mbar_wait(smem_u32(q_full + (seg & 1u)), (seg >> 1) & 1u, abort_flag);
+        for (int j = 0; j < s.tiles && ok; ++j) {
+          ok = mbar_wait(smem_u32(full + stage), phase, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t as = qdesc0 + (uint64_t)(((seg & 1u) * C::kQBytes) >> 4);
+          const uint64_t bs = kdesc0 + (uint64_t)((stage * C::kTileBytes) >> 4);
+          const uint32_t d_t = tmem + (q & 1u) * 128;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            constexpr int kChunk = (kTileKeys * 128) >> 4;
+            const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
+            mma_ss(d_t, as + off, bs + off, idesc_s, kk > 0);
+          }
+          mma_commit(smem_u32(s_full + (q & 1u)));
+          mma_commit(smem_u32(empty + stage));
+          if (j == s.tiles - 1) mma_commit(smem_u32(q_empty + (seg & 1u)));
+          advance<kStages>(stage, phase);
+          if (q > 0) ok = product();
+          ++q;
+          v_first = j == 0;
+          v_seg = seg;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++seg;
+      t += s.tiles;
+    }
+    if (lane == 0) {
+      if (ok && q > 0) product();
+      mma_commit(smem_u32(mma_end));    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
+      mbar_drain(smem_u32(mma_end), 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // --------------------------------------------------------- Q loader ---
+    constexpr int kVec = D / 8;                    // 16-byte pieces of a row
+    uint32_t seg = 0;
+    for (int t = begin; t < end && ok; ++seg) {
+      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      ok = warp_wait(q_empty + (seg & 1u), ((seg >> 1) & 1u) ^ 1u, abort_flag);
+      if (!ok) break;
+      const uint32_t base = smem_u32(q_smem) + (seg & 1u) * C::kQBytes;
+#pragma unroll 4
+      for (int x = threadIdx.x - 64; x < s.rows * kVec; x += 64) {
+        const int r = x / kVec, c = x % kVec;
+        const int row = s.row0 + r, b = row / p.TG, rem = row - b * p.TG, i = rem / p.G, g = rem - i * p.G;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_sb + i * p.q_ss + (s.hk * p.G + g) * p.q_sh) + c);
+        const uint32_t dst = base + (c / 8) * (kRowTile * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+      }
+      fence_async_shared();
+      mbar_arrive(smem_u32(q_full + (seg & 1u)));
+      t += s.tiles;
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------- softmax + results ---
+    const int wq = warp % 4;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    uint32_t seg = 0, q = 0;
+    const int all_tiles = end - begin;
+    // number of tile q's V among the ring's items (K_0, K_1, V_0, K_2, V_1 ..)
+    auto v_item = [&](int tile) { return tile == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * tile + 2; };
+    for (int t = begin; t < end && ok; ++seg) {
+      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      const uint32_t ob = seg & 1u;
+      const uint32_t o_t = tmem + lane_base + 256 + ob * 128;
+      const bool active = wq * 32 < s.rows;        // some row of this warp is real
+      const int row = s.row0 + r;
+      const int fb = row / p.TG, rem = row - fb * p.TG, i = rem / p.G, g = rem - i * p.G;
+      const int limit = s.b < 0 ? p.prefix_len : (r < s.rows ? min(seen_keys(p, s.kv, s.n, i), s.kv) : 0);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int j = 0; j < s.tiles; ++j, ++q) {
+        const uint32_t sb = q & 1u;
+        const uint32_t s_t = tmem + lane_base + sb * 128;
+        const int key0 = (s.tile0 + j) * kTileKeys;
+        ok = warp_wait(s_full + sb, (q >> 1) & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          float v[kTileKeys];
+#pragma unroll
+          for (int c = 0; c < kTileKeys / 32; ++c) tmem_ld32f(s_t + c * 32, v + c * 32);
+          tmem_wait_ld();
+          const int valid = limit - key0;
+          if (valid < kTileKeys) {
+#pragma unroll
+            for (int c = 0; c < kTileKeys; ++c)
+              if (c >= valid) v[c] = -INFINITY;
+          }
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kTileKeys; c += 8) {
+            m0 = max3f(m0, v[c], v[c + 1]);
+            m1 = max3f(m1, v[c + 2], v[c + 3]);
+            m2 = max3f(m2, v[c + 4], v[c + 5]);
+            m3 = max3f(m3, v[c + 6], v[c + 7]);
+          }
+          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+          const float m_new = fmaxf(m_ref, mx * p.scale_log2);
+          const bool grow = m_new > m_ref + 8.0f;
+          const bool rescale = grow && m_ref != -INFINITY;
+          const float alpha = rescale ? ex2_approx(m_ref - m_new) : 1.f;
+          if (grow) m_ref = m_new;
+          const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_use, -m_use);
+          float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int cc = 0; cc < kTileKeys / 64; ++cc) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+              const float2 a = __ffma2_rn(make_float2(v[cc * 64 + c], v[cc * 64 + c + 1]), sc2, nm2);
+              const float2 b = __ffma2_rn(make_float2(v[cc * 64 + c + 2], v[cc * 64 + c + 3]), sc2, nm2);
+              const float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+              const float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
+              ls0 = __fadd2_rn(ls0, e0);
+              ls1 = __fadd2_rn(ls1, e1);
+              pk[c / 2] = pack_bf16x2(e0.x, e0.y);
+              pk[c / 2 + 1] = pack_bf16x2(e1.x, e1.y);
+            }
+            tmem_st32(s_t + cc * 32, pk);
+          }
+          l = l * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
+          // O is rescaled only when the maximum grew by more than 2^8
+          if (__any_sync(0xffffffffu, rescale)) {
+            ok = warp_wait(pv_done, (q - 1) & 1u, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld32f(o_t + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32f(o_t + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        // The last tile's rows behind the keys hold whatever stood in the page:
+        // they are zeroed in V (0 times infinity or NaN is NaN).
+        const int there = s.keys - key0;
+        if (there < kTileKeys) {
+          const uint32_t item = (uint32_t)v_item((int)q);
+          ok = warp_wait(full + item % kStages, (item / kStages) & 1u, abort_flag);
+          if (!ok) break;
+          if (r >= there) {
+            const uint32_t at = smem_u32(ring) + (item % kStages) * C::kTileBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * (kTileKeys * 128) + e * 16), "r"(0)
+                             : "memory");
+          }
+          fence_async_shared();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(p_full + sb));
+      }
+      if (!ok) break;
+      ok = warp_wait(pv_done, (q - 1) & 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      if (active) {
+        const bool direct = p.pre_tiles == 0 && s.whole;
+        const bool mine = r < s.rows;
+        if (direct) {
+          const float inv_l = l > 0.f ? 1.f / l : 0.f;
+          const int h = s.hk * p.G + g;
+          __nv_bfloat16* orow = p.out + (((int64_t)fb * p.T + i) * p.Hq + h) * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32f(o_t + c * 32, o);
+            tmem_wait_ld();
+            if (mine) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
+              uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            }
+          }
+          if (mine && p.lse)
+            p.lse[((int64_t)fb * p.Hq + h) * p.T + i] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          const int slot_rows = s.b < 0 ? p.pre_slot_rows : p.own_slot_rows;
+          const int64_t at = (int64_t)s.slot * slot_rows + r;
+          float* orow = (s.b < 0 ? p.pre_o : p.own_o) + at * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld32f(o_t + c * 32, o);
+            tmem_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<float4*>(orow + c * 32)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+          if (mine) reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml)[at] = make_float2(m_ref, l);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(o_empty + ob));
+      t += s.tiles;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
+// Output row (b, i, h): joins the partial results of its prefix segment and of
+// its own segment.  kWarps warps share a row (many partial results: few rows).
+template <int D, int kWarps>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int kPer = D / 32;
+  constexpr int kRows = 4 / kWarps;                // rows per block
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int part = warp % kWarps;
+  const int64_t R = (int64_t)blockIdx.x * kRows + warp / kWarps;
+  const bool real = R < (int64_t)p.B * p.T * p.Hq;
+  const int h = real ? (int)(R % p.Hq) : 0;
+  const int64_t bt = real ? R / p.Hq : 0;
+  const int b = (int)(bt / p.T), i = (int)(bt % p.T), hk = h / p.G, g = h % p.G;
+  const int kv = own_keys(p, b), n = new_tokens(p, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+  const int W = p.cum[p.B] + pre, ctas = cta_count(p, W);
+  int pre_c0 = 0, pre_n = 0, own_c0 = 0, own_n = 0;
+  int64_t pre_at = 0, own_at = 0;
+  bool direct = false;
+  if (real && i < n) {
+    const int row = i * p.G + g;
+    if (pre > 0) {
+      const int flat = b * p.TG + row, seg = hk * p.pre_rt + flat / kRowTile;
+      pre_c0 = cta_of(seg * p.pre_tiles, ctas, W);
+      pre_n = cta_of(seg * p.pre_tiles + p.pre_tiles - 1, ctas, W) - pre_c0 + 1;
+      pre_at = (int64_t)(seg + pre_c0) * p.pre_slot_rows + flat % kRowTile;
+    }
+    const int rt = row / kRowTile;
+    const int mine = own_tiles(p, kv, n, rt);
+    if (mine > 0) {
+      int t0 = pre + p.cum[b];
+      if (p.own_rt == 1) {
+        t0 += hk * mine;
+      } else {
+        int all = 0, before = 0;
+        for (int x = 0; x < p.own_rt; ++x) {
+          const int m = own_tiles(p, kv, n, x);
+          if (x < rt) before += m;
+          all += m;
+        }
+        t0 += hk * all + before;
+      }
+      own_c0 = cta_of(t0, ctas, W);
+      own_n = cta_of(t0 + mine - 1, ctas, W) - own_c0 + 1;
+      own_at = (int64_t)((b * p.Hkv + hk) * p.own_rt + rt + own_c0) * p.own_slot_rows + row % kRowTile;
+      direct = pre == 0 && own_n == 1;             // written by the first kernel
+    }
+  }
+  const int parts = pre_n + own_n;
+  float m = -INFINITY, l = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  if (real && !direct) {
+#pragma unroll 4
+    for (int x = part; x < parts; x += kWarps) {
+      const bool first = x < pre_n;
+      const int64_t at = first ? pre_at + (int64_t)x * p.pre_slot_rows : own_at + (int64_t)(x - pre_n) * p.own_slot_rows;
+      const float2 ml = reinterpret_cast<const float2*>(first ? p.pre_ml : p.own_ml)[at];
+      const float* orow = (first ? p.pre_o : p.own_o) + at * D + lane * kPer;
+      float o[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(o + e) = *reinterpret_cast<const float2*>(orow + e);
+      const float m2 = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.f : ex2_approx(m - m2), w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m2);
+      m = m2;
+      l = l * a + ml.y * w;
+      // a row that sees none of the partial result's keys has no sums there
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * a + (w > 0.f ? o[e] * w : 0.f);
+    }
+  }
+  if constexpr (kWarps > 1) {
+    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
+    if (lane == 0) { sm[part] = m; sl[part] = l; }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) so[part][lane * kPer + e] = acc[e];
+    __syncthreads();
+    if (part != 0) return;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm[x]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      const float w = sm[x] == -INFINITY ? 0.f : ex2_approx(sm[x] - mm);
+      l += sl[x] * w;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += so[x][lane * kPer + e] * w;
+    }
+    m = mm;
+  }
+  if (!real || direct) return;
+  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+  uint32_t pk[kPer / 2];
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) pk[e] = l > 0.f ? pack_bf16x2(acc[2 * e] * inv_l, acc[2 * e + 1] * inv_l) : 0u;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + R * D + lane * kPer);
+#pragma unroll
+  for (int e = 0; e < kPer / 2; ++e) dst[e] = pk[e];
+  if (lane == 0 && p.lse)
+    p.lse[((int64_t)b * p.Hq + h) * p.T + i] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
 std::string s(int64_t v) { return std::to_string(v); }
+
+// Where the partial results lie in the workspace.
+struct PagedPlan {
+  int TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
+  size_t cum, pre_ml, pre_o, own_ml, own_o, bytes;
+};
+
+PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
+  PagedPlan w{};
+  const int64_t G = Hq / Hkv;
+  w.TG = (int)(T * G);
+  w.own_rt = (int)cdiv64(w.TG, kRowTile);
+  w.pre_rt = prefix ? (int)cdiv64(B * w.TG, kRowTile) : 0;
+  w.own_slot_rows = w.TG < kRowTile ? w.TG : kRowTile;
+  w.pre_slot_rows = (int)(B * w.TG < kRowTile ? B * w.TG : kRowTile);
+  auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  // a slot for every number segment + CTA
+  const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * w.own_slot_rows;
+  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * w.pre_slot_rows : 0;
+  w.cum = 0;
+  w.pre_ml = al((size_t)(B + 1) * 4);
+  w.pre_o = w.pre_ml + al(pre * 8);
+  w.own_ml = w.pre_o + al(pre * d * 4);
+  w.own_o = w.own_ml + al(own * 8);
+  w.bytes = w.own_o + al(own * d * 4);
+  return w;
+}
+
+// The driver's cuTensorMapEncodeTiled, looked up once per process.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static std::once_flag once;
+  static EncodeFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(f);
+  });
+  return fn;
+}
+
+// Map of a cache view: dims (D, slots, Hkv, pages), box (64, min(slots, 128),
+// 1, 1), 128-byte swizzle; a page number past the end reads zeros.
+bsa_status encode_cache(CUtensorMap* m, const bsa_tensor& t, const char* fn, const char* name) {
+  const EncodeFn enc = encode_fn();
+  if (!enc) return set_error(BSA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled is not available from the driver");
+  // strides of axes of length 1 are free: the smallest legal one
+  auto bytes = [](int64_t stride) { return (cuuint64_t)(stride > 0 ? stride * 2 : 16); };
+  cuuint64_t dims[4] = {(cuuint64_t)t.D, (cuuint64_t)t.S, (cuuint64_t)t.H, (cuuint64_t)t.B};
+  cuuint64_t strides[3] = {bytes(t.stride_s), bytes(t.stride_h), bytes(t.stride_b)};
+  cuuint32_t box[4] = {64u, (cuuint32_t)(t.S < kTileKeys ? t.S : kTileKeys), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(BSA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed for " + name + " (CUresult " +
+                                       s((int)r) + ")");
+  return BSA_OK;
+}
+
+template <int D>
+bsa_status set_smem() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  bsa_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != BSA_OK) return st;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 64 || !done[dev]) {
+    st = cuda_check(cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PagedCfg<D>::kSmemBytes),
+                    "cudaFuncSetAttribute(paged_attention_kernel)");
+    if (st != BSA_OK) return st;
+    if (dev < 64) done[dev] = true;
+  }
+  return BSA_OK;
+}
+
+template <int D>
+bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
+  bsa_status st = set_smem<D>();
+  if (st != BSA_OK) return st;
+  paged_attention_kernel<D><<<p.ctas, kPagedThreads, PagedCfg<D>::kSmemBytes, stream>>>(p);
+  if ((st = cuda_check(cudaGetLastError(), "paged_attention_kernel launch")) != BSA_OK) return st;
+  const int64_t rows = (int64_t)p.B * p.T * p.Hq;
+  const bool wide = rows < (int64_t)num_sms() * 16;    // few rows: their partial results are shared out to four warps
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(wide ? rows : cdiv64(rows, 4)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_check(wide ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 4>, p)
+                         : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 1>, p),
+                    "paged_join_kernel launch");
+}
 
 }  // namespace
 
@@ -116,10 +841,11 @@ using namespace bsa;
 
 extern "C" {
 
-size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has_prefix, int num_sms) {
-  (void)has_prefix; (void)num_sms;
-  if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (d != 64 && d != 128)) return 0;
-  return 256;
+size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has_prefix, int sms) {
+  if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq > kMaxHeads || Hq % Hkv ||
+      (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 4)
+    return 0;
+  return plan_paged(B, T, Hq, Hkv, d, has_prefix != 0, sms > 0 ? sms : num_sms()).bytes;
 }
 
 bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
@@ -151,8 +877,17 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": out is not 16-byte aligned");
   if (!std::isfinite(softmax_scale))
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": softmax_scale is not finite");
-  const size_t need = bsap_forward_workspace_size((int)qv.B, (int)qv.S, (int)qv.H, (int)a.k.H, (int)qv.D,
-                                                  prefix_len > 0, 0);
+  const int64_t G = qv.H / a.k.H;
+  const int sms = num_sms();
+  // rows, tiles and slot numbers are 32-bit on the device
+  const int64_t flat_rows = qv.B * qv.S * G, row_tiles = cdiv64(qv.S * G, kRowTile);
+  const int64_t most_tiles = qv.B * a.k.H * row_tiles * cdiv64(max_pages * a.k.S, kTileKeys) +
+                             a.k.H * cdiv64(flat_rows, kRowTile) * cdiv64(prefix_len, kTileKeys);
+  if (flat_rows > INT32_MAX / 4 || most_tiles > INT32_MAX / 2 || flat_rows * a.k.H > INT32_MAX)
+    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
+                                              s(max_pages * a.k.S + prefix_len) + " keys are too many for one call");
+  const PagedPlan plan = plan_paged(qv.B, qv.S, qv.H, a.k.H, qv.D, prefix_len > 0, sms);
+  const size_t need = plan.bytes;
   if (!workspace) return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is NULL (needs " + s(need) + " bytes)");
   if (ws_bytes < need)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace of " + s(ws_bytes) +
@@ -160,22 +895,27 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is not 256-byte aligned");
   PagedParams p{};
+  if ((st = encode_cache(&p.tk, a.k, fn, "k_cache")) != BSA_OK) return st;
+  if ((st = encode_cache(&p.tv, a.v, fn, "v_cache")) != BSA_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(qv.ptr); p.q_sb = qv.stride_b; p.q_ss = qv.stride_s; p.q_sh = qv.stride_h;
-  p.k = static_cast<const __nv_bfloat16*>(a.k.ptr); p.k_sp = a.k.stride_b; p.k_ss = a.k.stride_s; p.k_sh = a.k.stride_h;
-  p.v = static_cast<const __nv_bfloat16*>(a.v.ptr); p.v_sp = a.v.stride_b; p.v_ss = a.v.stride_s; p.v_sh = a.v.stride_h;
-  p.B = (int)qv.B; p.T = (int)qv.S; p.Hq = (int)qv.H; p.Hkv = (int)a.k.H; p.G = p.Hq / p.Hkv;
+  p.B = (int)qv.B; p.T = (int)qv.S; p.Hq = (int)qv.H; p.Hkv = (int)a.k.H; p.G = (int)G;
   p.page_shift = 4;
   while ((1 << p.page_shift) < a.k.S) ++p.page_shift;
   p.num_pages = (int)a.k.B; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
+  p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
+  p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
+  p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
+  p.ctas = sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
-  const unsigned rows = (unsigned)(qv.B * qv.S * qv.H);
+  char* ws = static_cast<char*>(workspace);
+  p.cum = reinterpret_cast<int32_t*>(ws + plan.cum);
+  p.pre_ml = reinterpret_cast<float*>(ws + plan.pre_ml); p.pre_o = reinterpret_cast<float*>(ws + plan.pre_o);
+  p.own_ml = reinterpret_cast<float*>(ws + plan.own_ml); p.own_o = reinterpret_cast<float*>(ws + plan.own_o);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (qv.D == 128) paged_rows_kernel<128><<<rows, 128, 0, cs>>>(p);
-  else paged_rows_kernel<64><<<rows, 128, 0, cs>>>(p);
-  return cuda_check(cudaGetLastError(), "paged_rows_kernel launch");
+  return qv.D == 128 ? launch_paged<128>(p, cs) : launch_paged<64>(p, cs);
 }
 
 }  // extern "C"
