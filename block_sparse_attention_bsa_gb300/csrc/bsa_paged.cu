@@ -229,15 +229,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   uint64_t* s_full = bars + 4;          // [2] commit
   uint64_t* p_full = bars + 6;          // [2] 4 softmax warps
   uint64_t* o_empty = bars + 8;         // [2] 4 softmax warps
-  uint64_t* pv_done = bars + 10;        // commit
-  uint64_t* mma_end = bars + 11;        // commit
-  uint64_t* full = bars + 12;           // [kStages] transaction bytes
+  // P V of even and of odd tiles [2], commit.  A parity tells only neighbouring
+  // phases apart.  When the softmax waits for P V of tile q it has seen S of
+  // tile q, whose commit covers P V of tile q - 2, but that of q - 1 may still
+  // run: one barrier for all tiles would let it pass too early.
+  uint64_t* pv_done = bars + 10;
+  uint64_t* mma_end = bars + 12;        // commit
+  uint64_t* full = bars + 13;           // [kStages] transaction bytes
   uint64_t* empty = full + kStages;     // [kStages] commit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* total_slot = reinterpret_cast<int*>(tmem_slot + 2);
   int* block_sum = total_slot + 1;      // [kMaxBlocks]
-  static_assert((12 + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes, "barrier block");
+  static_assert((13 + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes, "barrier block");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
@@ -248,8 +252,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       mbar_init(smem_u32(s_full + i), 1);
       mbar_init(smem_u32(p_full + i), 4);
       mbar_init(smem_u32(o_empty + i), 4);
+      mbar_init(smem_u32(pv_done + i), 1);
     }
-    mbar_init(smem_u32(pv_done), 1);
     mbar_init(smem_u32(mma_end), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(full + i), 1);
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       for (int kk = 0; kk < kTileKeys / 16; ++kk)
         mma_ts(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o, kk > 0 || !v_first);
       mma_commit(smem_u32(empty + stage));
-      mma_commit(smem_u32(pv_done));
+      mma_commit(smem_u32(pv_done + sb));
       advance<kStages>(stage, phase);
       return true;
     };
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           l = l * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
           // O is rescaled only when the maximum grew by more than 2^8
           if (__any_sync(0xffffffffu, rescale)) {
-            ok = warp_wait(pv_done, (q - 1) & 1u, abort_flag);
+            ok = warp_wait(pv_done + ((q - 1) & 1u), ((q - 1) >> 1) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         if (lane == 0) mbar_arrive(smem_u32(p_full + sb));
       }
       if (!ok) break;
-      ok = warp_wait(pv_done, (q - 1) & 1u, abort_flag);
+      ok = warp_wait(pv_done + ((q - 1) & 1u), ((q - 1) >> 1) & 1u, abort_flag);
       if (!ok) break;
       tc_fence_after();
       if (active) {

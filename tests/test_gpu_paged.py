@@ -293,3 +293,57 @@ def test_attention_reports_tables_that_name_no_page():
             bsa.bsa_device_status()
         if what != "prefix":
             assert torch.equal(out[1], good[1])                   # the other request is as it was
+
+
+def attend64_one(q, k, v, lens, prefix_k, prefix_v):
+    """One token per request, all requests at once on the GPU in 64 bits:
+    k, v [B, n, Hkv, d] (rows behind lens hold zeros).  (out, lse, bounds)"""
+    B, _, Hq, d = q.shape
+    Hkv, n = k.shape[2], k.shape[1]
+    qq = q.double().view(B, Hkv, Hq // Hkv, d)
+    z = torch.einsum("bhgd,bnhd->bhgn", qq, k.double()) * d ** -0.5
+    za = torch.einsum("bhgd,bnhd->bhgn", qq.abs(), k.double().abs()) * d ** -0.5
+    hidden = (torch.arange(n, device=q.device) >= lens[:, None])[:, None, None]
+    z, za = z.masked_fill(hidden, -math.inf), za.masked_fill(hidden, 0.0)
+    zp = torch.einsum("bhgd,nhd->bhgn", qq, prefix_k.double()) * d ** -0.5
+    zpa = torch.einsum("bhgd,nhd->bhgn", qq.abs(), prefix_k.double().abs()) * d ** -0.5
+    z, dz = torch.cat([zp, z], -1), 2.0 ** -15 * torch.cat([zpa, za], -1).amax(-1)
+    w = torch.softmax(z, -1)
+    P = prefix_k.shape[0]
+
+    def mix(f):
+        return torch.einsum("bhgn,bnhd->bhgd", w[..., P:], f(v.double())) + \
+            torch.einsum("bhgn,nhd->bhgd", w[..., :P], f(prefix_v.double()))
+
+    out, reach, lse = mix(lambda x: x), mix(torch.abs), torch.logsumexp(z, -1)
+    ob = 2.0 ** -8 * out.abs() + (2 * dz[..., None] + 2.0 ** -8 + 2.0 ** -12) * reach
+    lb = dz + 2.0 ** -19 * (lse.abs() + 1)
+    return tuple(x.cpu() for x in (out.reshape(B, 1, Hq, d), lse.reshape(B, Hq, 1), ob.reshape(B, 1, Hq, d), lb.reshape(B, Hq, 1)))
+
+
+@pytest.mark.parametrize("B,prefix,low,high,Hq,Hkv,d,page", [
+    (300, 0, 1, 300, 8, 4, 128, 64),          # many short segments in every CTA, none of them cut or joined but few
+    (300, 257, 0, 140, 8, 4, 64, 16),         # one or two tiles each, beside a prefix with ten row tiles
+    (700, 129, 100, 128, 4, 4, 128, 128),     # single tiles only
+    (6, 20000, 1000, 9000, 32, 2, 128, 128),  # long runs of tiles, cut many times
+    (64, 0, 4096, 4096, 16, 8, 128, 128),
+])
+def test_attention_over_many_segments_matches_64_bits(B, prefix, low, high, Hq, Hkv, d, page):
+    g = torch.Generator(device=DEV).manual_seed(B + high)
+    lens = torch.randint(low, high + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    width, shared = -(-high // page), -(-prefix // page)
+    total = B * width + shared + 1
+    kc, vc = (torch.randn(total, page, Hkv, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    order = torch.randperm(total, generator=g, device=DEV).int()
+    table, pt = order[:B * width].view(B, width), order[B * width:B * width + shared]
+    q = torch.randn(B, 1, Hq, d, generator=g, device=DEV).to(BF)
+    k, v = (c[table.long()].flatten(1, 2) for c in (kc, vc))
+    pk, pv = (c[pt.long()].flatten(0, 1)[:prefix] for c in (kc, vc))
+    ref = attend64_one(q, k, v, lens, pk, pv)
+    out, lse = bsa.bsa_forward_paged(q, kc, vc, table, lens, prefix_table=pt, prefix_len=prefix)
+    bsa.bsa_device_status()
+    check_attention(out, lse, ref)
+    for _ in range(3):
+        again, lse2 = bsa.bsa_forward_paged(q, kc, vc, table, lens, prefix_table=pt, prefix_len=prefix)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    bsa.bsa_device_status()
