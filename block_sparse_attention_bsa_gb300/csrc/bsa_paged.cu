@@ -22,13 +22,17 @@
 //    result per CTA; the pair (segment, CTA) only ever steps forward along the
 //    row, so segment + CTA numbers the partial results without gaps of meaning
 //    and without a table.
-//  * One CTA per SM: warp 0 gathers K and V tiles page by page with TMA into
-//    one ring in the order the products use them (K_0, K_1, V_0, K_2, V_1 ..),
-//    warp 1 issues the MMAs (S = Q K^T of tile q + 1 before O += P V of tile
-//    q), warps 2 and 3 load the next segment's Q rows, warps 4-7 do the online
-//    softmax with one row per thread, P staying in TMEM, and write the result.
-//    S and O each have two buffers in TMEM, so neither the next tile nor the
-//    next segment waits for the softmax or for the results' way out.
+//  * One CTA per SM: warp 3 goes through the CTA's segments and hands them to
+//    the others through a ring; warp 0 gathers K and V tiles page by page with
+//    TMA into a second ring, in the order the products use them (K_0, K_1,
+//    V_0, K_2, V_1 ..); warp 1 issues the MMAs (S = Q K^T of tile q + 1 before
+//    O += P V of tile q); warp 2 loads the next segment's Q rows; warps 4-7 do
+//    the online softmax with one row per thread, P staying in TMEM, and write
+//    the result.  S and O each have two buffers in TMEM, so neither the next
+//    tile nor the next segment waits for the softmax or for the results' way
+//    out.  Code is kept short (one copy of the schedule, rolled loops where
+//    nothing is gained by unrolling): short segments run each role's code once
+//    per microsecond, and with 143 KB of it they took 7 us each.
 //  * paged_join_kernel adds up the partial results (launched with programmatic
 //    dependence, so that it is resident when the first kernel ends).
 #include <cuda_bf16.h>
@@ -54,18 +58,32 @@ struct PagedCfg {
   static constexpr int kChunks = D / 64;                      // 128-byte chunks per row
   static constexpr int kQBytes = kRowTile * 128 * kChunks;
   static constexpr int kTileBytes = kTileKeys * 128 * kChunks;
-  static constexpr int kBarBytes = 1024;
+  static constexpr int kBarBytes = 2048;
   static constexpr int kSmemMax = 232448;                     // 227 KB per CTA
   static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - 2 * kQBytes) / kTileBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;       // 5 of 32 KB, 10 of 16 KB
   static constexpr int kSmemBytes = 1024 + kBarBytes + 2 * kQBytes + kStages * kTileBytes;
 };
 
+// Division by a fixed divisor: n / d = (umulhi(n, mul) + n) >> shift for
+// 0 <= n < 2^31 (Granlund and Montgomery, Division by invariant integers
+// using multiplication).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int quot(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  return FastDiv{d, (uint32_t)((((1ull << shift) - d) << 32) / d + 1), shift};
+}
+
 struct PagedParams {
   CUtensorMap tk, tv;             // [pages, Hkv, slots, D] of the whole cache
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
+  FastDiv div_G, div_TG;
   int TG;                         // rows of a request under one KV head
   int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
@@ -97,15 +115,15 @@ __device__ __forceinline__ int seen_keys(const PagedParams& p, int kv, int n, in
 }
 // Key tiles of row tile rt of such a request.
 __device__ __forceinline__ int own_tiles(const PagedParams& p, int kv, int n, int rt) {
-  const int first = rt * kRowTile / p.G;
+  const int first = p.div_G.quot(rt * kRowTile);
   if (first >= n) return 0;
-  const int last = min(n - 1, (rt * kRowTile + kRowTile - 1) / p.G);
+  const int last = min(n - 1, p.div_G.quot(rt * kRowTile + kRowTile - 1));
   return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
 }
-// Key tiles of request b under one KV head.
-__device__ __forceinline__ int request_tiles(const PagedParams& p, int b) {
-  const int kv = own_keys(p, b), n = new_tokens(p, b);
+// Key tiles of a request under one KV head.
+__device__ __forceinline__ int request_tiles(const PagedParams& p, int kv, int n) {
   int sum = 0;
+#pragma unroll 1
   for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles(p, kv, n, rt);
   return sum;
 }
@@ -126,8 +144,8 @@ __device__ __forceinline__ int cta_count(const PagedParams& p, int W) { return m
 __device__ __forceinline__ int cta_begin(int c, int n, int W) { return (int)((int64_t)c * W / n); }
 __device__ __forceinline__ int cta_of(int t, int n, int W) { return (int)((((int64_t)t + 1) * n - 1) / W); }
 
-// A segment's part that one CTA works on.
-struct Segment {
+// A segment's part that one CTA works on, as it stands in the segment ring.
+struct __align__(16) Segment {
   int b;               // request, -1: prefix
   int hk;
   int row0, rows;      // first flat row (b * T + i) * G + g, and how many
@@ -136,59 +154,10 @@ struct Segment {
   int whole;           // this CTA has all tiles of the segment
   int keys;            // keys that stand in the source
   int kv, n;           // of the request
+  int pad;
 };
-
-// The segment that holds tile t and its part before tile `end` (all lanes of
-// a warp call it; the CTA's tiles are [begin, end); block_sum[i] = tiles of own
-// keys before request 32 i).
-__device__ __forceinline__ Segment find_segment(const PagedParams& p, const int* block_sum, int cta, int begin, int t,
-                                                int end) {
-  Segment s;
-  const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
-  int t0, t1;
-  if (t < pre) {
-    const int seg = t / p.pre_tiles;
-    t0 = seg * p.pre_tiles;
-    t1 = t0 + p.pre_tiles;
-    s.b = -1;
-    s.hk = seg / p.pre_rt;
-    s.row0 = (seg % p.pre_rt) * kRowTile;
-    s.rows = min(kRowTile, p.B * p.TG - s.row0);
-    s.slot = seg + cta;
-    s.keys = p.prefix_len;
-    s.kv = s.n = 0;
-  } else {
-    const int u = t - pre, lane = threadIdx.x % 32;
-    int blk = 0;
-    for (int i = 32; i < p.B && block_sum[i / 32] <= u; i += 32) ++blk;
-    const int b0 = blk * 32 + lane;
-    const int mine = b0 < p.B ? request_tiles(p, b0) * p.Hkv : 0;
-    const int upto = warp_inclusive_sum(mine) + block_sum[blk];
-    const uint32_t past = __ballot_sync(0xffffffffu, upto > u);
-    const int src = __ffs(past) - 1;               // there is one: u < W - pre
-    s.b = blk * 32 + src;
-    const int all = __shfl_sync(0xffffffffu, mine, src), before = __shfl_sync(0xffffffffu, upto, src) - all;
-    const int per_head = all / p.Hkv;
-    s.hk = (u - before) / per_head;
-    s.kv = own_keys(p, s.b);
-    s.n = new_tokens(p, s.b);
-    t0 = pre + before + s.hk * per_head;
-    int rt = 0, m = own_tiles(p, s.kv, s.n, 0);
-    while (t >= t0 + m) {
-      t0 += m;
-      m = own_tiles(p, s.kv, s.n, ++rt);
-    }
-    t1 = t0 + m;
-    s.row0 = s.b * p.TG + rt * kRowTile;
-    s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
-    s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
-    s.keys = s.kv;
-  }
-  s.tile0 = t - t0;
-  s.tiles = min(t1, end) - t;
-  s.whole = begin <= t0 && t1 <= end;
-  return s;
-}
+constexpr int kSegRing = 4;
+constexpr int kSegReaders = 7;       // warps that read every segment
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3) {
@@ -203,11 +172,36 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
 // proxy (the MMAs read Q and V through it).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// mbar_wait by all lanes of a warp, with one answer for all of them (what
+// mbar_wait with one copy of its loop in the code.
+__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return mbar_try_wait(smem_u32(bar), parity) || wait_loop(smem_u32(bar), parity, abort);
+}
+// The same by all lanes of a warp, with one answer for all of them (what
 // follows uses warp-wide instructions).
 __device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort));
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
 }
+
+// A warp's place in the segment ring.
+struct SegmentReader {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ bool take(const Segment* ring, const uint64_t* seg_full, const uint64_t* seg_empty,
+                                       volatile int* abort, Segment& s) {
+    if (!warp_wait(seg_full + slot, phase, abort)) return false;
+    const int4* src = reinterpret_cast<const int4*>(ring + slot);
+    const int4 a = src[0], b = src[1], c = src[2];
+    s.b = a.x; s.hk = a.y; s.row0 = a.z; s.rows = a.w;
+    s.tile0 = b.x; s.tiles = b.y; s.slot = b.z; s.whole = b.w;
+    s.keys = c.x; s.kv = c.y; s.n = c.z;
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(smem_u32(seg_empty + slot));
+    if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+    return true;
+  }
+};
 
 template <int N>
 __device__ __forceinline__ void advance(uint32_t& stage, uint32_t& phase) {
@@ -223,8 +217,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* q_smem = smem;                                  // [2] Q buffers
   uint8_t* ring = smem + 2 * C::kQBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kStages * C::kTileBytes);
-  uint64_t* q_full = bars;              // [2] 64 loader threads
+  Segment* segs = reinterpret_cast<Segment*>(ring + kStages * C::kTileBytes);   // [kSegRing]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(segs + kSegRing);
+  uint64_t* q_full = bars;              // [2] 32 loader threads
   uint64_t* q_empty = bars + 2;         // [2] commit
   uint64_t* s_full = bars + 4;          // [2] commit
   uint64_t* p_full = bars + 6;          // [2] 4 softmax warps
@@ -235,19 +230,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   // run: one barrier for all tiles would let it pass too early.
   uint64_t* pv_done = bars + 10;
   uint64_t* mma_end = bars + 12;        // commit
-  uint64_t* full = bars + 13;           // [kStages] transaction bytes
+  uint64_t* seg_full = bars + 13;       // [kSegRing] the scheduler
+  uint64_t* seg_empty = seg_full + kSegRing;   // [kSegRing] 7 warps
+  uint64_t* full = seg_empty + kSegRing;       // [kStages] transaction bytes
   uint64_t* empty = full + kStages;     // [kStages] commit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + kStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* total_slot = reinterpret_cast<int*>(tmem_slot + 2);
-  int* block_sum = total_slot + 1;      // [kMaxBlocks]
-  static_assert((13 + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes, "barrier block");
+  int* block_sum = total_slot + 1;      // [kMaxBlocks]: tiles of own keys before request 32 i
+  static_assert(kSegRing * sizeof(Segment) + (13 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes,
+                "barrier block");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(q_full + i), 64);
+      mbar_init(smem_u32(q_full + i), 32);
       mbar_init(smem_u32(q_empty + i), 1);
       mbar_init(smem_u32(s_full + i), 1);
       mbar_init(smem_u32(p_full + i), 4);
@@ -255,6 +253,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       mbar_init(smem_u32(pv_done + i), 1);
     }
     mbar_init(smem_u32(mma_end), 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(smem_u32(seg_full + i), 1);
+      mbar_init(smem_u32(seg_empty + i), kSegReaders);
+    }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(full + i), 1);
       mbar_init(smem_u32(empty + i), 1);
@@ -270,13 +272,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
+#pragma unroll 1
   for (int blk = warp; blk < nblk; blk += kPagedThreads / 32) {
     const int b = blk * 32 + lane;
-    const int sum = warp_inclusive_sum(b < p.B ? request_tiles(p, b) * p.Hkv : 0);
-    if (lane == 31) block_sum[blk] = sum;
-    if (cta == 0 && b < p.B && p.max_pages > 0) {
-      const int kv = __ldg(p.kv_lens + b);
-      if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+    const int mine = b < p.B ? request_tiles(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
+    const int incl = warp_inclusive_sum(mine);
+    if (lane == 31) block_sum[blk] = incl;
+    if (cta == 0 && b < p.B) {
+      p.cum[b] = incl - mine;           // the join finds each request's tiles here (block sums are added below)
+      if (p.max_pages > 0) {
+        const int kv = __ldg(p.kv_lens + b);
+        if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+      }
     }
   }
   tc_fence_before();
@@ -284,6 +291,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   tc_fence_after();
   if (warp == 0) {
     int before = 0;
+#pragma unroll 1
     for (int i = 0; i < nblk; i += 32) {
       const int v = i + lane < nblk ? block_sum[i + lane] : 0;
       const int incl = warp_inclusive_sum(v) + before;
@@ -295,13 +303,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const int W = *total_slot + p.pre_tiles * p.pre_rt * p.Hkv;
-  if (cta == 0) {                       // the join finds each request's tiles here
-    for (int blk = warp; blk < nblk; blk += kPagedThreads / 32) {
-      const int b = blk * 32 + lane;
-      const int mine = b < p.B ? request_tiles(p, b) * p.Hkv : 0;
-      const int incl = warp_inclusive_sum(mine) + block_sum[blk];
-      if (b < p.B) p.cum[b] = incl - mine;
-    }
+  if (cta == 0) {
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) p.cum[b] += block_sum[b / 32];
     if (threadIdx.x == 0) p.cum[p.B] = *total_slot;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     auto load = [&](const CUtensorMap* map, int page, int slot, int hk) -> bool {
       bool go = true;
       if (lane == 0) {
-        go = mbar_wait(smem_u32(empty + stage), phase ^ 1u, abort_flag);
+        go = wait_for(empty + stage, phase ^ 1u, abort_flag);
         if (go) mbar_arrive_expect_tx(smem_u32(full + stage), C::kTileBytes);
       }
       go = __shfl_sync(0xffffffffu, go, 0);
@@ -334,8 +338,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       if (go) advance<kStages>(stage, phase);
       return go;
     };
+    SegmentReader reader;
     for (int t = begin; t < end && ok;) {
-      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
       const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
       auto page_of = [&](int j) {                  // lane's page of key tile j (a page past the end reads zeros)
         const int key = j * kTileKeys + lane * box_rows;
@@ -350,11 +356,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         return page;
       };
       int page = page_of(s.tile0);
+#pragma unroll 1
       for (int j = s.tile0; j < s.tile0 + s.tiles && ok; ++j) {
         const int next = j + 1 < s.tile0 + s.tiles ? page_of(j + 1) : 0;
         const int slot = (j * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
-        ok = load(&p.tk, page, slot, s.hk);
-        if (ok && (j > s.tile0 || t > begin)) ok = load(&p.tv, v_page, v_slot, v_hk);
+#pragma unroll 1
+        for (int which = 0; which < 2 && ok; ++which) {
+          if (which == 0) ok = load(&p.tk, page, slot, s.hk);
+          else if (j > s.tile0 || t > begin) ok = load(&p.tv, v_page, v_slot, v_hk);
+        }
         v_page = page; v_slot = slot; v_hk = s.hk;
         page = next;
       }
@@ -363,6 +373,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     if (ok && begin < end) load(&p.tv, v_page, v_slot, v_hk);
     // the copies in flight land before the CTA may leave
     if (lane == 0) {
+#pragma unroll 1
       for (int i = 0; i < kStages; ++i) {
         mbar_drain(smem_u32(full + stage), phase ^ 1u);
         advance<kStages>(stage, phase);
@@ -381,9 +392,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     uint32_t v_seg = 0;
     auto product = [&]() -> bool {      // O (+)= P V of tile q - 1
       const uint32_t tile = q - 1, sb = tile & 1u, ob = v_seg & 1u;
-      if (v_first && !mbar_wait(smem_u32(o_empty + ob), ((v_seg >> 1) & 1u) ^ 1u, abort_flag)) return false;
-      if (!mbar_wait(smem_u32(p_full + sb), (tile >> 1) & 1u, abort_flag)) return false;
-      if (!mbar_wait(smem_u32(full + stage), phase, abort_flag)) return false;
+      if (v_first && !wait_for(o_empty + ob, ((v_seg >> 1) & 1u) ^ 1u, abort_flag)) return false;
+      if (!wait_for(p_full + sb, (tile >> 1) & 1u, abort_flag)) return false;
+      if (!wait_for(full + stage, phase, abort_flag)) return false;
       tc_fence_after();
       const uint64_t bs = vdesc0 + (uint64_t)((stage * C::kTileBytes) >> 4);
       const uint32_t d_t = tmem + 256 + ob * 128, a_t = tmem + sb * 128;
@@ -395,12 +406,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       advance<kStages>(stage, phase);
       return true;
     };
+    SegmentReader reader;
     for (int t = begin; t < end && ok;) {
-      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
       if (lane == 0) {
-        ok = mbar_wait(smem_u32(q_full + (seg & 1u)), (seg >> 1) & 1u, abort_flag);
+        ok = wait_for(q_full + (seg & 1u), (seg >> 1) & 1u, abort_flag);
+#pragma unroll 1
         for (int j = 0; j < s.tiles && ok; ++j) {
-          ok = mbar_wait(smem_u32(full + stage), phase, abort_flag);
+          ok = wait_for(full + stage, phase, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint64_t as = qdesc0 + (uint64_t)(((seg & 1u) * C::kQBytes) >> 4);
@@ -432,26 +446,96 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       mbar_drain(smem_u32(mma_end), 0);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2) {
     // --------------------------------------------------------- Q loader ---
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
+    constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
+    const int c = lane % kVec;
     uint32_t seg = 0;
+    SegmentReader reader;
     for (int t = begin; t < end && ok; ++seg) {
-      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
-      ok = warp_wait(q_empty + (seg & 1u), ((seg >> 1) & 1u) ^ 1u, abort_flag);
-      if (!ok) break;
-      const uint32_t base = smem_u32(q_smem) + (seg & 1u) * C::kQBytes;
-#pragma unroll 4
-      for (int x = threadIdx.x - 64; x < s.rows * kVec; x += 64) {
-        const int r = x / kVec, c = x % kVec;
-        const int row = s.row0 + r, b = row / p.TG, rem = row - b * p.TG, i = rem / p.G, g = rem - i * p.G;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + b * p.q_sb + i * p.q_ss + (s.hk * p.G + g) * p.q_sh) + c);
-        const uint32_t dst = base + (c / 8) * (kRowTile * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
+      if (!(ok = warp_wait(q_empty + (seg & 1u), ((seg >> 1) & 1u) ^ 1u, abort_flag))) break;
+      const uint32_t base = smem_u32(q_smem) + (seg & 1u) * C::kQBytes + (c / 8) * (kRowTile * 128);
+      const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
+#pragma unroll 2
+      for (int r = lane / kVec; r < s.rows; r += kRowsPer) {
+        const int row = s.row0 + r, b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+        const __nv_bfloat16* src = head + b * p.q_sb + i * p.q_ss + g * p.q_sh;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + r * 128 + ((c % 8) ^ (r % 8)) * 16), "l"(src)
                      : "memory");
       }
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
       fence_async_shared();
       mbar_arrive(smem_u32(q_full + (seg & 1u)));
+      t += s.tiles;
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // -------------------------------------------------------- scheduler ---
+    // The segments of tiles [begin, end) in their order.  Lane l holds request
+    // 32 blk + l: its lengths, tiles, and the tiles up to its end.
+    const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+    int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
+    uint32_t slot = 0, phase = 0;
+    for (int t = begin; t < end && ok;) {
+      Segment s;
+      int t0, t1;
+      if (t < pre) {
+        const int seg = t / p.pre_tiles;
+        t0 = seg * p.pre_tiles;
+        t1 = t0 + p.pre_tiles;
+        s.b = -1;
+        s.hk = seg / p.pre_rt;
+        s.row0 = (seg - s.hk * p.pre_rt) * kRowTile;
+        s.rows = min(kRowTile, p.B * p.TG - s.row0);
+        s.slot = seg + cta;
+        s.keys = p.prefix_len;
+        s.kv = s.n = 0;
+      } else {
+        const int u = t - pre;
+        if (u >= blk_end) {                          // the last block that begins at or before u
+          ++blk;
+          while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
+          const int b = blk * 32 + lane;
+          kv = b < p.B ? own_keys(p, b) : 0;
+          n = b < p.B ? new_tokens(p, b) : 0;
+          mine = b < p.B ? request_tiles(p, kv, n) : 0;
+          upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
+          blk_end = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
+        const int per_head = __shfl_sync(0xffffffffu, mine, src);
+        const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
+        s.b = blk * 32 + src;
+        s.kv = __shfl_sync(0xffffffffu, kv, src);
+        s.n = __shfl_sync(0xffffffffu, n, src);
+        s.hk = (u - first) / per_head;
+        t0 = pre + first + s.hk * per_head;
+        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles(p, s.kv, s.n, 0);
+#pragma unroll 1
+        while (t >= t0 + m) {
+          t0 += m;
+          m = own_tiles(p, s.kv, s.n, ++rt);
+        }
+        t1 = t0 + m;
+        s.row0 = s.b * p.TG + rt * kRowTile;
+        s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
+        s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
+        s.keys = s.kv;
+      }
+      s.tile0 = t - t0;
+      s.tiles = min(t1, end) - t;
+      s.whole = begin <= t0 && t1 <= end;
+      s.pad = 0;
+      if (!(ok = warp_wait(seg_empty + slot, phase ^ 1u, abort_flag))) break;
+      if (lane == 0) {
+        segs[slot] = s;
+        mbar_arrive(smem_u32(seg_full + slot));
+      }
+      __syncwarp();
+      if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
       t += s.tiles;
     }
     __syncwarp();
@@ -464,15 +548,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const int all_tiles = end - begin;
     // number of tile q's V among the ring's items (K_0, K_1, V_0, K_2, V_1 ..)
     auto v_item = [&](int tile) { return tile == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * tile + 2; };
+    SegmentReader reader;
     for (int t = begin; t < end && ok; ++seg) {
-      const Segment s = find_segment(p, block_sum, cta, begin, t, end);
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
       const uint32_t ob = seg & 1u;
       const uint32_t o_t = tmem + lane_base + 256 + ob * 128;
       const bool active = wq * 32 < s.rows;        // some row of this warp is real
       const int row = s.row0 + r;
-      const int fb = row / p.TG, rem = row - fb * p.TG, i = rem / p.G, g = rem - i * p.G;
+      const int fb = p.div_TG.quot(row), rem = row - fb * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
       const int limit = s.b < 0 ? p.prefix_len : (r < s.rows ? min(seen_keys(p, s.kv, s.n, i), s.kv) : 0);
       float m_ref = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int j = 0; j < s.tiles; ++j, ++q) {
         const uint32_t sb = q & 1u;
         const uint32_t s_t = tmem + lane_base + sb * 128;
@@ -551,7 +638,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           if (!ok) break;
           if (r >= there) {
             const uint32_t at = smem_u32(ring) + (item % kStages) * C::kTileBytes + r * 128;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -571,42 +658,35 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       if (active) {
         const bool direct = p.pre_tiles == 0 && s.whole;
         const bool mine = r < s.rows;
-        if (direct) {
-          const float inv_l = l > 0.f ? 1.f / l : 0.f;
-          const int h = s.hk * p.G + g;
-          __nv_bfloat16* orow = p.out + (((int64_t)fb * p.T + i) * p.Hq + h) * D;
+        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
+        const int64_t at = (int64_t)s.slot * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
+        char* dst = direct ? reinterpret_cast<char*>(p.out + orow * D)
+                           : reinterpret_cast<char*>((s.b < 0 ? p.pre_o : p.own_o) + at * D);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32f(o_t + c * 32, o);
+          tmem_wait_ld();
+          if (mine && direct) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32f(o_t + c * 32, o);
-            tmem_wait_ld();
-            if (mine) {
-              uint32_t pk[16];
+            for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
 #pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
-              uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+            for (int e = 0; e < 4; ++e)
+              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          } else if (mine) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) dst[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-            }
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(dst)[c * 8 + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
-          if (mine && p.lse)
-            p.lse[((int64_t)fb * p.Hq + h) * p.T + i] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-        } else {
-          const int slot_rows = s.b < 0 ? p.pre_slot_rows : p.own_slot_rows;
-          const int64_t at = (int64_t)s.slot * slot_rows + r;
-          float* orow = (s.b < 0 ? p.pre_o : p.own_o) + at * D;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            tmem_ld32f(o_t + c * 32, o);
-            tmem_wait_ld();
-            if (mine) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<float4*>(orow + c * 32)[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-          }
-          if (mine) reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml)[at] = make_float2(m_ref, l);
+        }
+        if (mine) {
+          if (!direct)
+            reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml)[at] = make_float2(m_ref, l);
+          else if (p.lse)
+            p.lse[((int64_t)fb * p.Hq + s.hk * p.G + g) * p.T + i] =
+                l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       }
       tc_fence_before();
@@ -633,9 +713,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int part = warp % kWarps;
   const int64_t R = (int64_t)blockIdx.x * kRows + warp / kWarps;
   const bool real = R < (int64_t)p.B * p.T * p.Hq;
-  const int h = real ? (int)(R % p.Hq) : 0;
-  const int64_t bt = real ? R / p.Hq : 0;
-  const int b = (int)(bt / p.T), i = (int)(bt % p.T), hk = h / p.G, g = h % p.G;
+  const int r0 = real ? (int)R : 0;
+  const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
+  const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
@@ -659,6 +739,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         t0 += hk * mine;
       } else {
         int all = 0, before = 0;
+#pragma unroll 1
         for (int x = 0; x < p.own_rt; ++x) {
           const int m = own_tiles(p, kv, n, x);
           if (x < rt) before += m;
@@ -906,6 +987,7 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.page_shift = 4;
   while ((1 << p.page_shift) < a.k.S) ++p.page_shift;
   p.num_pages = (int)a.k.B; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
+  p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
   p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
   p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
