@@ -12,8 +12,8 @@
 // with hundreds of rows on one prefix, the exponentials (16 a clock and SM).
 //
 // Layout of the work:
-//  * A segment is up to 128 query rows that read the same keys: for the prefix
-//    any 128 rows (b, i, g) of the whole batch under one KV head, so that the
+//  * A segment is up to 256 query rows that read the same keys: for the prefix
+//    any 256 rows (b, i, g) of the whole batch under one KV head, so that the
 //    prefix is read once for all; for a request's own keys the rows (i, g) of
 //    that request under one KV head.  A GQA group's heads are rows of one tile.
 //  * All segments' 128-key tiles are put in one row and cut into equal pieces,
@@ -22,15 +22,19 @@
 //    result per CTA; the pair (segment, CTA) only ever steps forward along the
 //    row, so segment + CTA numbers the partial results without gaps of meaning
 //    and without a table.
-//  * One CTA per SM: warp 3 goes through the CTA's segments and hands them to
-//    the others through a ring; warp 0 gathers K and V tiles page by page with
+//  * One CTA per SM: warp 2 goes through the CTA's segments, hands them to the
+//    others through a ring and loads their Q rows; warp 0 gathers K and V tiles page by page with
 //    TMA into a second ring, in the order the products use them (K_0, K_1,
-//    V_0, K_2, V_1 ..); warp 1 issues the MMAs (S = Q K^T of tile q + 1 before
-//    O += P V of tile q); warp 2 loads the next segment's Q rows; warps 4-7 do
-//    the online softmax with one row per thread, P staying in TMEM, and write
-//    the result.  S and O each have two buffers in TMEM, so neither the next
-//    tile nor the next segment waits for the softmax or for the results' way
-//    out.  Code is kept short (one copy of the schedule, rolled loops where
+//    V_0, K_2, V_1 ..); warps 1 and 3 issue the MMAs, S = Q K^T and O += P V
+//    (one thread for both took 1.25 us a job of 16 MMAs); warps 4-7 and 8-11
+//    are two softmax groups, one row per
+//    thread, that take the jobs in turn, each with an S and an O of its own in
+//    TMEM and P staying there.  A job is 128 rows on one key tile: a segment of
+//    more rows makes two jobs of each tile, which read the same K and V; in a
+//    smaller one the groups take every other tile, and each leaves a partial
+//    result (one group took 1.1 us a tile of 128 rows, and 3 us for a segment
+//    of one tile, in which nothing hid the way from S to the result's store).
+//    Code is kept short (one copy of the schedule, rolled loops where
 //    nothing is gained by unrolling): short segments run each role's code once
 //    per microsecond, and with 143 KB of it they took 7 us each.
 //  * paged_join_kernel adds up the partial results (launched with programmatic
@@ -49,14 +53,15 @@ namespace bsa {
 namespace {
 
 constexpr int kTileKeys = 128;
-constexpr int kRowTile = 128;
-constexpr int kPagedThreads = 256;
+constexpr int kRowTile = 256;        // rows of a segment
+constexpr int kHalf = 128;           // rows of a job
+constexpr int kPagedThreads = 384;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;     // blocks of 32 requests in the schedule
 
 template <int D>
 struct PagedCfg {
   static constexpr int kChunks = D / 64;                      // 128-byte chunks per row
-  static constexpr int kQBytes = kRowTile * 128 * kChunks;
+  static constexpr int kQBytes = kHalf * 128 * kChunks;      // 128 rows
   static constexpr int kTileBytes = kTileKeys * 128 * kChunks;
   static constexpr int kBarBytes = 2048;
   static constexpr int kSmemMax = 232448;                     // 227 KB per CTA
@@ -88,8 +93,8 @@ struct PagedParams {
   int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
   int pre_tiles;                  // key tiles of the prefix
-  int pre_slot_rows, own_slot_rows;   // rows of a partial result's slot
-  int ctas;
+  int pre_slot_rows, own_slot_rows;   // rows of one of a slot's two partial results
+  int ctas, pre_w, own_w;
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
@@ -138,11 +143,42 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
   return v;
 }
 
-// Among W tiles, the CTAs that get some (every one of them at least one),
-// the first tile of CTA c of n, and the CTA of tile t.
-__device__ __forceinline__ int cta_count(const PagedParams& p, int W) { return min(p.ctas, W); }
-__device__ __forceinline__ int cta_begin(int c, int n, int W) { return (int)((int64_t)c * W / n); }
-__device__ __forceinline__ int cta_of(int t, int n, int W) { return (int)((((int64_t)t + 1) * n - 1) / W); }
+// The row of tiles is cut by weight: a prefix tile counts pre_w units, a tile
+// of own keys own_w.  The CTAs that get some (every one of them at least one
+// tile: its units are no fewer than a tile's), the first tile of CTA c of n,
+// and the CTA of tile t.
+struct Cut {
+  int pre, pre_w, own_w;          // prefix tiles, weights
+  int n, q, r;                    // CTAs, units of all tiles = q n + r
+  float inv_n, scale;             // 1 / n, n / units
+  __device__ __forceinline__ Cut(const PagedParams& p, int own) {
+    pre = p.pre_tiles * p.pre_rt * p.Hkv;
+    pre_w = p.pre_w;
+    own_w = p.own_w;
+    const int units = pre * pre_w + own * own_w;
+    n = min(p.ctas, units / max(pre > 0 ? pre_w : 0, own > 0 ? own_w : 1));
+    q = n > 0 ? units / n : 0;
+    r = units - q * n;
+    inv_n = 1.f / (float)max(n, 1);
+    scale = (float)n / (float)max(units, 1);
+  }
+  // floor(c units / n); the small quotient is exact in fp32 (c r < 2^20)
+  __device__ __forceinline__ int begin_unit(int c) const { return c * q + (int)(((float)(c * r) + 0.5f) * inv_n); }
+  // the first tile that begins at or behind a CTA's first unit
+  __device__ __forceinline__ int begin(int c) const {
+    const int u = begin_unit(c), pre_units = pre * pre_w;
+    return u < pre_units ? (u + pre_w - 1) / pre_w : pre + (u - pre_units + own_w - 1) / own_w;
+  }
+  __device__ __forceinline__ int cta_of(int t) const {
+    const int u = t < pre ? t * pre_w : pre * pre_w + (t - pre) * own_w;
+    int c = min((int)((float)u * scale), n - 1);     // off by two at most
+#pragma unroll 1
+    while (c + 1 < n && begin_unit(c + 1) <= u) ++c;
+#pragma unroll 1
+    while (begin_unit(c) > u) --c;
+    return c;
+  }
+};
 
 // A segment's part that one CTA works on, as it stands in the segment ring.
 struct __align__(16) Segment {
@@ -157,7 +193,7 @@ struct __align__(16) Segment {
   int pad;
 };
 constexpr int kSegRing = 4;
-constexpr int kSegReaders = 7;       // warps that read every segment
+constexpr int kSegReaders = 11;      // warps that read every segment
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3) {
@@ -172,34 +208,38 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
 // proxy (the MMAs read Q and V through it).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// mbar_wait with one copy of its loop in the code.
-__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return mbar_wait(bar, parity, abort);
+// mbar_wait with one copy of its loop in the code; `bar` and `abort` are
+// shared-memory addresses.
+__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, uint32_t abort) {
+  return mbar_wait(bar, parity, reinterpret_cast<volatile int*>(__cvta_shared_to_generic(abort)));
 }
-__device__ __forceinline__ bool wait_for(const uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return mbar_try_wait(smem_u32(bar), parity) || wait_loop(smem_u32(bar), parity, abort);
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t abort) {
+  return mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort);
 }
 // The same by all lanes of a warp, with one answer for all of them (what
 // follows uses warp-wide instructions).
-__device__ __forceinline__ bool warp_wait(const uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
   return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
 }
 
 // A warp's place in the segment ring.
 struct SegmentReader {
   uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ bool take(const Segment* ring, const uint64_t* seg_full, const uint64_t* seg_empty,
-                                       volatile int* abort, Segment& s) {
-    if (!warp_wait(seg_full + slot, phase, abort)) return false;
+  __device__ __forceinline__ bool take(const Segment* ring, uint32_t seg_full, uint32_t seg_empty, uint32_t abort,
+                                       Segment& s) {
+    if (!warp_wait(seg_full + 8 * slot, phase, abort)) return false;
     const int4* src = reinterpret_cast<const int4*>(ring + slot);
     const int4 a = src[0], b = src[1], c = src[2];
     s.b = a.x; s.hk = a.y; s.row0 = a.z; s.rows = a.w;
     s.tile0 = b.x; s.tiles = b.y; s.slot = b.z; s.whole = b.w;
     s.keys = c.x; s.kv = c.y; s.n = c.z;
-    __syncwarp();
-    if (threadIdx.x % 32 == 0) mbar_arrive(smem_u32(seg_empty + slot));
-    if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+    release(seg_empty);
     return true;
+  }
+  __device__ __forceinline__ void release(uint32_t seg_empty) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(seg_empty + 8 * slot);
+    if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
   }
 };
 
@@ -215,53 +255,52 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* q_smem = smem;                                  // [2] Q buffers
+  uint8_t* q_smem = smem;                                  // [2] Q buffers of 128 rows
   uint8_t* ring = smem + 2 * C::kQBytes;
   Segment* segs = reinterpret_cast<Segment*>(ring + kStages * C::kTileBytes);   // [kSegRing]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(segs + kSegRing);
-  uint64_t* q_full = bars;              // [2] 32 loader threads
-  uint64_t* q_empty = bars + 2;         // [2] commit
-  uint64_t* s_full = bars + 4;          // [2] commit
-  uint64_t* p_full = bars + 6;          // [2] 4 softmax warps
-  uint64_t* o_empty = bars + 8;         // [2] 4 softmax warps
-  // P V of even and of odd tiles [2], commit.  A parity tells only neighbouring
-  // phases apart.  When the softmax waits for P V of tile q it has seen S of
-  // tile q, whose commit covers P V of tile q - 2, but that of q - 1 may still
-  // run: one barrier for all tiles would let it pass too early.
-  uint64_t* pv_done = bars + 10;
-  uint64_t* mma_end = bars + 12;        // commit
-  uint64_t* seg_full = bars + 13;       // [kSegRing] the scheduler
-  uint64_t* seg_empty = seg_full + kSegRing;   // [kSegRing] 7 warps
-  uint64_t* full = seg_empty + kSegRing;       // [kStages] transaction bytes
-  uint64_t* empty = full + kStages;     // [kStages] commit
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(empty + kStages);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // barriers, as shared-memory addresses 8 bytes apart
+  const uint32_t q_full = smem_u32(segs + kSegRing);   // [2] 64 loader threads
+  const uint32_t q_empty = q_full + 16;                // [2] commit
+  const uint32_t s_full = q_full + 32;                 // [2] commit
+  const uint32_t p_full = q_full + 48;                 // [2] 4 softmax warps
+  const uint32_t o_empty = q_full + 64;                // [2] 4 softmax warps
+  // P V of even and of odd jobs [2], commit.  A parity tells only neighbouring
+  // phases apart: who waits for P V of job q knows that P V of job q - 2 is
+  // done, since S of job q was issued behind it.
+  const uint32_t pv_done = q_full + 80;
+  const uint32_t mma_end = q_full + 96;                // commit
+  const uint32_t seg_full = q_full + 112;              // [kSegRing] the scheduler
+  const uint32_t seg_empty = seg_full + 8 * kSegRing;  // [kSegRing] the 11 warps that read it
+  const uint32_t full = seg_empty + 8 * kSegRing;      // [kStages] transaction bytes
+  const uint32_t empty = full + 8 * kStages;           // [kStages] commit
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(segs + kSegRing) + 2 * (14 + 2 * kSegRing + 2 * kStages);
+  const uint32_t abort_flag = empty + 8 * kStages + 4; // behind tmem_slot
   int* total_slot = reinterpret_cast<int*>(tmem_slot + 2);
   int* block_sum = total_slot + 1;      // [kMaxBlocks]: tiles of own keys before request 32 i
-  static_assert(kSegRing * sizeof(Segment) + (13 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes,
+  static_assert(kSegRing * sizeof(Segment) + (14 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes,
                 "barrier block");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(q_full + i), 32);
-      mbar_init(smem_u32(q_empty + i), 1);
-      mbar_init(smem_u32(s_full + i), 1);
-      mbar_init(smem_u32(p_full + i), 4);
-      mbar_init(smem_u32(o_empty + i), 4);
-      mbar_init(smem_u32(pv_done + i), 1);
+      mbar_init(q_full + 8 * i, 64);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(o_empty + 8 * i, 4);
+      mbar_init(pv_done + 8 * i, 1);
     }
-    mbar_init(smem_u32(mma_end), 1);
+    mbar_init(mma_end, 1);
     for (int i = 0; i < kSegRing; ++i) {
-      mbar_init(smem_u32(seg_full + i), 1);
-      mbar_init(smem_u32(seg_empty + i), kSegReaders);
+      mbar_init(seg_full + 8 * i, 1);
+      mbar_init(seg_empty + 8 * i, kSegReaders);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(full + i), 1);
-      mbar_init(smem_u32(empty + i), 1);
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
-    *abort_flag = 0;
+    tmem_slot[1] = 0;                   // abort flag
     fence_mbar_init();
     tma_prefetch_desc(&p.tk);
     tma_prefetch_desc(&p.tv);
@@ -302,15 +341,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const int W = *total_slot + p.pre_tiles * p.pre_rt * p.Hkv;
   if (cta == 0) {
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kPagedThreads) p.cum[b] += block_sum[b / 32];
     if (threadIdx.x == 0) p.cum[p.B] = *total_slot;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int ctas = cta_count(p, W);
-  const int begin = cta < ctas ? cta_begin(cta, ctas, W) : 0, end = cta < ctas ? cta_begin(cta + 1, ctas, W) : 0;
+  int begin = 0, end = 0;
+  {
+    const Cut cut(p, *total_slot);
+    if (cta < cut.n) {
+      begin = cut.begin(cta);
+      end = cut.begin(cta + 1);
+    }
+  }
   bool ok = true;
 
   if (warp == 0) {
@@ -320,19 +364,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const int box_rows = kTileKeys / per_tile;
     const uint32_t ring_base = smem_u32(ring);
     uint32_t stage = 0, phase = 0;
-    int v_page = 0, v_slot = 0, v_hk = 0;          // of the tile whose V is still to come
+    int v_page = 0, v_slot = 0, v_hk = 0;          // the tile whose V is still to come,
+    bool v_left = false;                           // if there is one
     auto load = [&](const CUtensorMap* map, int page, int slot, int hk) -> bool {
       bool go = true;
       if (lane == 0) {
-        go = wait_for(empty + stage, phase ^ 1u, abort_flag);
-        if (go) mbar_arrive_expect_tx(smem_u32(full + stage), C::kTileBytes);
+        go = wait_for(empty + 8 * stage, phase ^ 1u, abort_flag);
+        if (go) mbar_arrive_expect_tx(full + 8 * stage, C::kTileBytes);
       }
       go = __shfl_sync(0xffffffffu, go, 0);
       if (go && lane < per_tile) {
         const uint32_t dst = ring_base + stage * C::kTileBytes + lane * box_rows * 128;
 #pragma unroll
         for (int c = 0; c < C::kChunks; ++c)
-          tma_load_4d(dst + c * (kTileKeys * 128), map, smem_u32(full + stage), c * 64, slot, hk, page);
+          tma_load_4d(dst + c * (kTileKeys * 128), map, full + 8 * stage, c * 64, slot, hk, page);
       }
       __syncwarp();
       if (go) advance<kStages>(stage, phase);
@@ -355,55 +400,67 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         }
         return page;
       };
+      // K of a job's tile, then V of the job before it, each at its first use
+      const bool wide = s.rows > kHalf;
       int page = page_of(s.tile0);
 #pragma unroll 1
       for (int j = s.tile0; j < s.tile0 + s.tiles && ok; ++j) {
         const int next = j + 1 < s.tile0 + s.tiles ? page_of(j + 1) : 0;
         const int slot = (j * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
 #pragma unroll 1
-        for (int which = 0; which < 2 && ok; ++which) {
-          if (which == 0) ok = load(&p.tk, page, slot, s.hk);
-          else if (j > s.tile0 || t > begin) ok = load(&p.tv, v_page, v_slot, v_hk);
+        for (int which = 0; which < 3 && ok; ++which) {
+          if (which == 1 ? !v_left : which == 2 && !wide) continue;
+          const bool old = which == 1;
+          ok = load(which == 0 ? &p.tk : &p.tv, old ? v_page : page, old ? v_slot : slot, old ? v_hk : s.hk);
         }
-        v_page = page; v_slot = slot; v_hk = s.hk;
+        v_left = !wide;
+        if (v_left) { v_page = page; v_slot = slot; v_hk = s.hk; }
         page = next;
       }
       t += s.tiles;
     }
-    if (ok && begin < end) load(&p.tv, v_page, v_slot, v_hk);
+    if (ok && v_left) load(&p.tv, v_page, v_slot, v_hk);
     // the copies in flight land before the CTA may leave
     if (lane == 0) {
 #pragma unroll 1
       for (int i = 0; i < kStages; ++i) {
-        mbar_drain(smem_u32(full + stage), phase ^ 1u);
+        mbar_drain(full + 8 * stage, phase ^ 1u);
         advance<kStages>(stage, phase);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer ---
+    // S of job q, then P V of job q - 1 (MMAs of one thread run in order, so S
+    // of job q may overwrite P of job q - 2 without a wait).
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, true);
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_smem), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t vdesc0 = sdesc_sw128(smem_u32(ring), kTileKeys * 128, 1024);
-    uint32_t stage = 0, phase = 0, q = 0, seg = 0;
-    bool v_first = false;               // of the tile whose P V is still to come
-    uint32_t v_seg = 0;
-    auto product = [&]() -> bool {      // O (+)= P V of tile q - 1
-      const uint32_t tile = q - 1, sb = tile & 1u, ob = v_seg & 1u;
-      if (v_first && !wait_for(o_empty + ob, ((v_seg >> 1) & 1u) ^ 1u, abort_flag)) return false;
-      if (!wait_for(p_full + sb, (tile >> 1) & 1u, abort_flag)) return false;
-      if (!wait_for(full + stage, phase, abort_flag)) return false;
+    uint32_t stage = 0, phase = 0;      // next item of the ring
+    uint32_t q = 0, qi = 0;             // next job, next Q buffer
+    uint32_t k_stage = 0, v_stage = 0;
+    uint32_t uses0 = 0, uses1 = 0;      // segments that each O has been used for
+    bool v_first = false, v_new = false, v_last = false;   // job q - 1: starts its O; takes, releases its V tile
+    auto product = [&]() -> bool {      // job q - 1
+      const uint32_t job = q - 1, w = job & 1u;
+      if (v_first && !wait_for(o_empty + 8 * w, ((w ? uses1++ : uses0++) & 1u) ^ 1u, abort_flag)) return false;
+      if (v_new) {
+        v_stage = stage;
+        if (!wait_for(full + 8 * stage, phase, abort_flag)) return false;
+        advance<kStages>(stage, phase);
+      }
+      if (!wait_for(p_full + 8 * w, (job >> 1) & 1u, abort_flag)) return false;
       tc_fence_after();
-      const uint64_t bs = vdesc0 + (uint64_t)((stage * C::kTileBytes) >> 4);
-      const uint32_t d_t = tmem + 256 + ob * 128, a_t = tmem + sb * 128;
+      const uint64_t bs = vdesc0 + (uint64_t)((v_stage * C::kTileBytes) >> 4);
+      const uint32_t d_t = tmem + 256 + w * 128, a_t = tmem + w * 128;
+      mma_ts(d_t, a_t, bs, idesc_o, !v_first);
 #pragma unroll
-      for (int kk = 0; kk < kTileKeys / 16; ++kk)
-        mma_ts(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o, kk > 0 || !v_first);
-      mma_commit(smem_u32(empty + stage));
-      mma_commit(smem_u32(pv_done + sb));
-      advance<kStages>(stage, phase);
+      for (int kk = 1; kk < kTileKeys / 16; ++kk)
+        mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
+      mma_commit(pv_done + 8 * w);
+      if (v_last) mma_commit(empty + 8 * v_stage);
       return true;
     };
     SegmentReader reader;
@@ -411,69 +468,89 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       Segment s;
       if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
       if (lane == 0) {
-        ok = wait_for(q_full + (seg & 1u), (seg >> 1) & 1u, abort_flag);
+        const bool wide = s.rows > kHalf;
+        const int jobs = wide ? 2 * s.tiles : s.tiles;
 #pragma unroll 1
-        for (int j = 0; j < s.tiles && ok; ++j) {
-          ok = wait_for(full + stage, phase, abort_flag);
-          if (!ok) break;
+        for (int j = 0; j < jobs; ++j) {
+          const uint32_t half = wide ? j & 1 : 0, qb = (qi + half) & 1u, w = q & 1u;
+          if (half == 0) {
+            ok = wait_for(full + 8 * stage, phase, abort_flag);
+            if (!ok) break;
+            k_stage = stage;
+            advance<kStages>(stage, phase);
+          }
+          if (j <= (int)half && !(ok = wait_for(q_full + 8 * qb, ((qi + half) >> 1) & 1u, abort_flag))) break;
           tc_fence_after();
-          const uint64_t as = qdesc0 + (uint64_t)(((seg & 1u) * C::kQBytes) >> 4);
-          const uint64_t bs = kdesc0 + (uint64_t)((stage * C::kTileBytes) >> 4);
-          const uint32_t d_t = tmem + (q & 1u) * 128;
+          const uint64_t as = qdesc0 + (uint64_t)((qb * C::kQBytes) >> 4);
+          const uint64_t bs = kdesc0 + (uint64_t)((k_stage * C::kTileBytes) >> 4);
+          const uint32_t d_t = tmem + w * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             constexpr int kChunk = (kTileKeys * 128) >> 4;
             const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
-            mma_ss(d_t, as + off, bs + off, idesc_s, kk > 0);
+            if (kk == 0) mma_ss_acc<0>(d_t, as + off, bs + off, idesc_s);
+            else mma_ss_acc<1>(d_t, as + off, bs + off, idesc_s);
           }
-          mma_commit(smem_u32(s_full + (q & 1u)));
-          mma_commit(smem_u32(empty + stage));
-          if (j == s.tiles - 1) mma_commit(smem_u32(q_empty + (seg & 1u)));
-          advance<kStages>(stage, phase);
-          if (q > 0) ok = product();
+          mma_commit(s_full + 8 * w);
+          if (!wide || half == 1) mma_commit(empty + 8 * k_stage);
+          if (j >= jobs - (wide ? 2 : 1)) mma_commit(q_empty + 8 * qb);
+          if (q > 0 && !(ok = product())) break;
           ++q;
-          v_first = j == 0;
-          v_seg = seg;
+          v_first = j < 2;
+          v_new = half == 0;
+          v_last = !wide || half == 1;
         }
+        qi += wide ? 2 : 1;
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
-      ++seg;
       t += s.tiles;
     }
     if (lane == 0) {
       if (ok && q > 0) product();
-      mma_commit(smem_u32(mma_end));    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
-      mbar_drain(smem_u32(mma_end), 0);
+      mma_commit(mma_end);    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
+      mbar_drain(mma_end, 0);
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // --------------------------------------------------------- Q loader ---
+  } else if (warp == 2 || warp == 3) {
+    // Q rows of a segment into the next one or two Q buffers: each lane works
+    // out the address of one of 32 rows, then 32 / kVec rows are copied at a
+    // time; the two warps take every other 32 rows, from r_first on.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
     const int c = lane % kVec;
-    uint32_t seg = 0;
-    SegmentReader reader;
-    for (int t = begin; t < end && ok; ++seg) {
-      Segment s;
-      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      if (!(ok = warp_wait(q_empty + (seg & 1u), ((seg >> 1) & 1u) ^ 1u, abort_flag))) break;
-      const uint32_t base = smem_u32(q_smem) + (seg & 1u) * C::kQBytes + (c / 8) * (kRowTile * 128);
+    uint32_t qi = 0;
+    auto load_q = [&](const Segment& s, int r_first) -> bool {
       const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
-#pragma unroll 2
-      for (int r = lane / kVec; r < s.rows; r += kRowsPer) {
-        const int row = s.row0 + r, b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
-        const __nv_bfloat16* src = head + b * p.q_sb + i * p.q_ss + g * p.q_sh;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + r * 128 + ((c % 8) ^ (r % 8)) * 16), "l"(src)
-                     : "memory");
+#pragma unroll 1
+      for (int r0 = 0; r0 < s.rows; r0 += kHalf, ++qi) {
+        const uint32_t qb = qi & 1u;
+        if (!warp_wait(q_empty + 8 * qb, ((qi >> 1) & 1u) ^ 1u, abort_flag)) return false;
+        const uint32_t base = smem_u32(q_smem) + qb * C::kQBytes + (c / 8) * (kHalf * 128) + (lane / kVec) * 128;
+        const int rows = min(kHalf, s.rows - r0);
+#pragma unroll 1
+        for (int r32 = r_first; r32 < rows; r32 += 64) {
+          const int row = s.row0 + r0 + min(r32 + lane, rows - 1);
+          const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+          const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
+#pragma unroll 4
+          for (int x = 0; x < kVec; ++x) {
+            const int in = x * kRowsPer + lane / kVec, r = r32 + in;
+            const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, in) * 8;
+            if (r < rows)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + (r32 + x * kRowsPer) * 128 +
+                                                                             ((c % 8) ^ (in % 8)) * 16),
+                           "l"(src)
+                           : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        fence_async_shared();
+        mbar_arrive(q_full + 8 * qb);
       }
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-      fence_async_shared();
-      mbar_arrive(smem_u32(q_full + (seg & 1u)));
-      t += s.tiles;
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // -------------------------------------------------------- scheduler ---
+      return true;
+    };
+    if (warp == 2) {
+    // ------------------------------------------------------- scheduler ---
     // The segments of tiles [begin, end) in their order.  Lane l holds request
     // 32 blk + l: its lengths, tiles, and the tiles up to its end.
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
@@ -529,64 +606,97 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       s.tiles = min(t1, end) - t;
       s.whole = begin <= t0 && t1 <= end;
       s.pad = 0;
-      if (!(ok = warp_wait(seg_empty + slot, phase ^ 1u, abort_flag))) break;
+      if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
       if (lane == 0) {
         segs[slot] = s;
-        mbar_arrive(smem_u32(seg_full + slot));
+        mbar_arrive(seg_full + 8 * slot);
       }
       __syncwarp();
       if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+      ok = load_q(s, 0);
       t += s.tiles;
     }
+    } else {
+    // the second loader
+    SegmentReader reader;
+    for (int t = begin; t < end && ok;) {
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
+      ok = load_q(s, 32);
+      t += s.tiles;
+    }
+    }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // --------------------------------------------------- softmax + results ---
+    const uint32_t w = (warp - 4) / 4;             // the group: it takes the jobs q with q % 2 == w
     const int wq = warp % 4;
     const int r = wq * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    uint32_t seg = 0, q = 0;
-    const int all_tiles = end - begin;
-    // number of tile q's V among the ring's items (K_0, K_1, V_0, K_2, V_1 ..)
-    auto v_item = [&](int tile) { return tile == all_tiles - 1 ? 2 * all_tiles - 1 : 2 * tile + 2; };
+    const uint32_t s_t = tmem + lane_base + w * 128;
+    const uint32_t o_t = tmem + lane_base + 256 + w * 128;
+    uint32_t q = 0;                                // first job of the segment
+    uint32_t items = 0;                            // ring items that the jobs before q have taken
+    bool v_left = false;                           // job q - 1 takes one for V in job q's turn
+    // The segment's fields stay in the ring until the group is through with it:
+    // with S in 128 registers there is no room to hold them.
     SegmentReader reader;
-    for (int t = begin; t < end && ok; ++seg) {
-      Segment s;
-      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      const uint32_t ob = seg & 1u;
-      const uint32_t o_t = tmem + lane_base + 256 + ob * 128;
-      const bool active = wq * 32 < s.rows;        // some row of this warp is real
-      const int row = s.row0 + r;
-      const int fb = p.div_TG.quot(row), rem = row - fb * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
-      const int limit = s.b < 0 ? p.prefix_len : (r < s.rows ? min(seen_keys(p, s.kv, s.n, i), s.kv) : 0);
+    for (int t = begin; t < end && ok;) {
+      if (!(ok = warp_wait(seg_full + 8 * reader.slot, reader.phase, abort_flag))) break;
+      const Segment& s = segs[reader.slot];
+      const bool wide = s.rows > kHalf;
+      const int jobs = wide ? 2 * s.tiles : s.tiles;
+      const int j0 = (int)((w ^ q) & 1u);          // this group's first job of the segment
+      const int half = wide ? j0 : 0;              // and the rows that its jobs have
+      const int rows = min(kHalf, s.rows - half * kHalf);
+      const bool active = wq * 32 < rows;          // some row of this warp is real
+      int limit = p.prefix_len;                    // keys that the row sees
+      if (s.b >= 0) {
+        const int rem = s.row0 + half * kHalf + r - s.b * p.TG;
+        limit = r < rows ? min(seen_keys(p, s.kv, s.n, p.div_G.quot(rem)), s.kv) : 0;
+      }
       float m_ref = -INFINITY, l = 0.f;
 #pragma unroll 1
-      for (int j = 0; j < s.tiles; ++j, ++q) {
-        const uint32_t sb = q & 1u;
-        const uint32_t s_t = tmem + lane_base + sb * 128;
-        const int key0 = (s.tile0 + j) * kTileKeys;
-        ok = warp_wait(s_full + sb, (q >> 1) & 1u, abort_flag);
+      for (int j = j0; j < jobs; j += 2) {
+        const int tile = wide ? j >> 1 : j;
+        const int key0 = (s.tile0 + tile) * kTileKeys;
+        ok = warp_wait(s_full + 8 * w, ((q + j) >> 1) & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          float v[kTileKeys];
-#pragma unroll
-          for (int c = 0; c < kTileKeys / 32; ++c) tmem_ld32f(s_t + c * 32, v + c * 32);
-          tmem_wait_ld();
+          // S is read twice, 64 columns at a time: held whole in registers the
+          // code is three times as long, and no longer fits the instruction cache.
           const int valid = limit - key0;
-          if (valid < kTileKeys) {
+          if (__any_sync(0xffffffffu, valid < kTileKeys)) {      // keys that some row of the warp does not see
+#pragma unroll 1
+            for (int c = 0; c < kTileKeys / 32; ++c) {
+              float v[32];
+              tmem_ld32f(s_t + c * 32, v);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kTileKeys; ++c)
-              if (c >= valid) v[c] = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= valid) v[e] = -INFINITY;
+              tmem_st32f(s_t + c * 32, v);
+            }
+            tmem_wait_st();
           }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kTileKeys; c += 64) {
+            float v[64];
+            tmem_ld32f(s_t + c, v);
+            tmem_ld32f(s_t + c + 32, v + 32);
+            tmem_wait_ld();
+            float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kTileKeys; c += 8) {
-            m0 = max3f(m0, v[c], v[c + 1]);
-            m1 = max3f(m1, v[c + 2], v[c + 3]);
-            m2 = max3f(m2, v[c + 4], v[c + 5]);
-            m3 = max3f(m3, v[c + 6], v[c + 7]);
+            for (int e = 0; e < 64; e += 8) {
+              m0 = max3f(m0, v[e], v[e + 1]);
+              m1 = max3f(m1, v[e + 2], v[e + 3]);
+              m2 = max3f(m2, v[e + 4], v[e + 5]);
+              m3 = max3f(m3, v[e + 6], v[e + 7]);
+            }
+            mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
           }
-          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
           const float m_new = fmaxf(m_ref, mx * p.scale_log2);
           const bool grow = m_new > m_ref + 8.0f;
           const bool rescale = grow && m_ref != -INFINITY;
@@ -595,28 +705,30 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_use, -m_use);
           float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int cc = 0; cc < kTileKeys / 64; ++cc) {
+#pragma unroll 1
+          for (int c = 0; c < kTileKeys; c += 64) {
+            float v[64];
             uint32_t pk[32];
+            tmem_ld32f(s_t + c, v);
+            tmem_ld32f(s_t + c + 32, v + 32);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-              const float2 a = __ffma2_rn(make_float2(v[cc * 64 + c], v[cc * 64 + c + 1]), sc2, nm2);
-              const float2 b = __ffma2_rn(make_float2(v[cc * 64 + c + 2], v[cc * 64 + c + 3]), sc2, nm2);
+            for (int e = 0; e < 64; e += 4) {
+              const float2 a = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, nm2);
+              const float2 b = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), sc2, nm2);
               const float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
               const float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
               ls0 = __fadd2_rn(ls0, e0);
               ls1 = __fadd2_rn(ls1, e1);
-              pk[c / 2] = pack_bf16x2(e0.x, e0.y);
-              pk[c / 2 + 1] = pack_bf16x2(e1.x, e1.y);
+              pk[e / 2] = pack_bf16x2(e0.x, e0.y);
+              pk[e / 2 + 1] = pack_bf16x2(e1.x, e1.y);
             }
-            tmem_st32(s_t + cc * 32, pk);
+            tmem_st32(s_t + c / 2, pk);            // P of these 64 keys over S of keys read already
           }
           l = l * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
-          // O is rescaled only when the maximum grew by more than 2^8
+          // O is rescaled only when the maximum grew by more than 2^8 (P V of the
+          // group's job before is done: S of this one was issued behind it)
           if (__any_sync(0xffffffffu, rescale)) {
-            ok = warp_wait(pv_done + ((q - 1) & 1u), ((q - 1) >> 1) & 1u, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float o[32];
@@ -630,11 +742,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           tmem_wait_st();
         }
         // The last tile's rows behind the keys hold whatever stood in the page:
-        // they are zeroed in V (0 times infinity or NaN is NaN).
+        // they are zeroed in V (0 times infinity or NaN is NaN), before the
+        // first of the jobs that use it.
         const int there = s.keys - key0;
-        if (there < kTileKeys) {
-          const uint32_t item = (uint32_t)v_item((int)q);
-          ok = warp_wait(full + item % kStages, (item / kStages) & 1u, abort_flag);
+        if (there < kTileKeys && half == 0) {
+          // Which ring item V is: in a wide segment the one behind the tile's K
+          // (its second job takes no K); else the one behind the next tile's K,
+          // if there is a next tile.
+          const bool last = t + s.tiles == end && tile == s.tiles - 1;
+          const uint32_t item = items + (v_left ? 1u : 0u) + 2u * (uint32_t)tile + (wide || last ? 1u : 2u);
+          ok = warp_wait(full + 8 * (item % kStages), (item / kStages) & 1u, abort_flag);
           if (!ok) break;
           if (r >= there) {
             const uint32_t at = smem_u32(ring) + (item % kStages) * C::kTileBytes + r * 128;
@@ -649,18 +766,28 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(p_full + sb));
+        if (lane == 0) mbar_arrive(p_full + 8 * w);
       }
       if (!ok) break;
-      ok = warp_wait(pv_done + ((q - 1) & 1u), ((q - 1) >> 1) & 1u, abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      if (active) {
-        const bool direct = p.pre_tiles == 0 && s.whole;
-        const bool mine = r < s.rows;
+      const int last_j = jobs - 1 - (int)((jobs - 1 - j0) & 1);     // this group's last job (below j0: none)
+      if (last_j >= j0) {
+        ok = warp_wait(pv_done + 8 * w, ((q + last_j) >> 1) & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // a segment of more rows, or of one tile, that no other CTA works on and
+      // no prefix stands beside: the result; else a partial one
+      const bool direct = p.pre_tiles == 0 && s.whole && (wide || s.tiles == 1);
+      const bool mine = r < rows;
+      const int row = s.row0 + half * kHalf + r;
+      const int fb = p.div_TG.quot(row), rem = row - fb * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+      const int64_t at = ((int64_t)s.slot * 2 + (wide ? half : (int)w)) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
+      float2* ml = reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml) + at;
+      if (last_j < j0) {
+        if (mine && !direct) *ml = make_float2(-INFINITY, 0.f);      // the other group had the segment's only tile
+      } else if (active) {
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
-        const int64_t at = (int64_t)s.slot * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
         char* dst = direct ? reinterpret_cast<char*>(p.out + orow * D)
                            : reinterpret_cast<char*>((s.b < 0 ? p.pre_o : p.own_o) + at * D);
 #pragma unroll 1
@@ -683,16 +810,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         }
         if (mine) {
           if (!direct)
-            reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml)[at] = make_float2(m_ref, l);
+            *ml = make_float2(m_ref, l);
           else if (p.lse)
             p.lse[((int64_t)fb * p.Hq + s.hk * p.G + g) * p.T + i] =
                 l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(o_empty + ob));
+      if (last_j >= j0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty + 8 * w);
+      }
+      items += (v_left ? 1u : 0u) + 2u * (uint32_t)s.tiles - (wide ? 0u : 1u);
+      v_left = !wide;
+      q += jobs;
       t += s.tiles;
+      reader.release(seg_empty);
     }
   }
   tc_fence_before();
@@ -709,6 +842,7 @@ template <int D, int kWarps>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / 32;
   constexpr int kRows = 4 / kWarps;                // rows per block
+  constexpr int kLoads = 8;                        // partial rows in flight per warp
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int part = warp % kWarps;
   const int64_t R = (int64_t)blockIdx.x * kRows + warp / kWarps;
@@ -718,20 +852,23 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
-  const int W = p.cum[p.B] + pre, ctas = cta_count(p, W);
-  int pre_c0 = 0, pre_n = 0, own_c0 = 0, own_n = 0;
+  const Cut cut(p, p.cum[p.B]);
+  const int pre = cut.pre;
+  // Partial results: from each CTA of a segment one, or two of a segment of up
+  // to 128 rows (one of each group).
+  int pre_n = 0, own_n = 0, pre_two = 0, own_two = 0;
   int64_t pre_at = 0, own_at = 0;
   bool direct = false;
   if (real && i < n) {
     const int row = i * p.G + g;
     if (pre > 0) {
-      const int flat = b * p.TG + row, seg = hk * p.pre_rt + flat / kRowTile;
-      pre_c0 = cta_of(seg * p.pre_tiles, ctas, W);
-      pre_n = cta_of(seg * p.pre_tiles + p.pre_tiles - 1, ctas, W) - pre_c0 + 1;
-      pre_at = (int64_t)(seg + pre_c0) * p.pre_slot_rows + flat % kRowTile;
+      const int flat = b * p.TG + row, rt = flat / kRowTile, in = flat % kRowTile, seg = hk * p.pre_rt + rt;
+      const int c0 = cut.cta_of(seg * p.pre_tiles);
+      pre_two = p.B * p.TG - rt * kRowTile <= kHalf;
+      pre_n = (cut.cta_of(seg * p.pre_tiles + p.pre_tiles - 1) - c0 + 1) << pre_two;
+      pre_at = ((int64_t)(seg + c0) * 2 + in / kHalf) * p.pre_slot_rows + in % kHalf;
     }
-    const int rt = row / kRowTile;
+    const int rt = row / kRowTile, in = row % kRowTile;
     const int mine = own_tiles(p, kv, n, rt);
     if (mine > 0) {
       int t0 = pre + p.cum[b];
@@ -747,56 +884,80 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         }
         t0 += hk * all + before;
       }
-      own_c0 = cta_of(t0, ctas, W);
-      own_n = cta_of(t0 + mine - 1, ctas, W) - own_c0 + 1;
-      own_at = (int64_t)((b * p.Hkv + hk) * p.own_rt + rt + own_c0) * p.own_slot_rows + row % kRowTile;
-      direct = pre == 0 && own_n == 1;             // written by the first kernel
+      const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + mine - 1);
+      own_two = n * p.G - rt * kRowTile <= kHalf;
+      direct = pre == 0 && c0 == c1 && (!own_two || mine == 1);      // written by the first kernel
+      own_n = (c1 - c0 + 1) << own_two;
+      own_at = ((int64_t)((b * p.Hkv + hk) * p.own_rt + rt + c0) * 2 + in / kHalf) * p.own_slot_rows + in % kHalf;
     }
   }
-  const int parts = pre_n + own_n;
+  // Lane x holds the maximum and the sum of partial result base + x; then the
+  // rows themselves are read, each warp every kWarps-th of them.
+  const int parts = real && !direct ? pre_n + own_n : 0;
   float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  if (real && !direct) {
-#pragma unroll 4
-    for (int x = part; x < parts; x += kWarps) {
-      const bool first = x < pre_n;
-      const int64_t at = first ? pre_at + (int64_t)x * p.pre_slot_rows : own_at + (int64_t)(x - pre_n) * p.own_slot_rows;
-      const float2 ml = reinterpret_cast<const float2*>(first ? p.pre_ml : p.own_ml)[at];
-      const float* orow = (first ? p.pre_o : p.own_o) + at * D + lane * kPer;
-      float o[kPer];
+#pragma unroll 1
+  for (int base = 0; base < parts; base += 32) {
+    const int x = base + lane;
+    const bool pre_part = x < pre_n;
+    // a segment's CTAs are a slot of two results apart, the groups' one
+    const int64_t at = pre_part ? pre_at + (int64_t)(pre_two ? x : 2 * x) * p.pre_slot_rows
+                                : own_at + (int64_t)(own_two ? x - pre_n : 2 * (x - pre_n)) * p.own_slot_rows;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (x < parts) ml = reinterpret_cast<const float2*>(pre_part ? p.pre_ml : p.own_ml)[at];
+    float m2 = fmaxf(m, ml.x);
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(o + e) = *reinterpret_cast<const float2*>(orow + e);
-      const float m2 = fmaxf(m, ml.x);
-      const float a = m == -INFINITY ? 0.f : ex2_approx(m - m2), w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m2);
-      m = m2;
-      l = l * a + ml.y * w;
-      // a row that sees none of the partial result's keys has no sums there
+    for (int o = 16; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    const float a = m == -INFINITY ? 0.f : ex2_approx(m - m2), w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m2);
+    float sum = ml.y * w;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * a + (w > 0.f ? o[e] * w : 0.f);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    m = m2;
+    l = l * a + sum;
+    const float* orow = (pre_part ? p.pre_o : p.own_o) + at * D;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= a;
+    const int n_here = min(32, parts - base);
+#pragma unroll 1
+    for (int y0 = part; y0 < n_here; y0 += kWarps * kLoads) {
+      float wy[kLoads];
+      float2 o[kLoads][kPer / 2];
+      // all loads before the first sum; a group without a tile, or a row
+      // without a key there, has left no row
+#pragma unroll
+      for (int z = 0; z < kLoads; ++z) {
+        const int y = y0 + z * kWarps;
+        wy[z] = __shfl_sync(0xffffffffu, w, y % 32);
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)orow, y % 32));
+        if (y >= n_here) wy[z] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e)
+          o[z][e] = wy[z] > 0.f ? *reinterpret_cast<const float2*>(src + lane * kPer + 2 * e) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int z = 0; z < kLoads; ++z) {
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) {
+          acc[2 * e] = fmaf(o[z][e].x, wy[z], acc[2 * e]);
+          acc[2 * e + 1] = fmaf(o[z][e].y, wy[z], acc[2 * e + 1]);
+        }
+      }
     }
   }
   if constexpr (kWarps > 1) {
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-    if (lane == 0) { sm[part] = m; sl[part] = l; }
+    __shared__ float so[kWarps][D];    // m and l are the same in all warps
 #pragma unroll
     for (int e = 0; e < kPer; ++e) so[part][lane * kPer + e] = acc[e];
     __syncthreads();
     if (part != 0) return;
-    float mm = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, sm[x]);
-    l = 0.f;
+    for (int e = 0; e < kPer; ++e) {
+      float o = so[0][lane * kPer + e];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-      const float w = sm[x] == -INFINITY ? 0.f : ex2_approx(sm[x] - mm);
-      l += sl[x] * w;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += so[x][lane * kPer + e] * w;
+      for (int x = 1; x < kWarps; ++x) o += so[x][lane * kPer + e];
+      acc[e] = o;
     }
-    m = mm;
   }
   if (!real || direct) return;
   const float inv_l = l > 0.f ? 1.f / l : 0.f;
@@ -824,12 +985,12 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   w.TG = (int)(T * G);
   w.own_rt = (int)cdiv64(w.TG, kRowTile);
   w.pre_rt = prefix ? (int)cdiv64(B * w.TG, kRowTile) : 0;
-  w.own_slot_rows = w.TG < kRowTile ? w.TG : kRowTile;
-  w.pre_slot_rows = (int)(B * w.TG < kRowTile ? B * w.TG : kRowTile);
+  w.own_slot_rows = w.TG < kHalf ? w.TG : kHalf;
+  w.pre_slot_rows = (int)(B * w.TG < kHalf ? B * w.TG : kHalf);
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  // a slot for every number segment + CTA
-  const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * w.own_slot_rows;
-  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * w.pre_slot_rows : 0;
+  // a slot of two partial results for every number segment + CTA
+  const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * 2 * w.own_slot_rows;
+  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
   w.cum = 0;
   w.pre_ml = al((size_t)(B + 1) * 4);
   w.pre_o = w.pre_ml + al(pre * 8);
@@ -966,9 +1127,12 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   const int sms = num_sms();
   // rows, tiles and slot numbers are 32-bit on the device
   const int64_t flat_rows = qv.B * qv.S * G, row_tiles = cdiv64(qv.S * G, kRowTile);
+  const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
+  if (q_extent >= (int64_t)1 << 35)
+    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": q reaches over " + s(q_extent) + " elements (2^35 at most)");
   const int64_t most_tiles = qv.B * a.k.H * row_tiles * cdiv64(max_pages * a.k.S, kTileKeys) +
                              a.k.H * cdiv64(flat_rows, kRowTile) * cdiv64(prefix_len, kTileKeys);
-  if (flat_rows > INT32_MAX / 4 || most_tiles > INT32_MAX / 2 || flat_rows * a.k.H > INT32_MAX)
+  if (flat_rows > INT32_MAX / 4 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.H > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
                                               s(max_pages * a.k.S + prefix_len) + " keys are too many for one call");
   const PagedPlan plan = plan_paged(qv.B, qv.S, qv.H, a.k.H, qv.D, prefix_len > 0, sms);
@@ -992,6 +1156,11 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = sms;
+  // A wide prefix tile (two jobs of 1 us on the tensor cores) takes longer than
+  // a tile of own keys for a few rows (1.5 us at its share of the memory rate).
+  const bool wide_pre = flat_rows > kHalf && qv.S * G <= kHalf;
+  p.pre_w = wide_pre ? 4 : 1;
+  p.own_w = wide_pre ? 3 : 1;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
