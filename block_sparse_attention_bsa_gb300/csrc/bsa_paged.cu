@@ -248,6 +248,13 @@ __device__ __forceinline__ void advance(uint32_t& stage, uint32_t& phase) {
   if (++stage == N) { stage = 0; phase ^= 1u; }
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
   using C = PagedCfg<D>;
@@ -432,7 +439,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer ---
     // S of job q, then P V of job q - 1 (MMAs of one thread run in order, so S
-    // of job q may overwrite P of job q - 2 without a wait).
+    // of job q may overwrite P of job q - 2 without a wait).  The whole warp
+    // goes through the loop and one lane issues: the descriptors then stay in
+    // uniform registers (in a branch of one lane each MMA took 26 instructions).
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, true);
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_smem), 16, 1024);
@@ -443,70 +452,75 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     uint32_t k_stage = 0, v_stage = 0;
     uint32_t uses0 = 0, uses1 = 0;      // segments that each O has been used for
     bool v_first = false, v_new = false, v_last = false;   // job q - 1: starts its O; takes, releases its V tile
-    auto product = [&]() -> bool {      // job q - 1
-      const uint32_t job = q - 1, w = job & 1u;
-      if (v_first && !wait_for(o_empty + 8 * w, ((w ? uses1++ : uses0++) & 1u) ^ 1u, abort_flag)) return false;
-      if (v_new) {
-        v_stage = stage;
-        if (!wait_for(full + 8 * stage, phase, abort_flag)) return false;
-        advance<kStages>(stage, phase);
-      }
-      if (!wait_for(p_full + 8 * w, (job >> 1) & 1u, abort_flag)) return false;
-      tc_fence_after();
-      const uint64_t bs = vdesc0 + (uint64_t)((v_stage * C::kTileBytes) >> 4);
-      const uint32_t d_t = tmem + 256 + w * 128, a_t = tmem + w * 128;
-      mma_ts(d_t, a_t, bs, idesc_o, !v_first);
-#pragma unroll
-      for (int kk = 1; kk < kTileKeys / 16; ++kk)
-        mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
-      mma_commit(pv_done + 8 * w);
-      if (v_last) mma_commit(empty + 8 * v_stage);
-      return true;
-    };
     SegmentReader reader;
-    for (int t = begin; t < end && ok;) {
-      Segment s;
-      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      if (lane == 0) {
-        const bool wide = s.rows > kHalf;
-        const int jobs = wide ? 2 * s.tiles : s.tiles;
 #pragma unroll 1
-        for (int j = 0; j < jobs; ++j) {
+    for (int t = begin; begin < end;) {
+      const bool more = t < end;        // after the last segment there is one P V left
+      Segment s;
+      s.rows = s.tiles = 1;
+      if (more && !reader.take(segs, seg_full, seg_empty, abort_flag, s)) break;
+      const bool wide = s.rows > kHalf;
+      const int jobs = wide ? 2 * s.tiles : s.tiles;
+#pragma unroll 1
+      for (int j = 0; j < jobs; ++j) {
+        if (more) {
           const uint32_t half = wide ? j & 1 : 0, qb = (qi + half) & 1u, w = q & 1u;
           if (half == 0) {
-            ok = wait_for(full + 8 * stage, phase, abort_flag);
-            if (!ok) break;
+            if (!(ok = warp_wait(full + 8 * stage, phase, abort_flag))) break;
             k_stage = stage;
             advance<kStages>(stage, phase);
           }
-          if (j <= (int)half && !(ok = wait_for(q_full + 8 * qb, ((qi + half) >> 1) & 1u, abort_flag))) break;
+          if (j <= (int)half && !(ok = warp_wait(q_full + 8 * qb, ((qi + half) >> 1) & 1u, abort_flag))) break;
           tc_fence_after();
           const uint64_t as = qdesc0 + (uint64_t)((qb * C::kQBytes) >> 4);
           const uint64_t bs = kdesc0 + (uint64_t)((k_stage * C::kTileBytes) >> 4);
           const uint32_t d_t = tmem + w * 128;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            constexpr int kChunk = (kTileKeys * 128) >> 4;
-            const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
-            if (kk == 0) mma_ss_acc<0>(d_t, as + off, bs + off, idesc_s);
-            else mma_ss_acc<1>(d_t, as + off, bs + off, idesc_s);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              constexpr int kChunk = (kTileKeys * 128) >> 4;
+              const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
+              if (kk == 0) mma_ss_acc<0>(d_t, as + off, bs + off, idesc_s);
+              else mma_ss_acc<1>(d_t, as + off, bs + off, idesc_s);
+            }
+            mma_commit(s_full + 8 * w);
+            if (!wide || half == 1) mma_commit(empty + 8 * k_stage);
+            if (j >= jobs - (wide ? 2 : 1)) mma_commit(q_empty + 8 * qb);
           }
-          mma_commit(s_full + 8 * w);
-          if (!wide || half == 1) mma_commit(empty + 8 * k_stage);
-          if (j >= jobs - (wide ? 2 : 1)) mma_commit(q_empty + 8 * qb);
-          if (q > 0 && !(ok = product())) break;
-          ++q;
-          v_first = j < 2;
-          v_new = half == 0;
-          v_last = !wide || half == 1;
+          __syncwarp();
         }
-        qi += wide ? 2 : 1;
+        if (q > 0) {                    // O (+)= P V of job q - 1
+          const uint32_t job = q - 1, w = job & 1u;
+          if (v_first && !(ok = warp_wait(o_empty + 8 * w, ((w ? uses1++ : uses0++) & 1u) ^ 1u, abort_flag))) break;
+          if (v_new) {
+            v_stage = stage;
+            if (!(ok = warp_wait(full + 8 * stage, phase, abort_flag))) break;
+            advance<kStages>(stage, phase);
+          }
+          if (!(ok = warp_wait(p_full + 8 * w, (job >> 1) & 1u, abort_flag))) break;
+          tc_fence_after();
+          const uint64_t bs = vdesc0 + (uint64_t)((v_stage * C::kTileBytes) >> 4);
+          const uint32_t d_t = tmem + 256 + w * 128, a_t = tmem + w * 128;
+          if (elect_one()) {
+            mma_ts(d_t, a_t, bs, idesc_o, !v_first);
+#pragma unroll
+            for (int kk = 1; kk < kTileKeys / 16; ++kk)
+              mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
+            mma_commit(pv_done + 8 * w);
+            if (v_last) mma_commit(empty + 8 * v_stage);
+          }
+          __syncwarp();
+        }
+        ++q;
+        v_first = j < 2;
+        v_new = !wide || (j & 1) == 0;
+        v_last = !wide || (j & 1) == 1;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok || !more) break;
+      qi += wide ? 2 : 1;
       t += s.tiles;
     }
-    if (lane == 0) {
-      if (ok && q > 0) product();
+    if (elect_one()) {
       mma_commit(mma_end);    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
       mbar_drain(mma_end, 0);
     }
