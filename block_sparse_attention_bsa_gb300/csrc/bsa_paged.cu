@@ -102,8 +102,9 @@ struct PagedParams {
   __nv_bfloat16* out;
   float* lse;
   int32_t* cum;                   // workspace: [B + 1] tiles of own keys before request b
-  float* pre_ml; float* pre_o;    // workspace: partial (max, sum) and rows, prefix
-  float* own_ml; float* own_o;    // the same, own keys
+  float* part_ml;                 // workspace: partial results' (max, sum) and rows,
+  float* part_o;                  // those of the prefix first,
+  int own_first;                  // from here on those of own keys
 };
 
 // Request b's own keys and new tokens, clamped to what the tables hold.
@@ -795,15 +796,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       const bool mine = r < rows;
       const int row = s.row0 + half * kHalf + r;
       const int fb = p.div_TG.quot(row), rem = row - fb * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
-      const int64_t at = ((int64_t)s.slot * 2 + (wide ? half : (int)w)) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
-      float2* ml = reinterpret_cast<float2*>(s.b < 0 ? p.pre_ml : p.own_ml) + at;
+      const int at = (s.b < 0 ? 0 : p.own_first) +
+                     (s.slot * 2 + (wide ? half : (int)w)) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
+      float2* ml = reinterpret_cast<float2*>(p.part_ml) + at;
       if (last_j < j0) {
         if (mine && !direct) *ml = make_float2(-INFINITY, 0.f);      // the other group had the segment's only tile
       } else if (active) {
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
         char* dst = direct ? reinterpret_cast<char*>(p.out + orow * D)
-                           : reinterpret_cast<char*>((s.b < 0 ? p.pre_o : p.own_o) + at * D);
+                           : reinterpret_cast<char*>(p.part_o + (int64_t)at * D);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
@@ -851,15 +853,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
 }
 
 // Output row (b, i, h): joins the partial results of its prefix segment and of
-// its own segment.  kWarps warps share a row (many partial results: few rows).
-template <int D, int kWarps>
+// its own segment.  kLanes lanes of kWarps warps share a row: eight lanes where
+// there are many rows (a warp's way through its dependent loads takes 4 us, so
+// four rows go it together), four warps where there are few rows of many
+// partial results.
+template <int D, int kLanes, int kWarps>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int kPer = D / 32;
-  constexpr int kRows = 4 / kWarps;                // rows per block
-  constexpr int kLoads = 8;                        // partial rows in flight per warp
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kPer = D / kLanes;                 // values per lane, kVec at a time
+  constexpr int kVec = kPer < 4 ? kPer : 4;
+  constexpr int kRows = 128 / (kLanes * kWarps);   // rows per block
+  constexpr int kLoads = kWarps > 1 ? 8 : 2;       // partial rows in flight per lane
+  static_assert(kWarps == 1 || kLanes == 32, "several warps take whole rows");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
   const int part = warp % kWarps;
-  const int64_t R = (int64_t)blockIdx.x * kRows + warp / kWarps;
+  const int64_t R = (int64_t)blockIdx.x * kRows + threadIdx.x / (kLanes * kWarps);
   const bool real = R < (int64_t)p.B * p.T * p.Hq;
   const int r0 = real ? (int)R : 0;
   const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
@@ -870,17 +877,17 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int pre = cut.pre;
   // Partial results: from each CTA of a segment one, or two of a segment of up
   // to 128 rows (one of each group).
-  int pre_n = 0, own_n = 0, pre_two = 0, own_two = 0;
-  int64_t pre_at = 0, own_at = 0;
+  int pre_n = 0, own_n = 0, pre_at = 0, own_at = 0, pre_step = 0, own_step = 0;
   bool direct = false;
   if (real && i < n) {
     const int row = i * p.G + g;
     if (pre > 0) {
       const int flat = b * p.TG + row, rt = flat / kRowTile, in = flat % kRowTile, seg = hk * p.pre_rt + rt;
       const int c0 = cut.cta_of(seg * p.pre_tiles);
-      pre_two = p.B * p.TG - rt * kRowTile <= kHalf;
-      pre_n = (cut.cta_of(seg * p.pre_tiles + p.pre_tiles - 1) - c0 + 1) << pre_two;
-      pre_at = ((int64_t)(seg + c0) * 2 + in / kHalf) * p.pre_slot_rows + in % kHalf;
+      const int two = p.B * p.TG - rt * kRowTile <= kHalf;
+      pre_n = (cut.cta_of(seg * p.pre_tiles + p.pre_tiles - 1) - c0 + 1) << two;
+      pre_at = ((seg + c0) * 2 + in / kHalf) * p.pre_slot_rows + in % kHalf;
+      pre_step = (2 - two) * p.pre_slot_rows;
     }
     const int rt = row / kRowTile, in = row % kRowTile;
     const int mine = own_tiles(p, kv, n, rt);
@@ -899,64 +906,64 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         t0 += hk * all + before;
       }
       const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + mine - 1);
-      own_two = n * p.G - rt * kRowTile <= kHalf;
-      direct = pre == 0 && c0 == c1 && (!own_two || mine == 1);      // written by the first kernel
-      own_n = (c1 - c0 + 1) << own_two;
-      own_at = ((int64_t)((b * p.Hkv + hk) * p.own_rt + rt + c0) * 2 + in / kHalf) * p.own_slot_rows + in % kHalf;
+      const int two = n * p.G - rt * kRowTile <= kHalf;
+      direct = pre == 0 && c0 == c1 && (!two || mine == 1);      // written by the first kernel
+      own_n = (c1 - c0 + 1) << two;
+      own_at = p.own_first + (((b * p.Hkv + hk) * p.own_rt + rt + c0) * 2 + in / kHalf) * p.own_slot_rows + in % kHalf;
+      own_step = (2 - two) * p.own_slot_rows;
     }
   }
   // Lane x holds the maximum and the sum of partial result base + x; then the
   // rows themselves are read, each warp every kWarps-th of them.
   const int parts = real && !direct ? pre_n + own_n : 0;
+  const int most = __reduce_max_sync(0xffffffffu, parts);
   float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll 1
-  for (int base = 0; base < parts; base += 32) {
+  for (int base = 0; base < most; base += kLanes) {
     const int x = base + lane;
-    const bool pre_part = x < pre_n;
-    // a segment's CTAs are a slot of two results apart, the groups' one
-    const int64_t at = pre_part ? pre_at + (int64_t)(pre_two ? x : 2 * x) * p.pre_slot_rows
-                                : own_at + (int64_t)(own_two ? x - pre_n : 2 * (x - pre_n)) * p.own_slot_rows;
+    const int at = x < pre_n ? pre_at + x * pre_step : own_at + (x - pre_n) * own_step;
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (x < parts) ml = reinterpret_cast<const float2*>(pre_part ? p.pre_ml : p.own_ml)[at];
+    if (x < parts) ml = reinterpret_cast<const float2*>(p.part_ml)[at];
     float m2 = fmaxf(m, ml.x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
     const float a = m == -INFINITY ? 0.f : ex2_approx(m - m2), w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m2);
     float sum = ml.y * w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     m = m2;
     l = l * a + sum;
-    const float* orow = (pre_part ? p.pre_o : p.own_o) + at * D;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] *= a;
-    const int n_here = min(32, parts - base);
+    const int here = min(kLanes, most - base);
 #pragma unroll 1
-    for (int y0 = part; y0 < n_here; y0 += kWarps * kLoads) {
-      float wy[kLoads];
-      float2 o[kLoads][kPer / 2];
+    for (int y0 = part; y0 < here; y0 += kWarps * kLoads) {
+      float wy[kLoads], o[kLoads][kPer];
       // all loads before the first sum; a group without a tile, or a row
       // without a key there, has left no row
 #pragma unroll
       for (int z = 0; z < kLoads; ++z) {
         const int y = y0 + z * kWarps;
-        wy[z] = __shfl_sync(0xffffffffu, w, y % 32);
-        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, (unsigned long long)orow, y % 32));
-        if (y >= n_here) wy[z] = 0.f;
+        wy[z] = __shfl_sync(0xffffffffu, w, y % kLanes, kLanes);
+        const float* src = p.part_o + (int64_t)__shfl_sync(0xffffffffu, at, y % kLanes, kLanes) * D + lane * kVec;
+        if (y >= here) wy[z] = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer / 2; ++e)
-          o[z][e] = wy[z] > 0.f ? *reinterpret_cast<const float2*>(src + lane * kPer + 2 * e) : make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int z = 0; z < kLoads; ++z) {
-#pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) {
-          acc[2 * e] = fmaf(o[z][e].x, wy[z], acc[2 * e]);
-          acc[2 * e + 1] = fmaf(o[z][e].y, wy[z], acc[2 * e + 1]);
+        for (int v = 0; v < kPer / kVec; ++v) {
+          if constexpr (kVec == 4) {
+            const float4 f = wy[z] > 0.f ? *reinterpret_cast<const float4*>(src + v * kLanes * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[z][4 * v] = f.x; o[z][4 * v + 1] = f.y; o[z][4 * v + 2] = f.z; o[z][4 * v + 3] = f.w;
+          } else {
+            const float2 f = wy[z] > 0.f ? *reinterpret_cast<const float2*>(src + v * kLanes * 2) : make_float2(0.f, 0.f);
+            o[z][2 * v] = f.x; o[z][2 * v + 1] = f.y;
+          }
         }
       }
+#pragma unroll
+      for (int z = 0; z < kLoads; ++z)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(o[z][e], wy[z], acc[e]);
     }
   }
   if constexpr (kWarps > 1) {
@@ -975,12 +982,18 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   }
   if (!real || direct) return;
   const float inv_l = l > 0.f ? 1.f / l : 0.f;
-  uint32_t pk[kPer / 2];
+  __nv_bfloat16* dst = p.out + R * D + lane * kVec;
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) pk[e] = l > 0.f ? pack_bf16x2(acc[2 * e] * inv_l, acc[2 * e + 1] * inv_l) : 0u;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + R * D + lane * kPer);
+  for (int v = 0; v < kPer / kVec; ++v) {
+    uint32_t pk[kVec / 2];
 #pragma unroll
-  for (int e = 0; e < kPer / 2; ++e) dst[e] = pk[e];
+    for (int e = 0; e < kVec / 2; ++e)
+      pk[e] = l > 0.f ? pack_bf16x2(acc[v * kVec + 2 * e] * inv_l, acc[v * kVec + 2 * e + 1] * inv_l) : 0u;
+    if constexpr (kVec == 4)
+      *reinterpret_cast<uint2*>(dst + v * kLanes * 4) = make_uint2(pk[0], pk[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst + v * kLanes * 2) = pk[0];
+  }
   if (lane == 0 && p.lse)
     p.lse[((int64_t)b * p.Hq + h) * p.T + i] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -990,7 +1003,7 @@ std::string s(int64_t v) { return std::to_string(v); }
 // Where the partial results lie in the workspace.
 struct PagedPlan {
   int TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
-  size_t cum, pre_ml, pre_o, own_ml, own_o, bytes;
+  size_t own_first, cum, part_ml, part_o, bytes;
 };
 
 PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
@@ -1005,12 +1018,11 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   // a slot of two partial results for every number segment + CTA
   const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * 2 * w.own_slot_rows;
   const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
+  w.own_first = pre;
   w.cum = 0;
-  w.pre_ml = al((size_t)(B + 1) * 4);
-  w.pre_o = w.pre_ml + al(pre * 8);
-  w.own_ml = w.pre_o + al(pre * d * 4);
-  w.own_o = w.own_ml + al(own * 8);
-  w.bytes = w.own_o + al(own * d * 4);
+  w.part_ml = al((size_t)(B + 1) * 4);
+  w.part_o = w.part_ml + al((pre + own) * 8);
+  w.bytes = w.part_o + al((pre + own) * d * 4);
   return w;
 }
 
@@ -1076,9 +1088,9 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   paged_attention_kernel<D><<<p.ctas, kPagedThreads, PagedCfg<D>::kSmemBytes, stream>>>(p);
   if ((st = cuda_check(cudaGetLastError(), "paged_attention_kernel launch")) != BSA_OK) return st;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  const bool wide = rows < (int64_t)num_sms() * 16;    // few rows: their partial results are shared out to four warps
+  const bool wide = rows < (int64_t)num_sms() * 16;    // few rows: four warps each
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(wide ? rows : cdiv64(rows, 4)));
+  cfg.gridDim = dim3((unsigned)(wide ? rows : cdiv64(rows, 16)));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -1086,8 +1098,8 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cuda_check(wide ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 4>, p)
-                         : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 1>, p),
+  return cuda_check(wide ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 4>, p)
+                         : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),
                     "paged_join_kernel launch");
 }
 
@@ -1103,7 +1115,7 @@ extern "C" {
 
 size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has_prefix, int sms) {
   if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq > kMaxHeads || Hq % Hkv ||
-      (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 4)
+      (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 16)
     return 0;
   return plan_paged(B, T, Hq, Hkv, d, has_prefix != 0, sms > 0 ? sms : num_sms()).bytes;
 }
@@ -1146,11 +1158,13 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": q reaches over " + s(q_extent) + " elements (2^35 at most)");
   const int64_t most_tiles = qv.B * a.k.H * row_tiles * cdiv64(max_pages * a.k.S, kTileKeys) +
                              a.k.H * cdiv64(flat_rows, kRowTile) * cdiv64(prefix_len, kTileKeys);
-  if (flat_rows > INT32_MAX / 4 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.H > INT32_MAX)
+  if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.H > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
                                               s(max_pages * a.k.S + prefix_len) + " keys are too many for one call");
   const PagedPlan plan = plan_paged(qv.B, qv.S, qv.H, a.k.H, qv.D, prefix_len > 0, sms);
   const size_t need = plan.bytes;
+  if (need / (4 * (size_t)qv.D) > INT32_MAX)
+    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": too many rows for one call");
   if (!workspace) return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is NULL (needs " + s(need) + " bytes)");
   if (ws_bytes < need)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace of " + s(ws_bytes) +
@@ -1181,8 +1195,9 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.cum = reinterpret_cast<int32_t*>(ws + plan.cum);
-  p.pre_ml = reinterpret_cast<float*>(ws + plan.pre_ml); p.pre_o = reinterpret_cast<float*>(ws + plan.pre_o);
-  p.own_ml = reinterpret_cast<float*>(ws + plan.own_ml); p.own_o = reinterpret_cast<float*>(ws + plan.own_o);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+  p.own_first = (int)plan.own_first;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   return qv.D == 128 ? launch_paged<128>(p, cs) : launch_paged<64>(p, cs);
 }
