@@ -25,6 +25,7 @@ class BsaTensor(ctypes.Structure):
     ]
 
 
+# The structs of include/bsa_paged.h (the binding passes packed bytes).
 class BsapRope(ctypes.Structure):
     _fields_ = [
         ("inv_freq", ctypes.c_void_p),
@@ -82,14 +83,11 @@ SIGNATURES = {
 
 # the calls of include/bsa_paged.h
 _I64 = ctypes.c_int64
-_RP = ctypes.POINTER(BsapRope)
-_PP = ctypes.POINTER(BsapPositions)
 PAGED_SIGNATURES = {
-    "bsap_rope_axes": (_I, [_TP, _TP, _PP, _PP, _RP, _I32, _P, _P, _P]),
-    "bsap_cache_append": (_I, [_TP, _TP, _TP, _TP, _P, _I64, _I32, _P, _P, _RP, _PP, _TP, _P, _P]),
+    "bsap_rope_axes": (_I, [_P, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "bsap_cache_append": (_I, [_P, _P, _P, _P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "bsap_forward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
-    "bsap_forward": (_I, [_TP, _TP, _TP, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ,
-                          _P]),
+    "bsap_forward": (_I, [_P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -100,6 +98,8 @@ def lib_path() -> str:
 def load(path: str | None = None):
     """Loads libbsa.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

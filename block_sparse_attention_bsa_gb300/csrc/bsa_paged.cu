@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   constexpr int kPer = D / kLanes;                 // values per lane, kVec at a time
   constexpr int kVec = kPer < 4 ? kPer : 4;
   constexpr int kRows = 128 / (kLanes * kWarps);   // rows per block
-  constexpr int kLoads = kWarps > 1 ? 8 : 2;       // partial rows in flight per lane
+  constexpr int kLoads = kWarps > 1 ? 4 : 2;       // partial rows in flight per lane
   static_assert(kWarps == 1 || kLanes == 32, "several warps take whole rows");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
   const int part = warp % kWarps;

@@ -11,33 +11,51 @@ outputs and workspaces that a call makes itself are allocated on that stream.
 from __future__ import annotations
 
 import contextlib
-import ctypes
+from struct import Struct
 from typing import Optional, Sequence
 
 import torch
 
-from . import _lib
+from ._lib import load as _load
 from .api import _check, _check_buffer
 
 PAGE_SIZES_SUPPORTED = (16, 32, 64, 128, 256)
 
 
-def _tensor(t, name: str, device=None) -> _lib.BsaTensor:
+# A single-token step is a few microseconds of GPU work, so the way into the
+# library is kept short: descriptors are packed bytes (laid out as the structs of
+# bsa.h and bsa_paged.h; ctypes passes their address), the stream handle is read
+# without building a torch.cuda.Stream, and no context manager is entered unless
+# another device or stream is asked for.
+_pack_tensor = Struct("8q").pack            # bsa_tensor
+_pack_positions = Struct("4q").pack         # bsap_positions
+_pack_rope = Struct("2q3i4x").pack          # bsap_rope
+_BF, _I32, _F64, _F32, _U8 = torch.bfloat16, torch.int32, torch.float64, torch.float32, torch.uint8
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _tensor(t, name: str, device=None) -> bytes:
+    """Packed bsa_tensor of a 4-D bf16 tensor on the GPU (on ``device``)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF:
         raise ValueError(f"{name} must be bfloat16 (got {t.dtype})")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be 4-D [B, S, H, d] (got {tuple(t.shape)})")
-    sb, ss, sh, sd = t.stride()
-    B, S, H, D = t.shape
-    if sd != 1 and D != 1:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 4:
+        raise ValueError(f"{name} must be 4-D [B, S, H, d] (got {tuple(shape)})")
+    if stride[3] != 1 and shape[3] != 1:
         raise ValueError(f"{name} must have a contiguous last dim")
-    return _lib.BsaTensor(t.data_ptr(), B, S, H, D, sb, ss, sh)
+    return _pack_tensor(t.data_ptr(), *shape, *stride[:3])
 
 
 def _ints(t, name: str, device, shape) -> Optional[int]:
@@ -46,7 +64,7 @@ def _ints(t, name: str, device, shape) -> Optional[int]:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous torch.int32 tensor of shape {shape} on {device} "
                          f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
     return t.data_ptr()
@@ -56,26 +74,28 @@ def _positions(t, name: str, device, B: int, S: int):
     """Descriptor of int32 positions [B, S, A] or [S, A] (shared by the batch)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32 or t.device != device:
+    if t.dtype is not _I32 or t.device != device:
         raise ValueError(f"{name} must be a torch.int32 tensor on {device} (got {t.dtype}, {t.device})")
-    if t.dim() == 2:
-        t = t.unsqueeze(0)
-    if t.dim() != 3 or t.shape[0] not in (1, B) or t.shape[1] != S:
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        shape, stride = (1, *shape), (0, *stride)
+    if len(shape) != 3 or shape[0] not in (1, B) or shape[1] != S:
         raise ValueError(f"{name} must be [B, S, axes] or [S, axes] with B = {B}, S = {S} (got {tuple(t.shape)})")
-    sb, ss, sa = t.stride()
-    return _lib.BsapPositions(t.data_ptr(), sb if t.shape[0] > 1 else 0, ss if S > 1 else 0, sa), t.shape[2]
+    return _pack_positions(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if S > 1 else 0,
+                           stride[2]), shape[2]
 
 
-def _rope(inv_freq, axes, n_axes: int, interleaved: bool, device) -> _lib.BsapRope:
-    for name, t, dtype in (("inv_freq", inv_freq, torch.float64), ("axes", axes, torch.int32)):
+def _rope(inv_freq, axes, n_axes: int, interleaved: bool, device) -> bytes:
+    for name, t, dtype in (("inv_freq", inv_freq, _F64), ("axes", axes, _I32)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
+        if t.dtype is not dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on {device} "
                              f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
-    if inv_freq.numel() != axes.numel():
-        raise ValueError(f"inv_freq has {inv_freq.numel()} pairs, axes {axes.numel()}")
-    return _lib.BsapRope(inv_freq.data_ptr(), axes.data_ptr(), axes.numel(), n_axes, 1 if interleaved else 0)
+    pairs = axes.shape[0]
+    if inv_freq.shape[0] != pairs:
+        raise ValueError(f"inv_freq has {inv_freq.shape[0]} pairs, axes {pairs}")
+    return _pack_rope(inv_freq.data_ptr(), axes.data_ptr(), pairs, n_axes, 1 if interleaved else 0)
 
 
 def _extent(t: torch.Tensor):
@@ -107,15 +127,14 @@ def _elsewhere(device, stream):
                 yield
 
 
-def _on(device, stream):
-    """Makes the tensors' device and the call's stream current."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _elsewhere(device, stream)
-
-
-def _current():
-    return torch.cuda.current_stream().cuda_stream
+def _on(device, stream, call, *args):
+    """``call(*args, stream handle)`` with the tensors' device and the call's
+    stream current."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return call(*args, _raw_stream(index))
+    with _elsewhere(device, stream):
+        return call(*args, _raw_stream(index))
 
 
 def bsa_axis_frequencies(sections: Sequence[int], theta: float = 10000.0, layout: str = "sections", device="cuda"):
@@ -164,23 +183,27 @@ def _rope_call(q, k, pos_q, pos_k, inv_freq, axes, interleaved, backward, q_out,
             raise ValueError(f"pos_q has {n_axes} axes, pos_k {nk}")
     elif k_out is not None:
         raise ValueError(f"{names[3]} is given without {names[1]}")
-    inputs = [t for t in (q, k) if t is not None]
-    with _on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    return _on(dev, stream, _rope_launch, q, k, qd, kd, pq, pk, rope, backward, q_out, k_out, names)
+
+
+def _rope_launch(q, k, qd, kd, pq, pk, rope, backward, q_out, k_out, names, handle):
+    dev = q.device
+    inputs = (q,) if k is None else (q, k)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=_BF, device=dev)
+    else:
+        _check_buffer(names[2], q_out, q.shape, _BF, dev)
+        _check_overlap(names[2], q_out, inputs, q)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=_BF, device=dev)
         else:
-            _check_buffer(names[2], q_out, q.shape, torch.bfloat16, dev)
-            _check_overlap(names[2], q_out, inputs, q)
-        if k is not None:
-            if k_out is None:
-                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-            else:
-                _check_buffer(names[3], k_out, k.shape, torch.bfloat16, dev)
-                _check_overlap(names[3], k_out, [*inputs, q_out], k)
-        _check(_lib.load().bsap_rope_axes(ctypes.byref(qd), ctypes.byref(kd) if kd is not None else None,
-                                          ctypes.byref(pq), ctypes.byref(pk) if pk is not None else None,
-                                          ctypes.byref(rope), 1 if backward else 0, q_out.data_ptr(),
-                                          k_out.data_ptr() if k is not None else None, _current()))
+            _check_buffer(names[3], k_out, k.shape, _BF, dev)
+            _check_overlap(names[3], k_out, (q, k, q_out), k)
+    st = _load().bsap_rope_axes(qd, kd, pq, pk, rope, 1 if backward else 0, q_out.data_ptr(),
+                                None if k is None else k_out.data_ptr(), handle)
+    if st:
+        _check(st)
     return q_out, k_out
 
 
@@ -216,7 +239,7 @@ def bsa_rope_axes_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], pos_q: 
 def _table(page_table, B: int, device):
     if not isinstance(page_table, torch.Tensor):
         raise TypeError("page_table must be a torch.Tensor")
-    if page_table.dtype != torch.int32 or page_table.device != device:
+    if page_table.dtype is not _I32 or page_table.device != device:
         raise ValueError(f"page_table must be a torch.int32 tensor on {device} (got {page_table.dtype}, "
                          f"{page_table.device})")
     if page_table.dim() != 2 or page_table.shape[0] != B:
@@ -261,22 +284,27 @@ def bsa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
         qd = _tensor(q, "q", dev)
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    with _on(dev, stream):
-        if q is not None:
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-            else:
-                _check_buffer("q_out", q_out, q.shape, torch.bfloat16, dev)
-                _check_overlap("q_out", q_out, (q, k, v, k_cache, v_cache), q)
-        _check(_lib.load().bsap_cache_append(
-            ctypes.byref(kd), ctypes.byref(vd), ctypes.byref(kc), ctypes.byref(vc), table, stride, n, lens, new,
-            ctypes.byref(rope) if rope is not None else None, ctypes.byref(pos) if pos is not None else None,
-            ctypes.byref(qd) if qd is not None else None, q_out.data_ptr() if q is not None else None, _current()))
+    return _on(dev, stream, _append_launch, (kd, vd, kc, vc, table, stride, n, lens, new, rope, pos, qd), q, q_out,
+               (q, k, v, k_cache, v_cache))
+
+
+def _append_launch(args, q, q_out, inputs, handle):
+    ptr = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=_BF, device=q.device)
+        else:
+            _check_buffer("q_out", q_out, q.shape, _BF, q.device)
+            _check_overlap("q_out", q_out, inputs, q)
+        ptr = q_out.data_ptr()
+    st = _load().bsap_cache_append(*args, ptr, handle)
+    if st:
+        _check(st)
     return q_out
 
 
 def bsa_forward_paged_workspace_size(B, T, Hq, Hkv, d, has_prefix, num_sms=0) -> int:
-    return int(_lib.load().bsap_forward_workspace_size(B, T, Hq, Hkv, d, 1 if has_prefix else 0, num_sms))
+    return int(_load().bsap_forward_workspace_size(B, T, Hq, Hkv, d, 1 if has_prefix else 0, num_sms))
 
 
 def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
@@ -314,24 +342,31 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         if prefix_table.numel() * k_cache.shape[1] < prefix_len:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages of {k_cache.shape[1]}, prefix_len is "
                              f"{prefix_len}")
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_buffer("out", out, (B, T, Hq, d), torch.bfloat16, dev)
-            _check_overlap("out", out, (q, k_cache, v_cache), None)
-        if lse is not None:
-            _check_buffer("lse", lse, (B, Hq, T), torch.float32, dev)
-        elif return_lse:
-            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        lib = _lib.load()
-        if workspace is None:
-            need = lib.bsap_forward_workspace_size(B, T, Hq, k_cache.shape[2], d, 1 if prefix_len > 0 else 0, 0)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        else:
-            _check_buffer("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
-        _check(lib.bsap_forward(ctypes.byref(qd), ctypes.byref(kc), ctypes.byref(vc), table, stride, n, lens, new,
-                                shared, prefix_len, 1 if causal else 0, float(softmax_scale), out.data_ptr(),
-                                lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-                                workspace.numel(), _current()))
+    return _on(dev, stream, _forward_launch, q, k_cache, v_cache,
+               (qd, kc, vc, table, stride, n, lens, new, shared, prefix_len, 1 if causal else 0, float(softmax_scale)),
+               out, lse, return_lse, workspace)
+
+
+def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, handle):
+    dev = q.device
+    B, T, Hq, d = q.shape
+    lib = _load()
+    if out is None:
+        out = torch.empty((B, T, Hq, d), dtype=_BF, device=dev)
+    else:
+        _check_buffer("out", out, (B, T, Hq, d), _BF, dev)
+        _check_overlap("out", out, (q, k_cache, v_cache), None)
+    if lse is not None:
+        _check_buffer("lse", lse, (B, Hq, T), _F32, dev)
+    elif return_lse:
+        lse = torch.empty((B, Hq, T), dtype=_F32, device=dev)
+    if workspace is None:
+        need = lib.bsap_forward_workspace_size(B, T, Hq, k_cache.shape[2], d, 1 if args[9] > 0 else 0, 0)
+        workspace = torch.empty(max(need, 256), dtype=_U8, device=dev)
+    else:
+        _check_buffer("workspace", workspace, (workspace.numel(),), _U8, dev)
+    st = lib.bsap_forward(*args, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                          workspace.numel(), handle)
+    if st:
+        _check(st)
     return out, lse
