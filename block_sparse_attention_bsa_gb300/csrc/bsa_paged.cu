@@ -529,26 +529,93 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   } else if (warp == 2 || warp == 3) {
     // Q rows of a segment into the next one or two Q buffers: each lane works
     // out the address of one of 32 rows, then 32 / kVec rows are copied at a
-    // time; the two warps take every other 32 rows, from r_first on.
+    // time; the two warps take every other 32 rows.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
     const int c = lane % kVec;
     uint32_t qi = 0;
-    auto load_q = [&](const Segment& s, int r_first) -> bool {
+    // Warp 2 is the scheduler, too: it finds the segments of tiles [begin, end)
+    // in their order.  Its lane l holds request 32 blk + l: its lengths, tiles,
+    // and the tiles up to its end.
+    const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+    int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
+    uint32_t slot = 0, phase = 0;
+    SegmentReader reader;
+    for (int t = begin; t < end && ok;) {
+      Segment s;
+      if (warp == 3) {
+        if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
+      } else {
+        int t0, t1;
+        if (t < pre) {
+          const int seg = t / p.pre_tiles;
+          t0 = seg * p.pre_tiles;
+          t1 = t0 + p.pre_tiles;
+          s.b = -1;
+          s.hk = seg / p.pre_rt;
+          s.row0 = (seg - s.hk * p.pre_rt) * kRowTile;
+          s.rows = min(kRowTile, p.B * p.TG - s.row0);
+          s.slot = seg + cta;
+          s.keys = p.prefix_len;
+          s.kv = s.n = 0;
+        } else {
+          const int u = t - pre;
+          if (u >= blk_end) {                          // the last block that begins at or before u
+            ++blk;
+            while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
+            const int b = blk * 32 + lane;
+            kv = b < p.B ? own_keys(p, b) : 0;
+            n = b < p.B ? new_tokens(p, b) : 0;
+            mine = b < p.B ? request_tiles(p, kv, n) : 0;
+            upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
+            blk_end = __shfl_sync(0xffffffffu, upto, 31);
+          }
+          const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
+          const int per_head = __shfl_sync(0xffffffffu, mine, src);
+          const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
+          s.b = blk * 32 + src;
+          s.kv = __shfl_sync(0xffffffffu, kv, src);
+          s.n = __shfl_sync(0xffffffffu, n, src);
+          s.hk = (u - first) / per_head;
+          t0 = pre + first + s.hk * per_head;
+          int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles(p, s.kv, s.n, 0);
+#pragma unroll 1
+          while (t >= t0 + m) {
+            t0 += m;
+            m = own_tiles(p, s.kv, s.n, ++rt);
+          }
+          t1 = t0 + m;
+          s.row0 = s.b * p.TG + rt * kRowTile;
+          s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
+          s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
+          s.keys = s.kv;
+        }
+        s.tile0 = t - t0;
+        s.tiles = min(t1, end) - t;
+        s.whole = begin <= t0 && t1 <= end;
+        s.pad = 0;
+        if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
+        if (lane == 0) {
+          segs[slot] = s;
+          mbar_arrive(seg_full + 8 * slot);
+        }
+        __syncwarp();
+        if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+      }
       const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
 #pragma unroll 1
       for (int r0 = 0; r0 < s.rows; r0 += kHalf, ++qi) {
         const uint32_t qb = qi & 1u;
-        if (!warp_wait(q_empty + 8 * qb, ((qi >> 1) & 1u) ^ 1u, abort_flag)) return false;
+        if (!warp_wait(q_empty + 8 * qb, ((qi >> 1) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
         const uint32_t base = smem_u32(q_smem) + qb * C::kQBytes + (c / 8) * (kHalf * 128) + (lane / kVec) * 128;
         const int rows = min(kHalf, s.rows - r0);
 #pragma unroll 1
-        for (int r32 = r_first; r32 < rows; r32 += 64) {
+        for (int r32 = (warp - 2) * 32; r32 < rows; r32 += 64) {
           const int row = s.row0 + r0 + min(r32 + lane, rows - 1);
           const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
           const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
-#pragma unroll 4
-          for (int x = 0; x < kVec; ++x) {
+#pragma unroll 2
+          for (int x = 0; x < kVec && r32 + x * kRowsPer < rows; ++x) {
             const int in = x * kRowsPer + lane / kVec, r = r32 + in;
             const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, in) * 8;
             if (r < rows)
@@ -562,84 +629,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         fence_async_shared();
         mbar_arrive(q_full + 8 * qb);
       }
-      return true;
-    };
-    if (warp == 2) {
-    // ------------------------------------------------------- scheduler ---
-    // The segments of tiles [begin, end) in their order.  Lane l holds request
-    // 32 blk + l: its lengths, tiles, and the tiles up to its end.
-    const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
-    int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
-    uint32_t slot = 0, phase = 0;
-    for (int t = begin; t < end && ok;) {
-      Segment s;
-      int t0, t1;
-      if (t < pre) {
-        const int seg = t / p.pre_tiles;
-        t0 = seg * p.pre_tiles;
-        t1 = t0 + p.pre_tiles;
-        s.b = -1;
-        s.hk = seg / p.pre_rt;
-        s.row0 = (seg - s.hk * p.pre_rt) * kRowTile;
-        s.rows = min(kRowTile, p.B * p.TG - s.row0);
-        s.slot = seg + cta;
-        s.keys = p.prefix_len;
-        s.kv = s.n = 0;
-      } else {
-        const int u = t - pre;
-        if (u >= blk_end) {                          // the last block that begins at or before u
-          ++blk;
-          while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
-          const int b = blk * 32 + lane;
-          kv = b < p.B ? own_keys(p, b) : 0;
-          n = b < p.B ? new_tokens(p, b) : 0;
-          mine = b < p.B ? request_tiles(p, kv, n) : 0;
-          upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
-          blk_end = __shfl_sync(0xffffffffu, upto, 31);
-        }
-        const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
-        const int per_head = __shfl_sync(0xffffffffu, mine, src);
-        const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
-        s.b = blk * 32 + src;
-        s.kv = __shfl_sync(0xffffffffu, kv, src);
-        s.n = __shfl_sync(0xffffffffu, n, src);
-        s.hk = (u - first) / per_head;
-        t0 = pre + first + s.hk * per_head;
-        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles(p, s.kv, s.n, 0);
-#pragma unroll 1
-        while (t >= t0 + m) {
-          t0 += m;
-          m = own_tiles(p, s.kv, s.n, ++rt);
-        }
-        t1 = t0 + m;
-        s.row0 = s.b * p.TG + rt * kRowTile;
-        s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
-        s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
-        s.keys = s.kv;
-      }
-      s.tile0 = t - t0;
-      s.tiles = min(t1, end) - t;
-      s.whole = begin <= t0 && t1 <= end;
-      s.pad = 0;
-      if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
-      if (lane == 0) {
-        segs[slot] = s;
-        mbar_arrive(seg_full + 8 * slot);
-      }
-      __syncwarp();
-      if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
-      ok = load_q(s, 0);
       t += s.tiles;
-    }
-    } else {
-    // the second loader
-    SegmentReader reader;
-    for (int t = begin; t < end && ok;) {
-      Segment s;
-      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      ok = load_q(s, 32);
-      t += s.tiles;
-    }
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -679,8 +669,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          // S is read twice, 64 columns at a time: held whole in registers the
-          // code is three times as long, and no longer fits the instruction cache.
+          // S is read twice, 32 columns at a time: held whole in registers the
+          // code is four times as long, and the roles' loops no longer fit the
+          // instruction cache together.
           const int valid = limit - key0;
           if (__any_sync(0xffffffffu, valid < kTileKeys)) {      // keys that some row of the warp does not see
 #pragma unroll 1
@@ -697,20 +688,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           }
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kTileKeys; c += 64) {
-            float v[64];
+          for (int c = 0; c < kTileKeys; c += 32) {
+            float v[32];
             tmem_ld32f(s_t + c, v);
-            tmem_ld32f(s_t + c + 32, v + 32);
             tmem_wait_ld();
-            float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+            float m0 = mx, m1 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 64; e += 8) {
+            for (int e = 0; e < 32; e += 4) {
               m0 = max3f(m0, v[e], v[e + 1]);
               m1 = max3f(m1, v[e + 2], v[e + 3]);
-              m2 = max3f(m2, v[e + 4], v[e + 5]);
-              m3 = max3f(m3, v[e + 6], v[e + 7]);
             }
-            mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            mx = fmaxf(m0, m1);
           }
           const float m_new = fmaxf(m_ref, mx * p.scale_log2);
           const bool grow = m_new > m_ref + 8.0f;
@@ -721,14 +709,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_use, -m_use);
           float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-          for (int c = 0; c < kTileKeys; c += 64) {
-            float v[64];
-            uint32_t pk[32];
+          for (int c = 0; c < kTileKeys; c += 32) {
+            float v[32];
+            uint32_t pk[16];
             tmem_ld32f(s_t + c, v);
-            tmem_ld32f(s_t + c + 32, v + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
               const float2 a = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, nm2);
               const float2 b = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), sc2, nm2);
               const float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
@@ -738,7 +725,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
               pk[e / 2] = pack_bf16x2(e0.x, e0.y);
               pk[e / 2 + 1] = pack_bf16x2(e1.x, e1.y);
             }
-            tmem_st32(s_t + c / 2, pk);            // P of these 64 keys over S of keys read already
+            tmem_st16(s_t + c / 2, pk);            // P of these 32 keys over S of keys read already
           }
           l = l * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
           // O is rescaled only when the maximum grew by more than 2^8 (P V of the
