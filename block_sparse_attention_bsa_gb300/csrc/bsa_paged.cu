@@ -209,6 +209,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
 // proxy (the MMAs read Q and V through it).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 // mbar_wait with one copy of its loop in the code; `bar` and `abort` are
 // shared-memory addresses.
 __device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, uint32_t abort) {
@@ -247,13 +254,6 @@ struct SegmentReader {
 template <int N>
 __device__ __forceinline__ void advance(uint32_t& stage, uint32_t& phase) {
   if (++stage == N) { stage = 0; phase ^= 1u; }
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
-  return e != 0;
 }
 
 template <int D>
@@ -374,29 +374,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     uint32_t stage = 0, phase = 0;
     int v_page = 0, v_slot = 0, v_hk = 0;          // the tile whose V is still to come,
     bool v_left = false;                           // if there is one
-    auto load = [&](const CUtensorMap* map, int page, int slot, int hk) -> bool {
-      bool go = true;
-      if (lane == 0) {
-        go = wait_for(empty + 8 * stage, phase ^ 1u, abort_flag);
-        if (go) mbar_arrive_expect_tx(full + 8 * stage, C::kTileBytes);
-      }
-      go = __shfl_sync(0xffffffffu, go, 0);
-      if (go && lane < per_tile) {
-        const uint32_t dst = ring_base + stage * C::kTileBytes + lane * box_rows * 128;
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_load_4d(dst + c * (kTileKeys * 128), map, full + 8 * stage, c * 64, slot, hk, page);
-      }
-      __syncwarp();
-      if (go) advance<kStages>(stage, phase);
-      return go;
-    };
     SegmentReader reader;
-    for (int t = begin; t < end && ok;) {
+#pragma unroll 1
+    for (int t = begin; begin < end;) {
+      const bool more = t < end;        // after the last segment there is one V left, or none
       Segment s;
-      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
+      s.rows = s.tiles = 1;
+      s.tile0 = s.hk = s.keys = 0;
+      s.b = -1;
+      if (more && !(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
       const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
-      auto page_of = [&](int j) {                  // lane's page of key tile j (a page past the end reads zeros)
+      // lane's page of key tile j (a page past the end reads zeros)
+      auto page_of = [&](int j) {
         const int key = j * kTileKeys + lane * box_rows;
         int page = p.num_pages;
         if (lane < per_tile && key < s.keys) {
@@ -410,24 +399,40 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       };
       // K of a job's tile, then V of the job before it, each at its first use
       const bool wide = s.rows > kHalf;
-      int page = page_of(s.tile0);
+      int page = p.num_pages;
 #pragma unroll 1
-      for (int j = s.tile0; j < s.tile0 + s.tiles && ok; ++j) {
-        const int next = j + 1 < s.tile0 + s.tiles ? page_of(j + 1) : 0;
-        const int slot = (j * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
+      for (int j = -1; j < s.tiles && ok; ++j) {
+        const int next = j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
+        const int slot = ((s.tile0 + j) * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
 #pragma unroll 1
-        for (int which = 0; which < 3 && ok; ++which) {
-          if (which == 1 ? !v_left : which == 2 && !wide) continue;
+        for (int which = j < 0 ? 3 : 0; which < 3; ++which) {
+          if (which == 0 ? !more : which == 1 ? !v_left : !more || !wide) continue;
+          if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
           const bool old = which == 1;
-          ok = load(which == 0 ? &p.tk : &p.tv, old ? v_page : page, old ? v_slot : slot, old ? v_hk : s.hk);
+          const int from = old ? v_page : page, at = old ? v_slot : slot, head = old ? v_hk : s.hk;
+          if (elect_one()) mbar_arrive_expect_tx(full + 8 * stage, C::kTileBytes);
+          uint32_t dst = ring_base + stage * C::kTileBytes;
+#pragma unroll 1
+          for (int x = 0; x < per_tile; ++x, dst += box_rows * 128) {
+            const int pg = __shfl_sync(0xffffffffu, from, x);
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_4d(dst + c * (kTileKeys * 128), which == 0 ? &p.tk : &p.tv, full + 8 * stage, c * 64, at, head, pg);
+            }
+            __syncwarp();
+          }
+          advance<kStages>(stage, phase);
         }
-        v_left = !wide;
-        if (v_left) { v_page = page; v_slot = slot; v_hk = s.hk; }
+        if (j >= 0) {
+          v_left = !wide;
+          v_page = page; v_slot = slot; v_hk = s.hk;
+        }
         page = next;
       }
+      if (!more || !ok) break;
       t += s.tiles;
     }
-    if (ok && v_left) load(&p.tv, v_page, v_slot, v_hk);
     // the copies in flight land before the CTA may leave
     if (lane == 0) {
 #pragma unroll 1
@@ -669,9 +674,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         if (!ok) break;
         tc_fence_after();
         if (active) {
-          // S is read twice, 32 columns at a time: held whole in registers the
-          // code is four times as long, and the roles' loops no longer fit the
-          // instruction cache together.
+          // S is read twice, 64 columns at a time: held whole in registers the
+          // code is three times as long, and the roles' loops no longer fit the
+          // instruction cache together (32 at a time measured 3 % slower).
           const int valid = limit - key0;
           if (__any_sync(0xffffffffu, valid < kTileKeys)) {      // keys that some row of the warp does not see
 #pragma unroll 1
@@ -688,17 +693,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           }
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kTileKeys; c += 32) {
-            float v[32];
+          for (int c = 0; c < kTileKeys; c += 64) {
+            float v[64];
             tmem_ld32f(s_t + c, v);
+            tmem_ld32f(s_t + c + 32, v + 32);
             tmem_wait_ld();
-            float m0 = mx, m1 = -INFINITY;
+            float m0 = mx, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 64; e += 8) {
               m0 = max3f(m0, v[e], v[e + 1]);
               m1 = max3f(m1, v[e + 2], v[e + 3]);
+              m2 = max3f(m2, v[e + 4], v[e + 5]);
+              m3 = max3f(m3, v[e + 6], v[e + 7]);
             }
-            mx = fmaxf(m0, m1);
+            mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
           }
           const float m_new = fmaxf(m_ref, mx * p.scale_log2);
           const bool grow = m_new > m_ref + 8.0f;
@@ -709,13 +717,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m_use, -m_use);
           float2 ls0 = make_float2(0.f, 0.f), ls1 = make_float2(0.f, 0.f);
 #pragma unroll 1
-          for (int c = 0; c < kTileKeys; c += 32) {
-            float v[32];
-            uint32_t pk[16];
+          for (int c = 0; c < kTileKeys; c += 64) {
+            float v[64];
+            uint32_t pk[32];
             tmem_ld32f(s_t + c, v);
+            tmem_ld32f(s_t + c + 32, v + 32);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 0; e < 64; e += 4) {
               const float2 a = __ffma2_rn(make_float2(v[e], v[e + 1]), sc2, nm2);
               const float2 b = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), sc2, nm2);
               const float2 e0 = make_float2(ex2_approx(a.x), ex2_approx(a.y));
@@ -725,7 +734,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
               pk[e / 2] = pack_bf16x2(e0.x, e0.y);
               pk[e / 2 + 1] = pack_bf16x2(e1.x, e1.y);
             }
-            tmem_st16(s_t + c / 2, pk);            // P of these 32 keys over S of keys read already
+            tmem_st32(s_t + c / 2, pk);            // P of these 64 keys over S of keys read already
           }
           l = l * alpha + ((ls0.x + ls0.y) + (ls1.x + ls1.y));
           // O is rescaled only when the maximum grew by more than 2^8 (P V of the
@@ -842,18 +851,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
 // Output row (b, i, h): joins the partial results of its prefix segment and of
 // its own segment.  kLanes lanes of kWarps warps share a row: eight lanes where
 // there are many rows (a warp's way through its dependent loads takes 4 us, so
-// four rows go it together), four warps where there are few rows of many
-// partial results.
+// four rows go it together), four or eight warps where there are few rows of
+// many partial results.
 template <int D, int kLanes, int kWarps>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / kLanes;                 // values per lane, kVec at a time
   constexpr int kVec = kPer < 4 ? kPer : 4;
-  constexpr int kRows = 128 / (kLanes * kWarps);   // rows per block
-  constexpr int kLoads = kWarps > 1 ? 4 : 2;       // partial rows in flight per lane
+  constexpr int kRows = kWarps > 1 ? 1 : 128 / kLanes;   // rows per block
+  constexpr int kLoads = kWarps == 8 ? 4 : kWarps == 4 ? 8 : 2;      // partial rows in flight per lane
   static_assert(kWarps == 1 || kLanes == 32, "several warps take whole rows");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
   const int part = warp % kWarps;
-  const int64_t R = (int64_t)blockIdx.x * kRows + threadIdx.x / (kLanes * kWarps);
+  const int64_t R = (int64_t)blockIdx.x * kRows + (kWarps > 1 ? 0 : threadIdx.x / kLanes);
   const bool real = R < (int64_t)p.B * p.T * p.Hq;
   const int r0 = real ? (int)R : 0;
   const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
@@ -1075,18 +1084,22 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   paged_attention_kernel<D><<<p.ctas, kPagedThreads, PagedCfg<D>::kSmemBytes, stream>>>(p);
   if ((st = cuda_check(cudaGetLastError(), "paged_attention_kernel launch")) != BSA_OK) return st;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  const bool wide = rows < (int64_t)num_sms() * 16;    // few rows: four warps each
+  // Warps per row by the number of rows (us of the join, 1 / 4 / 8 warps a row:
+  // 32 rows of 40 partial results - / 7.4 / 6.5; 2,048 rows of 20 partial
+  // results 20 / 8 / 11, of 2 to 6 13 / 10 / 15; 16,384 finished rows 4 / 10 / -).
+  const int warps = rows < (int64_t)num_sms() * 4 ? 8 : rows < (int64_t)num_sms() * 16 ? 4 : 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(wide ? rows : cdiv64(rows, 16)));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)(warps > 1 ? rows : cdiv64(rows, 16)));
+  cfg.blockDim = dim3(warps > 1 ? 32 * warps : 128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cuda_check(wide ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 4>, p)
-                         : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),
+  return cuda_check(warps == 8   ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 8>, p)
+                    : warps == 4 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 4>, p)
+                                 : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),
                     "paged_join_kernel launch");
 }
 
