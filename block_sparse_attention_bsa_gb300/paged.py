@@ -38,60 +38,69 @@ def _raw_stream(index: int) -> int:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _tensor(t, name: str, device=None) -> bytes:
-    """Packed bsa_tensor of a 4-D bf16 tensor on the GPU (on ``device``)."""
+def _wrong(t, name: str, index: int, what: str, dtype) -> Exception:
+    """What to raise for a tensor that is not one of ``dtype`` on GPU ``index``
+    (any GPU if that is None)."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {device}")
-    if t.dtype is not _BF:
-        raise ValueError(f"{name} must be bfloat16 (got {t.dtype})")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 4:
-        raise ValueError(f"{name} must be 4-D [B, S, H, d] (got {tuple(shape)})")
-    if stride[3] != 1 and shape[3] != 1:
-        raise ValueError(f"{name} must have a contiguous last dim")
-    return _pack_tensor(t.data_ptr(), *shape, *stride[:3])
+        return TypeError(f"{name} must be a torch.Tensor")
+    if index is None and t.get_device() < 0:
+        return ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if index is not None and t.get_device() != index:
+        return ValueError(f"{name} is on {t.device}, the call's first tensor on device {index}")
+    if t.dtype is not dtype:
+        return ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    return ValueError(f"{name} must be {what} (got shape {tuple(t.shape)}, strides {tuple(t.stride())})")
 
 
-def _ints(t, name: str, device, shape) -> Optional[int]:
-    """Pointer of an int32 vector on the call's device (None passes as NULL)."""
+def _tensor(t, name: str, index) -> bytes:
+    """Packed bsa_tensor of a 4-D bf16 tensor on GPU ``index``."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and index >= 0 and t.dtype is _BF:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 4 and (stride[3] == 1 or shape[3] == 1):
+            return _pack_tensor(t.data_ptr(), *shape, *stride[:3])
+    raise _wrong(t, name, index if index is None or index >= 0 else None,
+                 "4-D [B, S, H, d] with a contiguous last dim", _BF)
+
+
+def _gpu(t, name: str) -> int:
+    """The GPU of a call's first tensor."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if index < 0:
+        raise _wrong(t, name, None, "", _BF)
+    return index
+
+
+def _ints(t, name: str, index: int, n: int) -> Optional[int]:
+    """Pointer of an int32 vector of n on the call's GPU (None passes as NULL)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous torch.int32 tensor of shape {shape} on {device} "
-                         f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is _I32 and t.shape == (n,)
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise _wrong(t, name, index, f"contiguous [{n}]", _I32)
 
 
-def _positions(t, name: str, device, B: int, S: int):
-    """Descriptor of int32 positions [B, S, A] or [S, A] (shared by the batch)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not _I32 or t.device != device:
-        raise ValueError(f"{name} must be a torch.int32 tensor on {device} (got {t.dtype}, {t.device})")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 2:
-        shape, stride = (1, *shape), (0, *stride)
-    if len(shape) != 3 or shape[0] not in (1, B) or shape[1] != S:
-        raise ValueError(f"{name} must be [B, S, axes] or [S, axes] with B = {B}, S = {S} (got {tuple(t.shape)})")
-    return _pack_positions(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if S > 1 else 0,
-                           stride[2]), shape[2]
+def _positions(t, name: str, index: int, B: int, S: int):
+    """Packed bsap_positions of int32 positions [B, S, A] or [S, A] (shared by
+    the batch), and A."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is _I32:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2:
+            shape, stride = (1, *shape), (0, *stride)
+        if len(shape) == 3 and shape[1] == S and (shape[0] == B or shape[0] == 1):
+            return _pack_positions(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if S > 1 else 0,
+                                   stride[2]), shape[2]
+    raise _wrong(t, name, index, f"[B, S, axes] or [S, axes] with B = {B}, S = {S}", _I32)
 
 
-def _rope(inv_freq, axes, n_axes: int, interleaved: bool, device) -> bytes:
+def _rope(inv_freq, axes, n_axes: int, interleaved: bool, index: int) -> bytes:
     for name, t, dtype in (("inv_freq", inv_freq, _F64), ("axes", axes, _I32)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype is not dtype or t.dim() != 1 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor on {device} "
-                             f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+        if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.dim() == 1
+                and t.is_contiguous()):
+            raise _wrong(t, name, index, "contiguous [pairs]", dtype)
     pairs = axes.shape[0]
     if inv_freq.shape[0] != pairs:
         raise ValueError(f"inv_freq has {inv_freq.shape[0]} pairs, axes {pairs}")
@@ -114,26 +123,25 @@ def _check_overlap(name: str, out: torch.Tensor, inputs, in_place) -> None:
 
 
 @contextlib.contextmanager
-def _elsewhere(device, stream):
-    with torch.cuda.device(device):
+def _elsewhere(index, stream):
+    with torch.cuda.device(index):
         if stream is None:
             yield
         else:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device)
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+                stream = torch.cuda.ExternalStream(int(stream), torch.device("cuda", index))
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors on device {index}")
             with torch.cuda.stream(stream):
                 yield
 
 
-def _on(device, stream, call, *args):
-    """``call(*args, stream handle)`` with the tensors' device and the call's
+def _on(index, stream, call, *args):
+    """``call(*args, stream handle)`` with the tensors' GPU and the call's
     stream current."""
-    index = device.index
-    if stream is None and index == torch.cuda.current_device():
+    if stream is None and index == _current_device():
         return call(*args, _raw_stream(index))
-    with _elsewhere(device, stream):
+    with _elsewhere(index, stream):
         return call(*args, _raw_stream(index))
 
 
@@ -170,10 +178,9 @@ def bsa_axis_frequencies(sections: Sequence[int], theta: float = 10000.0, layout
 
 
 def _rope_call(q, k, pos_q, pos_k, inv_freq, axes, interleaved, backward, q_out, k_out, stream, names):
-    qd = _tensor(q, names[0])
-    dev = q.device
-    B, S, Hq, d = q.shape
-    pq, n_axes = _positions(pos_q, "pos_q", dev, B, S)
+    dev = _gpu(q, names[0])
+    qd = _tensor(q, names[0], dev)
+    pq, n_axes = _positions(pos_q, "pos_q", dev, q.shape[0], q.shape[1])
     rope = _rope(inv_freq, axes, n_axes, interleaved, dev)
     kd = pk = None
     if k is not None:
@@ -236,18 +243,12 @@ def bsa_rope_axes_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], pos_q: 
                       ("dq", "dk", "dq_out", "dk_out"))
 
 
-def _table(page_table, B: int, device):
-    if not isinstance(page_table, torch.Tensor):
-        raise TypeError("page_table must be a torch.Tensor")
-    if page_table.dtype is not _I32 or page_table.device != device:
-        raise ValueError(f"page_table must be a torch.int32 tensor on {device} (got {page_table.dtype}, "
-                         f"{page_table.device})")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table must be [B, max_pages] with B = {B} (got {tuple(page_table.shape)})")
-    n = page_table.shape[1]
-    if n > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table must have a contiguous last dim")
-    return page_table.data_ptr(), page_table.stride(0) if B > 1 else n, n
+def _table(t, B: int, index: int):
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is _I32:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2 and shape[0] == B and (shape[1] <= 1 or stride[1] == 1):
+            return t.data_ptr(), stride[0] if B > 1 else shape[1], shape[1]
+    raise _wrong(t, "page_table", index, f"[B, max_pages] with B = {B} and a contiguous last dim", _I32)
 
 
 def bsa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -267,13 +268,13 @@ def bsa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
     rotated as by ``bsa_rope_axes``, and so is ``q`` when given (all T rows);
     without them k is copied.  Returns the rotated q, or None.
     """
-    kd = _tensor(k, "k")
-    dev = k.device
+    dev = _gpu(k, "k")
+    kd = _tensor(k, "k", dev)
     vd, kc, vc = _tensor(v, "v", dev), _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
     B, T = k.shape[:2]
     table, stride, n = _table(page_table, B, dev)
-    lens = _ints(kv_lens, "kv_lens", dev, (B,))
-    new = _ints(new_lens, "new_lens", dev, (B,))
+    lens = _ints(kv_lens, "kv_lens", dev, B)
+    new = _ints(new_lens, "new_lens", dev, B)
     rope = pos = qd = None
     if positions is not None:
         pos, n_axes = _positions(positions, "positions", dev, B, T)
@@ -326,19 +327,20 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 
     Returns ``(out [B, T, Hq, d] bf16, lse [B, Hq, T] fp32 or None)``.
     """
-    qd = _tensor(q, "q")
-    dev = q.device
+    dev = _gpu(q, "q")
+    qd = _tensor(q, "q", dev)
     kc, vc = _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
     B, T, Hq, d = q.shape
     table, stride, n = _table(page_table, B, dev)
-    lens = _ints(kv_lens, "kv_lens", dev, (B,))
-    new = _ints(new_lens, "new_lens", dev, (B,))
+    lens = _ints(kv_lens, "kv_lens", dev, B)
+    new = _ints(new_lens, "new_lens", dev, B)
     prefix_len = int(prefix_len)
     shared = None
     if prefix_len > 0:
         if prefix_table is None:
             raise ValueError(f"prefix_len is {prefix_len}, prefix_table is None")
-        shared = _ints(prefix_table, "prefix_table", dev, (prefix_table.numel(),))
+        shared = _ints(prefix_table, "prefix_table", dev,
+                       prefix_table.numel() if isinstance(prefix_table, torch.Tensor) else 0)
         if prefix_table.numel() * k_cache.shape[1] < prefix_len:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages of {k_cache.shape[1]}, prefix_len is "
                              f"{prefix_len}")

@@ -155,13 +155,19 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
     q = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
     pos = torch.zeros(1, 3, dtype=torch.int32)
     inv, axes = bsa.bsa_axis_frequencies((8, 8, 8), device="cpu")
-    cpu = torch.device("cpu")
-    with pytest.raises(ValueError, match="CUDA tensor"):
+    cpu = q.get_device()                      # -1: the checks below are the ones that follow the first tensor's
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
         bsa.bsa_rope_axes(q, None, pos, None, inv, axes)
-    with pytest.raises(ValueError, match="CUDA tensor"):
+    with pytest.raises(ValueError, match="k must be a CUDA tensor"):
         bsa.bsa_cache_append(q, q, q, q, pos, pos)
-    with pytest.raises(ValueError, match="CUDA tensor"):
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
         bsa.bsa_forward_paged(q, q, q, pos, pos)
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        bsa.bsa_forward_paged(None, q, q, pos, pos)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        paged._tensor(q, "q", cpu)
+    with pytest.raises(ValueError, match="the call's first tensor on device 0"):
+        paged._tensor(q, "v", 0)
     with pytest.raises(TypeError, match="inv_freq"):
         paged._rope(None, axes, 3, False, cpu)
     with pytest.raises(ValueError, match="float64"):
@@ -173,7 +179,9 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
     with pytest.raises(ValueError, match="B = 1, S = 2"):
         paged._positions(pos, "pos_q", cpu, 1, 2)
     with pytest.raises(ValueError, match="kv_lens"):
-        paged._ints(pos, "kv_lens", cpu, (1,))
+        paged._ints(pos, "kv_lens", cpu, 1)
+    with pytest.raises(ValueError, match="kv_lens"):
+        paged._ints(torch.zeros(8, dtype=torch.int32)[::2], "kv_lens", cpu, 4)
     with pytest.raises(ValueError, match="contiguous last dim"):
         paged._table(torch.zeros(4, 3, dtype=torch.int32).t(), 3, cpu)
     with pytest.raises(ValueError, match="page_table must be"):
