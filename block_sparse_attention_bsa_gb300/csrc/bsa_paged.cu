@@ -458,12 +458,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     uint32_t k_stage = 0, v_stage = 0;
     uint32_t uses0 = 0, uses1 = 0;      // segments that each O has been used for
     bool v_first = false, v_new = false, v_last = false;   // job q - 1: starts its O; takes, releases its V tile
+    int v_keys = 0;                     // its tile's keys
     SegmentReader reader;
 #pragma unroll 1
     for (int t = begin; begin < end;) {
       const bool more = t < end;        // after the last segment there is one P V left
       Segment s;
       s.rows = s.tiles = 1;
+      s.keys = s.tile0 = 0;
       if (more && !reader.take(segs, seg_full, seg_empty, abort_flag, s)) break;
       const bool wide = s.rows > kHalf;
       const int jobs = wide ? 2 * s.tiles : s.tiles;
@@ -502,6 +504,23 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             v_stage = stage;
             if (!(ok = warp_wait(full + 8 * stage, phase, abort_flag))) break;
             advance<kStages>(stage, phase);
+            // Behind the last key the page holds whatever stood there: V rows
+            // up to the end of the MMA step that it lies in are zeroed (0 times
+            // infinity or NaN is NaN), the steps behind are left out.
+            const int rest = -v_keys & 15;
+            if (v_keys < kTileKeys && rest != 0) {
+              const uint32_t at = smem_u32(ring) + v_stage * C::kTileBytes + v_keys * 128;
+#pragma unroll 1
+              for (int x = lane; x < rest * (D / 8); x += 32) {
+                const int row = x / (D / 8), c = x % (D / 8);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + (c / 8) * (kTileKeys * 128) + row * 128 +
+                                                                             (c % 8) * 16),
+                             "r"(0)
+                             : "memory");
+              }
+              fence_async_shared();
+              __syncwarp();
+            }
           }
           if (!(ok = warp_wait(p_full + 8 * w, (job >> 1) & 1u, abort_flag))) break;
           tc_fence_after();
@@ -511,7 +530,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             mma_ts(d_t, a_t, bs, idesc_o, !v_first);
 #pragma unroll
             for (int kk = 1; kk < kTileKeys / 16; ++kk)
-              mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
+              if (kk * 16 < v_keys) mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
             mma_commit(pv_done + 8 * w);
             if (v_last) mma_commit(empty + 8 * v_stage);
           }
@@ -521,6 +540,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         v_first = j < 2;
         v_new = !wide || (j & 1) == 0;
         v_last = !wide || (j & 1) == 1;
+        v_keys = min(s.keys - (s.tile0 + (wide ? j >> 1 : j)) * kTileKeys, kTileKeys);
       }
       if (!ok || !more) break;
       qi += wide ? 2 : 1;
@@ -646,8 +666,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const uint32_t s_t = tmem + lane_base + w * 128;
     const uint32_t o_t = tmem + lane_base + 256 + w * 128;
     uint32_t q = 0;                                // first job of the segment
-    uint32_t items = 0;                            // ring items that the jobs before q have taken
-    bool v_left = false;                           // job q - 1 takes one for V in job q's turn
     // The segment's fields stay in the ring until the group is through with it:
     // with S in 128 registers there is no room to hold them.
     SegmentReader reader;
@@ -660,10 +678,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       const int half = wide ? j0 : 0;              // and the rows that its jobs have
       const int rows = min(kHalf, s.rows - half * kHalf);
       const bool active = wq * 32 < rows;          // some row of this warp is real
-      int limit = p.prefix_len;                    // keys that the row sees
-      if (s.b >= 0) {
+      int limit = s.keys;                          // keys that the row sees (a row that is none: all)
+      if (s.b >= 0 && r < rows) {
         const int rem = s.row0 + half * kHalf + r - s.b * p.TG;
-        limit = r < rows ? min(seen_keys(p, s.kv, s.n, p.div_G.quot(rem)), s.kv) : 0;
+        limit = min(seen_keys(p, s.kv, s.n, p.div_G.quot(rem)), s.kv);
       }
       float m_ref = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -678,22 +696,23 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           // code is three times as long, and the roles' loops no longer fit the
           // instruction cache together (32 at a time measured 3 % slower).
           const int valid = limit - key0;
-          if (__any_sync(0xffffffffu, valid < kTileKeys)) {      // keys that some row of the warp does not see
+          // columns below `least` are seen by all rows of the warp, those from
+          // `most` on by none
+          const int least = __reduce_min_sync(0xffffffffu, valid), most = __reduce_max_sync(0xffffffffu, valid);
 #pragma unroll 1
-            for (int c = 0; c < kTileKeys / 32; ++c) {
-              float v[32];
-              tmem_ld32f(s_t + c * 32, v);
-              tmem_wait_ld();
+          for (int c = max(least, 0) & ~31; c < min((most + 63) & ~63, kTileKeys); c += 32) {
+            float v[32];
+            tmem_ld32f(s_t + c, v);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c * 32 + e >= valid) v[e] = -INFINITY;
-              tmem_st32f(s_t + c * 32, v);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (c + e >= valid) v[e] = -INFINITY;
+            tmem_st32f(s_t + c, v);
             tmem_wait_st();
           }
           float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kTileKeys; c += 64) {
+          for (int c = 0; c < min(most, kTileKeys); c += 64) {
             float v[64];
             tmem_ld32f(s_t + c, v);
             tmem_ld32f(s_t + c + 32, v + 32);
@@ -720,6 +739,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           for (int c = 0; c < kTileKeys; c += 64) {
             float v[64];
             uint32_t pk[32];
+            if (c >= most) {                       // P of keys that no row sees
+#pragma unroll
+              for (int e = 0; e < 32; ++e) pk[e] = 0u;
+              tmem_st32(s_t + c / 2, pk);
+              continue;
+            }
             tmem_ld32f(s_t + c, v);
             tmem_ld32f(s_t + c + 32, v + 32);
             tmem_wait_ld();
@@ -751,29 +776,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             }
           }
           tmem_wait_st();
-        }
-        // The last tile's rows behind the keys hold whatever stood in the page:
-        // they are zeroed in V (0 times infinity or NaN is NaN), before the
-        // first of the jobs that use it.
-        const int there = s.keys - key0;
-        if (there < kTileKeys && half == 0) {
-          // Which ring item V is: in a wide segment the one behind the tile's K
-          // (its second job takes no K); else the one behind the next tile's K,
-          // if there is a next tile.
-          const bool last = t + s.tiles == end && tile == s.tiles - 1;
-          const uint32_t item = items + (v_left ? 1u : 0u) + 2u * (uint32_t)tile + (wide || last ? 1u : 2u);
-          ok = warp_wait(full + 8 * (item % kStages), (item / kStages) & 1u, abort_flag);
-          if (!ok) break;
-          if (r >= there) {
-            const uint32_t at = smem_u32(ring) + (item % kStages) * C::kTileBytes + r * 128;
-#pragma unroll 1
-            for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * (kTileKeys * 128) + e * 16), "r"(0)
-                             : "memory");
-          }
-          fence_async_shared();
         }
         tc_fence_before();
         __syncwarp();
@@ -833,8 +835,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty + 8 * w);
       }
-      items += (v_left ? 1u : 0u) + 2u * (uint32_t)s.tiles - (wide ? 0u : 1u);
-      v_left = !wide;
       q += jobs;
       t += s.tiles;
       reader.release(seg_empty);
