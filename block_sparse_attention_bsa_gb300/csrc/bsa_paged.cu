@@ -209,6 +209,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
 // proxy (the MMAs read Q and V through it).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// 32 bytes, a whole sector, to a 32-byte aligned address.
+__device__ __forceinline__ void store_32(void* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -814,12 +821,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e)              // out may be aligned to 16 bytes only
               reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
           } else if (mine) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(dst)[c * 8 + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) store_32(dst + (c * 4 + e) * 32, o + 8 * e);
           }
         }
         if (mine) {
@@ -851,14 +857,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
 // Output row (b, i, h): joins the partial results of its prefix segment and of
 // its own segment.  kLanes lanes of kWarps warps share a row: eight lanes where
 // there are many rows (a warp's way through its dependent loads takes 4 us, so
-// four rows go it together), four or eight warps where there are few rows of
-// many partial results.
+// four rows go it together), a warp or eight warps where there are fewer.
 template <int D, int kLanes, int kWarps>
 __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kPer = D / kLanes;                 // values per lane, kVec at a time
   constexpr int kVec = kPer < 4 ? kPer : 4;
   constexpr int kRows = kWarps > 1 ? 1 : 128 / kLanes;   // rows per block
-  constexpr int kLoads = kWarps == 8 ? 4 : kWarps == 4 ? 8 : 2;      // partial rows in flight per lane
+  constexpr int kLoads = kWarps == 8 ? 4 : kLanes == 32 ? 8 : 2;      // partial rows in flight per lane
   static_assert(kWarps == 1 || kLanes == 32, "several warps take whole rows");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % kLanes;
   const int part = warp % kWarps;
@@ -1084,22 +1089,23 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   paged_attention_kernel<D><<<p.ctas, kPagedThreads, PagedCfg<D>::kSmemBytes, stream>>>(p);
   if ((st = cuda_check(cudaGetLastError(), "paged_attention_kernel launch")) != BSA_OK) return st;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
-  // Warps per row by the number of rows (us of the join, 1 / 4 / 8 warps a row:
-  // 32 rows of 40 partial results - / 7.4 / 6.5; 2,048 rows of 20 partial
-  // results 20 / 8 / 11, of 2 to 6 13 / 10 / 15; 16,384 finished rows 4 / 10 / -).
-  const int warps = rows < (int64_t)num_sms() * 4 ? 8 : rows < (int64_t)num_sms() * 16 ? 4 : 1;
+  // Eight warps, one warp or eight lanes a row, by the number of rows (us of the
+  // join: 32 rows of 40 partial results 6.4, with one warp 9; 2,048 rows of 2 to
+  // 10 with one warp 7.7, four 11, eight lanes 13; 24,000 rows of 2 to 4 with
+  // eight lanes 12, one warp 19; 8,192 rows 12 either way).
+  const int lanes = rows < (int64_t)num_sms() * 4 ? 256 : rows < (int64_t)num_sms() * 40 ? 32 : 8;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(warps > 1 ? rows : cdiv64(rows, 16)));
-  cfg.blockDim = dim3(warps > 1 ? 32 * warps : 128);
+  cfg.blockDim = dim3(lanes == 256 ? 256 : 128);
+  cfg.gridDim = dim3((unsigned)cdiv64(rows, cfg.blockDim.x / lanes));
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cuda_check(warps == 8   ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 8>, p)
-                    : warps == 4 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 4>, p)
-                                 : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),
+  return cuda_check(lanes == 256  ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 8>, p)
+                    : lanes == 32 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 1>, p)
+                                  : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),
                     "paged_join_kernel launch");
 }
 
