@@ -102,6 +102,7 @@ struct PagedParams {
   __nv_bfloat16* out;
   float* lse;
   int32_t* cum;                   // workspace: [B + 1] tiles of own keys before request b
+  int32_t* rt_before;             // workspace, own_rt > 1: [B, own_rt + 1] a head's tiles before row tile rt
   float* part_ml;                 // workspace: partial results' (max, sum) and rows,
   float* part_o;                  // those of the prefix first,
   int own_first;                  // from here on those of own keys
@@ -359,6 +360,21 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   if (cta == 0) {
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kPagedThreads) p.cum[b] += block_sum[b / 32];
+    if (p.own_rt > 1) {
+#pragma unroll 1
+      for (int b = warp; b < p.B; b += kPagedThreads / 32) {
+        const int kv = own_keys(p, b), n = new_tokens(p, b);
+        int before = 0;
+#pragma unroll 1
+        for (int rt0 = 0; rt0 <= p.own_rt; rt0 += 32) {
+          const int rt = rt0 + lane;
+          const int m = rt < p.own_rt ? own_tiles(p, kv, n, rt) : 0;
+          const int incl = warp_inclusive_sum(m) + before;
+          if (rt <= p.own_rt) p.rt_before[b * (p.own_rt + 1) + rt] = incl - m;
+          before = __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+    }
     if (threadIdx.x == 0) p.cum[p.B] = *total_slot;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -897,14 +913,8 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
       if (p.own_rt == 1) {
         t0 += hk * mine;
       } else {
-        int all = 0, before = 0;
-#pragma unroll 1
-        for (int x = 0; x < p.own_rt; ++x) {
-          const int m = own_tiles(p, kv, n, x);
-          if (x < rt) before += m;
-          all += m;
-        }
-        t0 += hk * all + before;
+        const int32_t* before = p.rt_before + b * (p.own_rt + 1);
+        t0 += hk * before[p.own_rt] + before[rt];
       }
       const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + mine - 1);
       const int two = n * p.G - rt * kRowTile <= kHalf;
@@ -1004,7 +1014,7 @@ std::string s(int64_t v) { return std::to_string(v); }
 // Where the partial results lie in the workspace.
 struct PagedPlan {
   int TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
-  size_t own_first, cum, part_ml, part_o, bytes;
+  size_t own_first, cum, rt_before, part_ml, part_o, bytes;
 };
 
 PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
@@ -1021,7 +1031,8 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
   w.own_first = pre;
   w.cum = 0;
-  w.part_ml = al((size_t)(B + 1) * 4);
+  w.rt_before = al((size_t)(B + 1) * 4);
+  w.part_ml = w.rt_before + (w.own_rt > 1 ? al((size_t)B * (w.own_rt + 1) * 4) : 0);
   w.part_o = w.part_ml + al((pre + own) * 8);
   w.bytes = w.part_o + al((pre + own) * d * 4);
   return w;
@@ -1190,10 +1201,14 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = sms;
-  // A wide prefix tile (two jobs of 1 us on the tensor cores) takes longer than
-  // a tile of own keys for a few rows (1.5 us at its share of the memory rate).
+  // A wide prefix tile (two jobs of 0.9 us on the tensor cores) against a tile
+  // of own keys for a few rows (1.5 us at its share of the memory rate, less
+  // while others compute).  us at prefix : own = 1:1 / 4:3 / 5:3 / 2:1 --
+  // 64 requests, 8k prefix, 512 own keys 57 / 52 / 49 / 46; 64, 4k, 1,024
+  // 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188; 256, 32k, ragged up
+  // to 512 187 / 177 / 180 / 205.
   const bool wide_pre = flat_rows > kHalf && qv.S * G <= kHalf;
-  p.pre_w = wide_pre ? 4 : 1;
+  p.pre_w = wide_pre ? 5 : 1;
   p.own_w = wide_pre ? 3 : 1;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
@@ -1201,6 +1216,7 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.cum = reinterpret_cast<int32_t*>(ws + plan.cum);
+  p.rt_before = reinterpret_cast<int32_t*>(ws + plan.rt_before);
   p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
   p.own_first = (int)plan.own_first;

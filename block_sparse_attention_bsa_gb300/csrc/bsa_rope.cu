@@ -14,7 +14,9 @@
 // operations per clock and SM.  The top 32 bits give the half-turns in
 // [-1, 1) for sincospif.
 //
-// What bounds it: memory.  A thread owns 16 channels of a token (8 pairs), so
+// What bounds it: memory (720p latent, 32 + 8 heads of 128: 527 us, 6.72 TB/s;
+// 480p, 24 + 8 heads: 129 us, 6.16 TB/s; append with Q of 5 x 4,099 ragged
+// tokens: 62 us, 5.5 TB/s).  A thread owns 16 channels of a token (8 pairs), so
 // both its accesses are 16 bytes and neighbouring threads make whole 128-byte
 // lines, and goes through a group of heads, so that the sines and cosines of
 // a token are computed once per thread and not once per head.
@@ -32,7 +34,7 @@ __device__ unsigned int g_rope_error = 0;
 
 constexpr int kRopeThreads = 128;
 constexpr int kMaxAxes = 4;
-constexpr int kBatch = 4;         // heads whose loads are in flight together
+constexpr int kBatch = 4;         // heads whose loads are in flight together (720p: 2 550 us, 4 527, 8 533)
 
 struct RotJob {
   const __nv_bfloat16* x;
@@ -262,9 +264,11 @@ bsa_status launch_rotate(RotParams& p, int n_jobs, int64_t D, bool interleaved, 
     if (p.job[i].H > heads) heads = p.job[i].H;
   }
   const int64_t blocks = cdiv64(most, tokens_per_block);
-  // Heads per thread: as many as leave the GPU full (16 blocks of 128 threads
-  // per SM), since a thread's sines and cosines serve all its heads.
-  const int64_t full = (int64_t)num_sms() * 16;
+  // Heads per thread: as many as leave 8 blocks of 128 threads per SM, since a
+  // thread's sines and cosines, and its way through the page table, serve all
+  // its heads (at 32 blocks per SM the 480p rotation took 133 us instead of
+  // 129, the append of 5 x 4,099 tokens 81 us instead of 62).
+  const int64_t full = (int64_t)num_sms() * 8;
   int hpg = heads;
   while (hpg > 1 && blocks * cdiv64(heads, hpg) < full) hpg = (hpg + 1) / 2;
   p.heads_per_group = hpg;

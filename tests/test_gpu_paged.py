@@ -347,3 +347,57 @@ def test_attention_over_many_segments_matches_64_bits(B, prefix, low, high, Hq, 
         again, lse2 = bsa.bsa_forward_paged(q, kc, vc, table, lens, prefix_table=pt, prefix_len=prefix)
         assert torch.equal(out, again) and torch.equal(lse, lse2)
     bsa.bsa_device_status()
+
+
+@pytest.mark.parametrize("T,new,kv,prefix,Hq,Hkv,d,page,causal", [
+    (1500, [1500, 700], [1500, 2100], 300, 4, 1, 128, 64, True),      # 24 row tiles a request, a prefix beside them
+    (1100, [1100, 0, 257], [1300, 40, 257], 0, 6, 2, 64, 16, True),   # no prefix: whole segments are written at once
+    (600, [600, 431], [900, 431], 129, 3, 3, 128, 256, False),
+    (8200, [8200], [8200], 0, 1, 1, 64, 128, True),                   # 33 row tiles
+])
+def test_attention_of_long_chunks_matches_64_bits(T, new, kv, prefix, Hq, Hkv, d, page, causal):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    B, G = len(kv), Hq // Hkv
+    width, shared = -(-max(kv) // page), -(-prefix // page)
+    total = B * width + shared + 1
+    kc, vc = (torch.randn(total, page, Hkv, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    order = torch.randperm(total, generator=g, device=DEV).int()
+    table, pt = order[:B * width].view(B, width), order[B * width:B * width + shared]
+    q = torch.randn(B, T, Hq, d, generator=g, device=DEV).to(BF)
+    lens, new_t = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (kv, new))
+    out, lse = bsa.bsa_forward_paged(q, kc, vc, table, lens, new_lens=new_t, prefix_table=pt, prefix_len=prefix,
+                                     causal=causal)
+    bsa.bsa_device_status()
+    for b in range(B):
+        n = new[b]
+        assert (out[b, n:] == 0).all() and torch.isneginf(lse[b, :, n:]).all()
+        if n == 0:
+            continue
+        k, v = (torch.cat([c[pt.long()].flatten(0, 1)[:prefix], c[table[b].long()].flatten(0, 1)[:kv[b]]]).double()
+                for c in (kc, vc))
+        hidden = None
+        if causal:
+            hidden = torch.arange(prefix + kv[b], device=DEV) > prefix + kv[b] - n + torch.arange(n, device=DEV)[:, None]
+        for h in range(Hq):
+            qq, kk, vv = q[b, :n, h].double(), k[:, h // G], v[:, h // G]
+            z = qq @ kk.T * d ** -0.5
+            za = qq.abs() @ kk.abs().T * d ** -0.5
+            if hidden is not None:
+                z, za = z.masked_fill(hidden, -math.inf), za.masked_fill(hidden, 0.0)
+            dz = 2.0 ** -15 * za.amax(-1)
+            w, ref_lse = torch.softmax(z, -1), torch.logsumexp(z, -1)
+            ref = w @ vv
+            bound = 2.0 ** -8 * ref.abs() + (2 * dz[:, None] + 2.0 ** -8 + 2.0 ** -12) * (w @ vv.abs())
+            assert ((out[b, :n, h].double() - ref).abs() <= bound).all(), (b, h)
+            assert ((lse[b, h, :n].double() - ref_lse).abs() <= dz + 2.0 ** -19 * (ref_lse.abs() + 1)).all(), (b, h)
+
+
+def test_attention_over_the_prefix_alone():
+    """A table without pages: no own keys at all."""
+    pool = Pool([0, 0, 0], 333, 2, 64, 32, DEV, 40)
+    q = randn((3, 2, 6, 64), 41)
+    none = torch.empty((3, 0), dtype=torch.int32, device=DEV)
+    out, lse = bsa.bsa_forward_paged(q.to(DEV), pool.gk, pool.gv, none, pool.kv_lens, prefix_table=pool.gprefix,
+                                     prefix_len=333)
+    bsa.bsa_device_status()
+    check_attention(out, lse, attend64(q, pool))
