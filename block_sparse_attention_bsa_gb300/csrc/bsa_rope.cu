@@ -14,9 +14,9 @@
 // operations per clock and SM.  The top 32 bits give the half-turns in
 // [-1, 1) for sincospif.
 //
-// What bounds it: memory (720p latent, 32 + 8 heads of 128: 527 us, 6.72 TB/s;
-// 480p, 24 + 8 heads: 129 us, 6.16 TB/s; append with Q of 5 x 4,099 ragged
-// tokens: 62 us, 5.5 TB/s).  A thread owns 16 channels of a token (8 pairs), so
+// What bounds it: memory (720p latent, 32 + 8 heads of 128: 513 us, 6.9 TB/s;
+// 480p, 24 + 8 heads: 122 us, 6.5 TB/s; append with Q of 5 x 4,099 ragged
+// tokens: 59 us, 5.8 TB/s).  A thread owns 16 channels of a token (8 pairs), so
 // both its accesses are 16 bytes and neighbouring threads make whole 128-byte
 // lines, and goes through a group of heads, so that the sines and cosines of
 // a token are computed once per thread and not once per head.
@@ -34,7 +34,7 @@ __device__ unsigned int g_rope_error = 0;
 
 constexpr int kRopeThreads = 128;
 constexpr int kMaxAxes = 4;
-constexpr int kBatch = 4;         // heads whose loads are in flight together (720p: 2 550 us, 4 527, 8 533)
+constexpr int kBatch = 4;         // heads whose loads are in flight together (720p: 2 550 us, 4 527, 8 533 with a loop over tokens)
 
 struct RotJob {
   const __nv_bfloat16* x;
@@ -140,72 +140,66 @@ __global__ void __launch_bounds__(kRopeThreads) rotate_kernel(const __grid_const
   const int c0 = apart ? unit * 8 : unit * 16;
   const int c1 = apart ? unit * 8 + p.pairs : c0 + 8;
 
-  uint64_t freq[8];
-  int axis[8];
+  const int tok = blockIdx.x * kTokens + threadIdx.x / kUnits;
+  if (tok >= jb.n_tokens) return;
+  const int b = tok / jb.S, s = tok - b * jb.S;
+  const __nv_bfloat16* xr = jb.x + b * jb.sb + s * jb.ss;
+  __nv_bfloat16* yr;
+  if (jb.paged) {
+    const int n = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), jb.S) : jb.S;
+    if (s >= n) return;
+    const int64_t slot = (int64_t)__ldg(p.kv_lens + b) - n + s;
+    const int64_t at = slot >> p.page_shift;
+    int page = -1;
+    if (slot >= 0 && at < p.max_pages) page = __ldg(p.page_table + b * p.table_stride + at);
+    if (page < 0 || page >= p.num_pages) {
+      if (unit == 0) atomicOr(&g_rope_error, kErrPage);
+      return;
+    }
+    yr = jb.y + page * jb.yb + (slot & ((1 << p.page_shift) - 1)) * jb.ys;
+  } else {
+    yr = jb.y + b * jb.yb + s * jb.ys;
+  }
+  // four heads at a time: all their loads are in flight before the first
+  // store (which may be to the same memory, so the compiler keeps the order);
+  // the first ones are on their way while the angles are worked out
+  uint4 u0[kBatch], u1[kBatch];
+  auto load = [&](int h) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    freq[i] = 0;
-    axis[i] = -1;
-    if (turn) {
-      freq[i] = turns_per_position(__ldg(p.inv_freq + unit * 8 + i));
-      if (p.back) freq[i] = 0 - freq[i];
-      axis[i] = __ldg(p.axes + unit * 8 + i);
+    for (int j = 0; j < kBatch; ++j) {
+      if (h + j < h1) {
+        u0[j] = *reinterpret_cast<const uint4*>(xr + (h + j) * jb.sh + c0);
+        u1[j] = *reinterpret_cast<const uint4*>(xr + (h + j) * jb.sh + c1);
+      }
+    }
+  };
+  load(h0);
+  float cs[8], sn[8];
+  if (turn) {
+    const int32_t* pr = jb.pos + b * jb.pb + s * jb.ps;
+    int where[kMaxAxes];
+#pragma unroll
+    for (int a = 0; a < kMaxAxes; ++a) where[a] = a < p.n_axes ? __ldg(pr + a * jb.pa) : 0;
+    const int sign = p.back ? -1 : 1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t f = turns_per_position(__ldg(p.inv_freq + unit * 8 + i));
+      const int a = __ldg(p.axes + unit * 8 + i);
+      const int w = a == 0 ? where[0] : a == 1 ? where[1] : a == 2 ? where[2] : a == 3 ? where[3] : 0;
+      const uint64_t t = f * (uint64_t)((int64_t)w * sign);       // an axis outside [0, n_axes) reads 0: no turn
+      sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn[i], &cs[i]);
     }
   }
-
-  for (int tok = blockIdx.x * kTokens + threadIdx.x / kUnits; tok < jb.n_tokens; tok += gridDim.x * kTokens) {
-    const int b = tok / jb.S, s = tok - b * jb.S;
-    const __nv_bfloat16* xr = jb.x + b * jb.sb + s * jb.ss;
-    __nv_bfloat16* yr;
-    if (jb.paged) {
-      const int n = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), jb.S) : jb.S;
-      if (s >= n) continue;
-      const int64_t slot = (int64_t)__ldg(p.kv_lens + b) - n + s;
-      const int64_t at = slot >> p.page_shift;
-      int page = -1;
-      if (slot >= 0 && at < p.max_pages) page = __ldg(p.page_table + b * p.table_stride + at);
-      if (page < 0 || page >= p.num_pages) {
-        if (unit == 0) atomicOr(&g_rope_error, kErrPage);
-        continue;
-      }
-      yr = jb.y + page * jb.yb + (slot & ((1 << p.page_shift) - 1)) * jb.ys;
-    } else {
-      yr = jb.y + b * jb.yb + s * jb.ys;
-    }
-    float cs[8], sn[8];
-    if (turn) {
-      const int32_t* pr = jb.pos + b * jb.pb + s * jb.ps;
-      int where[kMaxAxes];
+  for (int h = h0; h < h1; h += kBatch) {
 #pragma unroll
-      for (int a = 0; a < kMaxAxes; ++a) where[a] = a < p.n_axes ? __ldg(pr + a * jb.pa) : 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int a = axis[i];
-        const int w = a == 0 ? where[0] : a == 1 ? where[1] : a == 2 ? where[2] : a == 3 ? where[3] : 0;
-        const uint64_t t = freq[i] * (uint64_t)(int64_t)w;        // an axis outside [0, n_axes) reads 0: no turn
-        sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn[i], &cs[i]);
+    for (int j = 0; j < kBatch; ++j) {
+      if (h + j < h1) {
+        if (turn) turn_unit<kInterleaved>(u0[j], u1[j], cs, sn);
+        *reinterpret_cast<uint4*>(yr + (h + j) * jb.yh + c0) = u0[j];
+        *reinterpret_cast<uint4*>(yr + (h + j) * jb.yh + c1) = u1[j];
       }
     }
-    // four heads at a time: all their loads are in flight before the first
-    // store (which may be to the same memory, so the compiler keeps the order)
-    for (int h = h0; h < h1; h += kBatch) {
-      uint4 u0[kBatch], u1[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (h + j < h1) {
-          u0[j] = *reinterpret_cast<const uint4*>(xr + (h + j) * jb.sh + c0);
-          u1[j] = *reinterpret_cast<const uint4*>(xr + (h + j) * jb.sh + c1);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (h + j < h1) {
-          if (turn) turn_unit<kInterleaved>(u0[j], u1[j], cs, sn);
-          *reinterpret_cast<uint4*>(yr + (h + j) * jb.yh + c0) = u0[j];
-          *reinterpret_cast<uint4*>(yr + (h + j) * jb.yh + c1) = u1[j];
-        }
-      }
-    }
+    load(h + kBatch);
   }
 }
 
@@ -266,8 +260,8 @@ bsa_status launch_rotate(RotParams& p, int n_jobs, int64_t D, bool interleaved, 
   const int64_t blocks = cdiv64(most, tokens_per_block);
   // Heads per thread: as many as leave 8 blocks of 128 threads per SM, since a
   // thread's sines and cosines, and its way through the page table, serve all
-  // its heads (at 32 blocks per SM the 480p rotation took 133 us instead of
-  // 129, the append of 5 x 4,099 tokens 81 us instead of 62).
+  // its heads (at 32 blocks per SM the 480p rotation took 3 % longer, the
+  // append of 5 x 4,099 tokens 30 %).
   const int64_t full = (int64_t)num_sms() * 8;
   int hpg = heads;
   while (hpg > 1 && blocks * cdiv64(heads, hpg) < full) hpg = (hpg + 1) / 2;
