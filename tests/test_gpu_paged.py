@@ -229,6 +229,9 @@ ATTEND_CASES = [
     ([0, 0], 2, None, 0, 5, 1, 128, 16, True, "slots"),              # no key at all
     ([20] * 70, 1, None, 130, 4, 1, 64, 16, True, "slots"),          # more than one block of requests, 3 row tiles
     ([1, 2, 3, 128, 129, 255, 256, 257], 2, None, 127, 64, 1, 64, 16, True, "slots"),
+    ([50, 300], 1, None, 40, 256, 1, 64, 16, True, "heads"),          # one token fills two jobs' rows
+    ([200, 70, 66], 65, [65, 30, 64], 0, 2, 1, 128, 32, True, "slots"),   # rows of one request in two jobs, of another in one
+    ([33], 1, None, 5, 256, 256, 64, 16, True, "slots"),
 ]
 
 
@@ -327,6 +330,8 @@ def attend64_one(q, k, v, lens, prefix_k, prefix_v):
     (700, 129, 100, 128, 4, 4, 128, 128),     # single tiles only
     (6, 20000, 1000, 9000, 32, 2, 128, 128),  # long runs of tiles, cut many times
     (64, 0, 4096, 4096, 16, 8, 128, 128),
+    (4096, 100, 0, 40, 2, 1, 64, 16),         # the largest batch
+    (97, 0, 30, 31, 8, 8, 64, 32),            # fewer tiles than a CTA has warps, many requests without a cut
 ])
 def test_attention_over_many_segments_matches_64_bits(B, prefix, low, high, Hq, Hkv, d, page):
     g = torch.Generator(device=DEV).manual_seed(B + high)
@@ -401,3 +406,16 @@ def test_attention_over_the_prefix_alone():
                                      prefix_len=333)
     bsa.bsa_device_status()
     check_attention(out, lse, attend64(q, pool))
+
+
+def test_append_rotates_queries_in_place():
+    pool = Pool([9, 30], 0, 2, 128, 16, DEV, 42, fill=0.0)
+    q, k = randn((2, 5, 4, 128), 43).to(DEV), randn((2, 5, 2, 128), 44).to(DEV)
+    pos = torch.randint(0, 99, (2, 5, 2), dtype=torch.int32, generator=torch.Generator().manual_seed(45)).to(DEV)
+    inv, axes = bsa.bsa_axis_frequencies((20, 12), layout="per_axis", device=DEV)
+    want, _ = bsa.bsa_rope_axes(q, None, pos, None, inv, axes)
+    mine = q.clone()
+    got = bsa.bsa_cache_append(k, k, pool.gk, pool.gv, pool.gtable, pool.kv_lens, q=mine, q_out=mine, positions=pos,
+                               inv_freq=inv, axes=axes)
+    assert got is mine and torch.equal(mine, want)
+    bsa.bsa_device_status()
