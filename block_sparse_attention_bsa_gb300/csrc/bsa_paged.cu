@@ -217,6 +217,55 @@ __device__ __forceinline__ void store_32(void* dst, const float* v) {
                : "memory");
 }
 
+// 8 columns from `col` on of a row at `row`: fp32, or divided by the row's sum
+// to bf16 (which may be aligned to 16 bytes only).
+__device__ __forceinline__ void store_row(unsigned long long row, int col, const float* v, float inv_l, bool bf16,
+                                          bool real) {
+  if (!real) return;
+  if (bf16) {
+    uint32_t pk[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pk[e] = inv_l > 0.f ? pack_bf16x2(v[2 * e] * inv_l, v[2 * e + 1] * inv_l) : 0u;
+    *reinterpret_cast<uint4*>(row + col * 2) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  } else {
+    store_32(reinterpret_cast<void*>(row + col * 4), v);
+  }
+}
+
+// 16 lanes x 32 columns: lane t gets of row t / 4 (a) and of row t / 4 + 8 (b)
+// columns 8 j + 2 (t % 4) and the next one, j = 0 .. 3.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float* a, float* b) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(a[0]), "=f"(a[1]), "=f"(b[0]), "=f"(b[1]), "=f"(a[2]), "=f"(a[3]), "=f"(b[2]), "=f"(b[3]), "=f"(a[4]),
+        "=f"(a[5]), "=f"(b[4]), "=f"(b[5]), "=f"(a[6]), "=f"(a[7]), "=f"(b[6]), "=f"(b[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Lane k of four holds pairs (columns 8 j + 2 k, + 1) in v[2 j], v[2 j + 1];
+// afterwards columns 8 k .. 8 k + 7.
+__device__ __forceinline__ void quad_transpose(float* v) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+  for (int j = 0; j < 4; j += 2)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * j + e] : v[2 * j + 2 + e], 1);
+      if (odd) v[2 * j + e] = got;
+      else v[2 * j + 2 + e] = got;
+    }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float got = __shfl_xor_sync(0xffffffffu, high ? v[2 * j + e] : v[2 * j + 4 + e], 2);
+      if (high) v[2 * j + e] = got;
+      else v[2 * j + 4 + e] = got;
+    }
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -825,23 +874,49 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       } else if (active) {
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
-        char* dst = direct ? reinterpret_cast<char*>(p.out + orow * D)
-                           : reinterpret_cast<char*>(p.part_o + (int64_t)at * D);
+        const unsigned long long dst = direct ? reinterpret_cast<unsigned long long>(p.out + orow * D)
+                                              : reinterpret_cast<unsigned long long>(p.part_o + (int64_t)at * D);
+        if (rows > 32) {
+          // 16 rows and 32 columns at a time: four lanes share a row, and after
+          // the exchange each holds 8 columns in a row of it, so that a store
+          // covers whole lines (with a row per lane, one store of 32 bytes each,
+          // 16 MB of partial results took 6 us to drain behind the kernel).
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tmem_ld32f(o_t + c * 32, o);
-          tmem_wait_ld();
-          if (mine && direct) {
-            uint32_t pk[16];
+          for (int hf = 0; hf < 32 && wq * 32 + hf < rows; hf += 16) {
+            const int ra = hf + lane / 4, rb = ra + 8;
+            const unsigned long long da = __shfl_sync(0xffffffffu, dst, ra), db = __shfl_sync(0xffffffffu, dst, rb);
+            const float ia = __shfl_sync(0xffffffffu, inv_l, ra), ib = __shfl_sync(0xffffffffu, inv_l, rb);
+            const int at_col = 8 * (lane % 4);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float a[8], b[8];
+              tmem_ld_16x32(o_t + (static_cast<uint32_t>(hf) << 16) + c, a, b);
+              tmem_wait_ld();
+              quad_transpose(a);
+              quad_transpose(b);
+              store_row(da, c + at_col, a, ia, direct, wq * 32 + ra < rows);
+              store_row(db, c + at_col, b, ib, direct, wq * 32 + rb < rows);
+            }
+          }
+        } else {
+          // few rows: the shorter code (256 requests with 256 own keys 164 us,
+          // through the exchange 189)
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32f(o_t + c, o);
+            tmem_wait_ld();
+            if (mine && direct) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
+              for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)              // out may be aligned to 16 bytes only
-              reinterpret_cast<uint4*>(dst)[c * 4 + e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-          } else if (mine) {
+              for (int e = 0; e < 4; ++e)            // out may be aligned to 16 bytes only
+                reinterpret_cast<uint4*>(dst + c * 2)[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            } else if (mine) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store_32(dst + (c * 4 + e) * 32, o + 8 * e);
+              for (int e = 0; e < 4; ++e) store_32(reinterpret_cast<void*>(dst + c * 4 + e * 32), o + 8 * e);
+            }
           }
         }
         if (mine) {
