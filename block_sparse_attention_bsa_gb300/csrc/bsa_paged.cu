@@ -101,8 +101,7 @@ struct PagedParams {
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
-  int32_t* cum;                   // workspace: [B + 1] tiles of own keys before request b
-  int32_t* rt_before;             // workspace, own_rt > 1: [B, own_rt + 1] a head's tiles before row tile rt
+  int2* seg_ctas;                 // workspace: first and last CTA of each segment that has tiles
   float* part_ml;                 // workspace: partial results' (max, sum) and rows,
   float* part_o;                  // those of the prefix first,
   int own_first;                  // from here on those of own keys
@@ -147,12 +146,11 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 
 // The row of tiles is cut by weight: a prefix tile counts pre_w units, a tile
 // of own keys own_w.  The CTAs that get some (every one of them at least one
-// tile: its units are no fewer than a tile's), the first tile of CTA c of n,
-// and the CTA of tile t.
+// tile: its units are no fewer than a tile's), and the first tile of CTA c of n.
 struct Cut {
   int pre, pre_w, own_w;          // prefix tiles, weights
   int n, q, r;                    // CTAs, units of all tiles = q n + r
-  float inv_n, scale;             // 1 / n, n / units
+  float inv_n;                    // 1 / n
   __device__ __forceinline__ Cut(const PagedParams& p, int own) {
     pre = p.pre_tiles * p.pre_rt * p.Hkv;
     pre_w = p.pre_w;
@@ -162,7 +160,6 @@ struct Cut {
     q = n > 0 ? units / n : 0;
     r = units - q * n;
     inv_n = 1.f / (float)max(n, 1);
-    scale = (float)n / (float)max(units, 1);
   }
   // floor(c units / n); the small quotient is exact in fp32 (c r < 2^20)
   __device__ __forceinline__ int begin_unit(int c) const { return c * q + (int)(((float)(c * r) + 0.5f) * inv_n); }
@@ -170,15 +167,6 @@ struct Cut {
   __device__ __forceinline__ int begin(int c) const {
     const int u = begin_unit(c), pre_units = pre * pre_w;
     return u < pre_units ? (u + pre_w - 1) / pre_w : pre + (u - pre_units + own_w - 1) / own_w;
-  }
-  __device__ __forceinline__ int cta_of(int t) const {
-    const int u = t < pre ? t * pre_w : pre * pre_w + (t - pre) * own_w;
-    int c = min((int)((float)u * scale), n - 1);     // off by two at most
-#pragma unroll 1
-    while (c + 1 < n && begin_unit(c + 1) <= u) ++c;
-#pragma unroll 1
-    while (begin_unit(c) > u) --c;
-    return c;
   }
 };
 
@@ -383,7 +371,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const int incl = warp_inclusive_sum(mine);
     if (lane == 31) block_sum[blk] = incl;
     if (cta == 0 && b < p.B) {
-      p.cum[b] = incl - mine;           // the join finds each request's tiles here (block sums are added below)
       if (p.max_pages > 0) {
         const int kv = __ldg(p.kv_lens + b);
         if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
@@ -406,26 +393,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  if (cta == 0) {
-#pragma unroll 1
-    for (int b = threadIdx.x; b < p.B; b += kPagedThreads) p.cum[b] += block_sum[b / 32];
-    if (p.own_rt > 1) {
-#pragma unroll 1
-      for (int b = warp; b < p.B; b += kPagedThreads / 32) {
-        const int kv = own_keys(p, b), n = new_tokens(p, b);
-        int before = 0;
-#pragma unroll 1
-        for (int rt0 = 0; rt0 <= p.own_rt; rt0 += 32) {
-          const int rt = rt0 + lane;
-          const int m = rt < p.own_rt ? own_tiles(p, kv, n, rt) : 0;
-          const int incl = warp_inclusive_sum(m) + before;
-          if (rt <= p.own_rt) p.rt_before[b * (p.own_rt + 1) + rt] = incl - m;
-          before = __shfl_sync(0xffffffffu, incl, 31);
-        }
-      }
-    }
-    if (threadIdx.x == 0) p.cum[p.B] = *total_slot;
-  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int begin = 0, end = 0;
   {
@@ -693,6 +660,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         s.pad = 0;
         if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
         if (lane == 0) {
+          int2* who = p.seg_ctas + (s.b < 0 ? 0 : p.pre_rt * p.Hkv) + s.slot - cta;     // the join looks here
+          if (t == t0) who->x = cta;
+          if (t1 <= end) who->y = cta;
           segs[slot] = s;
           mbar_arrive(seg_full + 8 * slot);
         }
@@ -965,37 +935,29 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
   const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Cut cut(p, p.cum[p.B]);
-  const int pre = cut.pre;
   // Partial results: from each CTA of a segment one, or two of a segment of up
   // to 128 rows (one of each group).
   int pre_n = 0, own_n = 0, pre_at = 0, own_at = 0, pre_step = 0, own_step = 0;
   bool direct = false;
   if (real && i < n) {
-    const int row = i * p.G + g;
-    if (pre > 0) {
-      const int flat = b * p.TG + row, rt = flat / kRowTile, in = flat % kRowTile, seg = hk * p.pre_rt + rt;
-      const int c0 = cut.cta_of(seg * p.pre_tiles);
-      const int two = p.B * p.TG - rt * kRowTile <= kHalf;
-      pre_n = (cut.cta_of(seg * p.pre_tiles + p.pre_tiles - 1) - c0 + 1) << two;
-      pre_at = ((seg + c0) * 2 + in / kHalf) * p.pre_slot_rows + in % kHalf;
+    const int row = i * p.G + g, flat = b * p.TG + row;
+    const int pre_seg = hk * p.pre_rt + flat / kRowTile;
+    const int rt = row / kRowTile, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
+    const int mine = own_tiles(p, kv, n, rt);
+    int2 pc = make_int2(0, 0), oc = make_int2(0, 0);
+    if (p.pre_tiles > 0) pc = p.seg_ctas[pre_seg];
+    if (mine > 0) oc = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
+    if (p.pre_tiles > 0) {
+      const int two = p.B * p.TG - (flat - flat % kRowTile) <= kHalf;
+      pre_n = (pc.y - pc.x + 1) << two;
+      pre_at = ((pre_seg + pc.x) * 2 + flat % kRowTile / kHalf) * p.pre_slot_rows + flat % kHalf;
       pre_step = (2 - two) * p.pre_slot_rows;
     }
-    const int rt = row / kRowTile, in = row % kRowTile;
-    const int mine = own_tiles(p, kv, n, rt);
     if (mine > 0) {
-      int t0 = pre + p.cum[b];
-      if (p.own_rt == 1) {
-        t0 += hk * mine;
-      } else {
-        const int32_t* before = p.rt_before + b * (p.own_rt + 1);
-        t0 += hk * before[p.own_rt] + before[rt];
-      }
-      const int c0 = cut.cta_of(t0), c1 = cut.cta_of(t0 + mine - 1);
       const int two = n * p.G - rt * kRowTile <= kHalf;
-      direct = pre == 0 && c0 == c1 && (!two || mine == 1);      // written by the first kernel
-      own_n = (c1 - c0 + 1) << two;
-      own_at = p.own_first + (((b * p.Hkv + hk) * p.own_rt + rt + c0) * 2 + in / kHalf) * p.own_slot_rows + in % kHalf;
+      direct = p.pre_tiles == 0 && oc.x == oc.y && (!two || mine == 1);      // written by the first kernel
+      own_n = (oc.y - oc.x + 1) << two;
+      own_at = p.own_first + ((own_seg + oc.x) * 2 + row % kRowTile / kHalf) * p.own_slot_rows + row % kHalf;
       own_step = (2 - two) * p.own_slot_rows;
     }
   }
@@ -1089,7 +1051,7 @@ std::string s(int64_t v) { return std::to_string(v); }
 // Where the partial results lie in the workspace.
 struct PagedPlan {
   int TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
-  size_t own_first, cum, rt_before, part_ml, part_o, bytes;
+  size_t own_first, part_ml, part_o, bytes;
 };
 
 PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
@@ -1105,9 +1067,7 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * 2 * w.own_slot_rows;
   const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
   w.own_first = pre;
-  w.cum = 0;
-  w.rt_before = al((size_t)(B + 1) * 4);
-  w.part_ml = w.rt_before + (w.own_rt > 1 ? al((size_t)B * (w.own_rt + 1) * 4) : 0);
+  w.part_ml = al((size_t)Hkv * (w.pre_rt + B * w.own_rt) * 8);      // behind the segments' CTAs
   w.part_o = w.part_ml + al((pre + own) * 8);
   w.bytes = w.part_o + al((pre + own) * d * 4);
   return w;
@@ -1290,8 +1250,7 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
   char* ws = static_cast<char*>(workspace);
-  p.cum = reinterpret_cast<int32_t*>(ws + plan.cum);
-  p.rt_before = reinterpret_cast<int32_t*>(ws + plan.rt_before);
+  p.seg_ctas = reinterpret_cast<int2*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
   p.own_first = (int)plan.own_first;
