@@ -393,7 +393,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int begin = 0, end = 0;
   {
     const Cut cut(p, *total_slot);
