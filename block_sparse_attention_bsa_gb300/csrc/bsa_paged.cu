@@ -16,6 +16,8 @@
 //    any 256 rows (b, i, g) of the whole batch under one KV head, so that the
 //    prefix is read once for all; for a request's own keys the rows (i, g) of
 //    that request under one KV head.  A GQA group's heads are rows of one tile.
+//    Where the requests' own rows fill their tiles, sharing saves nothing: the
+//    prefix is folded into the own segments then, as their first key tiles.
 //  * All segments' 128-key tiles are put in one row and cut into equal pieces,
 //    one for each CTA, whatever the lengths are (they are read from the device,
 //    so a captured graph follows them).  A cut segment leaves one partial
@@ -92,7 +94,8 @@ struct PagedParams {
   int TG;                         // rows of a request under one KV head
   int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
-  int pre_tiles;                  // key tiles of the prefix
+  int pre_tiles;                  // key tiles of the prefix as segments of its own
+  int fold;                       // key tiles of the prefix at the head of each own segment (one of the two is 0)
   int pre_slot_rows, own_slot_rows;   // rows of one of a slot's two partial results
   int ctas, pre_w, own_w;
   const int32_t* page_table; int64_t table_stride;
@@ -119,12 +122,12 @@ __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
 __device__ __forceinline__ int seen_keys(const PagedParams& p, int kv, int n, int i) {
   return p.causal ? max(kv - n + i + 1, 0) : kv;
 }
-// Key tiles of row tile rt of such a request.
+// Key tiles of row tile rt of such a request (behind those of a folded prefix).
 __device__ __forceinline__ int own_tiles(const PagedParams& p, int kv, int n, int rt) {
   const int first = p.div_G.quot(rt * kRowTile);
   if (first >= n) return 0;
   const int last = min(n - 1, p.div_G.quot(rt * kRowTile + kRowTile - 1));
-  return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
+  return p.fold + (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
 }
 // Key tiles of a request under one KV head.
 __device__ __forceinline__ int request_tiles(const PagedParams& p, int kv, int n) {
@@ -175,6 +178,12 @@ struct Cut {
   }
 };
 
+// Keys of a segment's key tile, whose keys end at `end` (the last tile of a
+// folded prefix ends with the prefix).
+__device__ __forceinline__ int tile_keys(const PagedParams& p, int end, int tile) {
+  return min((tile == p.fold - 1 ? p.prefix_len : end) - tile * kTileKeys, kTileKeys);
+}
+
 // A segment's part that one CTA works on, as it stands in the segment ring.
 struct __align__(16) Segment {
   int b;               // request, -1: prefix
@@ -183,7 +192,7 @@ struct __align__(16) Segment {
   int tile0, tiles;    // first key tile and how many
   int slot;            // number of the partial result (segment + CTA)
   int whole;           // this CTA has all tiles of the segment
-  int keys;            // keys that stand in the source
+  int keys;            // where its keys end, counted in tiles of 128 from its first one
   int kv, n;           // of the request
   int pad;
 };
@@ -423,16 +432,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       const bool more = t < end;        // after the last segment there is one V left, or none
       Segment s;
       s.rows = s.tiles = 1;
-      s.tile0 = s.hk = s.keys = 0;
+      s.tile0 = s.hk = s.kv = 0;
       s.b = -1;
       if (more && !(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+      const int32_t* own_table = p.page_table + s.b * p.table_stride;
       // lane's page of key tile j (a page past the end reads zeros)
       auto page_of = [&](int j) {
-        const int key = j * kTileKeys + lane * box_rows;
+        const bool pre = s.b < 0 || j < p.fold;
+        const int key = (pre ? j : j - p.fold) * kTileKeys + lane * box_rows;
         int page = p.num_pages;
-        if (lane < per_tile && key < s.keys) {
-          page = __ldg(table + (key >> p.page_shift));
+        if (lane < per_tile && key < (pre ? p.prefix_len : s.kv)) {
+          page = __ldg((pre ? p.prefix_table : own_table) + (key >> p.page_shift));
           if (page < 0 || page >= p.num_pages) {
             atomicOr(&g_bsa_error, kErrPage);
             page = p.num_pages;
@@ -445,8 +455,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       int page = p.num_pages;
 #pragma unroll 1
       for (int j = -1; j < s.tiles && ok; ++j) {
-        const int next = j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
-        const int slot = ((s.tile0 + j) * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
+        const int next = more && j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
+        const int source = s.tile0 + j - (s.tile0 + j < p.fold ? 0 : p.fold);       // tile of its table
+        const int slot = (source * kTileKeys) & ((1 << p.page_shift) - 1) & ~(box_rows - 1);
 #pragma unroll 1
         for (int which = j < 0 ? 3 : 0; which < 3; ++which) {
           if (which == 0 ? !more : which == 1 ? !v_left : !more || !wide) continue;
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         v_first = j < 2;
         v_new = !wide || (j & 1) == 0;
         v_last = !wide || (j & 1) == 1;
-        v_keys = min(s.keys - (s.tile0 + (wide ? j >> 1 : j)) * kTileKeys, kTileKeys);
+        v_keys = tile_keys(p, s.keys, s.tile0 + (wide ? j >> 1 : j));
       }
       if (!ok || !more) break;
       qi += wide ? 2 : 1;
@@ -656,7 +667,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           s.row0 = s.b * p.TG + rt * kRowTile;
           s.rows = min(kRowTile, s.n * p.G - rt * kRowTile);
           s.slot = (s.b * p.Hkv + s.hk) * p.own_rt + rt + cta;
-          s.keys = s.kv;
+          s.keys = p.fold * kTileKeys + s.kv;
         }
         s.tile0 = t - t0;
         s.tiles = min(t1, end) - t;
@@ -712,8 +723,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const uint32_t s_t = tmem + lane_base + w * 128;
     const uint32_t o_t = tmem + lane_base + 256 + w * 128;
     uint32_t q = 0;                                // first job of the segment
-    // The segment's fields stay in the ring until the group is through with it:
-    // with S in 128 registers there is no room to hold them.
+    // The segment's fields stay in the ring until the group is through with it.
     SegmentReader reader;
     for (int t = begin; t < end && ok;) {
       if (!(ok = warp_wait(seg_full + 8 * reader.slot, reader.phase, abort_flag))) break;
@@ -721,19 +731,29 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       const bool wide = s.rows > kHalf;
       const int jobs = wide ? 2 * s.tiles : s.tiles;
       const int j0 = (int)((w ^ q) & 1u);          // this group's first job of the segment
+      if (j0 >= jobs) {                            // the other group has the segment's only tile
+        const bool direct = p.pre_tiles == 0 && s.whole;
+        if (!direct && r < s.rows)
+          reinterpret_cast<float2*>(p.part_ml)[(s.b < 0 ? 0 : p.own_first) +
+                                               (s.slot * 2 + (int)w) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r] =
+              make_float2(-INFINITY, 0.f);
+        q += jobs;
+        t += s.tiles;
+        reader.release(seg_empty);
+        continue;
+      }
       const int half = wide ? j0 : 0;              // and the rows that its jobs have
       const int rows = min(kHalf, s.rows - half * kHalf);
       const bool active = wq * 32 < rows;          // some row of this warp is real
       int limit = s.keys;                          // keys that the row sees (a row that is none: all)
       if (s.b >= 0 && r < rows) {
         const int rem = s.row0 + half * kHalf + r - s.b * p.TG;
-        limit = min(seen_keys(p, s.kv, s.n, p.div_G.quot(rem)), s.kv);
+        limit = p.fold * kTileKeys + min(seen_keys(p, s.kv, s.n, p.div_G.quot(rem)), s.kv);
       }
       float m_ref = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int j = j0; j < jobs; j += 2) {
         const int tile = wide ? j >> 1 : j;
-        const int key0 = (s.tile0 + tile) * kTileKeys;
         ok = warp_wait(s_full + 8 * w, ((q + j) >> 1) & 1u, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -741,7 +761,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           // S is read twice, 64 columns at a time: held whole in registers the
           // code is three times as long, and the roles' loops no longer fit the
           // instruction cache together (32 at a time measured 3 % slower).
-          const int valid = limit - key0;
+          const int valid = tile_keys(p, limit, s.tile0 + tile);
           // columns below `least` are seen by all rows of the warp, those from
           // `most` on by none
           const int least = __reduce_min_sync(0xffffffffu, valid), most = __reduce_max_sync(0xffffffffu, valid);
@@ -828,12 +848,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         if (lane == 0) mbar_arrive(p_full + 8 * w);
       }
       if (!ok) break;
-      const int last_j = jobs - 1 - (int)((jobs - 1 - j0) & 1);     // this group's last job (below j0: none)
-      if (last_j >= j0) {
-        ok = warp_wait(pv_done + 8 * w, ((q + last_j) >> 1) & 1u, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-      }
+      const int last_j = jobs - 1 - ((jobs - 1 - j0) & 1);     // this group's last job
+      ok = warp_wait(pv_done + 8 * w, ((q + last_j) >> 1) & 1u, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
       // a segment of more rows, or of one tile, that no other CTA works on and
       // no prefix stands beside: the result; else a partial one
       const bool direct = p.pre_tiles == 0 && s.whole && (wide || s.tiles == 1);
@@ -843,9 +861,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       const int at = (s.b < 0 ? 0 : p.own_first) +
                      (s.slot * 2 + (wide ? half : (int)w)) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
       float2* ml = reinterpret_cast<float2*>(p.part_ml) + at;
-      if (last_j < j0) {
-        if (mine && !direct) *ml = make_float2(-INFINITY, 0.f);      // the other group had the segment's only tile
-      } else if (active) {
+      if (active) {
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
         const unsigned long long dst = direct ? reinterpret_cast<unsigned long long>(p.out + orow * D)
@@ -901,11 +917,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
                 l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       }
-      if (last_j >= j0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty + 8 * w);
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty + 8 * w);
       q += jobs;
       t += s.tiles;
       reader.release(seg_empty);
@@ -1055,6 +1069,7 @@ std::string s(int64_t v) { return std::to_string(v); }
 // Where the partial results lie in the workspace.
 struct PagedPlan {
   int TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
+  bool fold;
   size_t own_first, part_ml, part_o, bytes;
 };
 
@@ -1063,6 +1078,10 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   const int64_t G = Hq / Hkv;
   w.TG = (int)(T * G);
   w.own_rt = (int)cdiv64(w.TG, kRowTile);
+  // The prefix is folded into the own segments where that adds at most an
+  // eighth of jobs: rows of 128 per request against rows of 128 of the batch.
+  w.fold = prefix && 8 * B * cdiv64(w.TG, kHalf) <= 9 * cdiv64(B * w.TG, kHalf);
+  prefix = prefix && !w.fold;
   w.pre_rt = prefix ? (int)cdiv64(B * w.TG, kRowTile) : 0;
   w.own_slot_rows = w.TG < kHalf ? w.TG : kHalf;
   w.pre_slot_rows = (int)(B * w.TG < kHalf ? B * w.TG : kHalf);
@@ -1212,7 +1231,7 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   if (q_extent >= (int64_t)1 << 35)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": q reaches over " + s(q_extent) + " elements (2^35 at most)");
-  const int64_t most_tiles = qv.B * a.k.H * row_tiles * cdiv64(max_pages * a.k.S, kTileKeys) +
+  const int64_t most_tiles = qv.B * a.k.H * row_tiles * (cdiv64(max_pages * a.k.S, kTileKeys) + cdiv64(prefix_len, kTileKeys)) +
                              a.k.H * cdiv64(flat_rows, kRowTile) * cdiv64(prefix_len, kTileKeys);
   if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.H > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
@@ -1237,7 +1256,8 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.num_pages = (int)a.k.B; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
   p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
   p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
-  p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
+  p.pre_tiles = plan.fold ? 0 : (int)cdiv64(prefix_len, kTileKeys);
+  p.fold = plan.fold ? (int)cdiv64(prefix_len, kTileKeys) : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = sms;
   // A wide prefix tile (two jobs of 0.9 us on the tensor cores) against a tile
@@ -1246,7 +1266,7 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   // 64 requests, 8k prefix, 512 own keys 57 / 52 / 49 / 46; 64, 4k, 1,024
   // 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188; 256, 32k, ragged up
   // to 512 187 / 177 / 180 / 205.
-  const bool wide_pre = flat_rows > kHalf && qv.S * G <= kHalf;
+  const bool wide_pre = flat_rows > kHalf && qv.S * G <= kHalf && !plan.fold;
   p.pre_w = wide_pre ? 5 : 1;
   p.own_w = wide_pre ? 3 : 1;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;

@@ -232,6 +232,9 @@ ATTEND_CASES = [
     ([50, 300], 1, None, 40, 256, 1, 64, 16, True, "heads"),          # one token fills two jobs' rows
     ([200, 70, 66], 65, [65, 30, 64], 0, 2, 1, 128, 32, True, "slots"),   # rows of one request in two jobs, of another in one
     ([33], 1, None, 5, 256, 256, 64, 16, True, "slots"),
+    ([300], 1, None, 1000, 4, 2, 64, 64, True, "slots"),              # one request: prefix and own keys in one segment
+    ([0], 3, None, 129, 4, 2, 128, 16, True, "heads"),
+    ([2], 9, None, 128, 4, 2, 64, 16, True, "pairs"),
 ]
 
 
@@ -359,6 +362,8 @@ def test_attention_over_many_segments_matches_64_bits(B, prefix, low, high, Hq, 
     (1100, [1100, 0, 257], [1300, 40, 257], 0, 6, 2, 64, 16, True),   # no prefix: whole segments are written at once
     (600, [600, 431], [900, 431], 129, 3, 3, 128, 256, False),
     (8200, [8200], [8200], 0, 1, 1, 64, 128, True),                   # 33 row tiles
+    (700, [700, 700, 333], [700, 1000, 333], 128, 2, 1, 64, 32, True),    # a prefix of one whole tile at the head of each
+    (512, [512, 0, 100, 512], [512, 7, 100, 600], 1000, 8, 2, 128, 16, True),
 ])
 def test_attention_of_long_chunks_matches_64_bits(T, new, kv, prefix, Hq, Hkv, d, page, causal):
     g = torch.Generator(device=DEV).manual_seed(T)
