@@ -1124,8 +1124,14 @@ bsa_status encode_cache(CUtensorMap* m, const bsa_tensor& t, const char* fn, con
   cuuint64_t strides[3] = {bytes(t.stride_s), bytes(t.stride_h), bytes(t.stride_b)};
   cuuint32_t box[4] = {64u, (cuuint32_t)(t.S < kTileKeys ? t.S : kTileKeys), 1u, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  // What a tile reads in a row: a slot's D values, or all of them where slots
+  // follow one another.  Fetching 256 bytes for a lone 128 would bring another
+  // head's keys, which are gone from L2 when their turn comes (16 requests of
+  // 32,768 keys, 8 heads of 64: 216 us, with 256 bytes 265).
+  const CUtensorMapL2promotion promotion =
+      t.D == 64 && t.stride_s != t.D ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.ptr), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return set_error(BSA_ERR_CUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed for " + name + " (CUresult " +
