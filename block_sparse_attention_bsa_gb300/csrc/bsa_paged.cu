@@ -97,7 +97,7 @@ struct PagedParams {
   int pre_tiles;                  // key tiles of the prefix as segments of its own
   int fold;                       // key tiles of the prefix at the head of each own segment (one of the two is 0)
   int pre_slot_rows, own_slot_rows;   // rows of one of a slot's two partial results
-  int ctas, pre_w, own_w;
+  int ctas, pre_w, pre_over, own_w;    // weights: see where they are set
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
@@ -158,13 +158,15 @@ struct Cut {
     pre = p.pre_tiles * p.pre_rt * p.Hkv;
     pre_w = p.pre_w;
     own_w = p.own_w;
+    // the way in and out of the prefix's segments, as far as a block's share is
+    // more than a tile (a tile that weighs more would leave blocks without one)
+    pre_w += min(p.pre_over, max((pre * pre_w + own * own_w) / p.ctas - pre_w, 0));
     const int units = pre * pre_w + own * own_w;
+    n = min(p.ctas, units / max(pre > 0 ? pre_w : 0, own > 0 ? own_w : 1));
     // Two tiles each where some CTA has two anyway, or where a tile leaves 128 KB
     // of partial results (33 tiles of 8 heads 13.0 -> 12.3 us, 16 prefix tiles of
     // 8 heads for 256 rows 21.4 -> 19.1 us).
-    const int most = units / max(pre > 0 ? pre_w : 0, own > 0 ? own_w : 1);
-    const bool two = most > p.ctas || (pre > 0 && p.B * p.TG > kHalf);
-    n = min(p.ctas, two ? max(most / 2, min(most, 1)) : most);
+    if (pre + own > p.ctas || (pre > 0 && p.B * p.TG > kHalf)) n = min(n, max((pre + own) / 2, min(n, 1)));
     q = n > 0 ? units / n : 0;
     r = units - q * n;
     inv_n = 1.f / (float)max(n, 1);
@@ -1266,15 +1268,23 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   p.fold = plan.fold ? (int)cdiv64(prefix_len, kTileKeys) : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = sms;
-  // A wide prefix tile (two jobs of 0.9 us on the tensor cores) against a tile
-  // of own keys for a few rows (1.5 us at its share of the memory rate, less
-  // while others compute).  us at prefix : own = 1:1 / 4:3 / 5:3 / 2:1 --
-  // 64 requests, 8k prefix, 512 own keys 57 / 52 / 49 / 46; 64, 4k, 1,024
-  // 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188; 256, 32k, ragged up
-  // to 512 187 / 177 / 180 / 205.
-  const bool wide_pre = flat_rows > kHalf && qv.S * G <= kHalf && !plan.fold;
-  p.pre_w = wide_pre ? 5 : 1;
-  p.own_w = wide_pre ? 3 : 1;
+  // Weights of about an eighth of a microsecond: a wide prefix tile (two jobs of
+  // 0.9 us on the tensor cores, more while others fetch) against a tile of own
+  // keys for a few rows (1.5 us at its share of the memory rate).  us at prefix :
+  // own = 1:1 / 4:3 / 5:3 / 2:1 -- 64 requests, 8k prefix, 512 own keys 57 / 52 /
+  // 49 / 46; 64, 4k, 1,024 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188;
+  // 256, 32k, ragged up to 512 187 / 177 / 180 / 205.  The way in and out of the
+  // prefix's segment (Q rows, results: 7 us where it is wide) is spread over its
+  // tiles: 61 requests with 28 shared and 775 own keys 70 -> 47 us, their prefix
+  // being 8 segments of one tile that one block got; nothing from 8k on.
+  p.pre_w = p.own_w = 1;
+  p.pre_over = 0;
+  if (p.pre_tiles > 0 && most_tiles < INT32_MAX / 80) {
+    const bool wide_pre = flat_rows > kHalf, wide_own = qv.S * G > kHalf;
+    p.pre_w = wide_pre ? 20 : 12;
+    p.pre_over = (wide_pre ? 56 : 24) / p.pre_tiles;
+    p.own_w = wide_own ? 20 : 12;
+  }
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
