@@ -9,7 +9,10 @@
 // What bounds it: for one token per request, reading K and V once (each 64 KB
 // of a 128-key tile of K and V at head dim 128 takes an SM 1.5 us at its share
 // of the memory rate, while its two products and its softmax take 0.7 us);
-// with hundreds of rows on one prefix, the exponentials (16 a clock and SM).
+// with hundreds of rows on one prefix, the chain S -> softmax -> P V (0.87 us a
+// job of 128 rows and 128 keys with two groups in turn, of which the tensor
+// cores are busy 0.53 us and the exponential unit 0.27 us); with a few short
+// requests, the way from the launch to the join (10 us, one tile included).
 //
 // Layout of the work:
 //  * A segment is up to 256 query rows that read the same keys: for the prefix
