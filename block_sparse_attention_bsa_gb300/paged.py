@@ -114,12 +114,15 @@ def _extent(t: torch.Tensor):
 
 def _check_overlap(name: str, out: torch.Tensor, inputs, in_place) -> None:
     """Refuses an output that shares memory with an input, but for ``in_place``
-    itself when it is contiguous and starts where the output does."""
+    itself when it is contiguous, starts where the output does and is one input
+    only (given as q and as k it would be read and overwritten at once)."""
     lo, hi = _extent(out)
     for t in inputs:
         a, z = _extent(t)
-        if lo < z and a < hi and not (t is in_place and a == lo and t.is_contiguous()):
-            raise ValueError(f"{name} overlaps an input (in place takes the whole contiguous input)")
+        if lo < z and a < hi:
+            if not (t is in_place and a == lo and t.is_contiguous()):
+                raise ValueError(f"{name} overlaps an input (in place takes the whole contiguous input)")
+            in_place = None
 
 
 @contextlib.contextmanager

@@ -201,6 +201,15 @@ def test_overlap_check():
         paged._check_overlap("out", flat[:256].view(1, 1, 4, 64), (wide[:, :, ::2],), wide)
 
 
+def test_overlap_check_of_one_tensor_as_two_inputs():
+    x, y = (torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16) for _ in range(2))
+    with pytest.raises(ValueError, match="overlaps"):
+        paged._check_overlap("q_out", x, (x, x), x)
+    with pytest.raises(ValueError, match="overlaps"):
+        paged._check_overlap("k_out", x, (x, x, y), x)
+    paged._check_overlap("k_out", y, (x, x), x)
+
+
 def test_axis_frequencies():
     inv, axes = bsa.bsa_axis_frequencies((2, 3, 3), 100.0, device="cpu")
     assert axes.tolist() == [0, 0, 1, 1, 1, 2, 2, 2]
