@@ -1257,6 +1257,10 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
                                             " bytes is smaller than the " + s(need) + " bytes needed");
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is not 256-byte aligned");
+  const bsa_tensor ov = contiguous_like(qv, out);
+  if ((st = check_apart(fn, "q", qv, "out", ov)) != BSA_OK) return st;
+  if ((st = check_apart(fn, "k_cache", a.k, "out", ov)) != BSA_OK) return st;
+  if ((st = check_apart(fn, "v_cache", a.v, "out", ov)) != BSA_OK) return st;
   PagedParams p{};
   if ((st = encode_cache(&p.tk, a.k, fn, "k_cache")) != BSA_OK) return st;
   if ((st = encode_cache(&p.tv, a.v, fn, "v_cache")) != BSA_OK) return st;

@@ -21,6 +21,14 @@ constexpr int kMaxPagedBatch = 4096;
 // length 1 are replaced by 0; `cache`: strides of longer axes must be positive.
 bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, bool cache, bsa_tensor* view);
 
+// Refuses memory that a call writes while it reads or writes it elsewhere:
+// from the first to behind the last byte of each view.  `in_place`: the same
+// memory is fine where x, contiguous, starts where y does.
+bsa_status check_apart(const char* fn, const char* x_name, const bsa_tensor& x, const char* y_name,
+                       const bsa_tensor& y, bool in_place = false);
+// The view of a contiguous output of x's shape.
+bsa_tensor contiguous_like(const bsa_tensor& x, void* ptr);
+
 // The paged cache and its tables, checked.
 struct PagedArgs {
   bsa_tensor k, v;

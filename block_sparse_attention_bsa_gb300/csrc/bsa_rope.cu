@@ -334,6 +334,27 @@ bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, boo
   return BSA_OK;
 }
 
+bsa_tensor contiguous_like(const bsa_tensor& x, void* ptr) {
+  bsa_tensor y = x;
+  y.ptr = ptr;
+  y.stride_h = x.D; y.stride_s = x.H * x.D; y.stride_b = x.S * y.stride_s;
+  return y;
+}
+
+bsa_status check_apart(const char* fn, const char* x_name, const bsa_tensor& x, const char* y_name,
+                       const bsa_tensor& y, bool in_place) {
+  auto end = [](const bsa_tensor& t) {
+    return reinterpret_cast<uintptr_t>(t.ptr) +
+           2 * (uintptr_t)((t.B - 1) * t.stride_b + (t.S - 1) * t.stride_s + (t.H - 1) * t.stride_h + t.D);
+  };
+  const uintptr_t xb = reinterpret_cast<uintptr_t>(x.ptr), yb = reinterpret_cast<uintptr_t>(y.ptr);
+  if (xb >= end(y) || yb >= end(x)) return BSA_OK;
+  if (in_place && xb == yb && (x.H == 1 || x.stride_h == x.D) && (x.S == 1 || x.stride_s == x.H * x.D) &&
+      (x.B == 1 || x.stride_b == x.S * x.H * x.D))
+    return BSA_OK;
+  return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + y_name + " shares memory with " + x_name);
+}
+
 bsa_status check_paged(const char* fn, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
                        const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
                        const int32_t* new_lens, int64_t B, PagedArgs* a) {
@@ -387,6 +408,15 @@ bsa_status bsap_rope_axes(const bsa_tensor* q, const bsa_tensor* k, const bsap_p
     if ((st = check_positions(fn, "pos_k", pos_k)) != BSA_OK) return st;
     if ((st = check_out(fn, "k_out", k_out)) != BSA_OK) return st;
   }
+  const bsa_tensor qo = contiguous_like(qv, q_out);
+  if ((st = check_apart(fn, "q", qv, "q_out", qo, true)) != BSA_OK) return st;
+  if (k) {
+    const bsa_tensor ko = contiguous_like(kv, k_out);
+    if ((st = check_apart(fn, "k", kv, "k_out", ko, true)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "k", kv, "q_out", qo)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "q", qv, "k_out", ko)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "q_out", qo, "k_out", ko)) != BSA_OK) return st;
+  }
   RotParams p{};
   p.inv_freq = rope->inv_freq; p.axes = rope->axes; p.pairs = rope->pairs; p.n_axes = rope->n_axes;
   p.back = backward ? 1 : 0;
@@ -431,6 +461,21 @@ bsa_status bsap_cache_append(const bsa_tensor* k, const bsa_tensor* v, const bsa
       return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": q's batch, length or head dim differs from k's");
     if ((st = check_out(fn, "q_out", q_out)) != BSA_OK) return st;
   }
+  const bsa_tensor* caches[2] = {&a.k, &a.v};
+  if (a.k.ptr == a.v.ptr) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": v_cache shares memory with k_cache");
+  const bsa_tensor qo = q ? contiguous_like(qv, q_out) : bsa_tensor{};
+  if (q) {
+    if ((st = check_apart(fn, "q", qv, "q_out", qo, true)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "k", kv, "q_out", qo)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "v", vv, "q_out", qo)) != BSA_OK) return st;
+  }
+  for (const bsa_tensor* c : caches) {
+    const char* name = c == &a.k ? "k_cache" : "v_cache";
+    if ((st = check_apart(fn, "k", kv, name, *c)) != BSA_OK) return st;
+    if ((st = check_apart(fn, "v", vv, name, *c)) != BSA_OK) return st;
+    if (q && (st = check_apart(fn, "q", qv, name, *c)) != BSA_OK) return st;
+    if (q && (st = check_apart(fn, "q_out", qo, name, *c)) != BSA_OK) return st;
+  }
   RotParams p{};
   if (rope) {
     p.inv_freq = rope->inv_freq; p.axes = rope->axes; p.pairs = rope->pairs; p.n_axes = rope->n_axes;
@@ -442,7 +487,6 @@ bsa_status bsap_cache_append(const bsa_tensor* k, const bsa_tensor* v, const bsa
   p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.job[0] = make_job(kv, pos, rope != nullptr);
   p.job[1] = make_job(vv, nullptr, false);
-  const bsa_tensor* caches[2] = {&a.k, &a.v};
   for (int i = 0; i < 2; ++i) {
     p.job[i].paged = 1;
     p.job[i].y = static_cast<__nv_bfloat16*>(const_cast<void*>(caches[i]->ptr));

@@ -269,7 +269,8 @@ def bsa_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_
     request b's pages in order (entries behind its length are not read).
     With ``positions`` (int32 ``[B, T, A]``), ``inv_freq`` and ``axes`` k is
     rotated as by ``bsa_rope_axes``, and so is ``q`` when given (all T rows);
-    without them k is copied.  Returns the rotated q, or None.
+    without them k is copied.  New tokens may not lie inside a cache, nor K and
+    V share slots.  Returns the rotated q, or None.
     """
     dev = _gpu(k, "k")
     kd = _tensor(k, "k", dev)

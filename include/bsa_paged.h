@@ -90,7 +90,10 @@ BSA_API bsa_status bsap_rope_axes(const bsa_tensor* q, const bsa_tensor* k, cons
  *   Hq, D] into q_out (contiguous, all T rows, also behind new_lens; in place
  *   when q is contiguous); q may be NULL, and rope NULL copies k (q must then
  *   be NULL).  Two tokens with the same page and slot are the caller's
- *   mistake: which of them stays, K and V each, is unspecified. */
+ *   mistake: which of them stays, K and V each, is unspecified.  k, v, q and
+ *   q_out may not lie between a cache's first and last byte, q_out not overlap
+ *   k or v, and k_cache and v_cache not share slots (refused where they are the
+ *   same pointer). */
 BSA_API bsa_status bsap_cache_append(const bsa_tensor* k, const bsa_tensor* v, const bsa_tensor* k_cache,
                                      const bsa_tensor* v_cache, const int32_t* page_table, int64_t table_stride,
                                      int32_t max_pages, const int32_t* kv_lens, const int32_t* new_lens,
@@ -113,7 +116,7 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  * lse_i = ln sum_j exp(z_j).  Rows i >= n and rows without a key: out 0, lse
  * -inf.  Slots behind a request's keys are never read into a result, whatever
  * they hold; the values of real keys have to be finite.
- * out: bf16 [B, T, Hq, D] contiguous; lse: fp32 [B, Hq, T] contiguous or NULL.
+ * out: bf16 [B, T, Hq, D] contiguous, apart from q and the caches; lse: fp32 [B, Hq, T] contiguous or NULL.
  * softmax_scale <= 0 selects D^-1/2.  prefix_len 0: prefix_table may be NULL.
  * max_pages 0: no own keys (page_table and kv_lens may be NULL).
  * Results do not depend on scheduling (no atomics), but the split of the keys

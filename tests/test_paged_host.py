@@ -210,6 +210,55 @@ def test_overlap_check_of_one_tensor_as_two_inputs():
     paged._check_overlap("k_out", y, (x, x), x)
 
 
+# q 2 x 4 x 4 heads of 128 (8,192 bytes), k half of it; where the outputs lie
+@pytest.mark.parametrize("q,k,qo,ko,needle", [
+    (0, 1 << 16, 256, 1 << 17, "q_out shares memory with q"),
+    (0, 1 << 16, 8192 - 16, 1 << 17, "q_out shares memory with q"),
+    (0, 0, 0, 1 << 17, "q_out shares memory with k"),
+    (0, 0, 1 << 17, 0, "k_out shares memory with q"),
+    (0, 8192, 1 << 16, 8192 + 16, "k_out shares memory with k"),
+    (0, 1 << 16, 1 << 17, (1 << 17) + 8192 - 16, "k_out shares memory with q_out"),
+])
+def test_rotation_refuses_shared_memory(lib, q, k, qo, ko, needle):
+    st = lib.bsap_rope_axes(ref(T(ptr=FAKE + q)), ref(T(H=2, ptr=FAKE + k)), ref(P()), ref(P()), ref(R()), 0,
+                            FAKE + qo, FAKE + ko, None)
+    assert st == 1 and needle in err(lib)
+
+
+def test_rotation_in_place_takes_contiguous_inputs_only(lib):
+    st = lib.bsap_rope_axes(ref(T(ss=1024, sb=4096)), None, ref(P()), None, ref(R()), 0, FAKE, None, None)
+    assert st == 1 and "q_out shares memory with q" in err(lib)
+
+
+# caches of 8 pages of 16 slots, 2 heads of 128: 65,536 bytes
+@pytest.mark.parametrize("change,needle", [
+    (dict(vc=0), "v_cache shares memory with k_cache"),
+    (dict(k=256), "k_cache shares memory with k"),
+    (dict(v=(1 << 20) + 65536 - 16), "v_cache shares memory with v"),
+    (dict(q=65536 - 16), "k_cache shares memory with q"),
+    (dict(qo=1 << 20), "v_cache shares memory with q_out"),
+    (dict(qo=(2 << 20) + 16), "q_out shares memory with k"),
+    (dict(qo=3 << 20), "q_out shares memory with v"),
+    (dict(qo=(4 << 20) + 16), "q_out shares memory with q"),
+])
+def test_append_refuses_shared_memory(lib, change, needle):
+    at = dict(kc=0, vc=1 << 20, k=2 << 20, v=3 << 20, q=4 << 20, qo=5 << 20)
+    at.update(change)
+    at = {name: FAKE + x for name, x in at.items()}
+    st = lib.bsap_cache_append(ref(T(H=2, ptr=at["k"])), ref(T(H=2, ptr=at["v"])),
+                               ref(T(B=8, S=16, H=2, ptr=at["kc"])), ref(T(B=8, S=16, H=2, ptr=at["vc"])), FAKE, 4, 4,
+                               FAKE, None, ref(R()), ref(P()), ref(T(ptr=at["q"])), at["qo"], None)
+    assert st == 1 and needle in err(lib)
+
+
+@pytest.mark.parametrize("out,needle", [(4 << 20, "out shares memory with q"), (65536 - 16, "out shares memory with k_cache"),
+                                        ((1 << 20) + 256, "out shares memory with v_cache")])
+def test_attention_refuses_an_output_in_its_inputs(lib, out, needle):
+    st = lib.bsap_forward(ref(T(ptr=FAKE + (4 << 20))), ref(T(B=8, S=16, H=2)), ref(T(B=8, S=16, H=2, ptr=FAKE + (1 << 20))),
+                          FAKE, 4, 4, FAKE, None, None, 0, 1, 0.0, FAKE + out, None, FAKE, 1 << 40, None)
+    assert st == 1 and needle in err(lib)
+
+
 def test_axis_frequencies():
     inv, axes = bsa.bsa_axis_frequencies((2, 3, 3), 100.0, device="cpu")
     assert axes.tolist() == [0, 0, 1, 1, 1, 2, 2, 2]
