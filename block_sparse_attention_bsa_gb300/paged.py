@@ -331,6 +331,9 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
 
     Returns ``(out [B, T, Hq, d] bf16, lse [B, Hq, T] fp32 or None)``.
     """
+    prefix_len = int(prefix_len)
+    if not 0 <= prefix_len < 1 << 31:          # ctypes would take it modulo 2^32
+        raise ValueError(f"prefix_len {prefix_len} is out of range")
     dev = _gpu(q, "q")
     qd = _tensor(q, "q", dev)
     kc, vc = _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
@@ -338,7 +341,6 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     table, stride, n = _table(page_table, B, dev)
     lens = _ints(kv_lens, "kv_lens", dev, B)
     new = _ints(new_lens, "new_lens", dev, B)
-    prefix_len = int(prefix_len)
     shared = None
     if prefix_len > 0:
         if prefix_table is None:

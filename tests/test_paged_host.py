@@ -259,6 +259,13 @@ def test_attention_refuses_an_output_in_its_inputs(lib, out, needle):
     assert st == 1 and needle in err(lib)
 
 
+@pytest.mark.parametrize("prefix_len", [-1, 1 << 31, (1 << 32) + 5])
+def test_binding_refuses_prefix_lengths_that_do_not_fit(prefix_len):
+    x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="prefix_len"):
+        bsa.bsa_forward_paged(x, x, x, x, x, prefix_len=prefix_len)
+
+
 def test_axis_frequencies():
     inv, axes = bsa.bsa_axis_frequencies((2, 3, 3), 100.0, device="cpu")
     assert axes.tolist() == [0, 0, 1, 1, 1, 2, 2, 2]
