@@ -46,6 +46,7 @@
 //    dependence, so that it is resident when the first kernel ends).
 #include <cuda_bf16.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -1235,6 +1236,9 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": out is not 16-byte aligned");
   if (!std::isfinite(softmax_scale))
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": softmax_scale is not finite");
+  // times -inf and log2(e) on the device, where subnormal numbers may count as 0
+  if (softmax_scale > 0.f && (softmax_scale < FLT_MIN || softmax_scale > FLT_MAX / 2))
+    return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": softmax_scale is subnormal or above half the largest float");
   const int64_t G = qv.H / a.k.H;
   const int sms = num_sms();
   // rows, tiles and slot numbers are 32-bit on the device

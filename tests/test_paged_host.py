@@ -210,6 +210,13 @@ def test_overlap_check_of_one_tensor_as_two_inputs():
     paged._check_overlap("k_out", y, (x, x), x)
 
 
+@pytest.mark.parametrize("scale", [1e-40, 3e38, float("nan")])
+def test_attention_refuses_scales_out_of_range(lib, scale):
+    st = lib.bsap_forward(ref(T()), ref(CACHE), ref(CACHE), FAKE, 8, 8, FAKE, None, None, 0, 1, scale, FAKE, None, FAKE,
+                          1 << 40, None)
+    assert st == 1 and "softmax_scale" in err(lib)
+
+
 # q 2 x 4 x 4 heads of 128 (8,192 bytes), k half of it; where the outputs lie
 @pytest.mark.parametrize("q,k,qo,ko,needle", [
     (0, 1 << 16, 256, 1 << 17, "q_out shares memory with q"),
