@@ -538,7 +538,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             k_stage = stage;
             advance<kStages>(stage, phase);
           }
-          if (j <= (int)half && !(ok = warp_wait(q_full + 8 * qb, ((qi + half) >> 1) & 1u, abort_flag))) break;
+          if (j <= (int)half) {
+            if (!(ok = warp_wait(q_full + 8 * qb, ((qi + half) >> 1) & 1u, abort_flag))) break;
+            fence_async_shared();                  // Q rows come by ordinary copies
+          }
           tc_fence_after();
           const uint64_t as = qdesc0 + (uint64_t)((qb * C::kQBytes) >> 4);
           const uint64_t bs = kdesc0 + (uint64_t)((k_stage * C::kTileBytes) >> 4);
@@ -713,12 +716,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
                            : "memory");
           }
         }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        fence_async_shared();
-        mbar_arrive(q_full + 8 * qb);
+        // arrives when this lane's copies have landed; the warp goes on
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(q_full + 8 * qb) : "memory");
       }
       t += s.tiles;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");         // after an abort, too
     __syncwarp();
   } else if (warp >= 4) {
     // --------------------------------------------------- softmax + results ---
