@@ -28,11 +28,10 @@
 //    row, so segment + CTA numbers the partial results without gaps of meaning
 //    and without a table.
 //  * One CTA per SM: warp 2 goes through the CTA's segments, hands them to the
-//    others through a ring and loads their Q rows; warp 0 gathers K and V tiles page by page with
-//    TMA into a second ring, in the order the products use them (K_0, K_1,
-//    V_0, K_2, V_1 ..); warps 1 and 3 issue the MMAs, S = Q K^T and O += P V
-//    (one thread for both took 1.25 us a job of 16 MMAs); warps 4-7 and 8-11
-//    are two softmax groups, one row per
+//    others through a ring and loads their Q rows; warps 0 and 3 gather K and V
+//    tiles page by page with TMA into a second ring, in the order the products
+//    use them (K_0, K_1, V_0, K_2, V_1 ..); warp 1 issues the MMAs, S = Q K^T
+//    and O += P V; warps 4-7 and 8-11 are two softmax groups, one row per
 //    thread, that take the jobs in turn, each with an S and an O of its own in
 //    TMEM and P staying there.  A job is 128 rows on one key tile: a segment of
 //    more rows makes two jobs of each tile, which read the same K and V; in a
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   uint8_t* ring = smem + 2 * C::kQBytes;
   Segment* segs = reinterpret_cast<Segment*>(ring + kStages * C::kTileBytes);   // [kSegRing]
   // barriers, as shared-memory addresses 8 bytes apart
-  const uint32_t q_full = smem_u32(segs + kSegRing);   // [2] 64 loader threads
+  const uint32_t q_full = smem_u32(segs + kSegRing);   // [2] 32 loader threads
   const uint32_t q_empty = q_full + 16;                // [2] commit
   const uint32_t s_full = q_full + 32;                 // [2] commit
   const uint32_t p_full = q_full + 48;                 // [2] 4 softmax warps
@@ -357,7 +356,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 64);
+      mbar_init(q_full + 8 * i, 32);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 4);
@@ -423,13 +422,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------ TMA producer ---
-    // K of tile q, then V of tile q - 1, for every tile of the CTA's row.
+  if (warp == 0 || warp == 3) {
+    // ----------------------------------------------------- TMA producers ---
+    // K of tile q, then V of tile q - 1, for every tile of the CTA's row: warp 0
+    // fetches K and warp 3 V, each at its places in the ring.  (One warp for both
+    // was busy all the time where pages are small: looking up a tile's pages
+    // takes it 0.4 us, asking for 8 of them 0.5.  137 requests of 1,700 keys in
+    // pages of 32 124 -> 100 us, 103 x 30 in pages of 16 25.3 -> 22.6.)
     const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;   // pages per tile
     const int box_rows = kTileKeys / per_tile;
     const uint32_t ring_base = smem_u32(ring);
-    uint32_t stage = 0, phase = 0;
+    uint32_t stage = 0, phase = 0, issued = 0;     // whose last copy is this warp's
     int v_page = 0, v_slot = 0, v_hk = 0;          // the tile whose V is still to come,
     bool v_left = false;                           // if there is one
     SegmentReader reader;
@@ -467,7 +470,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
 #pragma unroll 1
         for (int which = j < 0 ? 3 : 0; which < 3; ++which) {
           if (which == 0 ? !more : which == 1 ? !v_left : !more || !wide) continue;
+          if ((which == 0) != (warp == 0)) {       // not awaited: it may be used up and gone by now
+            issued &= ~(1u << stage);
+            advance<kStages>(stage, phase);
+            continue;
+          }
           if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
+          issued |= 1u << stage;
           const bool old = which == 1;
           const int from = old ? v_page : page, at = old ? v_slot : slot, head = old ? v_hk : s.hk;
           if (elect_one()) mbar_arrive_expect_tx(full + 8 * stage, C::kTileBytes);
@@ -497,7 +506,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     if (lane == 0) {
 #pragma unroll 1
       for (int i = 0; i < kStages; ++i) {
-        mbar_drain(full + 8 * stage, phase ^ 1u);
+        if (issued >> stage & 1u) mbar_drain(full + 8 * stage, phase ^ 1u);
         advance<kStages>(stage, phase);
       }
     }
@@ -614,10 +623,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
       mbar_drain(mma_end, 0);
     }
     __syncwarp();
-  } else if (warp == 2 || warp == 3) {
+  } else if (warp == 2) {
     // Q rows of a segment into the next one or two Q buffers: each lane works
-    // out the address of one of 32 rows, then 32 / kVec rows are copied at a
-    // time; the two warps take every other 32 rows.
+    // out the address of one of 32 rows, then 32 / kVec rows are copied at a time.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
     const int c = lane % kVec;
@@ -628,12 +636,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
     int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
     uint32_t slot = 0, phase = 0;
-    SegmentReader reader;
     for (int t = begin; t < end && ok;) {
       Segment s;
-      if (warp == 3) {
-        if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
-      } else {
+      {
         int t0, t1;
         if (t < pre) {
           const int seg = t / p.pre_tiles;
@@ -701,11 +706,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         const uint32_t base = smem_u32(q_smem) + qb * C::kQBytes + (c / 8) * (kHalf * 128) + (lane / kVec) * 128;
         const int rows = min(kHalf, s.rows - r0);
 #pragma unroll 1
-        for (int r32 = (warp - 2) * 32; r32 < rows; r32 += 64) {
+        for (int r32 = 0; r32 < rows; r32 += 32) {
           const int row = s.row0 + r0 + min(r32 + lane, rows - 1);
           const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
           const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
-#pragma unroll 2
+#pragma unroll 8
           for (int x = 0; x < kVec && r32 + x * kRowsPer < rows; ++x) {
             const int in = x * kRowsPer + lane / kVec, r = r32 + in;
             const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, in) * 8;
