@@ -424,3 +424,26 @@ def test_append_rotates_queries_in_place():
                                inv_freq=inv, axes=axes)
     assert got is mine and torch.equal(mine, want)
     bsa.bsa_device_status()
+
+
+@pytest.mark.parametrize("prefix,Hq,Hkv,d,page", [(0, 8, 2, 128, 64), (0, 4, 4, 64, 16), (300, 8, 2, 128, 32)])
+def test_attention_of_single_tokens_beside_chunks(prefix, Hq, Hkv, d, page):
+    """Single tokens and chunks of up to 80 in turn: blocks go from segments of a
+    few rows to segments of several row tiles and back, with ends inside tiles."""
+    g = torch.Generator().manual_seed(prefix + page)
+    new = [(1, 80, 2, 33, 1, 1, 64, 17, 0, 40)[b % 10] for b in range(100)]
+    lens = [max(n, int(torch.randint(0, 400, (1,), generator=g))) for n in new]
+    pool = Pool(lens, prefix, Hkv, d, page, DEV, 40)
+    q = randn((100, 80, Hq, d), 41)
+    for b, n in enumerate(new):
+        q[b, n:] = float("nan")
+    new_t = torch.tensor(new, dtype=torch.int32, device=DEV)
+    out, lse = bsa.bsa_forward_paged(q.to(DEV), pool.gk, pool.gv, pool.gtable, pool.kv_lens, new_lens=new_t,
+                                     prefix_table=pool.gprefix, prefix_len=prefix)
+    bsa.bsa_device_status()
+    check_attention(out, lse, attend64(q, pool, new, True))
+    for _ in range(20):
+        again, lse2 = bsa.bsa_forward_paged(q.to(DEV), pool.gk, pool.gv, pool.gtable, pool.kv_lens, new_lens=new_t,
+                                            prefix_table=pool.gprefix, prefix_len=prefix)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+    bsa.bsa_device_status()
