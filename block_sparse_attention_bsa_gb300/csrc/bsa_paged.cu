@@ -116,10 +116,10 @@ struct PagedParams {
 // Request b's own keys and new tokens, clamped to what the tables hold.
 __device__ __forceinline__ int own_keys(const PagedParams& p, int b) {
   if (p.max_pages == 0) return 0;
-  return min(max(__ldg(p.kv_lens + b), 0), p.max_pages << p.page_shift);
+  return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
 }
 __device__ __forceinline__ int new_tokens(const PagedParams& p, int b) {
-  return p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.T) : p.T;
+  return p.new_lens ? min(max(p.new_lens[b], 0), p.T) : p.T;
 }
 // Own keys that row i of a request with kv keys and n new tokens sees.
 __device__ __forceinline__ int seen_keys(const PagedParams& p, int kv, int n, int i) {
@@ -381,6 +381,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // Launched when the blocks of the kernel before leave: up to here nothing is
+  // read or written that it uses (and nothing by the read-only path, whose loads
+  // may be taken from before this point).  2 us less a call in a row of them.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
 #pragma unroll 1
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     if (lane == 31) block_sum[blk] = incl;
     if (cta == 0 && b < p.B) {
       if (p.max_pages > 0) {
-        const int kv = __ldg(p.kv_lens + b);
+        const int kv = p.kv_lens[b];
         if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
       }
     }
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
         const int key = (pre ? j : j - p.fold) * kTileKeys + lane * box_rows;
         int page = p.num_pages;
         if (lane < per_tile && key < (pre ? p.prefix_len : s.kv)) {
-          page = __ldg((pre ? p.prefix_table : own_table) + (key >> p.page_shift));
+          page = (pre ? p.prefix_table : own_table)[key >> p.page_shift];
           if (page < 0 || page >= p.num_pages) {
             atomicOr(&g_bsa_error, kErrPage);
             page = p.num_pages;
@@ -1175,23 +1179,27 @@ template <int D>
 bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   bsa_status st = set_smem<D>();
   if (st != BSA_OK) return st;
-  paged_attention_kernel<D><<<p.ctas, kPagedThreads, PagedCfg<D>::kSmemBytes, stream>>>(p);
-  if ((st = cuda_check(cudaGetLastError(), "paged_attention_kernel launch")) != BSA_OK) return st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kPagedThreads);
+  cfg.dynamicSmemBytes = PagedCfg<D>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, paged_attention_kernel<D>, p), "paged_attention_kernel launch")) != BSA_OK)
+    return st;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   // Eight warps, one warp or eight lanes a row, by the number of rows (us of the
   // join: 32 rows of 40 partial results 6.4, with one warp 9; 2,048 rows of 2 to
   // 10 with one warp 7.7, four 11, eight lanes 13; 24,000 rows of 2 to 4 with
   // eight lanes 12, one warp 19; 8,192 rows 12 either way).
   const int lanes = rows < (int64_t)num_sms() * 4 ? 256 : rows < (int64_t)num_sms() * 40 ? 32 : 8;
-  cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(lanes == 256 ? 256 : 128);
   cfg.gridDim = dim3((unsigned)cdiv64(rows, cfg.blockDim.x / lanes));
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cuda_check(lanes == 256  ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 8>, p)
                     : lanes == 32 ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 32, 1>, p)
                                   : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, 8, 1>, p),

@@ -296,3 +296,66 @@ def test_binding_refusals_on_the_gpu():
         bsa.bsa_forward_paged(q[:, :, :3], *args)
     bsa.bsa_device_status()
     assert math.isfinite(float(bsa.bsa_forward_paged(q, *args)[0].float().sum()))
+
+
+def test_calls_right_behind_what_writes_their_inputs():
+    """Lengths, tables, positions and rows written by the kernel just before a
+    call, eager, captured, and behind a join of two streams: the bits of calls
+    with a synchronisation after every operation."""
+    B, Hq, Hkv, d, page, steps = 8, 8, 2, 128, 64, 40
+    g = torch.Generator(device=DEV).manual_seed(70)
+    kc0, vc0 = (torch.randn(100, page, Hkv, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    tables = [torch.randperm(100, generator=g, device=DEV)[:64].int().view(8, 8) for _ in range(3)]
+    rows = torch.randn(B, 1, Hq + 2 * Hkv, d, generator=g, device=DEV).to(BF)
+    inv, axes = bsa.bsa_axis_frequencies((16, 24, 24), device=DEV)
+    table, lens, pos = tables[0].clone(), torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(
+        B, 1, 3, dtype=torch.int32, device=DEV)
+    x, kc, vc = rows.clone(), kc0.clone(), vc0.clone()
+    side = torch.cuda.Stream()
+
+    def start():
+        lens.fill_(100), pos.zero_(), x.copy_(rows), kc.copy_(kc0), vc.copy_(vc0)
+
+    def step(i, between=lambda: None):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):                 # the rows come from another stream
+            x.mul_(1.0625 if i % 2 else 0.9375)
+        between()
+        table.copy_(tables[i % 3])
+        between()
+        pos.add_(3)
+        main.wait_stream(side)
+        lens.add_(1)
+        between()
+        q = bsa.bsa_cache_append(x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:], kc, vc, table, lens, q=x[:, :, :Hq],
+                                 positions=pos, inv_freq=inv, axes=axes)
+        between()
+        out, lse = bsa.bsa_forward_paged(q, kc, vc, table, lens)
+        between()
+        x[:, :, :Hq].add_(out)
+        between()
+        return out, lse
+
+    def same(a, b):
+        return all(torch.equal(s, t) for x, y in zip(a, b) for s, t in zip(x, y))
+
+    start()
+    want = [step(i, torch.cuda.synchronize) for i in range(steps)]
+    run = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(run):
+        for _ in range(5):
+            start()
+            got = [step(i) for i in range(steps)]
+            run.synchronize()
+            assert same(got, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=run):
+            start()
+            got = [step(i) for i in range(steps)]
+        for _ in range(5):
+            graph.replay()
+            run.synchronize()
+            assert same(got, want)
+    bsa.bsa_device_status()
