@@ -41,8 +41,8 @@
 //    Code is kept short (one copy of the schedule, rolled loops where
 //    nothing is gained by unrolling): short segments run each role's code once
 //    per microsecond, and with 143 KB of it they took 7 us each.
-//  * paged_join_kernel adds up the partial results (launched with programmatic
-//    dependence, so that it is resident when the first kernel ends).
+//  * paged_join_kernel adds up the partial results (launched when the blocks of
+//    the first kernel leave).
 #include <cuda_bf16.h>
 
 #include <cfloat>

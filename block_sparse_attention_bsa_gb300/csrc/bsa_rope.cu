@@ -14,9 +14,9 @@
 // operations per clock and SM.  The top 32 bits give the half-turns in
 // [-1, 1) for sincospif.
 //
-// What bounds it: memory (720p latent, 32 + 8 heads of 128: 513 us, 6.9 TB/s;
-// 480p, 24 + 8 heads: 122 us, 6.5 TB/s; append with Q of 5 x 4,099 ragged
-// tokens: 59 us, 5.8 TB/s).  A thread owns 16 channels of a token (8 pairs), so
+// What bounds it: memory (720p latent, 32 + 8 heads of 128: 510 us, 6.9 TB/s;
+// 480p, 24 + 8 heads: 119 us, 6.7 TB/s; append with Q of 5 x 4,099 ragged
+// tokens: 56 us, 6.0 TB/s).  A thread owns 16 channels of a token (8 pairs), so
 // both its accesses are 16 bytes and neighbouring threads make whole 128-byte
 // lines, and goes through a group of heads, so that the sines and cosines of
 // a token are computed once per thread and not once per head.
