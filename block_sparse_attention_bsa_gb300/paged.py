@@ -11,6 +11,7 @@ outputs and workspaces that a call makes itself are allocated on that stream.
 from __future__ import annotations
 
 import contextlib
+import functools
 from struct import Struct
 from typing import Optional, Sequence
 
@@ -355,6 +356,12 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                out, lse, return_lse, workspace)
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(dev, B, T, Hq, Hkv, d, has_prefix) -> int:
+    """What a call on ``dev``, which is current, needs; asking the library takes 2 us."""
+    return max(bsa_forward_paged_workspace_size(B, T, Hq, Hkv, d, has_prefix), 256)
+
+
 def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, handle):
     dev = q.device
     B, T, Hq, d = q.shape
@@ -369,8 +376,7 @@ def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, 
     elif return_lse:
         lse = torch.empty((B, Hq, T), dtype=_F32, device=dev)
     if workspace is None:
-        need = lib.bsap_forward_workspace_size(B, T, Hq, k_cache.shape[2], d, 1 if args[9] > 0 else 0, 0)
-        workspace = torch.empty(max(need, 256), dtype=_U8, device=dev)
+        workspace = torch.empty(_workspace_bytes(dev, B, T, Hq, k_cache.shape[2], d, args[9] > 0), dtype=_U8, device=dev)
     else:
         _check_buffer("workspace", workspace, (workspace.numel(),), _U8, dev)
     st = lib.bsap_forward(*args, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
