@@ -224,6 +224,19 @@ __device__ __forceinline__ void store_32(void* dst, const float* v) {
                : "memory");
 }
 
+// 1 / (sum of a row's weights), 0 for a row without a key.  Whether it has one
+// follows from the lengths: the sum of a row with a NaN or an infinite score is
+// NaN, which no comparison with 0 tells from an empty row's, and so is the result.
+__device__ __forceinline__ float inverse_sum(bool keyed, float l) { return keyed ? 1.f / l : 0.f; }
+// Such a row's log-sum-exp from its largest score (in units of log 2) and its sum.
+__device__ __forceinline__ float row_lse(bool keyed, float m, float l) {
+  return keyed ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+// Two values of its output.
+__device__ __forceinline__ uint32_t output_pair(float inv_l, float a, float b) {
+  return inv_l != 0.f ? pack_bf16x2(a * inv_l, b * inv_l) : 0u;
+}
+
 // 8 columns from `col` on of a row at `row`: fp32, or divided by the row's sum
 // to bf16 (which may be aligned to 16 bytes only).
 __device__ __forceinline__ void store_row(unsigned long long row, int col, const float* v, float inv_l, bool bf16,
@@ -232,7 +245,7 @@ __device__ __forceinline__ void store_row(unsigned long long row, int col, const
   if (bf16) {
     uint32_t pk[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) pk[e] = inv_l > 0.f ? pack_bf16x2(v[2 * e] * inv_l, v[2 * e + 1] * inv_l) : 0u;
+    for (int e = 0; e < 4; ++e) pk[e] = output_pair(inv_l, v[2 * e], v[2 * e + 1]);
     *reinterpret_cast<uint4*>(row + col * 2) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   } else {
     store_32(reinterpret_cast<void*>(row + col * 4), v);
@@ -880,7 +893,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
                      (s.slot * 2 + (wide ? half : (int)w)) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + r;
       float2* ml = reinterpret_cast<float2*>(p.part_ml) + at;
       if (active) {
-        const float inv_l = l > 0.f ? 1.f / l : 0.f;
+        const float inv_l = inverse_sum(limit > 0, l);
         const int64_t orow = ((int64_t)fb * p.T + i) * p.Hq + s.hk * p.G + g;
         const unsigned long long dst = direct ? reinterpret_cast<unsigned long long>(p.out + orow * D)
                                               : reinterpret_cast<unsigned long long>(p.part_o + (int64_t)at * D);
@@ -917,7 +930,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             if (mine && direct) {
               uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = l > 0.f ? pack_bf16x2(o[2 * e] * inv_l, o[2 * e + 1] * inv_l) : 0u;
+              for (int e = 0; e < 16; ++e) pk[e] = output_pair(inv_l, o[2 * e], o[2 * e + 1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)            // out may be aligned to 16 bytes only
                 reinterpret_cast<uint4*>(dst + c * 2)[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
@@ -931,8 +944,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
           if (!direct)
             *ml = make_float2(m_ref, l);
           else if (p.lse)
-            p.lse[((int64_t)fb * p.Hq + s.hk * p.G + g) * p.T + i] =
-                l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            p.lse[((int64_t)fb * p.Hq + s.hk * p.G + g) * p.T + i] = row_lse(limit > 0, m_ref, l);
         }
       }
       tc_fence_before();
@@ -975,6 +987,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
   // to 128 rows (one of each group).
   int pre_n = 0, own_n = 0, pre_at = 0, own_at = 0, pre_step = 0, own_step = 0;
   bool direct = false;
+  const bool keyed = real && i < n && (p.prefix_len > 0 || min(seen_keys(p, kv, n, i), kv) > 0);
   if (real && i < n) {
     const int row = i * p.G + g, flat = b * p.TG + row;
     const int pre_seg = hk * p.pre_rt + flat / kRowTile;
@@ -1065,21 +1078,21 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
     }
   }
   if (!real || direct) return;
-  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+  const float inv_l = inverse_sum(keyed, l);
   __nv_bfloat16* dst = p.out + R * D + lane * kVec;
 #pragma unroll
   for (int v = 0; v < kPer / kVec; ++v) {
     uint32_t pk[kVec / 2];
 #pragma unroll
     for (int e = 0; e < kVec / 2; ++e)
-      pk[e] = l > 0.f ? pack_bf16x2(acc[v * kVec + 2 * e] * inv_l, acc[v * kVec + 2 * e + 1] * inv_l) : 0u;
+      pk[e] = output_pair(inv_l, acc[v * kVec + 2 * e], acc[v * kVec + 2 * e + 1]);
     if constexpr (kVec == 4)
       *reinterpret_cast<uint2*>(dst + v * kLanes * 4) = make_uint2(pk[0], pk[1]);
     else
       *reinterpret_cast<uint32_t*>(dst + v * kLanes * 2) = pk[0];
   }
   if (lane == 0 && p.lse)
-    p.lse[((int64_t)b * p.Hq + h) * p.T + i] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    p.lse[((int64_t)b * p.Hq + h) * p.T + i] = row_lse(keyed, m, l);
 }
 
 std::string s(int64_t v) { return std::to_string(v); }

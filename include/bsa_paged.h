@@ -114,8 +114,11 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  *     j <= kv_lens[b] - n + i.
  * out_i = sum_j softmax(z)_j v_j (bf16), z_j = softmax_scale q_i . k_j;
  * lse_i = ln sum_j exp(z_j).  Rows i >= n and rows without a key: out 0, lse
- * -inf.  Slots behind a request's keys are never read into a result, whatever
- * they hold; the values of real keys have to be finite.
+ * -inf.  A row with a score of NaN or +infinity (of a Q that is not finite, or a
+ * product past the range of fp32), or with scores of -infinity alone, has NaN as
+ * its output; other rows do not feel it.  Slots behind a request's keys are never
+ * read into a result, whatever they hold; real keys and their values have to be
+ * finite.
  * out: bf16 [B, T, Hq, D] contiguous, apart from q and the caches; lse: fp32 [B, Hq, T] contiguous or NULL.
  * softmax_scale <= 0 selects D^-1/2.  prefix_len 0: prefix_table may be NULL.
  * max_pages 0: no own keys (page_table and kv_lens may be NULL).
