@@ -51,6 +51,7 @@
 #include <mutex>
 #include <string>
 
+#include "bsa_join.h"
 #include "bsa_paged.h"
 #include "bsa_ptx.cuh"
 
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Partial results: from each CTA of a segment one, or two of a segment of up
   // to 128 rows (one of each group).
-  int pre_n = 0, own_n = 0, pre_at = 0, own_at = 0, pre_step = 0, own_step = 0;
+  Parts pre{0, 0, 0}, own{0, 0, 0};
   bool direct = false;
   const bool keyed = real && i < n && (p.prefix_len > 0 || min(seen_keys(p, kv, n, i), kv) > 0);
   if (real && i < n) {
@@ -997,22 +998,19 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
     if (p.pre_tiles > 0) pc = p.seg_ctas[pre_seg];
     if (mine > 0) oc = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
     if (p.pre_tiles > 0) {
-      const int two = p.B * p.TG - (flat - flat % kRowTile) <= kHalf;
-      pre_n = (pc.y - pc.x + 1) << two;
-      pre_at = ((pre_seg + pc.x) * 2 + flat % kRowTile / kHalf) * p.pre_slot_rows + flat % kHalf;
-      pre_step = (2 - two) * p.pre_slot_rows;
+      const bool two = p.B * p.TG - (flat - flat % kRowTile) <= kHalf;
+      pre = segment_parts(pc.x, pc.y, p.ctas, pre_seg, two, flat % kRowTile / kHalf, p.pre_slot_rows, flat % kHalf);
     }
     if (mine > 0) {
-      const int two = n * p.G - rt * kRowTile <= kHalf;
-      direct = p.pre_tiles == 0 && oc.x == oc.y && (!two || mine == 1);      // written by the first kernel
-      own_n = (oc.y - oc.x + 1) << two;
-      own_at = p.own_first + ((own_seg + oc.x) * 2 + row % kRowTile / kHalf) * p.own_slot_rows + row % kHalf;
-      own_step = (2 - two) * p.own_slot_rows;
+      const bool two = n * p.G - rt * kRowTile <= kHalf;
+      own = segment_parts(oc.x, oc.y, p.ctas, own_seg, two, row % kRowTile / kHalf, p.own_slot_rows, row % kHalf);
+      own.at += p.own_first;
+      direct = p.pre_tiles == 0 && own.n > 0 && oc.x == oc.y && (!two || mine == 1);   // written by the first kernel
     }
   }
   // Lane x holds the maximum and the sum of partial result base + x; then the
   // rows themselves are read, each warp every kWarps-th of them.
-  const int parts = real && !direct ? pre_n + own_n : 0;
+  const int parts = real && !direct ? pre.n + own.n : 0;
   const int most = __reduce_max_sync(0xffffffffu, parts);
   float m = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
@@ -1020,7 +1018,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
 #pragma unroll 1
   for (int base = 0; base < most; base += kLanes) {
     const int x = base + lane;
-    const int at = x < pre_n ? pre_at + x * pre_step : own_at + (x - pre_n) * own_step;
+    const int at = x < pre.n ? pre.at + x * pre.step : own.at + (x - pre.n) * own.step;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (x < parts) ml = reinterpret_cast<const float2*>(p.part_ml)[at];
     float m2 = fmaxf(m, ml.x);
