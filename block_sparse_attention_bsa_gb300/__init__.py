@@ -28,6 +28,7 @@ from .paged import (  # noqa: F401
     PAGE_SIZES_SUPPORTED,
     bsa_axis_frequencies,
     bsa_cache_append,
+    bsa_debug_paged_wait_probe,
     bsa_forward_paged,
     bsa_forward_paged_workspace_size,
     bsa_rope_axes,

@@ -88,6 +88,7 @@ PAGED_SIGNATURES = {
     "bsap_cache_append": (_I, [_P, _P, _P, _P, _P, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "bsap_forward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "bsap_forward": (_I, [_P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "bsap_debug_wait_probe": (_I, [ctypes.c_uint64, _P]),
 }
 
 

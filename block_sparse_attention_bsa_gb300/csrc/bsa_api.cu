@@ -543,14 +543,24 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
   return BSA_OK;
 }
 
+static bsa_status check_probe_limit(const char* fn, uint64_t limit_ns) {
+  if (limit_ns >= 1000000ull && limit_ns <= 10000000000ull) return BSA_OK;
+  return set_error(BSA_ERR_INVALID_ARG,
+                   std::string(fn) + ": limit_ns " + std::to_string(limit_ns) + " is outside [1 ms, 10 s]");
+}
+
+bsa_status bsap_debug_wait_probe(uint64_t limit_ns, bsa_stream_t stream) {
+  clear_error();
+  const bsa_status st = check_probe_limit("bsap_debug_wait_probe", limit_ns);
+  return st != BSA_OK ? st : launch_paged_wait_probe(limit_ns, reinterpret_cast<cudaStream_t>(stream));
+}
+
 bsa_status bsa_debug_wait_probe(int32_t family, uint64_t limit_ns, bsa_stream_t stream) {
   clear_error();
   if (family != 0 && family != 1)
     return set_error(BSA_ERR_INVALID_ARG, "bsa_debug_wait_probe: family " + s(family) +
                                               " is not 0 (forward kernels) or 1 (backward kernels)");
-  if (limit_ns < 1000000ull || limit_ns > 10000000000ull)
-    return set_error(BSA_ERR_INVALID_ARG, "bsa_debug_wait_probe: limit_ns " + std::to_string(limit_ns) +
-                                              " is outside [1 ms, 10 s]");
+  if (check_probe_limit("bsa_debug_wait_probe", limit_ns) != BSA_OK) return BSA_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return family == 0 ? launch_fwd_wait_probe(limit_ns, st) : launch_bwd_wait_probe(limit_ns, st);
 }

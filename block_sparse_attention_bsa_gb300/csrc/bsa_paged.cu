@@ -1221,6 +1221,11 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
 
 unsigned int read_and_clear_paged_error() { return take_error_word(); }
 
+bsa_status launch_paged_wait_probe(unsigned long long limit_ns, cudaStream_t stream) {
+  wait_probe_kernel<<<1, 32, 0, stream>>>(limit_ns);
+  return cuda_check(cudaGetLastError(), "wait_probe_kernel launch (paged attention)");
+}
+
 }  // namespace bsa
 
 using namespace bsa;

@@ -14,6 +14,7 @@ namespace bsa {
 constexpr unsigned int kErrPage = 2u;
 unsigned int read_and_clear_rope_error();
 unsigned int read_and_clear_paged_error();
+bsa_status launch_paged_wait_probe(unsigned long long limit_ns, cudaStream_t stream);
 
 constexpr int kMaxPagedBatch = 4096;
 

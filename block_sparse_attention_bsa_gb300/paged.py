@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 import torch
 
 from ._lib import load as _load
-from .api import _check, _check_buffer
+from .api import _check, _check_buffer, _stream_ptr
 
 PAGE_SIZES_SUPPORTED = (16, 32, 64, 128, 256)
 
@@ -384,3 +384,8 @@ def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, 
     if st:
         _check(st)
     return out, lse
+
+
+def bsa_debug_paged_wait_probe(limit_ns: int, stream=None) -> None:
+    """``bsa_debug_wait_probe`` for the paged attention's kernels."""
+    _check(_load().bsap_debug_wait_probe(int(limit_ns), _stream_ptr(stream)))

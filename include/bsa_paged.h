@@ -133,6 +133,11 @@ BSA_API bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, 
                                 int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
                                 void* workspace, size_t ws_bytes, bsa_stream_t stream);
 
+/* bsa_debug_wait_probe for the paged attention: the bounded wait of one thread
+ * gives up after limit_ns (1 ms to 10 s) and the next bsa_device_status() returns
+ * BSA_ERR_TIMEOUT.  No fault, trap or hang is involved. */
+BSA_API bsa_status bsap_debug_wait_probe(uint64_t limit_ns, bsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -294,3 +294,9 @@ def test_workspace_size_refuses_what_the_call_refuses(lib):
     assert f(1, 1, 32, 8, 128, True, 152) > 0
     for bad in ((0, 1, 32, 8, 128), (1, 0, 32, 8, 128), (1, 1, 30, 8, 128), (1, 1, 32, 8, 96), (4097, 1, 32, 8, 128)):
         assert f(*bad, True, 152) == 0
+
+
+@pytest.mark.parametrize("limit", [999_999, 10 ** 10 + 1])
+def test_wait_probe_refuses_limits_out_of_range(lib, limit):
+    assert lib.bsap_debug_wait_probe(limit, None) == 1
+    assert err(lib).startswith("bsap_debug_wait_probe: limit_ns")
