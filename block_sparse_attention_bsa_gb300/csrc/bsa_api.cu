@@ -516,6 +516,13 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
   if ((st = cuda_check(cudaMemcpyFromSymbol(&bad, g_debug_bad_rows, sizeof(bad)), "read BSA_DEBUG counter")) !=
       BSA_OK)
     return st;
+  // All that was read is cleared, so all of it is told.
+  const std::string wait = ((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : "";
+  std::string page;
+  if ((er | ep) & kErrPage)
+    page = std::string("a page table entry outside the cache, or a length without pages, reached ") +
+           ((er & kErrPage) ? ((ep & kErrPage) ? "bsap_cache_append and bsap_forward" : "bsap_cache_append")
+                            : "bsap_forward");
   if (bad != 0) {
     if ((st = cuda_check(cudaMemcpyToSymbol(g_debug_bad_rows, &zero, sizeof(zero)), "clear BSA_DEBUG counter")) !=
         BSA_OK)
@@ -524,14 +531,9 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
                      std::to_string(bad) + " malformed index-list rows reached bsa_forward / bsa_backward "
                      "(BSA_DEBUG validation: indices in range of the request's real key blocks and strictly "
                      "ascending, count 0 for query blocks without real rows)" +
-                         (((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : ""));
+                         (page.empty() ? "" : "; " + page) + wait);
   }
-  if ((er | ep) & kErrPage)
-    return set_error(BSA_ERR_INVALID_INDICES,
-                     std::string("a page table entry outside the cache, or a length without pages, reached ") +
-                         ((er & kErrPage) ? ((ep & kErrPage) ? "bsap_cache_append and bsap_forward" : "bsap_cache_append")
-                                          : "bsap_forward") +
-                         (((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : ""));
+  if (!page.empty()) return set_error(BSA_ERR_INVALID_INDICES, page + wait);
   if (ep & 1u)
     return set_error(BSA_ERR_TIMEOUT, std::string("a bounded device wait gave up in the ") +
                                           (((ef | eb) & 1u) ? "paged attention and other" : "paged attention") +

@@ -298,8 +298,11 @@ BSA_API bsa_status bsa_validate_indices(const int32_t* indices, const int32_t* c
 
 /* Synchronises `stream`, then reports and clears the device error words of
  * the current device: BSA_ERR_INVALID_INDICES if BSA_DEBUG validation found
- * malformed lists since the last call, BSA_ERR_TIMEOUT if a bounded wait in a
- * kernel gave up, BSA_ERR_CUDA if the stream reports an error, else BSA_OK. */
+ * malformed lists since the last call or a call of bsa_paged.h met a page or a
+ * length that its tables do not hold, BSA_ERR_TIMEOUT if a bounded wait in a
+ * kernel gave up, BSA_ERR_CUDA if the stream reports an error, else BSA_OK.
+ * Where several of these happened, the status is the first of them and the
+ * message tells of all. */
 BSA_API bsa_status bsa_device_status(bsa_stream_t stream);
 
 /* Diagnostics for the timeout path above.  Enqueues on `stream` one

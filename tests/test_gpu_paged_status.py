@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_bsa_gb300 as bsa
+from bsa_inputs import CONFIGS, make_inputs
 from paged_utils import Pool, attend64, check_attention
 
 pytestmark = pytest.mark.gpu
@@ -45,5 +46,34 @@ def test_a_wait_that_gave_up_is_told_of_beside_a_bad_page():
     bsa.bsa_forward_paged(x, pool.gk, pool.gv, table, pool.kv_lens)
     bsa.bsa_debug_paged_wait_probe(20_000_000)
     with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES.*bsap_forward; a bounded device wait also gave up"):
+        bsa.bsa_device_status()
+    bsa.bsa_device_status()
+
+
+def test_bad_pages_are_reported_beside_malformed_lists(monkeypatch):
+    """With BSA_DEBUG, an index list out of order and a page table entry that
+    names no page between two status calls: both are told of, once."""
+    monkeypatch.setenv("BSA_DEBUG", "1")
+    bsa.bsa_device_status()
+    cfg = CONFIGS["small_gqa"]
+    inp = make_inputs(cfg, "cuda", pad_fill=0.0)
+    q, k, v, lens = inp["q"], inp["k"], inp["v"], inp["seq_lens"]
+    idx, cnt = bsa.bsa_select(q, k, cfg.prefix, lens, cfg.block_q, cfg.block_k, inp["keep_ratio"])
+    bad = idx.clone()
+    assert int(cnt[0, 0, 0]) >= 2
+    bad[0, 0, 0, 0], bad[0, 0, 0, 1] = idx[0, 0, 0, 1], idx[0, 0, 0, 0]
+    pool = Pool([40, 20], 0, 2, 64, 16, DEV, 110, fill=1.0)
+    table = pool.gtable.clone()
+    table[0, 1] = pool.total
+    x = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    new = torch.zeros(2, 20, 2, 64, dtype=torch.bfloat16, device=DEV)
+    bsa.bsa_forward(q, k, v, bad, cnt, cfg.prefix, lens, cfg.block_q, cfg.block_k)
+    bsa.bsa_forward_paged(x, pool.gk, pool.gv, table, pool.kv_lens)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES: 1 malformed.*bsap_forward"):
+        bsa.bsa_device_status()
+    bsa.bsa_device_status()
+    bsa.bsa_forward(q, k, v, bad, cnt, cfg.prefix, lens, cfg.block_q, cfg.block_k)
+    bsa.bsa_cache_append(new, new, pool.gk, pool.gv, table, pool.kv_lens)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES: 1 malformed.*bsap_cache_append"):
         bsa.bsa_device_status()
     bsa.bsa_device_status()
