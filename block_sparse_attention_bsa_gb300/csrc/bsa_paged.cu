@@ -1294,9 +1294,20 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is not 256-byte aligned");
   const bsa_tensor ov = contiguous_like(qv, out);
-  if ((st = check_apart(fn, "q", qv, "out", ov)) != BSA_OK) return st;
-  if ((st = check_apart(fn, "k_cache", a.k, "out", ov)) != BSA_OK) return st;
-  if ((st = check_apart(fn, "v_cache", a.v, "out", ov)) != BSA_OK) return st;
+  // What is written against what other blocks, or the join, still read.
+  const Bytes writes[] = {bytes_of("out", ov), bytes_at("lse", lse, 4 * qv.B * qv.H * qv.S),
+                          bytes_at("workspace", workspace, (int64_t)need)};
+  const Bytes reads[] = {bytes_of("q", qv), bytes_of("k_cache", a.k), bytes_of("v_cache", a.v),
+                         bytes_at("page_table", max_pages ? page_table : nullptr,
+                                  4 * ((qv.B - 1) * table_stride + max_pages)),
+                         bytes_at("kv_lens", max_pages ? kv_lens : nullptr, 4 * qv.B), bytes_at("new_lens", new_lens, 4 * qv.B),
+                         bytes_at("prefix_table", prefix_len ? prefix_table : nullptr, 4 * cdiv64(prefix_len, a.k.S))};
+  for (const Bytes& w : writes)
+    for (const Bytes& r : reads)
+      if ((st = check_apart(fn, r, w)) != BSA_OK) return st;
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((st = check_apart(fn, writes[j], writes[i])) != BSA_OK) return st;
   PagedParams p{};
   if ((st = encode_cache(&p.tk, a.k, fn, "k_cache")) != BSA_OK) return st;
   if ((st = encode_cache(&p.tv, a.v, fn, "v_cache")) != BSA_OK) return st;

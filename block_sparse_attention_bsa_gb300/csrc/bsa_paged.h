@@ -27,6 +27,14 @@ bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, boo
 // memory is fine where x, contiguous, starts where y does.
 bsa_status check_apart(const char* fn, const char* x_name, const bsa_tensor& x, const char* y_name,
                        const bsa_tensor& y, bool in_place = false);
+// The same for the bytes [lo, hi) that a call writes, against others.
+struct Bytes {
+  const char* name;
+  uintptr_t lo, hi;
+};
+Bytes bytes_at(const char* name, const void* ptr, int64_t n);
+Bytes bytes_of(const char* name, const bsa_tensor& t);
+bsa_status check_apart(const char* fn, const Bytes& x, const Bytes& y);
 // The view of a contiguous output of x's shape.
 bsa_tensor contiguous_like(const bsa_tensor& x, void* ptr);
 

@@ -352,18 +352,27 @@ bsa_tensor contiguous_like(const bsa_tensor& x, void* ptr) {
   return y;
 }
 
+Bytes bytes_at(const char* name, const void* ptr, int64_t n) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(ptr);
+  return Bytes{name, lo, ptr ? lo + (uintptr_t)n : lo};
+}
+
+Bytes bytes_of(const char* name, const bsa_tensor& t) {
+  return bytes_at(name, t.ptr,
+                  2 * ((t.B - 1) * t.stride_b + (t.S - 1) * t.stride_s + (t.H - 1) * t.stride_h + t.D));
+}
+
+bsa_status check_apart(const char* fn, const Bytes& x, const Bytes& y) {
+  if (x.lo >= y.hi || y.lo >= x.hi) return BSA_OK;
+  return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + y.name + " shares memory with " + x.name);
+}
+
 bsa_status check_apart(const char* fn, const char* x_name, const bsa_tensor& x, const char* y_name,
                        const bsa_tensor& y, bool in_place) {
-  auto end = [](const bsa_tensor& t) {
-    return reinterpret_cast<uintptr_t>(t.ptr) +
-           2 * (uintptr_t)((t.B - 1) * t.stride_b + (t.S - 1) * t.stride_s + (t.H - 1) * t.stride_h + t.D);
-  };
-  const uintptr_t xb = reinterpret_cast<uintptr_t>(x.ptr), yb = reinterpret_cast<uintptr_t>(y.ptr);
-  if (xb >= end(y) || yb >= end(x)) return BSA_OK;
-  if (in_place && xb == yb && (x.H == 1 || x.stride_h == x.D) && (x.S == 1 || x.stride_s == x.H * x.D) &&
+  if (in_place && x.ptr == y.ptr && (x.H == 1 || x.stride_h == x.D) && (x.S == 1 || x.stride_s == x.H * x.D) &&
       (x.B == 1 || x.stride_b == x.S * x.H * x.D))
     return BSA_OK;
-  return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + y_name + " shares memory with " + x_name);
+  return check_apart(fn, bytes_of(x_name, x), bytes_of(y_name, y));
 }
 
 bsa_status check_paged(const char* fn, const bsa_tensor* k_cache, const bsa_tensor* v_cache,

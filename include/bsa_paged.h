@@ -119,7 +119,9 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  * its output; other rows do not feel it.  Slots behind a request's keys are never
  * read into a result, whatever they hold; real keys and their values have to be
  * finite.
- * out: bf16 [B, T, Hq, D] contiguous, apart from q and the caches; lse: fp32 [B, Hq, T] contiguous or NULL.
+ * out: bf16 [B, T, Hq, D] contiguous; lse: fp32 [B, Hq, T] contiguous or NULL.
+ * out, lse and workspace share no memory with one another nor with anything that
+ * the call reads (refused from the first to behind the last byte of each).
  * softmax_scale <= 0 selects D^-1/2.  prefix_len 0: prefix_table may be NULL.
  * max_pages 0: no own keys (page_table and kv_lens may be NULL).
  * Results do not depend on scheduling (no atomics), but the split of the keys
