@@ -1263,9 +1263,10 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": prefix_len " + s(prefix_len) + " out of range");
   if (prefix_len > 0 && !prefix_table)
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": prefix_table is NULL");
+  if (prefix_len > 0 && (st = check_aligned(fn, "prefix_table", prefix_table, 4)) != BSA_OK) return st;
   if (!out) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": out is NULL");
-  if (reinterpret_cast<uintptr_t>(out) & 15u)
-    return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": out is not 16-byte aligned");
+  if ((st = check_aligned(fn, "out", out, 16)) != BSA_OK) return st;
+  if ((st = check_aligned(fn, "lse", lse, 4)) != BSA_OK) return st;
   if (!std::isfinite(softmax_scale))
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": softmax_scale is not finite");
   // times -inf and log2(e) on the device, where subnormal numbers may count as 0

@@ -22,6 +22,10 @@ constexpr int kMaxPagedBatch = 4096;
 // length 1 are replaced by 0; `cache`: strides of longer axes must be positive.
 bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, bool cache, bsa_tensor* view);
 
+// Refuses an array whose elements of `size` bytes the kernels could not read or
+// write where it lies (a misaligned access is a fault); NULL passes.
+bsa_status check_aligned(const char* fn, const char* name, const void* ptr, int size);
+
 // Refuses memory that a call writes while it reads or writes it elsewhere:
 // from the first to behind the last byte of each view.  `in_place`: the same
 // memory is fine where x, contiguous, starts where y does.

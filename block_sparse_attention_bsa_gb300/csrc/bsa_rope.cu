@@ -213,8 +213,9 @@ bsa_status check_rope(const char* fn, const bsap_rope* r, int64_t D) {
   if (!r) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": rope is NULL");
   if (!r->inv_freq || !r->axes)
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": inv_freq and axes must be non-NULL");
-  if (reinterpret_cast<uintptr_t>(r->inv_freq) & 7u)
-    return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": inv_freq is not 8-byte aligned");
+  bsa_status st;
+  if ((st = check_aligned(fn, "inv_freq", r->inv_freq, 8)) != BSA_OK) return st;
+  if ((st = check_aligned(fn, "axes", r->axes, 4)) != BSA_OK) return st;
   if (r->pairs <= 0 || 2 * (int64_t)r->pairs > D)
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + s(r->pairs) + " pairs for head dim " + s(D));
   if (r->pairs % 8)
@@ -228,14 +229,12 @@ bsa_status check_positions(const char* fn, const char* name, const bsap_position
   if (!p || !p->ptr) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + name + " is NULL");
   if (p->stride_b < 0 || p->stride_s < 0 || p->stride_a < 0)
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + name + " strides must not be negative");
-  return BSA_OK;
+  return check_aligned(fn, name, p->ptr, 4);
 }
 
 bsa_status check_out(const char* fn, const char* name, const void* out) {
   if (!out) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + name + " is NULL");
-  if (reinterpret_cast<uintptr_t>(out) & 15u)
-    return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + name + " is not 16-byte aligned");
-  return BSA_OK;
+  return check_aligned(fn, name, out, 16);
 }
 
 RotJob make_job(const bsa_tensor& x, const bsap_positions* pos, bool rotate) {
@@ -299,6 +298,11 @@ unsigned int read_and_clear_rope_error() {
   if (cudaMemcpyFromSymbol(&v, g_rope_error, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
   if (v != 0 && cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(zero)) != cudaSuccess) return 0xFFFFFFFFu;
   return v;
+}
+
+bsa_status check_aligned(const char* fn, const char* name, const void* ptr, int size) {
+  if (reinterpret_cast<uintptr_t>(ptr) % (uintptr_t)size == 0) return BSA_OK;
+  return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": " + name + " is not " + s(size) + "-byte aligned");
 }
 
 bsa_status check_view(const bsa_tensor* t, const char* fn, const char* name, bool cache, bsa_tensor* view) {
@@ -397,7 +401,10 @@ bsa_status check_paged(const char* fn, const bsa_tensor* k_cache, const bsa_tens
     if (table_stride < max_pages && B > 1)
       return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": table_stride " + s(table_stride) +
                                                 " is below max_pages " + s(max_pages));
+    if ((st = check_aligned(fn, "page_table", page_table, 4)) != BSA_OK) return st;
+    if ((st = check_aligned(fn, "kv_lens", kv_lens, 4)) != BSA_OK) return st;
   }
+  if ((st = check_aligned(fn, "new_lens", new_lens, 4)) != BSA_OK) return st;
   a->page_table = page_table; a->table_stride = table_stride; a->max_pages = max_pages;
   a->kv_lens = kv_lens; a->new_lens = new_lens;
   return BSA_OK;

@@ -330,3 +330,33 @@ def test_attention_refuses_results_and_workspaces_in_what_it_reads_or_in_one_ano
                           at["table"], 4, 4, at["lens"], at["new"], at["shared"], 33, 1, 0.0, at["out"], at["lse"], at["ws"],
                           need, None)
     assert st == 1 and needle in err(lib), err(lib)
+
+
+@pytest.mark.parametrize("name", ["page_table", "kv_lens", "new_lens", "prefix_table", "lse"])
+def test_attention_refuses_misaligned_arrays(lib, name):
+    at = {n: FAKE * (i + 2) + (2 if n == name else 0)
+          for i, n in enumerate(("page_table", "kv_lens", "new_lens", "prefix_table", "lse"))}
+    st = lib.bsap_forward(ref(T(ptr=1 << 30)), ref(T(B=8, S=16, H=2, ptr=1 << 31)), ref(T(B=8, S=16, H=2, ptr=1 << 32)),
+                          at["page_table"], 4, 4, at["kv_lens"], at["new_lens"], at["prefix_table"], 33, 1, 0.0, 1 << 33,
+                          at["lse"], 1 << 34, 1 << 30, None)
+    assert st == 1 and f"{name} is not 4-byte aligned" in err(lib)
+
+
+@pytest.mark.parametrize("name", ["page_table", "kv_lens", "new_lens", "axes", "pos"])
+def test_append_refuses_misaligned_arrays(lib, name):
+    at = {n: FAKE * (i + 2) + (1 if n == name else 0)
+          for i, n in enumerate(("page_table", "kv_lens", "new_lens", "axes", "pos"))}
+    st = lib.bsap_cache_append(ref(T(H=2, ptr=1 << 30)), ref(T(H=2, ptr=1 << 31)), ref(T(B=8, S=16, H=2, ptr=1 << 32)),
+                               ref(T(B=8, S=16, H=2, ptr=1 << 33)), at["page_table"], 4, 4, at["kv_lens"], at["new_lens"],
+                               ref(R(axes=at["axes"])), ref(P(ptr=at["pos"])), None, None, None)
+    assert st == 1 and f"{name} is not 4-byte aligned" in err(lib)
+
+
+@pytest.mark.parametrize("change,needle", [(dict(pos_q=P(ptr=FAKE + 2)), "pos_q"), (dict(pos_k=P(ptr=FAKE + 3)), "pos_k"),
+                                           (dict(rope=R(axes=FAKE + 2)), "axes")])
+def test_rotation_refuses_misaligned_arrays(lib, change, needle):
+    a = dict(pos_q=P(), pos_k=P(), rope=R())
+    a.update(change)
+    st = lib.bsap_rope_axes(ref(T()), ref(T(H=2, ptr=1 << 20)), ref(a["pos_q"]), ref(a["pos_k"]), ref(a["rope"]), 0, 1 << 21,
+                            1 << 22, None)
+    assert st == 1 and f"{needle} is not 4-byte aligned" in err(lib)
