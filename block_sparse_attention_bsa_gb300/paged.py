@@ -335,6 +335,9 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     prefix_len = int(prefix_len)
     if not 0 <= prefix_len < 1 << 31:          # ctypes would take it modulo 2^32
         raise ValueError(f"prefix_len {prefix_len} is out of range")
+    softmax_scale = float(softmax_scale)
+    if 0.0 < softmax_scale < 2.0 ** -126:      # as a float it may be 0, which selects d^-1/2
+        raise ValueError(f"softmax_scale {softmax_scale} is below the smallest normal float")
     dev = _gpu(q, "q")
     qd = _tensor(q, "q", dev)
     kc, vc = _tensor(k_cache, "k_cache", dev), _tensor(v_cache, "v_cache", dev)
@@ -352,7 +355,7 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages of {k_cache.shape[1]}, prefix_len is "
                              f"{prefix_len}")
     return _on(dev, stream, _forward_launch, q, k_cache, v_cache,
-               (qd, kc, vc, table, stride, n, lens, new, shared, prefix_len, 1 if causal else 0, float(softmax_scale)),
+               (qd, kc, vc, table, stride, n, lens, new, shared, prefix_len, 1 if causal else 0, softmax_scale),
                out, lse, return_lse, workspace)
 
 

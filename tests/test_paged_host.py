@@ -360,3 +360,11 @@ def test_rotation_refuses_misaligned_arrays(lib, change, needle):
     st = lib.bsap_rope_axes(ref(T()), ref(T(H=2, ptr=1 << 20)), ref(a["pos_q"]), ref(a["pos_k"]), ref(a["rope"]), 0, 1 << 21,
                             1 << 22, None)
     assert st == 1 and f"{needle} is not 4-byte aligned" in err(lib)
+
+
+@pytest.mark.parametrize("scale", [5e-324, 1e-300, 1e-46, 1e-40])
+def test_binding_refuses_scales_that_round_to_zero(scale):
+    """0 selects d^-1/2; a scale that a float cannot hold must not."""
+    x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="softmax_scale"):
+        bsa.bsa_forward_paged(x, x, x, x, x, softmax_scale=scale)
