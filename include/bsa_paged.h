@@ -41,7 +41,7 @@ extern "C" {
  * is position[axes[p]] * inv_freq[p], and
  *     y_lo = x_lo cos - x_hi sin,    y_hi = x_hi cos + x_lo sin.
  * Channels from 2 * pairs on, and pairs whose axis is outside [0, n_axes),
- * are passed through.  Angles are formed in 64-bit fixed point (turns modulo
+ * are passed through bit for bit.  Angles are formed in 64-bit fixed point (turns modulo
  * one), so that they are as exact at position 2^30 as at position 1; products
  * are fp32, rounded to bf16 once.
  * inv_freq: device double [pairs], finite, |inv_freq| < 2^10 (radians per

@@ -1,6 +1,6 @@
-"""Numbers that are not finite in the paged attention: a row of Q that holds
-them comes out as NaN (0 and -inf mean "no key" and nothing else), and no other
-row feels it.
+"""Numbers that are not finite in the paged attention and the rotation: a row of
+Q that holds them comes out of the attention as NaN (0 and -inf mean "no key" and
+nothing else), and no other row feels it; a pair without an axis keeps them.
 
 The rows' scores, from the formula alone: a NaN in q makes every score NaN; an
 infinity in one channel makes them infinite with the signs of that channel of K;
@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import block_sparse_attention_bsa_gb300 as bsa
-from paged_utils import BF, Pool
+from paged_utils import BF, Pool, rotate64
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -110,3 +110,34 @@ def test_scores_of_minus_infinity_alone_are_no_empty_row():
     bsa.bsa_device_status()
     assert torch.isnan(out[0, 0, 0]).all() and torch.isneginf(lse[0, 0, 0])
     assert torch.isfinite(out[0, 0, 1]).all() and torch.isfinite(lse[0, 1, 0])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("back", [False, True])
+def test_pairs_without_an_axis_pass_through_bit_for_bit(inter, back):
+    """Axes -1 and 3 of three: infinities, NaN and zeros of either sign go through
+    as they are, as in the channels behind the pairs; in place, too."""
+    B, S, H, d, pairs = 2, 5, 7, 64, 16
+    x = randn((B, S, H, d), 106)
+    odd = torch.tensor([float("inf"), float("nan"), -0.0, 0.0, -float("inf"), -1.5], dtype=BF)
+    lo = [2 * p for p in range(pairs)] if inter else list(range(pairs))
+    hi = [2 * p + 1 for p in range(pairs)] if inter else list(range(pairs, 2 * pairs))
+    axes = torch.tensor([0, -1, 2, 3, 1, 5, -7, 1 << 30] * 2, dtype=torch.int32)
+    free = [p for p in range(pairs) if not 0 <= int(axes[p]) < 3]
+    for n, p in enumerate(free):
+        x[..., lo[p]], x[..., hi[p]] = odd[n % 6], odd[(n // 6 + n + 1) % 6]
+    x[0, 0, :, 2 * pairs:] = odd[1]
+    pos = torch.randint(-50, 50, (B, S, 3), generator=torch.Generator().manual_seed(107), dtype=torch.int32)
+    inv, _ = bsa.bsa_axis_frequencies((pairs,), device=DEV)
+    call = bsa.bsa_rope_axes_backward if back else bsa.bsa_rope_axes
+    y, _ = call(x.to(DEV), None, pos.to(DEV), None, inv, axes.to(DEV), interleaved=inter)
+    through = [ch for p in free for ch in (lo[p], hi[p])] + list(range(2 * pairs, d))
+    bits = torch.int16
+    assert torch.equal(y.cpu()[..., through].view(bits), x[..., through].view(bits))
+    turned = [ch for p in range(pairs) if p not in free for ch in (lo[p], hi[p])]
+    ref, bound = rotate64(x, pos, inv.cpu(), axes, inter, back)
+    assert ((y.double().cpu() - ref).abs() <= bound)[..., turned].all()
+    mine = x.to(DEV)
+    out = dict(dq_out=mine) if back else dict(q_out=mine)
+    call(mine, None, pos.to(DEV), None, inv, axes.to(DEV), interleaved=inter, **out)
+    assert torch.equal(mine.view(bits), y.view(bits))
