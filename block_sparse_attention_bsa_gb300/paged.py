@@ -381,7 +381,7 @@ def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, 
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(dev, B, T, Hq, k_cache.shape[2], d, args[9] > 0), dtype=_U8, device=dev)
     else:
-        _check_buffer("workspace", workspace, (workspace.numel(),), _U8, dev)
+        _check_buffer("workspace", workspace, (workspace.numel() if isinstance(workspace, torch.Tensor) else 0,), _U8, dev)
     st = lib.bsap_forward(*args, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                           workspace.numel(), handle)
     if st:

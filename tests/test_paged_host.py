@@ -368,3 +368,9 @@ def test_binding_refuses_scales_that_round_to_zero(scale):
     x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="softmax_scale"):
         bsa.bsa_forward_paged(x, x, x, x, x, softmax_scale=scale)
+
+
+def test_binding_refuses_a_workspace_that_is_no_tensor(lib):
+    q, out = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="workspace must be a torch.Tensor"):
+        paged._forward_launch(q, q, q, (), out, None, False, bytearray(256), 0)
