@@ -854,6 +854,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
               const float2 e1 = make_float2(ex2_approx(b.x), ex2_approx(b.y));
               ls0 = __fadd2_rn(ls0, e0);
               ls1 = __fadd2_rn(ls1, e1);
+              // The weights meet V in bf16, as the tensor cores take it beside
+              // bf16 V (a second product with what the rounding leaves would
+              // double P V); their sum is of the unrounded ones.  Relative error
+              // of the output against 64 bits 0.0023, with fp32 weights 0.0017.
               pk[e / 2] = pack_bf16x2(e0.x, e0.y);
               pk[e / 2 + 1] = pack_bf16x2(e1.x, e1.y);
             }
@@ -982,6 +986,8 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
   const int r0 = real ? (int)R : 0;
   const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
   const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
+  // Read before the wait: this grid starts when the main kernel's blocks have all
+  // left, each of which has waited for whatever wrote the lengths.
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Partial results: from each CTA of a segment one, or two of a segment of up
@@ -1108,7 +1114,10 @@ PagedPlan plan_paged(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   w.TG = (int)(T * G);
   w.own_rt = (int)cdiv64(w.TG, kRowTile);
   // The prefix is folded into the own segments where that adds at most an
-  // eighth of jobs: rows of 128 per request against rows of 128 of the batch.
+  // eighth of jobs: rows of 128 per request against rows of 128 of the batch (500
+  // tokens of two prompts 92 -> 90 us).  The host knows T, not the lengths: a
+  // batch of single tokens padded to one request's chunk counts as full (a chunk
+  // of 500 and 63 single tokens on 8,192 shared keys 551 us, in two calls 76 + 47).
   w.fold = prefix && 8 * B * cdiv64(w.TG, kHalf) <= 9 * cdiv64(B * w.TG, kHalf);
   prefix = prefix && !w.fold;
   w.pre_rt = prefix ? (int)cdiv64(B * w.TG, kRowTile) : 0;

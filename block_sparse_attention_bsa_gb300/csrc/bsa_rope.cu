@@ -14,12 +14,16 @@
 // operations per clock and SM.  The top 32 bits give the half-turns in
 // [-1, 1) for sincospif.
 //
-// What bounds it: memory (720p latent, 32 + 8 heads of 128: 510 us, 6.9 TB/s;
-// 480p, 24 + 8 heads: 119 us, 6.7 TB/s; append with Q of 5 x 4,099 ragged
-// tokens: 56 us, 6.0 TB/s).  A thread owns 16 channels of a token (8 pairs), so
-// both its accesses are 16 bytes and neighbouring threads make whole 128-byte
-// lines, and goes through a group of heads, so that the sines and cosines of
-// a token are computed once per thread and not once per head.
+// What bounds it: memory (720p latent, 32 + 8 heads of 128: 512 us, 6.9 TB/s;
+// 480p, 24 + 8 heads: 120.7 us, 6.6 TB/s, neighbours paired 120.1, half of the
+// channels 120.9; append with Q of 5 x 4,099 ragged tokens: 56.4 us, 6.0 TB/s,
+// of K and V alone without rotation 16.0 us, 5.3 TB/s).  A thread owns 16 channels
+// of a token (8 pairs) in two accesses of 16 bytes, and goes through a group of
+// heads, so that the sines and cosines of a token are computed once per thread
+// and not once per head.  Where halves are paired, neighbouring threads make
+// whole 128-byte lines with each access; where neighbours are, and in channels
+// that are copied, a thread's two accesses lie beside each other and only the two
+// together make whole lines (which takes the same time, see above).
 #include <cuda_bf16.h>
 #include <math_constants.h>
 

@@ -222,7 +222,9 @@ def bsa_rope_axes(q: torch.Tensor, k: Optional[torch.Tensor], pos_q: torch.Tenso
                   inv_freq: torch.Tensor, axes: torch.Tensor, *, interleaved: bool = False,
                   q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
     """Rotary positions with several axes: pair p of a head's channels is turned
-    by ``position[axes[p]] * inv_freq[p]``.
+    by ``position[axes[p]] * inv_freq[p]``.  (``bsa_select_rope`` rotates by
+    tables of fp32 sines and cosines, halves paired, in the selector's own pass
+    over Q and K.)
 
     q ``[B, S, Hq, d]``, k ``[B2, S2, Hkv, d]`` or None; positions int32 ``[B,
     S, A]`` or ``[S, A]`` (A = 1..4, any strides: a permuted ``[A, B, S]`` is
@@ -325,10 +327,17 @@ def bsa_forward_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     q ``[B, T, Hq, d]``; cache, ``page_table``, ``kv_lens`` and ``new_lens`` as
     in ``bsa_cache_append`` (which is called first: ``kv_lens`` includes the new
     tokens).  Row i < n of request b sees the first ``prefix_len`` keys of the
-    pages ``prefix_table`` (int32 ``[pages]``), which all requests share and
-    which are read once for the batch, and its request's own keys, with
-    ``causal`` only those up to position ``kv_lens[b] - n + i``.  Rows from n
-    on, and rows without a key, get output 0 and LSE -inf.
+    pages ``prefix_table`` (int32 ``[pages]``), which all requests share, and its
+    request's own keys, with ``causal`` only those up to position ``kv_lens[b] -
+    n + i``.  With ``prefix_len`` 0 there is no prefix, whatever ``prefix_table``
+    is.  Rows from n on, and rows without a key, get output 0 and LSE -inf; a row
+    whose scores are not finite gets NaN.  The softmax's weights are rounded to
+    bf16 where they meet V.
+
+    The prefix is read once for up to 256 rows (tokens times query heads per KV
+    head) of the whole batch, padded ones counted, or with each request's own
+    keys where T fills tiles: a request with many new tokens goes into a call of
+    its own, apart from those with one.
 
     Returns ``(out [B, T, Hq, d] bf16, lse [B, Hq, T] fp32 or None)``.
     """

@@ -14,14 +14,14 @@
  * allocated, no call synchronises, all work is enqueued on the caller's
  * stream, arguments are checked on the host before anything is launched, the
  * message of a refusal comes from bsa_get_last_error(), and every call can be
- * captured in a CUDA graph.  Head dim 64 or 128, bf16.  The symbols carry the
- * prefix bsap_.
+ * captured in a CUDA graph.  Head dim 64 or 128, bf16.  Sizes of zero are
+ * refused, as in bsa.h.  The symbols carry the prefix bsap_.
  *
  * Lengths and tables that change from step to step (kv_lens, new_lens, the
  * page tables, positions, frequencies) are DEVICE arrays that the kernels read
- * when they run, so that a captured step follows them.  The host cannot check
- * their values.  The kernels do: they never read or write outside the given
- * buffers, and a table entry that names no page, or a length that the table
+ * when they run, so that a captured step follows them; they may not change while
+ * a call runs.  The host cannot check their values.  The kernels do: they never
+ * read or write outside the given buffers, and a table entry that names no page, or a length that the table
  * has no pages for, sets an error word that the next bsa_device_status()
  * returns as BSA_ERR_INVALID_INDICES (results of the requests concerned are
  * then unspecified).
@@ -36,6 +36,12 @@ extern "C" {
 #endif
 
 /* ------------------------------------------------------------- rotation ---
+ * For Q and K that bsa_select reads next and whose positions are a table of fp32
+ * sines and cosines per row, halves paired, bsa_select_rope rotates in the
+ * selector's pooling pass (one reading of Q and K less); positions with axes,
+ * neighbours paired, part of the channels, positions per request, far positions,
+ * the gradient, and keys on their way into pages are here.
+ *
  * Pair p of `pairs` (a multiple of 8, at most D / 2) is the channels
  * (p, p + pairs), or with interleaved != 0 (2p, 2p + 1).  Its angle at a token
  * is position[axes[p]] * inv_freq[p], and
@@ -109,7 +115,8 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
 /* Row i < n = new_lens[b] of request b (q [B, T, Hq, D]) attends, with query
  * head h reading KV head h / (Hq / Hkv),
  *   - the prefix_len first keys of the pages prefix_table[0 .. ceil(prefix_len
- *     / S)), the same for every request, read once for the whole batch, and
+ *     / S)), the same for every request (see below on how often they are read),
+ *     and
  *   - its request's own keys j < kv_lens[b]; with causal != 0 only
  *     j <= kv_lens[b] - n + i.
  * out_i = sum_j softmax(z)_j v_j (bf16), z_j = softmax_scale q_i . k_j;
@@ -126,6 +133,22 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  * max_pages 0: no own keys (page_table and kv_lens may be NULL).
  * Results do not depend on scheduling (no atomics), but the split of the keys
  * depends on the lengths of the whole batch and on the number of SMs.
+ * Scores, weights' sums, maxima and partial results are fp32; the weights are
+ * rounded to bf16 (off by at most 2^-8 of each) where they meet V on the tensor cores, as
+ * in bsa_forward.
+ * The prefix is read once for every 256 rows (b, i, g) of the batch under a KV
+ * head, padded rows counted: once for up to 256 / (Hq / Hkv) single tokens.
+ * Where T tokens fill tiles of 128 rows by themselves, it is read with each
+ * request's own keys instead.  Both go by T, whatever new_lens says: the padded
+ * rows of a batch in which one request has many new tokens and the others one
+ * cost what real ones do, and two calls, one for each kind, take a fraction of
+ * the time (a chunk of 500 tokens beside 63 single tokens on a prefix of 8,192
+ * keys, 32/8 heads of 128: 551 us in one call, 76 + 47 in two).
+ * Sizes above 2^28 key tiles, B Hkv ceil(T Hq / Hkv / 256) ceil(keys / 128) with
+ * the keys that the tables could hold, are refused, and from 2.7 10^7 on prefix
+ * tiles and others weigh the same in the division of work (up to a third slower,
+ * or half where the prefix is a tile or two): pass a view of the table's first
+ * columns where it is much wider than the requests are long.
  * B <= 4096, Hq <= 256.  workspace: device, 256-byte aligned; every byte that
  * is read was written by the same call, so calls that follow one another on a
  * stream, captured or not, may share one; calls that overlap may not. */
