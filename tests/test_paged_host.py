@@ -302,30 +302,31 @@ def test_wait_probe_refuses_limits_out_of_range(lib, limit):
     assert err(lib).startswith("bsap_debug_wait_probe: limit_ns")
 
 
-# q, out 4,096 values each; caches of 8 pages of 16 slots, 2 heads of 128; lse 2 x 4 x 4 floats; tables of 2 x 4 pages
+# q, out 4,096 values each; caches of 8 pages of 16 slots, 2 heads of 128; lse 2 x 4 x 4 floats; tables of 2 x 4 pages;
+# a workspace of megabytes, by the number of SMs (one is assumed where there is no GPU): 16 MB for each
 @pytest.mark.parametrize("change,needle", [
-    (dict(lse=(4 << 20) + 8192 - 4), "lse shares memory with q"),
+    (dict(lse=(4 << 24) + 8192 - 4), "lse shares memory with q"),
     (dict(lse=65536 - 64), "lse shares memory with k_cache"),
-    (dict(lse=1 << 20), "lse shares memory with v_cache"),
-    (dict(lse=(5 << 20) + 128), "lse shares memory with out"),
-    (dict(lse=(8 << 20) + 4), "lse shares memory with kv_lens"),
-    (dict(lse=(9 << 20) + 28), "lse shares memory with page_table"),
-    (dict(ws=4 << 20), "workspace shares memory with q"),
+    (dict(lse=1 << 24), "lse shares memory with v_cache"),
+    (dict(lse=(5 << 24) + 128), "lse shares memory with out"),
+    (dict(lse=(8 << 24) + 4), "lse shares memory with kv_lens"),
+    (dict(lse=(9 << 24) + 28), "lse shares memory with page_table"),
+    (dict(ws=4 << 24), "workspace shares memory with q"),
     (dict(ws=65536 - 256), "workspace shares memory with k_cache"),
-    (dict(ws=(1 << 20) + 256), "workspace shares memory with v_cache"),
-    (dict(ws=5 << 20), "workspace shares memory with out"),
-    (dict(ws=(6 << 20) - 256), "workspace shares memory with lse"),
-    (dict(new=(7 << 20) + 4), "workspace shares memory with new_lens"),
-    (dict(shared=(7 << 20) + 64), "workspace shares memory with prefix_table"),
-    (dict(out=9 << 20), "out shares memory with page_table"),
+    (dict(ws=(1 << 24) + 256), "workspace shares memory with v_cache"),
+    (dict(ws=5 << 24), "workspace shares memory with out"),
+    (dict(ws=(6 << 24) - 256), "workspace shares memory with lse"),
+    (dict(new=(7 << 24) + 4), "workspace shares memory with new_lens"),
+    (dict(shared=(7 << 24) + 64), "workspace shares memory with prefix_table"),
+    (dict(out=9 << 24), "out shares memory with page_table"),
 ])
 def test_attention_refuses_results_and_workspaces_in_what_it_reads_or_in_one_another(lib, change, needle):
-    at = dict(kc=0, vc=1 << 20, q=4 << 20, out=5 << 20, lse=6 << 20, ws=7 << 20, lens=8 << 20, table=9 << 20, new=10 << 20,
-              shared=11 << 20)
+    at = dict(kc=0, vc=1, q=4, out=5, lse=6, ws=7, lens=8, table=9, new=10, shared=11)
+    at = {name: x << 24 for name, x in at.items()}
     at.update(change)
     at = {name: FAKE + x for name, x in at.items()}
     need = lib.bsap_forward_workspace_size(2, 4, 4, 2, 128, 1, 0)
-    assert 512 < need < 1 << 20
+    assert 512 < need < 1 << 24
     st = lib.bsap_forward(ref(T(ptr=at["q"])), ref(T(B=8, S=16, H=2, ptr=at["kc"])), ref(T(B=8, S=16, H=2, ptr=at["vc"])),
                           at["table"], 4, 4, at["lens"], at["new"], at["shared"], 33, 1, 0.0, at["out"], at["lse"], at["ws"],
                           need, None)
