@@ -21,10 +21,10 @@
  * page tables, positions, frequencies) are DEVICE arrays that the kernels read
  * when they run, so that a captured step follows them; they may not change while
  * a call runs.  The host cannot check their values.  The kernels do: they never
- * read or write outside the given buffers, and a table entry that names no page, or a length that the table
- * has no pages for, sets an error word that the next bsa_device_status()
- * returns as BSA_ERR_INVALID_INDICES (results of the requests concerned are
- * then unspecified).
+ * read or write outside the given buffers, and a table entry that names no
+ * page, or a length that the table has no pages for, sets an error word that the
+ * next bsa_device_status() returns as BSA_ERR_INVALID_INDICES (results of the
+ * requests concerned are then unspecified, as are all after BSA_ERR_TIMEOUT).
  */
 #ifndef BSA_PAGED_H_
 #define BSA_PAGED_H_
@@ -47,9 +47,9 @@ extern "C" {
  * is position[axes[p]] * inv_freq[p], and
  *     y_lo = x_lo cos - x_hi sin,    y_hi = x_hi cos + x_lo sin.
  * Channels from 2 * pairs on, and pairs whose axis is outside [0, n_axes),
- * are passed through bit for bit.  Angles are formed in 64-bit fixed point (turns modulo
- * one), so that they are as exact at position 2^30 as at position 1; products
- * are fp32, rounded to bf16 once.
+ * are passed through bit for bit.  Angles are formed in 64-bit fixed point
+ * (turns modulo one), so that they are as exact at position 2^30 as at position
+ * 1; products are fp32, rounded to bf16 once.
  * inv_freq: device double [pairs], finite, |inv_freq| < 2^10 (radians per
  *   position).  axes: device int32 [pairs].  n_axes: 1 to 4. */
 typedef struct bsap_rope {
@@ -134,8 +134,8 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  * Results do not depend on scheduling (no atomics), but the split of the keys
  * depends on the lengths of the whole batch and on the number of SMs.
  * Scores, weights' sums, maxima and partial results are fp32; the weights are
- * rounded to bf16 (off by at most 2^-8 of each) where they meet V on the tensor cores, as
- * in bsa_forward.
+ * rounded to bf16 (off by at most 2^-8 of each) where they meet V on the tensor
+ * cores, as in bsa_forward.
  * The prefix is read once for every 256 rows (b, i, g) of the batch under a KV
  * head, padded rows counted: once for up to 256 / (Hq / Hkv) single tokens.
  * Where T tokens fill tiles of 128 rows by themselves, it is read with each
@@ -150,7 +150,7 @@ BSA_API size_t bsap_forward_workspace_size(int B, int T, int Hq, int Hkv, int d,
  * or half where the prefix is a tile or two): pass a view of the table's first
  * columns where it is much wider than the requests are long.
  * B <= 4096, Hq <= 256.  workspace: device, 256-byte aligned; every byte that
- * is read was written by the same call, so calls that follow one another on a
+ * counts was written by the same call, so calls that follow one another on a
  * stream, captured or not, may share one; calls that overlap may not. */
 BSA_API bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
                                 const int32_t* page_table, int64_t table_stride, int32_t max_pages,
