@@ -135,10 +135,11 @@ def _codes(x):
     x = x.to(F32).unflatten(-1, (-1, GROUP))
     most = x.abs().amax(-1)
     fine = torch.isfinite(most)
-    m, e = torch.frexp(most.masked_fill(~fine, 1.0) / 7.0)
+    most = most.masked_fill(~fine, 1.0).to(F64)
+    m, e = torch.frexp(most / torch.full_like(most, 7.0))             # by a number it would be a product, off at ties
     m = torch.round(m * 16.0)                                         # four bits of the quotient, ties to even
     byte = ((e + 14) * 8 + m.to(I32) - 8).clamp(0, 254).masked_fill(most == 0, 0)
-    scale = torch.ldexp(1.0 + (byte % 8) / 8.0, byte // 8 - 15)
+    scale = torch.ldexp(1.0 + (byte % 8) / 8.0, byte // 8 - 15).to(F32)
     n = torch.floor(x.abs() / scale[..., None] + 0.5).clamp(max=7.0).copysign(x).masked_fill(~fine[..., None], 0.0)
     return (n + 8.0).to(U8).flatten(-2), byte.masked_fill(~fine, 255).to(U8)
 
@@ -368,7 +369,8 @@ def _held64(x):
     then the nearest multiple, the larger one of two."""
     x = x.to(F64).reshape(*x.shape[:-1], -1, GROUP)
     table = _scale_table()[:255]
-    want = x.abs().max(-1).values / 7
+    want = x.abs().max(-1).values
+    want = want / torch.full_like(want, 7)
     upper = torch.searchsorted(table, want.contiguous()).clamp(max=254)
     lower = (upper - 1).clamp(min=0)
     above, below = (table[upper] - want).abs(), (want - table[lower]).abs()
