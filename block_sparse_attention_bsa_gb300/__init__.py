@@ -1,8 +1,8 @@
 """GB300-native selected-block (block-sparse) attention.
 
 The compute path is libbsa.so (hand-written sm_103a CUDA behind a C ABI,
-include/bsa.h and include/bsa_paged.h); this package only builds it and marshals torch tensors into
-its calls.
+include/bsa.h, include/bsa_paged.h and include/bsa_quant.h); this package only builds it and marshals
+torch tensors into its calls.
 """
 
 from .api import (  # noqa: F401
@@ -33,5 +33,12 @@ from .paged import (  # noqa: F401
     bsa_forward_paged_workspace_size,
     bsa_rope_axes,
     bsa_rope_axes_backward,
+)
+from .quant import (  # noqa: F401
+    bsa_cache_append_q4,
+    bsa_cache_q4_shape,
+    bsa_cache_read_q4,
+    bsa_forward_paged_q4,
+    bsa_forward_paged_q4_workspace_size,
 )
 from .build import build  # noqa: F401

@@ -1,4 +1,4 @@
-"""ctypes declarations of the libbsa C ABI (include/bsa.h, include/bsa_paged.h)."""
+"""ctypes declarations of the libbsa C ABI (include/bsa.h, include/bsa_paged.h, include/bsa_quant.h)."""
 
 from __future__ import annotations
 
@@ -42,6 +42,19 @@ class BsapPositions(ctypes.Structure):
         ("stride_b", ctypes.c_int64),
         ("stride_s", ctypes.c_int64),
         ("stride_a", ctypes.c_int64),
+    ]
+
+
+# The cache of include/bsa_quant.h (packed bytes, too).
+class BsaqCache(ctypes.Structure):
+    _fields_ = [
+        ("ptr", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("blocks", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("stride_page", ctypes.c_int64),
+        ("stride_head", ctypes.c_int64),
     ]
 
 
@@ -91,6 +104,14 @@ PAGED_SIGNATURES = {
     "bsap_debug_wait_probe": (_I, [ctypes.c_uint64, _P]),
 }
 
+# the calls of include/bsa_quant.h
+QUANT_SIGNATURES = {
+    "bsaq_cache_append": (_I, [_P, _P, _P, _P, _P, _I64, _I32, _P, _P, _P]),
+    "bsaq_cache_read": (_I, [_P, _P, _P, _I64, _I32, _P, _P, _P, _P, _P]),
+    "bsaq_forward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "bsaq_forward": (_I, [_P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+}
+
 
 def lib_path() -> str:
     return LIB
@@ -110,7 +131,7 @@ def load(path: str | None = None):
                 f"libbsa.so not found at {p}: build it first "
                 "(python -m block_sparse_attention_bsa_gb300.build); there is no fallback path")
         lib = ctypes.CDLL(p)
-        for name, (res, args) in (*SIGNATURES.items(), *PAGED_SIGNATURES.items()):
+        for name, (res, args) in (*SIGNATURES.items(), *PAGED_SIGNATURES.items(), *QUANT_SIGNATURES.items()):
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

@@ -10,9 +10,11 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <utility>
 
 #include "bsa_internal.h"
 #include "bsa_paged.h"
+#include "bsa_quant.h"
 
 namespace bsa {
 
@@ -509,7 +511,11 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
   // and those of the cache append and the paged attention
   const unsigned int er = read_and_clear_rope_error();
   const unsigned int ep = read_and_clear_paged_error();
-  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || er == 0xFFFFFFFFu || ep == 0xFFFFFFFFu)
+  // and those of the 4-bit cache's calls
+  const unsigned int eq = read_and_clear_quant_error();
+  const unsigned int ea = read_and_clear_quant_attn_error();
+  if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || er == 0xFFFFFFFFu || ep == 0xFFFFFFFFu || eq == 0xFFFFFFFFu ||
+      ea == 0xFFFFFFFFu)
     return set_error(BSA_ERR_CUDA, "bsa_device_status: cannot read the device error word");
   int bad = 0;
   const int zero = 0;
@@ -517,12 +523,14 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
       BSA_OK)
     return st;
   // All that was read is cleared, so all of it is told.
-  const std::string wait = ((ef | eb | ep) & 1u) ? "; a bounded device wait also gave up" : "";
+  const std::string wait = ((ef | eb | ep | ea) & 1u) ? "; a bounded device wait also gave up" : "";
   std::string page;
-  if ((er | ep) & kErrPage)
-    page = std::string("a page table entry outside the cache, or a length without pages, reached ") +
-           ((er & kErrPage) ? ((ep & kErrPage) ? "bsap_cache_append and bsap_forward" : "bsap_cache_append")
-                            : "bsap_forward");
+  const std::pair<unsigned int, const char*> paged[] = {
+      {er, "bsap_cache_append"}, {ep, "bsap_forward"}, {eq, "bsaq_cache_append or bsaq_cache_read"}, {ea, "bsaq_forward"}};
+  for (const auto& x : paged)
+    if (x.first & kErrPage)
+      page += (page.empty() ? "a page table entry outside the cache, or a length without pages, reached " : " and ") +
+              std::string(x.second);
   if (bad != 0) {
     if ((st = cuda_check(cudaMemcpyToSymbol(g_debug_bad_rows, &zero, sizeof(zero)), "clear BSA_DEBUG counter")) !=
         BSA_OK)
@@ -534,7 +542,7 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
                          (page.empty() ? "" : "; " + page) + wait);
   }
   if (!page.empty()) return set_error(BSA_ERR_INVALID_INDICES, page + wait);
-  if (ep & 1u)
+  if ((ep | ea) & 1u)
     return set_error(BSA_ERR_TIMEOUT, std::string("a bounded device wait gave up in the ") +
                                           (((ef | eb) & 1u) ? "paged attention and other" : "paged attention") +
                                           " kernels (the kernel aborted its tiles)");

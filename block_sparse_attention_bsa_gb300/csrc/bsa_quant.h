@@ -1,0 +1,59 @@
+// Host- and device-side declarations of the 4-bit cache calls.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "../../include/bsa_quant.h"
+#include "bsa_paged.h"
+
+namespace bsa {
+
+unsigned int read_and_clear_quant_error();        // append and read
+unsigned int read_and_clear_quant_attn_error();
+
+constexpr int kGroup = 32;                        // channels that share a scale
+constexpr int kBlockSlots = 16;
+// Bytes of a block of 16 slots of one head: codes and scales.
+__host__ __device__ constexpr int code_bytes(int D) { return kBlockSlots * D / 2; }
+__host__ __device__ constexpr int block_bytes(int D) { return code_bytes(D) + kBlockSlots * D / kGroup; }
+
+// The two caches and their tables, checked.
+struct QuantArgs {
+  bsaq_cache k, v;
+  const int32_t* page_table; int64_t table_stride; int max_pages;
+  const int32_t* kv_lens;
+};
+bsa_status check_quant(const char* fn, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
+                       const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
+                       int64_t B, QuantArgs* a);
+Bytes bytes_of(const char* name, const bsaq_cache& c);
+
+#ifdef __CUDACC__
+// ---- the format on the device ----
+
+// Twice a scale, as bf16 bits (NaN for 255).  The byte's eight bits stand in a
+// bf16's exponent and mantissa as they are, shifted; 15 becomes 127.
+__device__ __forceinline__ uint32_t twice_scale(uint32_t b) { return b == 255u ? 0x7FFFu : (b << 4) + 0x3880u; }
+
+// The codes of two neighbours from bits 4 i of a word: the four bits below the
+// exponent of 8.0 are 8 + (c + 8) / 2 in bf16.
+__device__ __forceinline__ uint32_t raised_codes(uint32_t word, int i) {
+  const uint32_t at = i == 0 ? word << 3 : word >> (4 * i - 3);
+  return (at & 0x00780078u) | 0x41004100u;
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+// Two values c s from raised codes and twice their scales: (8 + (c + 8) / 2 - 12)
+// 2 s.  12 times twice a scale has six significant bits and the result seven, so
+// that one multiply-add gives it without a rounding.
+__device__ __forceinline__ uint32_t code_values(uint32_t raised, uint32_t scales2, uint32_t offset) {
+  return as_u32(__hfma2(as_bf16x2(raised), as_bf16x2(scales2), as_bf16x2(offset)));
+}
+__device__ __forceinline__ uint32_t scale_offset(uint32_t scales2) {
+  return as_u32(__hmul2(as_bf16x2(scales2), as_bf16x2(0xC140C140u)));        // times -12
+}
+#endif
+
+}  // namespace bsa
