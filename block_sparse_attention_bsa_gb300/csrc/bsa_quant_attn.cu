@@ -1,116 +1,927 @@
 // Attention of new tokens over a paged key/value cache held in 4 bits, whose
-// first prefix_len keys all requests share.
+// first prefix_len keys all requests share (tcgen05 + TMEM + bulk copies).
 //
 // Mathematics: that of bsa_paged.cu, with k_j and v_j = codes times scales of
-// their groups of 32 channels (bsa_quant.h).
+// their groups of 32 channels (bsa_quant.h).  A code times a scale is exact in
+// bf16, so that the products are those of bf16 pages that hold the same values.
+//
+// Layout of the work:
+//  * The keys are the rows of the products, S^T = K Q^T and O^T += V^T P^T: K and
+//    V become bf16 on their way from the pages' bytes, a thread a key of K or a
+//    channel of V, straight into TMEM, where the tensor cores take their first
+//    operand from; Q and P, which are few rows, are the second, in shared memory.
+//    (As second operands K and V would go through shared memory, which a tile
+//    would then pass 195 KB of, where it now passes 45.)
+//  * A segment is up to N query rows that read the same keys: for the prefix any N
+//    rows (b, i, g) of the whole batch under one KV head, for a request's own keys
+//    the rows (i, g) of that request.  All segments' tiles of 128 keys are put in
+//    one row and cut into equal pieces, one for each CTA, whatever the lengths are
+//    (they are read from the device).  A cut segment leaves partial results, which
+//    paged_join_kernel's sums (join_row) put together; segment + CTA numbers them.
+//  * One CTA per SM.  Warp 2 goes through the CTA's segments, hands them to the
+//    others through a ring and loads their Q rows; warp 0 copies each tile's blocks
+//    page by page into a ring; warps 4-7 turn K tiles into bf16, warps 8-11 V
+//    tiles; warp 1 issues the MMAs; warps 12-15 and 16-19 are two softmax groups
+//    that take the tiles in turn, a key per thread, each with an O of its own (two
+//    partial results of each segment and CTA).
 #include <cuda_bf16.h>
 
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
-#include "bsa_ptx.cuh"
+#include "bsa_paged_device.cuh"
 #include "bsa_quant.h"
 
 namespace bsa {
 namespace {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileBlocks = kTileKeys / kBlockSlots;
+constexpr int kThreads = 640;
+constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
+constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
+
+template <int D, int N>
+struct Cfg {
+  static constexpr int kQBytes = N * D * 2;
+  static constexpr int kPBytes = N * kTileKeys * 2;
+  static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = D == 128 ? 8 : 12;
+  static constexpr int kScaleBytes = (D / kGroup) * kTileKeys * 2;
+  static constexpr int kBarBytes = 4096;
+  static constexpr int kSmemBytes = 1024 + 2 * kQBytes + 2 * kPBytes + kStages * kStageBytes + 2 * kScaleBytes + kBarBytes;
+  // TMEM columns
+  static constexpr int kK = 0, kV = D, kS = kV + 128, kO = kS + 2 * N;       // two buffers each
+  static_assert(kO + 2 * N <= 512 && kSmemBytes <= 232448, "");
+};
 
 struct QAttnParams {
   const uint8_t* k; const uint8_t* v;
   int64_t k_page, k_head, v_page, v_head;      // byte strides
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
-  int B, T, Hq, Hkv, G, blocks_shift, num_pages, max_pages, prefix_len, causal;
+  int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
+  FastDiv div_G, div_TG;
+  int TG;                         // rows of a request under one KV head
+  int own_rt;                     // row tiles of a request
+  int pre_rt;                     // row tiles of the whole batch (prefix)
+  int pre_tiles;                  // key tiles of the prefix
+  int pre_slot_rows, own_slot_rows;   // rows of one of a slot's two partial results
+  int ctas;
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
+  int2* seg_ctas;                 // workspace: first and last CTA of each segment that has tiles
+  float* part_ml;                 // workspace: partial results' (max, sum) and rows,
+  float* part_o;                  // those of the prefix first,
+  int own_first;                  // from here on those of own keys
 };
 
-// Channel c of slot i of a block: K by slot, V by channel.
-template <int D, bool kV>
-__device__ __forceinline__ float held(const uint8_t* block, int i, int c) {
-  const int number = kV ? i : c % kGroup;
-  const int base = kV ? c * 8 : (c / kGroup * kBlockSlots + i) * (kGroup / 2);
-  const uint32_t word = *reinterpret_cast<const uint32_t*>(block + base + number / 8 * 4);
-  const int code = (int)((word >> (4 * (number % 8 / 2) + 16 * (number % 2))) & 15u) - 8;
-  const uint32_t s2 = twice_scale(block[code_bytes(D) + c / kGroup * kBlockSlots + i]);
-  return (float)code * 0.5f * __uint_as_float(s2 << 16);
+// Request b's own keys and new tokens, clamped to what the tables hold.
+__device__ __forceinline__ int own_keys(const QAttnParams& p, int b) {
+  if (p.max_pages == 0) return 0;
+  return min(max(p.kv_lens[b], 0), p.max_pages << p.page_shift);
+}
+__device__ __forceinline__ int new_tokens(const QAttnParams& p, int b) {
+  return p.new_lens ? min(max(p.new_lens[b], 0), p.T) : p.T;
+}
+// Own keys that row i of a request with kv keys and n new tokens sees.
+__device__ __forceinline__ int seen_keys(const QAttnParams& p, int kv, int n, int i) {
+  return p.causal ? min(max(kv - n + i + 1, 0), kv) : kv;
+}
+// Key tiles of row tile rt of such a request.
+template <int N>
+__device__ __forceinline__ int own_tiles(const QAttnParams& p, int kv, int n, int rt) {
+  const int first = p.div_G.quot(rt * N);
+  if (first >= n) return 0;
+  const int last = min(n - 1, p.div_G.quot(rt * N + N - 1));
+  return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
+}
+// Key tiles of a request under one KV head.
+template <int N>
+__device__ __forceinline__ int request_tiles(const QAttnParams& p, int kv, int n) {
+  int sum = 0;
+#pragma unroll 1
+  for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles<N>(p, kv, n, rt);
+  return sum;
 }
 
-// Block: token i of request b under one KV head; four warps take every fourth key.
-template <int D>
-__global__ void __launch_bounds__(128) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
-  constexpr int kPer = D / 32;
-  __shared__ float sm[4], sl[4], so[4][D];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int i = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  const int n = p.new_lens ? min(max(p.new_lens[b], 0), p.T) : p.T;
-  int kv = 0;
-  if (p.max_pages > 0) {
-    kv = p.kv_lens[b];
-    if (threadIdx.x == 0 && (kv < 0 || kv > p.max_pages << (4 + p.blocks_shift))) atomicOr(&g_bsa_error, kErrPage);
-    kv = min(max(kv, 0), p.max_pages << (4 + p.blocks_shift));
+// The row of tiles, cut into equal pieces.
+struct Cut {
+  int n, q, r;                    // CTAs that get some; tiles = q n + r
+  __device__ __forceinline__ Cut(const QAttnParams& p, int own) {
+    const int tiles = p.pre_tiles * p.pre_rt * p.Hkv + own;
+    n = min(p.ctas, tiles);
+    q = n > 0 ? tiles / n : 0;
+    r = tiles - q * n;
   }
-  const int own = p.causal ? min(max(kv - n + i + 1, 0), kv) : kv;
-  const int keys = i < n ? p.prefix_len + own : 0;
-  for (int g = 0; g < p.G; ++g) {
-    const int h = hk * p.G + g;
-    float q[kPer], o[kPer] = {}, m = -INFINITY, l = 0.f;
-    for (int e = 0; e < kPer; ++e)
-      q[e] = __bfloat162float(p.q[b * p.q_sb + i * p.q_ss + h * p.q_sh + lane * kPer + e]);
-    for (int j = warp; j < keys; j += 4) {
-      const bool pre = j < p.prefix_len;
-      const int key = pre ? j : j - p.prefix_len;
-      const int32_t* table = pre ? p.prefix_table : p.page_table + b * p.table_stride;
-      int page = table[key >> (4 + p.blocks_shift)];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) atomicOr(&g_bsa_error, kErrPage);
+  __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
+};
+
+// A segment's part that one CTA works on, as it stands in the segment ring.
+struct __align__(16) Segment {
+  int b;               // request, -1: prefix
+  int hk;
+  int row0, rows;      // first flat row (b * T + i) * G + g, and how many
+  int tile0, tiles;    // first key tile and how many
+  int slot;            // number of the partial result (segment + CTA)
+  int keys;            // where its keys end
+  int kv, n;           // of the request
+  int pad[2];
+};
+constexpr int kSegRing = 4;
+constexpr int kSegReaders = 10;      // warps that read every segment
+
+// A warp's place in the segment ring.
+struct SegmentReader {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ bool wait(uint32_t seg_full, uint32_t abort) const {
+    return warp_wait(seg_full + 8 * slot, phase, abort);
+  }
+  __device__ __forceinline__ void release(uint32_t seg_empty) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(seg_empty + 8 * slot);
+    if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+  }
+};
+
+// A barrier of four warps that gives up as every other wait does.
+struct GroupSync {
+  uint32_t bar, phase = 0;
+  __device__ __forceinline__ explicit GroupSync(uint32_t b) : bar(b) {}
+  __device__ __forceinline__ bool operator()(uint32_t abort) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+    const bool ok = warp_wait(bar, phase, abort);
+    phase ^= 1u;
+    return ok;
+  }
+};
+
+// N consecutive 32-bit columns of this thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float* r) {
+  if constexpr (N == 32) {
+    tmem_ld32f(taddr, r);
+  } else {
+    static_assert(N == 16, "");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void tmem_ld_4(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_4(uint32_t taddr, const float* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "f"(r[0]), "f"(r[1]), "f"(r[2]),
+               "f"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tst.shared.b16 [%0], lo;\n\t}" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The largest of a warp's numbers; NaN counts as kLowest, and so does all below it.
+__device__ __forceinline__ float warp_max(float z) {
+  int u = __float_as_int(z > kLowest ? z : kLowest);
+  u = __reduce_max_sync(0xffffffffu, u ^ (u >> 31 & 0x7FFFFFFF));
+  return __int_as_float(u ^ (u >> 31 & 0x7FFFFFFF));
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
+  using C = Cfg<D, N>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t q_smem = smem_u32(smem);                              // [2] Q rows
+  const uint32_t p_smem = q_smem + 2 * C::kQBytes;                     // [2] P rows
+  const uint32_t ring = p_smem + 2 * C::kPBytes;                       // [kStages] K blocks, V blocks
+  const uint32_t vscale = ring + kStages * C::kStageBytes;             // [2][D / 32][128] twice the scales of V, bf16
+  uint8_t* rest = smem + 2 * C::kQBytes + 2 * C::kPBytes + kStages * C::kStageBytes + 2 * C::kScaleBytes;
+  float* m_ref = reinterpret_cast<float*>(rest);                       // [2][N] the groups' running maxima
+  float* warp_part = m_ref + 2 * N;                                    // [2][4][N] of each warp
+  Segment* segs = reinterpret_cast<Segment*>(warp_part + 8 * N);       // [kSegRing]
+  int* stage_keys = reinterpret_cast<int*>(segs + kSegRing);           // [kStages] keys of the tile
+  int* block_sum = stage_keys + kStages;                               // [kMaxBlocks] tiles of own keys before request 32 i
+  int* total_slot = block_sum + kMaxBlocks;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
+  int* abort_slot = total_slot + 2;
+  volatile int* grow_mark = abort_slot + 1;                            // [2] the last job + 1 whose maximum has to move
+  // barriers, as shared-memory addresses 8 bytes apart
+  const uint32_t q_full = smem_u32(total_slot + 6);    // [2] 32 loader threads
+  const uint32_t q_empty = q_full + 16;                // [2] commit
+  const uint32_t k_full = q_full + 32;                 // [2] 4 warps
+  const uint32_t v_full = q_full + 48;                 // [2] 4 warps
+  const uint32_t s_full = q_full + 64;                 // [2] commit: S is there, the K tile is free
+  const uint32_t s_empty = q_full + 80;                // [2] 4 softmax warps
+  const uint32_t p_full = q_full + 96;                 // [2] 4 softmax warps
+  const uint32_t pv_done = q_full + 112;               // [2] commit: O is there, the V and P tiles are free
+  const uint32_t o_empty = q_full + 128;               // [2] 4 softmax warps
+  const uint32_t group_bar = q_full + 144;             // [3] softmax groups, V warps
+  const uint32_t mma_end = q_full + 168;               // commit
+  const uint32_t seg_full = q_full + 176;              // [kSegRing] the scheduler
+  const uint32_t seg_empty = seg_full + 8 * kSegRing;  // [kSegRing] their readers
+  const uint32_t full = seg_empty + 8 * kSegRing;      // [kStages] transaction bytes
+  const uint32_t empty = full + 8 * kStages;           // [kStages] 8 warps
+  static_assert((10 * N + kStages + kMaxBlocks + 6) * 4 + kSegRing * sizeof(Segment) + 176 + 16 * (kSegRing + kStages) <= C::kBarBytes,
+                "barrier block");
+  const uint32_t abort_flag = smem_u32(abort_slot);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 32);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(k_full + 8 * i, 4);
+      mbar_init(v_full + 8 * i, 4);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, 4);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(pv_done + 8 * i, 1);
+      mbar_init(o_empty + 8 * i, 4);
+      grow_mark[i] = 0;
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(group_bar + 8 * i, 4);
+    mbar_init(mma_end, 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(seg_full + 8 * i, 1);
+      mbar_init(seg_empty + 8 * i, kSegReaders);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 8);
+    }
+    *abort_slot = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // Launched when the blocks of the kernel before leave: up to here nothing is
+  // read or written that it uses.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the schedule: tiles of own keys per block of 32 requests, then their sums
+  const int nblk = (p.B + 31) / 32;
+#pragma unroll 1
+  for (int blk = warp; blk < nblk; blk += kThreads / 32) {
+    const int b = blk * 32 + lane;
+    const int mine = b < p.B ? request_tiles<N>(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
+    const int incl = warp_inclusive_sum(mine);
+    if (lane == 31) block_sum[blk] = incl;
+    if (cta == 0 && b < p.B && p.max_pages > 0) {
+      const int kv = p.kv_lens[b];
+      if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {
+    int before = 0;
+#pragma unroll 1
+    for (int i = 0; i < nblk; i += 32) {
+      const int v = i + lane < nblk ? block_sum[i + lane] : 0;
+      const int incl = warp_inclusive_sum(v) + before;
+      if (i + lane < nblk) block_sum[i + lane] = incl - v;
+      before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) *total_slot = before;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  int begin = 0, end = 0;
+  {
+    const Cut cut(p, *total_slot);
+    if (cta < cut.n) {
+      begin = cut.begin(cta);
+      end = cut.begin(cta + 1);
+    }
+  }
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer ---
+    // Lane x copies page x of a tile's K, lane 8 + x of its V.
+    const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
+    const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
+    const int x = lane % 8;
+    const bool is_v = lane >= 8;
+    const bool mine = lane < 16 && x < per_tile;
+    uint32_t it = 0;
+    SegmentReader reader;
+#pragma unroll 1
+    for (int t = begin; t < end && ok;) {
+      if (!(ok = reader.wait(seg_full, abort_flag))) break;
+      const Segment& s = segs[reader.slot];
+      const int hk = s.hk, tile0 = s.tile0, tiles = s.tiles, keys_end = s.keys;
+      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+      reader.release(seg_empty);
+      const uint8_t* head = is_v ? p.v + hk * p.v_head : p.k + hk * p.k_head;
+      const int64_t page_stride = is_v ? p.v_page : p.k_page;
+      auto page_of = [&](int tile) {
+        const int key = tile * kTileKeys + x * per_page * kBlockSlots;
+        int page = 0;
+        if (mine && key < keys_end) {
+          page = table[key >> p.page_shift];
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_bsa_error, kErrPage);
+            page = 0;
+          }
+        }
+        return page;
+      };
+      int page = page_of(tile0);
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j, ++it) {
+        const int next = j + 1 < tiles ? page_of(tile0 + j + 1) : 0;
+        const uint32_t stage = it % kStages;
+        if (!(ok = warp_wait(empty + 8 * stage, (it / kStages & 1u) ^ 1u, abort_flag))) break;
+        const int keys = min(keys_end - (tile0 + j) * kTileKeys, kTileKeys);
+        const int blocks = (keys + kBlockSlots - 1) / kBlockSlots;
+        if (lane == 0) {
+          stage_keys[stage] = keys;
+          mbar_arrive_expect_tx(full + 8 * stage, 2 * blocks * block_bytes(D));
+        }
+        __syncwarp();
+        const int count = min(blocks - x * per_page, per_page);
+        if (mine && count > 0) {
+          const int in_page = (tile0 + j) * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
+          bulk_load(ring + stage * C::kStageBytes + (is_v ? C::kTileBytes : 0) + x * per_page * block_bytes(D),
+                    head + page * page_stride + in_page * block_bytes(D), count * block_bytes(D), full + 8 * stage);
+        }
+        page = next;
+      }
+      t += tiles;
+    }
+    // the copies in flight land before the CTA may leave
+    if (lane == 0)
+#pragma unroll 1
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1u);
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer ---
+    // S of job q, then P V of job q - 1.  The whole warp goes through the loop and
+    // one lane issues.
+    constexpr uint32_t idesc = idesc_bf16_f32(128, N, false);
+    const uint64_t qdesc = sdesc_sw128(q_smem, 16, 1024), pdesc = sdesc_sw128(p_smem, 16, 1024);
+    constexpr int kChunk = (N * 128) >> 4;
+    uint32_t q = 0, qi = 0, uses0 = 0, uses1 = 0;
+    bool v_first = false;
+    SegmentReader reader;
+#pragma unroll 1
+    for (int t = begin; t <= end && begin < end;) {
+      const bool more = t < end;                     // after the last segment one P V is left
+      int tiles = 1;
+      if (more) {
+        if (!(ok = reader.wait(seg_full, abort_flag))) break;
+        tiles = segs[reader.slot].tiles;
+        reader.release(seg_empty);
+      }
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j) {
+        if (more) {
+          const uint32_t w = q & 1u, u = q >> 1 & 1u;
+          if (j == 0 && !(ok = warp_wait(q_full + 8 * (qi & 1u), qi >> 1 & 1u, abort_flag))) break;
+          if (j == 0) fence_async_shared();          // Q rows come by ordinary copies
+          if (!(ok = warp_wait(s_empty + 8 * w, u ^ 1u, abort_flag))) break;
+          if (!(ok = warp_wait(k_full + 8 * w, u, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t d_t = tmem + C::kS + w * N, a_t = tmem + C::kK + w * (D / 2);
+          const uint64_t bs = qdesc + (uint64_t)(((qi & 1u) * C::kQBytes) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
+              if (kk == 0) mma_ts_acc<0>(d_t, a_t, bs, idesc);
+              else mma_ts_acc<1>(d_t, a_t + kk * 8, bs + off, idesc);
+            }
+            mma_commit(s_full + 8 * w);
+            if (j == tiles - 1) mma_commit(q_empty + 8 * (qi & 1u));
+          }
+          __syncwarp();
+        }
+        if (q > 0) {                                 // O^T (+)= V^T P^T of job q - 1
+          const uint32_t w = (q - 1) & 1u, u = (q - 1) >> 1 & 1u;
+          if (v_first && !(ok = warp_wait(o_empty + 8 * w, ((w ? uses1++ : uses0++) & 1u) ^ 1u, abort_flag))) break;
+          if (!(ok = warp_wait(v_full + 8 * w, u, abort_flag))) break;
+          if (!(ok = warp_wait(p_full + 8 * w, u, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t d_t = tmem + C::kO + w * N, a_t = tmem + C::kV + w * 64;
+          const uint64_t bs = pdesc + (uint64_t)((w * C::kPBytes) >> 4);
+          if (elect_one()) {
+            mma_ts(d_t, a_t, bs, idesc, !v_first);
+#pragma unroll
+            for (int kk = 1; kk < kTileKeys / 16; ++kk)
+              mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
+            mma_commit(pv_done + 8 * w);
+          }
+          __syncwarp();
+        }
+        ++q;
+        v_first = j < 2;
+      }
+      if (!ok || !more) break;
+      ++qi;
+      t += tiles;
+    }
+    if (elect_one()) {
+      mma_commit(mma_end);    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
+      mbar_drain(mma_end, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // -------------------------------------------------- scheduler, Q rows ---
+    // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
+    constexpr int kVec = D / 8;                    // 16-byte pieces of a row
+    constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
+    const int c = lane % kVec;
+    uint32_t qi = 0;
+    const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+    int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
+    uint32_t slot = 0, phase = 0;
+#pragma unroll 1
+    for (int t = begin; t < end && ok; ++qi) {
+      Segment s;
+      int t0, t1, seg;
+      if (t < pre) {
+        seg = t / p.pre_tiles;
+        t0 = seg * p.pre_tiles;
+        t1 = t0 + p.pre_tiles;
+        s.b = -1;
+        s.hk = seg / p.pre_rt;
+        s.row0 = (seg - s.hk * p.pre_rt) * N;
+        s.rows = min(N, p.B * p.TG - s.row0);
+        s.slot = seg + cta;
+        s.keys = p.prefix_len;
+        s.kv = s.n = 0;
+      } else {
+        const int u = t - pre;
+        if (u >= blk_end) {                          // the last block that begins at or before u
+          ++blk;
+          while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
+          const int b = blk * 32 + lane;
+          kv = b < p.B ? own_keys(p, b) : 0;
+          n = b < p.B ? new_tokens(p, b) : 0;
+          mine = b < p.B ? request_tiles<N>(p, kv, n) : 0;
+          upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
+          blk_end = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
+        const int per_head = __shfl_sync(0xffffffffu, mine, src);
+        const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
+        s.b = blk * 32 + src;
+        s.kv = __shfl_sync(0xffffffffu, kv, src);
+        s.n = __shfl_sync(0xffffffffu, n, src);
+        s.hk = (u - first) / per_head;
+        t0 = pre + first + s.hk * per_head;
+        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles<N>(p, s.kv, s.n, 0);
+#pragma unroll 1
+        while (t >= t0 + m) {
+          t0 += m;
+          m = own_tiles<N>(p, s.kv, s.n, ++rt);
+        }
+        t1 = t0 + m;
+        s.row0 = s.b * p.TG + rt * N;
+        s.rows = min(N, s.n * p.G - rt * N);
+        seg = (s.b * p.Hkv + s.hk) * p.own_rt + rt;
+        s.slot = seg + cta;
+        s.keys = s.kv;
+      }
+      s.tile0 = t - t0;
+      s.tiles = min(t1, end) - t;
+      s.pad[0] = s.pad[1] = 0;
+      if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
+      if (lane == 0) {
+        int2* who = p.seg_ctas + (s.b < 0 ? 0 : p.pre_rt * p.Hkv) + seg;     // the join looks here
+        if (t == t0) who->x = cta;
+        if (t1 <= end) who->y = cta;
+        segs[slot] = s;
+        mbar_arrive(seg_full + 8 * slot);
+      }
+      __syncwarp();
+      if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
+      // Q rows, and rows of zeros up to a multiple of four
+      const uint32_t qb = qi & 1u;
+      if (!(ok = warp_wait(q_empty + 8 * qb, ((qi >> 1) & 1u) ^ 1u, abort_flag))) break;
+      const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
+      const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (N * 128) + (lane / kVec) * 128;
+      const int row = s.row0 + min(lane, s.rows - 1);
+      const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+      const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
+#pragma unroll 4
+      for (int x = 0; x * kRowsPer < ((s.rows + 3) & ~3); ++x) {
+        const int r = x * kRowsPer + lane / kVec;
+        const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + x * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
+                     "l"(src), "r"(r < s.rows ? 16 : 0)
+                     : "memory");
+      }
+      // arrives when this lane's copies have landed; the warp goes on
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(q_full + 8 * qb) : "memory");
+      t += s.tiles;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");         // after an abort, too
+    __syncwarp();
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------ codes to bf16 ---
+    const bool is_v = warp >= 8;
+    const int th = threadIdx.x % 128;              // key of K, channel of V, TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t done = is_v ? pv_done : s_full, filled = is_v ? v_full : k_full;
+    const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
+    GroupSync sync(group_bar + 16);
+#pragma unroll 1
+    for (uint32_t q = 0; q < (uint32_t)(end - begin); ++q) {
+      const uint32_t w = q & 1u, stage = q % kStages;
+      if (!(ok = warp_wait(full + 8 * stage, q / kStages & 1u, abort_flag))) break;
+      const uint32_t tile = ring + stage * C::kStageBytes + (is_v ? C::kTileBytes : 0);
+      if (!is_v) {
+        if (!(ok = warp_wait(done + 8 * w, (q >> 1 & 1u) ^ 1u, abort_flag))) break;
+        tc_fence_after();
+        const uint32_t dst = tmem + lanes + C::kK + w * (D / 2);
+        uint32_t from = tile + slot_at + slot * 16, scale_at = tile + slot_at + code_bytes(D) + slot;
+#pragma unroll 1
+        for (int g = 0; g < D / kGroup; ++g, from += 256, scale_at += kBlockSlots) {
+          const uint4 c = lds128(from);
+          const uint32_t s2 = twice_scale(lds8(scale_at)) * 0x10001u, off = scale_offset(s2);
+          uint32_t r[16];
+          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4), s2, off);
+          tmem_st16(dst + g * 16, r);
+        }
+      } else {
+        // twice the scales of 128 keys, 0 behind the last one: what stands there must not count
+        const int keys = stage_keys[stage];
+        const uint32_t mine = vscale + w * C::kScaleBytes;
+#pragma unroll
+        for (int g = 0; g < D / kGroup; ++g) {
+          const uint32_t s2 = th < keys ? twice_scale(lds8(tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u;
+          sts16(mine + (g * kTileKeys + th) * 2, s2);
+        }
+        if (!(ok = sync(abort_flag))) break;
+        if (!(ok = warp_wait(done + 8 * w, (q >> 1 & 1u) ^ 1u, abort_flag))) break;
+        tc_fence_after();
+        if (th < D) {
+          const uint32_t dst = tmem + lanes + C::kV + w * 64;
+          uint32_t from = tile + th * 8, scale_at = mine + (th / kGroup) * (kTileKeys * 2);
+#pragma unroll 1
+          for (int x = 0; x < kTileBlocks; x += 2) {
+            uint32_t r[16];
+#pragma unroll
+            for (int y = 0; y < 2; ++y, from += block_bytes(D), scale_at += 32) {
+              const uint2 c = lds64(from);
+              const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
+              const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
+            }
+            tmem_st16(dst + x * 8, r);
+          }
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(filled + 8 * w);
+        mbar_arrive(empty + 8 * stage);
+      }
+    }
+  } else if (warp >= 12) {
+    // --------------------------------------------------- softmax + results ---
+    const uint32_t w = (warp - 12) / 4;            // the group: it takes the jobs q with q % 2 == w
+    const int wq = warp % 4, th = threadIdx.x % 128;       // this thread's key of a tile, and its channel of O
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t s_t = tmem + lanes + C::kS + w * N, o_t = tmem + lanes + C::kO + w * N;
+    // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
+    const uint32_t p_at = p_smem + w * C::kPBytes + (th / 64) * (N * 128) + th % 64 * 2;
+    float* const mr = m_ref + w * N;
+    float* const parts = warp_part + w * 4 * N;
+    GroupSync sync(group_bar + 8 * w);
+    uint32_t q = 0;                                // first job of the segment
+    SegmentReader reader;
+#pragma unroll 1
+    for (int t = begin; t < end && ok;) {
+      if (!(ok = reader.wait(seg_full, abort_flag))) break;
+      const Segment& s = segs[reader.slot];        // stays in the ring until the group is through with it
+      const int j0 = (int)((w ^ q) & 1u), rows = s.rows, tiles = s.tiles;
+      const int at = (s.b < 0 ? 0 : p.own_first) + (s.slot * 2 + (int)w) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows);
+      float2* const ml = reinterpret_cast<float2*>(p.part_ml) + at;
+      if (j0 >= tiles) {                           // the other group has the segment's only tile
+        if (th < rows) ml[th] = make_float2(-INFINITY, 0.f);
+        q += tiles;
+        t += tiles;
+        reader.release(seg_empty);
         continue;
       }
-      const int64_t in_page = ((key >> 4) & ((1 << p.blocks_shift) - 1)) * block_bytes(D);
-      const uint8_t* kb = p.k + page * p.k_page + hk * p.k_head + in_page;
-      const uint8_t* vb = p.v + page * p.v_page + hk * p.v_head + in_page;
-      float z = 0.f;
-      for (int e = 0; e < kPer; ++e) z = fmaf(q[e], held<D, false>(kb, key & 15, lane * kPer + e), z);
-      for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-      z *= p.scale_log2;
-      const float m2 = fmaxf(m, z), use = m2 == -INFINITY ? 0.f : m2;
-      const float a = m == -INFINITY ? 0.f : exp2f(m - use), w = exp2f(z - use);
-      m = m2;
-      l = l * a + w;
-      for (int e = 0; e < kPer; ++e) o[e] = o[e] * a + w * held<D, true>(vb, key & 15, lane * kPer + e);
-    }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-    for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = o[e];
-    __syncthreads();
-    if (warp == 0) {
-      const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])), use = top == -INFINITY ? 0.f : top;
-      float w[4], sum = 0.f;
-      for (int x = 0; x < 4; ++x) { w[x] = exp2f(sm[x] - use); sum += sl[x] * w[x]; }
-      const int64_t row = ((int64_t)b * p.T + i) * p.Hq + h;
-      for (int e = 0; e < kPer; ++e) {
-        float y = 0.f;
-        for (int x = 0; x < 4; ++x) y += so[x][lane * kPer + e] * w[x];
-        p.out[row * D + lane * kPer + e] = __float2bfloat16(keys > 0 ? y / sum : 0.f);
+      // the first and the last row's keys; between them they rise with the token
+      const int rem0 = s.row0 - s.b * p.TG;
+      const bool even = s.b < 0 || !p.causal;
+      const int least = even ? s.keys : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0));
+      if (th < N) mr[th] = kLowest;
+      if (!(ok = sync(abort_flag))) break;
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+#pragma unroll 1
+      for (int j = j0; j < tiles; j += 2) {
+        const uint32_t job = q + j, u = job >> 1 & 1u;
+        if (!(ok = warp_wait(s_full + 8 * w, u, abort_flag))) break;
+        tc_fence_after();
+        const int key = (s.tile0 + j) * kTileKeys + th;
+        const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
+        float v[N];
+        // Scores in units of log 2, those of keys that a row does not see -inf.
+        auto load = [&]() {
+          tmem_ld_n<N>(s_t, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r4 = 0; r4 < N; r4 += 4)
+            if (r4 < rows) {
+#pragma unroll
+              for (int r = r4; r < r4 + 4; ++r) v[r] *= p.scale_log2;
+            }
+          if (cut) {
+#pragma unroll
+            for (int r4 = 0; r4 < N; r4 += 4)
+              if (r4 < rows) {
+#pragma unroll
+                for (int r = r4; r < r4 + 4; ++r) {
+                  const int seen = even ? least : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0 + r));
+                  if (key >= min(seen, s.keys)) v[r] = -INFINITY;
+                }
+              }
+          }
+        };
+        auto minus_max = [&]() {
+#pragma unroll
+          for (int r4 = 0; r4 < N; r4 += 4)
+            if (r4 < rows) {
+              const float4 m = *reinterpret_cast<const float4*>(mr + r4);
+              v[r4] -= m.x; v[r4 + 1] -= m.y; v[r4 + 2] -= m.z; v[r4 + 3] -= m.w;
+            }
+        };
+        load();
+        bool grow = j == j0;
+        if (!grow) {
+          minus_max();
+          float top = -INFINITY;
+#pragma unroll
+          for (int r4 = 0; r4 < N; r4 += 4)
+            if (r4 < rows) top = max3f(max3f(top, v[r4], v[r4 + 1]), v[r4 + 2], v[r4 + 3]);
+          // weights of up to 2^8 are as exact as others; above, the maximum moves
+          if (__any_sync(0xffffffffu, top > 8.f) && lane == 0) grow_mark[w] = (int)job + 1;
+          if (!(ok = sync(abort_flag))) break;
+          grow = grow_mark[w] == (int)job + 1;
+          if (grow) load();
+        }
+        // P V of the group's job before is done: its P may be overwritten, O read
+        if (!(ok = warp_wait(pv_done + 8 * w, u ^ 1u, abort_flag))) break;
+        if (grow) {
+          tc_fence_after();
+#pragma unroll
+          for (int r4 = 0; r4 < N; r4 += 4)
+            if (r4 < rows) {
+#pragma unroll
+              for (int r = r4; r < r4 + 4; ++r) {
+                const float top = warp_max(v[r]);
+                if (lane == 0) parts[wq * N + r] = top;
+              }
+            }
+          if (!(ok = sync(abort_flag))) break;
+#pragma unroll
+          for (int r4 = 0; r4 < N; r4 += 4)
+            if (r4 < rows) {
+              float o[4] = {};
+              if (j != j0) {
+                tmem_ld_4(o_t + r4, o);
+                tmem_wait_ld();
+              }
+#pragma unroll
+              for (int r = r4; r < r4 + 4; ++r) {
+                const float m = mr[r];
+                const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[N + r])), fmaxf(parts[2 * N + r], parts[3 * N + r]));
+                const float alpha = ex2_approx(m - m2);
+                l[r] *= alpha;
+                o[r - r4] *= alpha;
+              }
+              if (j != j0) tmem_st_4(o_t + r4, o);
+            }
+          if (j != j0) tmem_wait_st();
+          if (!(ok = sync(abort_flag))) break;     // all have read the old maxima
+          if (th < ((rows + 3) & ~3)) {
+            const float m = fmaxf(fmaxf(parts[th], parts[N + th]), fmaxf(parts[2 * N + th], parts[3 * N + th]));
+            mr[th] = fmaxf(mr[th], m);
+          }
+          if (!(ok = sync(abort_flag))) break;
+          minus_max();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty + 8 * w);
+#pragma unroll
+        for (int r4 = 0; r4 < N; r4 += 4)
+          if (r4 < rows) {
+#pragma unroll
+            for (int r = r4; r < r4 + 4; r += 2) {
+              const float a = ex2_approx(v[r]), b = ex2_approx(v[r + 1]);
+              l[r] += a;
+              l[r + 1] += b;
+              // The weights meet V in bf16; their sum is of the unrounded ones.
+              const uint32_t both = pack_bf16x2(a, b);
+              sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
+              sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
+            }
+          }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 8 * w);
       }
-      if (lane == 0 && p.lse)
-        p.lse[((int64_t)b * p.Hq + h) * p.T + i] = keys > 0 ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      if (!ok) break;
+      // sums over the keys of a warp, then of the four
+#pragma unroll
+      for (int r4 = 0; r4 < N; r4 += 4)
+        if (r4 < rows) {
+#pragma unroll
+          for (int r = r4; r < r4 + 4; ++r) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+            if (lane == 0) parts[wq * N + r] = l[r];
+          }
+        }
+      if (!(ok = sync(abort_flag))) break;
+      if (th < rows) {
+        const float sum = (parts[th] + parts[N + th]) + (parts[2 * N + th] + parts[3 * N + th]);
+        // no score above kLowest: nothing is left, or NaN
+        ml[th] = make_float2(mr[th] > kLowest ? mr[th] : sum == 0.f ? -INFINITY : 0.f, sum);
+      }
+      const uint32_t last = q + (uint32_t)(tiles - 1 - ((tiles - 1 - j0) & 1));      // this group's last job
+      if (!(ok = warp_wait(pv_done + 8 * w, last >> 1 & 1u, abort_flag))) break;
+      tc_fence_after();
+      float o[N];
+      tmem_ld_n<N>(o_t, o);
+      tmem_wait_ld();
+      if (th < D) {
+        float* dst = p.part_o + (int64_t)at * D + th;
+#pragma unroll
+        for (int r = 0; r < N; ++r)
+          if (r < rows) dst[r * D] = o[r];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty + 8 * w);
+      q += tiles;
+      t += tiles;
+      reader.release(seg_empty);
     }
-    __syncthreads();
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Output row (b, i, h): joins the partial results of its prefix segment and of its
+// own segment, two from each CTA.
+template <int D, int N, int kLanes, int kWarps>
+__global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_kernel(const __grid_constant__ QAttnParams p) {
+  constexpr int kRows = kWarps > 1 ? 1 : 128 / kLanes;   // rows per block
+  const int64_t R = (int64_t)blockIdx.x * kRows + (kWarps > 1 ? 0 : threadIdx.x / kLanes);
+  const bool real = R < (int64_t)p.B * p.T * p.Hq;
+  const int r0 = real ? (int)R : 0;
+  const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
+  const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
+  // Read before the wait: this grid starts when the main kernel's blocks have all
+  // left, each of which has waited for whatever wrote the lengths.
+  const int kv = own_keys(p, b), n = new_tokens(p, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Parts pre{0, 0, 0}, own{0, 0, 0};
+  const bool keyed = real && i < n && (p.prefix_len > 0 || seen_keys(p, kv, n, i) > 0);
+  if (real && i < n) {
+    const int row = i * p.G + g, flat = b * p.TG + row;
+    const int pre_seg = hk * p.pre_rt + flat / N;
+    const int rt = row / N, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
+    if (p.pre_tiles > 0) {
+      const int2 c = p.seg_ctas[pre_seg];
+      pre = segment_parts(c.x, c.y, p.ctas, pre_seg, true, 0, p.pre_slot_rows, flat % N);
+    }
+    if (own_tiles<N>(p, kv, n, rt) > 0) {
+      const int2 c = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
+      own = segment_parts(c.x, c.y, p.ctas, own_seg, true, 0, p.own_slot_rows, row % N);
+      own.at += p.own_first;
+    }
+  }
+  join_row<D, kLanes, kWarps>(p.part_ml, p.part_o, pre, own, real, keyed, p.out + R * D,
+                              p.lse ? p.lse + ((int64_t)b * p.Hq + h) * p.T + i : nullptr);
 }
 
 std::string s(int64_t v) { return std::to_string(v); }
 
+// Rows of a segment, and where the partial results lie in the workspace.
 struct QAttnPlan {
-  size_t bytes;
+  int N, TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
+  size_t own_first, part_ml, part_o, bytes;
 };
 
-QAttnPlan plan_quant(int64_t, int64_t, int64_t, int64_t, int64_t, bool, int) { return QAttnPlan{256}; }
+QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
+  QAttnPlan w{};
+  w.TG = (int)(T * (Hq / Hkv));
+  const int64_t most = prefix ? B * w.TG : w.TG;
+  w.N = most <= 16 ? 16 : 32;
+  w.own_rt = (int)cdiv64(w.TG, w.N);
+  w.pre_rt = prefix ? (int)cdiv64(B * w.TG, w.N) : 0;
+  w.own_slot_rows = w.TG < w.N ? w.TG : w.N;
+  w.pre_slot_rows = (int)(B * w.TG < w.N ? B * w.TG : w.N);
+  auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  // a slot of two partial results for every number segment + CTA
+  const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * 2 * w.own_slot_rows;
+  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
+  w.own_first = pre;
+  w.part_ml = al((size_t)Hkv * (w.pre_rt + B * w.own_rt) * 8);      // behind the segments' CTAs
+  w.part_o = w.part_ml + al((pre + own) * 8);
+  w.bytes = w.part_o + al((pre + own) * d * 4);
+  return w;
+}
+
+template <int D, int N>
+bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  bsa_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != BSA_OK) return st;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 64 || !done[dev]) {
+      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Cfg<D, N>::kSmemBytes),
+                      "cudaFuncSetAttribute(quant_attention_kernel)");
+      if (st != BSA_OK) return st;
+      if (dev < 64) done[dev] = true;
+    }
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D, N>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, N>, p), "quant_attention_kernel launch")) != BSA_OK)
+    return st;
+  // Eight warps, one warp or eight lanes a row, as in the join of bsa_paged.cu.
+  const int64_t rows = (int64_t)p.B * p.T * p.Hq;
+  const int lanes = rows < (int64_t)num_sms() * 4 ? 256 : rows < (int64_t)num_sms() * 40 ? 32 : 8;
+  cfg.blockDim = dim3(lanes == 256 ? 256 : 128);
+  cfg.gridDim = dim3((unsigned)cdiv64(rows, cfg.blockDim.x / lanes));
+  cfg.dynamicSmemBytes = 0;
+  return cuda_check(lanes == 256  ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 32, 8>, p)
+                    : lanes == 32 ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 32, 1>, p)
+                                  : cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 8, 1>, p),
+                    "quant_join_kernel launch");
+}
 
 }  // namespace
 
@@ -163,10 +974,19 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
     return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": softmax_scale is subnormal or above half the largest float");
   const int64_t G = qv.H / a.k.heads;
   const int sms = num_sms();
-  if (qv.B * qv.S * G > INT32_MAX / 16)
-    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(qv.B * qv.S * G) + " rows are too many for one call");
+  // rows, tiles and slot numbers are 32-bit on the device
+  const int64_t flat_rows = qv.B * qv.S * G, page = a.k.blocks * kBlockSlots;
+  const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms);
+  const int64_t most_tiles = a.k.heads * (qv.B * plan.own_rt * cdiv64(max_pages * page, kTileKeys) +
+                                          plan.pre_rt * cdiv64(prefix_len, kTileKeys));
   const size_t need = plan.bytes;
+  if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.heads > INT32_MAX ||
+      need / (4 * (size_t)qv.D) > INT32_MAX)
+    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
+                                              s(max_pages * page + prefix_len) + " keys are too many for one call");
+  if (q_extent >= (int64_t)1 << 35)
+    return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": q reaches over " + s(q_extent) + " elements (2^35 at most)");
   if (!workspace) return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace is NULL (needs " + s(need) + " bytes)");
   if (ws_bytes < need)
     return set_error(BSA_ERR_WORKSPACE, std::string(fn) + ": workspace of " + s(ws_bytes) +
@@ -182,7 +1002,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
                                   4 * ((qv.B - 1) * table_stride + max_pages)),
                          bytes_at("kv_lens", max_pages ? kv_lens : nullptr, 4 * qv.B), bytes_at("new_lens", new_lens, 4 * qv.B),
                          bytes_at("prefix_table", prefix_len ? prefix_table : nullptr,
-                                  4 * cdiv64(prefix_len, a.k.blocks * kBlockSlots))};
+                                  4 * cdiv64(prefix_len, page))};
   for (const Bytes& w : writes)
     for (const Bytes& r : reads)
       if ((st = check_apart(fn, r, w)) != BSA_OK) return st;
@@ -194,17 +1014,26 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.k_page = a.k.stride_page; p.k_head = a.k.stride_head; p.v_page = a.v.stride_page; p.v_head = a.v.stride_head;
   p.q = static_cast<const __nv_bfloat16*>(qv.ptr); p.q_sb = qv.stride_b; p.q_ss = qv.stride_s; p.q_sh = qv.stride_h;
   p.B = (int)qv.B; p.T = (int)qv.S; p.Hq = (int)qv.H; p.Hkv = (int)a.k.heads; p.G = (int)G;
-  while ((1 << p.blocks_shift) < a.k.blocks) ++p.blocks_shift;
+  p.page_shift = 4;
+  while ((1 << p.page_shift) < page) ++p.page_shift;
   p.num_pages = (int)a.k.pages; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
+  p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
+  p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
+  p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
+  p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
+  p.ctas = sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.seg_ctas = reinterpret_cast<int2*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+  p.own_first = (int)plan.own_first;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)p.T, (unsigned)p.Hkv, (unsigned)p.B);
-  if (qv.D == 128) quant_attention_kernel<128><<<grid, 128, 0, cs>>>(p);
-  else quant_attention_kernel<64><<<grid, 128, 0, cs>>>(p);
-  return cuda_check(cudaGetLastError(), "quant_attention_kernel launch");
+  if (plan.N == 16) return qv.D == 128 ? launch_quant<128, 16>(p, cs) : launch_quant<64, 16>(p, cs);
+  return qv.D == 128 ? launch_quant<128, 32>(p, cs) : launch_quant<64, 32>(p, cs);
 }
 
 }  // extern "C"
