@@ -16,14 +16,16 @@
 //    rows (b, i, g) of the whole batch under one KV head, for a request's own keys
 //    the rows (i, g) of that request.  All segments' tiles of 128 keys are put in
 //    one row and cut into equal pieces, one for each CTA, whatever the lengths are
-//    (they are read from the device).  A cut segment leaves partial results, which
-//    paged_join_kernel's sums (join_row) put together; segment + CTA numbers them.
-//  * One CTA per SM.  Warp 2 goes through the CTA's segments, hands them to the
-//    others through a ring and loads their Q rows; warp 0 copies each tile's blocks
-//    page by page into a ring; warps 4-7 turn K tiles into bf16, warps 8-11 V
-//    tiles; warp 1 issues the MMAs; warps 12-15 and 16-19 are two softmax groups
-//    that take the tiles in turn, a key per thread, each with an O of its own (two
-//    partial results of each segment and CTA).
+//    (they are read from the device).  A cut segment, or one beside a prefix, leaves
+//    partial results that quant_join_kernel puts together; segment + CTA numbers them.
+//  * Four CTAs per SM, each through its piece by itself: while one waits for its
+//    products or its data the others work, with no hand-over between them.  (One CTA
+//    of 20 warps, each role's warps handing tiles to the next role's, took 1,790
+//    cycles a tile, most of it in one warp's way through its part of a tile.)  A CTA's
+//    warp 4 goes through its segments, loads their Q rows and copies each tile's
+//    blocks page by page; warps 0-3 turn K into bf16, a key per thread; one of their
+//    lanes issues S; they turn scores into weights, then V into bf16, a channel per
+//    thread, over K's place in TMEM; one lane issues P V.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -40,7 +42,8 @@ namespace {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileBlocks = kTileKeys / kBlockSlots;
-constexpr int kThreads = 640;
+constexpr int kThreads = 160;
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
 constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
 
@@ -49,14 +52,13 @@ struct Cfg {
   static constexpr int kQBytes = N * D * 2;
   static constexpr int kPBytes = N * kTileKeys * 2;
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
-  static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 8 : 12;
+  static constexpr int kKSlots = 2, kVSlots = N == 16 ? 2 : 1;
   static constexpr int kScaleBytes = (D / kGroup) * kTileKeys * 2;
-  static constexpr int kBarBytes = 4096;
-  static constexpr int kSmemBytes = 1024 + 2 * kQBytes + 2 * kPBytes + kStages * kStageBytes + 2 * kScaleBytes + kBarBytes;
-  // TMEM columns
-  static constexpr int kK = 0, kV = D, kS = kV + 128, kO = kS + 2 * N;       // two buffers each
-  static_assert(kO + 2 * N <= 512 && kSmemBytes <= 232448, "");
+  static constexpr int kBarBytes = 2048;
+  static constexpr int kSmemBytes = 1024 + 2 * kQBytes + kPBytes + (kKSlots + kVSlots) * kTileBytes + kScaleBytes + kBarBytes;
+  // TMEM columns: K, then V; S; O
+  static constexpr int kA = 0, kS = 64, kO = 64 + N, kColumns = 128;
+  static_assert(kO + N <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
 };
 
 struct QAttnParams {
@@ -70,7 +72,7 @@ struct QAttnParams {
   int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
   int pre_tiles;                  // key tiles of the prefix
-  int pre_slot_rows, own_slot_rows;   // rows of one of a slot's two partial results
+  int pre_slot_rows, own_slot_rows;   // rows of a partial result
   int ctas;
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
@@ -134,36 +136,25 @@ struct __align__(16) Segment {
   int slot;            // number of the partial result (segment + CTA)
   int keys;            // where its keys end
   int kv, n;           // of the request
-  int pad[2];
-};
-constexpr int kSegRing = 4;
-constexpr int kSegReaders = 10;      // warps that read every segment
-
-// A warp's place in the segment ring.
-struct SegmentReader {
-  uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ bool wait(uint32_t seg_full, uint32_t abort) const {
-    return warp_wait(seg_full + 8 * slot, phase, abort);
-  }
-  __device__ __forceinline__ void release(uint32_t seg_empty) {
-    __syncwarp();
-    if (threadIdx.x % 32 == 0) mbar_arrive(seg_empty + 8 * slot);
-    if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
-  }
+  int whole;           // this CTA has all tiles of the segment
+  int pad;
 };
 
-// A barrier of four warps that gives up as every other wait does.
-struct GroupSync {
-  uint32_t bar, phase = 0;
-  __device__ __forceinline__ explicit GroupSync(uint32_t b) : bar(b) {}
-  __device__ __forceinline__ bool operator()(uint32_t abort) {
-    __syncwarp();
-    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
-    const bool ok = warp_wait(bar, phase, abort);
-    phase ^= 1u;
-    return ok;
-  }
-};
+// A barrier of warps 0-3 that tells all of them whether some thread says yes.  No
+// warp leaves them between two of these but all together, so that none waits for one
+// that gave up.
+__device__ __forceinline__ bool sync_any(bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)mine)
+      : "memory");
+  return r != 0;
+}
 
 // N consecutive 32-bit columns of this thread's lane.
 template <int N>
@@ -220,76 +211,54 @@ __device__ __forceinline__ float warp_max(float z) {
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
   using C = Cfg<D, N>;
-  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t q_smem = smem_u32(smem);                              // [2] Q rows
-  const uint32_t p_smem = q_smem + 2 * C::kQBytes;                     // [2] P rows
-  const uint32_t ring = p_smem + 2 * C::kPBytes;                       // [kStages] K blocks, V blocks
-  const uint32_t vscale = ring + kStages * C::kStageBytes;             // [2][D / 32][128] twice the scales of V, bf16
-  uint8_t* rest = smem + 2 * C::kQBytes + 2 * C::kPBytes + kStages * C::kStageBytes + 2 * C::kScaleBytes;
-  float* m_ref = reinterpret_cast<float*>(rest);                       // [2][N] the groups' running maxima
-  float* warp_part = m_ref + 2 * N;                                    // [2][4][N] of each warp
-  Segment* segs = reinterpret_cast<Segment*>(warp_part + 8 * N);       // [kSegRing]
-  int* stage_keys = reinterpret_cast<int*>(segs + kSegRing);           // [kStages] keys of the tile
-  int* block_sum = stage_keys + kStages;                               // [kMaxBlocks] tiles of own keys before request 32 i
+  const uint32_t p_smem = q_smem + 2 * C::kQBytes;                     // P rows
+  const uint32_t k_ring = p_smem + C::kPBytes;                         // [kKSlots] blocks of K
+  const uint32_t v_ring = k_ring + C::kKSlots * C::kTileBytes;         // [kVSlots] blocks of V
+  const uint32_t vscale = v_ring + C::kVSlots * C::kTileBytes;         // [D / 32][128] twice the scales of V, bf16
+  uint8_t* rest = smem + (vscale - q_smem) + C::kScaleBytes;
+  float* mr = reinterpret_cast<float*>(rest);                          // [N] running maxima
+  float* parts = mr + N;                                               // [4][N] of each warp
+  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * N);           // [2]
+  int* block_sum = reinterpret_cast<int*>(segs + 2);                   // [kMaxBlocks] tiles of own keys before request 32 i
   int* total_slot = block_sum + kMaxBlocks;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
   int* abort_slot = total_slot + 2;
-  volatile int* grow_mark = abort_slot + 1;                            // [2] the last job + 1 whose maximum has to move
   // barriers, as shared-memory addresses 8 bytes apart
-  const uint32_t q_full = smem_u32(total_slot + 6);    // [2] 32 loader threads
-  const uint32_t q_empty = q_full + 16;                // [2] commit
-  const uint32_t k_full = q_full + 32;                 // [2] 4 warps
-  const uint32_t v_full = q_full + 48;                 // [2] 4 warps
-  const uint32_t s_full = q_full + 64;                 // [2] commit: S is there, the K tile is free
-  const uint32_t s_empty = q_full + 80;                // [2] 4 softmax warps
-  const uint32_t p_full = q_full + 96;                 // [2] 4 softmax warps
-  const uint32_t pv_done = q_full + 112;               // [2] commit: O is there, the V and P tiles are free
-  const uint32_t o_empty = q_full + 128;               // [2] 4 softmax warps
-  const uint32_t group_bar = q_full + 144;             // [3] softmax groups, V warps
-  const uint32_t mma_end = q_full + 168;               // commit
-  const uint32_t seg_full = q_full + 176;              // [kSegRing] the scheduler
-  const uint32_t seg_empty = seg_full + 8 * kSegRing;  // [kSegRing] their readers
-  const uint32_t full = seg_empty + 8 * kSegRing;      // [kStages] transaction bytes
-  const uint32_t empty = full + 8 * kStages;           // [kStages] 8 warps
-  static_assert((10 * N + kStages + kMaxBlocks + 6) * 4 + kSegRing * sizeof(Segment) + 176 + 16 * (kSegRing + kStages) <= C::kBarBytes,
-                "barrier block");
+  const uint32_t seg_full = smem_u32(total_slot + 4);  // [2] the segment, and 32 lanes' copies of Q rows
+  const uint32_t seg_empty = seg_full + 16;            // [2] 4 warps
+  const uint32_t k_full = seg_full + 32;               // [2] transaction bytes
+  const uint32_t k_empty = seg_full + 48;              // [2] 4 warps
+  const uint32_t v_full = seg_full + 64;               // [2] transaction bytes
+  const uint32_t v_empty = seg_full + 80;              // [2] 4 warps
+  const uint32_t s_done = seg_full + 96;               // commit
+  const uint32_t pv_done = seg_full + 104;             // commit
+  static_assert((5 * N + kMaxBlocks + 4) * 4 + 2 * sizeof(Segment) + 112 <= C::kBarBytes, "barrier block");
   const uint32_t abort_flag = smem_u32(abort_slot);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 32);
-      mbar_init(q_empty + 8 * i, 1);
-      mbar_init(k_full + 8 * i, 4);
-      mbar_init(v_full + 8 * i, 4);
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_empty + 8 * i, 4);
-      mbar_init(p_full + 8 * i, 4);
-      mbar_init(pv_done + 8 * i, 1);
-      mbar_init(o_empty + 8 * i, 4);
-      grow_mark[i] = 0;
+      mbar_init(seg_full + 8 * i, 33);
+      mbar_init(seg_empty + 8 * i, 4);
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 4);
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 4);
     }
-    for (int i = 0; i < 3; ++i) mbar_init(group_bar + 8 * i, 4);
-    mbar_init(mma_end, 1);
-    for (int i = 0; i < kSegRing; ++i) {
-      mbar_init(seg_full + 8 * i, 1);
-      mbar_init(seg_empty + 8 * i, kSegReaders);
-    }
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 8);
-    }
+    mbar_init(s_done, 1);
+    mbar_init(pv_done, 1);
     *abort_slot = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), C::kColumns);
     tmem_relinquish();
   }
   // Launched when the blocks of the kernel before leave: up to here nothing is
@@ -334,148 +303,22 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
   }
   bool ok = true;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer ---
-    // Lane x copies page x of a tile's K, lane 8 + x of its V.
-    const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
-    const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
-    const int x = lane % 8;
-    const bool is_v = lane >= 8;
-    const bool mine = lane < 16 && x < per_tile;
-    uint32_t it = 0;
-    SegmentReader reader;
-#pragma unroll 1
-    for (int t = begin; t < end && ok;) {
-      if (!(ok = reader.wait(seg_full, abort_flag))) break;
-      const Segment& s = segs[reader.slot];
-      const int hk = s.hk, tile0 = s.tile0, tiles = s.tiles, keys_end = s.keys;
-      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
-      reader.release(seg_empty);
-      const uint8_t* head = is_v ? p.v + hk * p.v_head : p.k + hk * p.k_head;
-      const int64_t page_stride = is_v ? p.v_page : p.k_page;
-      auto page_of = [&](int tile) {
-        const int key = tile * kTileKeys + x * per_page * kBlockSlots;
-        int page = 0;
-        if (mine && key < keys_end) {
-          page = table[key >> p.page_shift];
-          if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_bsa_error, kErrPage);
-            page = 0;
-          }
-        }
-        return page;
-      };
-      int page = page_of(tile0);
-#pragma unroll 1
-      for (int j = 0; j < tiles; ++j, ++it) {
-        const int next = j + 1 < tiles ? page_of(tile0 + j + 1) : 0;
-        const uint32_t stage = it % kStages;
-        if (!(ok = warp_wait(empty + 8 * stage, (it / kStages & 1u) ^ 1u, abort_flag))) break;
-        const int keys = min(keys_end - (tile0 + j) * kTileKeys, kTileKeys);
-        const int blocks = (keys + kBlockSlots - 1) / kBlockSlots;
-        if (lane == 0) {
-          stage_keys[stage] = keys;
-          mbar_arrive_expect_tx(full + 8 * stage, 2 * blocks * block_bytes(D));
-        }
-        __syncwarp();
-        const int count = min(blocks - x * per_page, per_page);
-        if (mine && count > 0) {
-          const int in_page = (tile0 + j) * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
-          bulk_load(ring + stage * C::kStageBytes + (is_v ? C::kTileBytes : 0) + x * per_page * block_bytes(D),
-                    head + page * page_stride + in_page * block_bytes(D), count * block_bytes(D), full + 8 * stage);
-        }
-        page = next;
-      }
-      t += tiles;
-    }
-    // the copies in flight land before the CTA may leave
-    if (lane == 0)
-#pragma unroll 1
-      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) mbar_drain(full + 8 * (i % kStages), i / kStages & 1u);
-    __syncwarp();
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer ---
-    // S of job q, then P V of job q - 1.  The whole warp goes through the loop and
-    // one lane issues.
-    constexpr uint32_t idesc = idesc_bf16_f32(128, N, false);
-    const uint64_t qdesc = sdesc_sw128(q_smem, 16, 1024), pdesc = sdesc_sw128(p_smem, 16, 1024);
-    constexpr int kChunk = (N * 128) >> 4;
-    uint32_t q = 0, qi = 0, uses0 = 0, uses1 = 0;
-    bool v_first = false;
-    SegmentReader reader;
-#pragma unroll 1
-    for (int t = begin; t <= end && begin < end;) {
-      const bool more = t < end;                     // after the last segment one P V is left
-      int tiles = 1;
-      if (more) {
-        if (!(ok = reader.wait(seg_full, abort_flag))) break;
-        tiles = segs[reader.slot].tiles;
-        reader.release(seg_empty);
-      }
-#pragma unroll 1
-      for (int j = 0; j < tiles; ++j) {
-        if (more) {
-          const uint32_t w = q & 1u, u = q >> 1 & 1u;
-          if (j == 0 && !(ok = warp_wait(q_full + 8 * (qi & 1u), qi >> 1 & 1u, abort_flag))) break;
-          if (j == 0) fence_async_shared();          // Q rows come by ordinary copies
-          if (!(ok = warp_wait(s_empty + 8 * w, u ^ 1u, abort_flag))) break;
-          if (!(ok = warp_wait(k_full + 8 * w, u, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t d_t = tmem + C::kS + w * N, a_t = tmem + C::kK + w * (D / 2);
-          const uint64_t bs = qdesc + (uint64_t)(((qi & 1u) * C::kQBytes) >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
-              if (kk == 0) mma_ts_acc<0>(d_t, a_t, bs, idesc);
-              else mma_ts_acc<1>(d_t, a_t + kk * 8, bs + off, idesc);
-            }
-            mma_commit(s_full + 8 * w);
-            if (j == tiles - 1) mma_commit(q_empty + 8 * (qi & 1u));
-          }
-          __syncwarp();
-        }
-        if (q > 0) {                                 // O^T (+)= V^T P^T of job q - 1
-          const uint32_t w = (q - 1) & 1u, u = (q - 1) >> 1 & 1u;
-          if (v_first && !(ok = warp_wait(o_empty + 8 * w, ((w ? uses1++ : uses0++) & 1u) ^ 1u, abort_flag))) break;
-          if (!(ok = warp_wait(v_full + 8 * w, u, abort_flag))) break;
-          if (!(ok = warp_wait(p_full + 8 * w, u, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t d_t = tmem + C::kO + w * N, a_t = tmem + C::kV + w * 64;
-          const uint64_t bs = pdesc + (uint64_t)((w * C::kPBytes) >> 4);
-          if (elect_one()) {
-            mma_ts(d_t, a_t, bs, idesc, !v_first);
-#pragma unroll
-            for (int kk = 1; kk < kTileKeys / 16; ++kk)
-              mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
-            mma_commit(pv_done + 8 * w);
-          }
-          __syncwarp();
-        }
-        ++q;
-        v_first = j < 2;
-      }
-      if (!ok || !more) break;
-      ++qi;
-      t += tiles;
-    }
-    if (elect_one()) {
-      mma_commit(mma_end);    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
-      mbar_drain(mma_end, 0);
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // -------------------------------------------------- scheduler, Q rows ---
+  if (warp == 4) {
+    // ---------------------------------------- segments, Q rows, copies of tiles ---
     // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
     const int c = lane % kVec;
-    uint32_t qi = 0;
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
     int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
-    uint32_t slot = 0, phase = 0;
+    uint32_t seg_no = 0, it = 0, issued[2] = {0, 0};
+    // Lane x copies page x of a tile's K, lane 8 + x of its V.
+    const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
+    const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
+    const int x = lane % 8;
+    const bool is_v = lane >= 8, copies = lane < 16 && x < per_tile;
 #pragma unroll 1
-    for (int t = begin; t < end && ok; ++qi) {
+    for (int t = begin; t < end && ok; ++seg_no) {
       Segment s;
       int t0, t1, seg;
       if (t < pre) {
@@ -524,152 +367,173 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
       }
       s.tile0 = t - t0;
       s.tiles = min(t1, end) - t;
-      s.pad[0] = s.pad[1] = 0;
-      if (!(ok = warp_wait(seg_empty + 8 * slot, phase ^ 1u, abort_flag))) break;
+      s.whole = begin <= t0 && t1 <= end;
+      s.pad = 0;
+      const uint32_t qb = seg_no & 1u;
+      if (!(ok = warp_wait(seg_empty + 8 * qb, (seg_no >> 1 & 1u) ^ 1u, abort_flag))) break;
       if (lane == 0) {
         int2* who = p.seg_ctas + (s.b < 0 ? 0 : p.pre_rt * p.Hkv) + seg;     // the join looks here
         if (t == t0) who->x = cta;
         if (t1 <= end) who->y = cta;
-        segs[slot] = s;
-        mbar_arrive(seg_full + 8 * slot);
+        segs[qb] = s;
+        mbar_arrive(seg_full + 8 * qb);
       }
       __syncwarp();
-      if (++slot == kSegRing) { slot = 0; phase ^= 1u; }
       // Q rows, and rows of zeros up to a multiple of four
-      const uint32_t qb = qi & 1u;
-      if (!(ok = warp_wait(q_empty + 8 * qb, ((qi >> 1) & 1u) ^ 1u, abort_flag))) break;
-      const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
-      const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (N * 128) + (lane / kVec) * 128;
-      const int row = s.row0 + min(lane, s.rows - 1);
-      const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
-      const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
+      {
+        const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
+        const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (N * 128) + (lane / kVec) * 128;
+        const int row = s.row0 + min(lane, s.rows - 1);
+        const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+        const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
 #pragma unroll 4
-      for (int x = 0; x * kRowsPer < ((s.rows + 3) & ~3); ++x) {
-        const int r = x * kRowsPer + lane / kVec;
-        const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + x * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
-                     "l"(src), "r"(r < s.rows ? 16 : 0)
-                     : "memory");
+        for (int y = 0; y * kRowsPer < ((s.rows + 3) & ~3); ++y) {
+          const int r = y * kRowsPer + lane / kVec;
+          const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + y * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
+                       "l"(src), "r"(r < s.rows ? 16 : 0)
+                       : "memory");
+        }
+        // arrives when this lane's copies have landed; the warp goes on
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(seg_full + 8 * qb) : "memory");
       }
-      // arrives when this lane's copies have landed; the warp goes on
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(q_full + 8 * qb) : "memory");
-      t += s.tiles;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");         // after an abort, too
-    __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------------ codes to bf16 ---
-    const bool is_v = warp >= 8;
-    const int th = threadIdx.x % 128;              // key of K, channel of V, TMEM lane
-    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t done = is_v ? pv_done : s_full, filled = is_v ? v_full : k_full;
-    const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
-    GroupSync sync(group_bar + 16);
-#pragma unroll 1
-    for (uint32_t q = 0; q < (uint32_t)(end - begin); ++q) {
-      const uint32_t w = q & 1u, stage = q % kStages;
-      if (!(ok = warp_wait(full + 8 * stage, q / kStages & 1u, abort_flag))) break;
-      const uint32_t tile = ring + stage * C::kStageBytes + (is_v ? C::kTileBytes : 0);
-      if (!is_v) {
-        if (!(ok = warp_wait(done + 8 * w, (q >> 1 & 1u) ^ 1u, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t dst = tmem + lanes + C::kK + w * (D / 2);
-        uint32_t from = tile + slot_at + slot * 16, scale_at = tile + slot_at + code_bytes(D) + slot;
-#pragma unroll 1
-        for (int g = 0; g < D / kGroup; ++g, from += 256, scale_at += kBlockSlots) {
-          const uint4 c = lds128(from);
-          const uint32_t s2 = twice_scale(lds8(scale_at)) * 0x10001u, off = scale_offset(s2);
-          uint32_t r[16];
-          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4), s2, off);
-          tmem_st16(dst + g * 16, r);
-        }
-      } else {
-        // twice the scales of 128 keys, 0 behind the last one: what stands there must not count
-        const int keys = stage_keys[stage];
-        const uint32_t mine = vscale + w * C::kScaleBytes;
-#pragma unroll
-        for (int g = 0; g < D / kGroup; ++g) {
-          const uint32_t s2 = th < keys ? twice_scale(lds8(tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u;
-          sts16(mine + (g * kTileKeys + th) * 2, s2);
-        }
-        if (!(ok = sync(abort_flag))) break;
-        if (!(ok = warp_wait(done + 8 * w, (q >> 1 & 1u) ^ 1u, abort_flag))) break;
-        tc_fence_after();
-        if (th < D) {
-          const uint32_t dst = tmem + lanes + C::kV + w * 64;
-          uint32_t from = tile + th * 8, scale_at = mine + (th / kGroup) * (kTileKeys * 2);
-#pragma unroll 1
-          for (int x = 0; x < kTileBlocks; x += 2) {
-            uint32_t r[16];
-#pragma unroll
-            for (int y = 0; y < 2; ++y, from += block_bytes(D), scale_at += 32) {
-              const uint2 c = lds64(from);
-              const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
-              const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
-            }
-            tmem_st16(dst + x * 8, r);
+      // the tiles
+      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+      const uint8_t* head = is_v ? p.v + s.hk * p.v_head : p.k + s.hk * p.k_head;
+      const int64_t page_stride = is_v ? p.v_page : p.k_page;
+      auto page_of = [&](int tile) {
+        const int key = tile * kTileKeys + x * per_page * kBlockSlots;
+        int page = 0;
+        if (copies && key < s.keys) {
+          page = table[key >> p.page_shift];
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_bsa_error, kErrPage);
+            page = 0;
           }
         }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(filled + 8 * w);
-        mbar_arrive(empty + 8 * stage);
-      }
-    }
-  } else if (warp >= 12) {
-    // --------------------------------------------------- softmax + results ---
-    const uint32_t w = (warp - 12) / 4;            // the group: it takes the jobs q with q % 2 == w
-    const int wq = warp % 4, th = threadIdx.x % 128;       // this thread's key of a tile, and its channel of O
-    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t s_t = tmem + lanes + C::kS + w * N, o_t = tmem + lanes + C::kO + w * N;
-    // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
-    const uint32_t p_at = p_smem + w * C::kPBytes + (th / 64) * (N * 128) + th % 64 * 2;
-    float* const mr = m_ref + w * N;
-    float* const parts = warp_part + w * 4 * N;
-    GroupSync sync(group_bar + 8 * w);
-    uint32_t q = 0;                                // first job of the segment
-    SegmentReader reader;
+        return page;
+      };
+      int page = page_of(s.tile0);
 #pragma unroll 1
-    for (int t = begin; t < end && ok;) {
-      if (!(ok = reader.wait(seg_full, abort_flag))) break;
-      const Segment& s = segs[reader.slot];        // stays in the ring until the group is through with it
-      const int j0 = (int)((w ^ q) & 1u), rows = s.rows, tiles = s.tiles;
-      const int at = (s.b < 0 ? 0 : p.own_first) + (s.slot * 2 + (int)w) * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows);
-      float2* const ml = reinterpret_cast<float2*>(p.part_ml) + at;
-      if (j0 >= tiles) {                           // the other group has the segment's only tile
-        if (th < rows) ml[th] = make_float2(-INFINITY, 0.f);
-        q += tiles;
-        t += tiles;
-        reader.release(seg_empty);
-        continue;
+      for (int j = 0; j < s.tiles && ok; ++j, ++it) {
+        const int next = j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
+        const int tile = s.tile0 + j;
+        const int blocks = (min(s.keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
+        const int count = min(blocks - x * per_page, per_page);
+        const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
+        const uint8_t* from = head + page * page_stride + in_page * block_bytes(D);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          const uint32_t slots = which ? C::kVSlots : C::kKSlots, slot = it % slots;
+          const uint32_t full = (which ? v_full : k_full) + 8 * slot, empty = (which ? v_empty : k_empty) + 8 * slot;
+          if (!(ok = warp_wait(empty, (it / slots & 1u) ^ 1u, abort_flag))) break;
+          if (lane == 0) mbar_arrive_expect_tx(full, blocks * block_bytes(D));
+          if (which) ++issued[1];
+          else ++issued[0];
+          __syncwarp();
+          if (copies && count > 0 && is_v == (which == 1))
+            bulk_load((which ? v_ring : k_ring) + slot * C::kTileBytes + x * per_page * block_bytes(D), from,
+                      count * block_bytes(D), full);
+        }
+        page = next;
       }
-      // the first and the last row's keys; between them they rise with the token
+      t += s.tiles;
+    }
+    // the copies in flight land before the CTA may leave, after an abort, too
+    if (lane == 0) {
+#pragma unroll 1
+      for (uint32_t i = issued[0] > C::kKSlots ? issued[0] - C::kKSlots : 0; i < issued[0]; ++i)
+        mbar_drain(k_full + 8 * (i % C::kKSlots), i / C::kKSlots & 1u);
+#pragma unroll 1
+      for (uint32_t i = issued[1] > C::kVSlots ? issued[1] - C::kVSlots : 0; i < issued[1]; ++i)
+        mbar_drain(v_full + 8 * (i % C::kVSlots), i / C::kVSlots & 1u);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+  } else {
+    // ------------------------------------------- codes, products, weights, results ---
+    const int th = threadIdx.x;                    // key of a tile, and channel of V and O
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t a_t = tmem + lanes + C::kA, s_t = tmem + lanes + C::kS, o_t = tmem + lanes + C::kO;
+    const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
+    // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
+    const uint32_t p_at = p_smem + (th / 64) * (N * 128) + th % 64 * 2;
+    constexpr uint32_t idesc = idesc_bf16_f32(128, N, false);
+    constexpr int kChunk = (N * 128) >> 4;
+    const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
+    uint32_t it = 0, seg_no = 0;
+#pragma unroll 1
+    for (int t = begin; t < end; ++seg_no) {
+      const uint32_t qb = seg_no & 1u;
+      ok = warp_wait(seg_full + 8 * qb, seg_no >> 1 & 1u, abort_flag);
+      fence_async_shared();                        // Q rows come by ordinary copies
+      const Segment& s = segs[qb];                 // stays there until all are through with it
+      if (th < N) mr[th] = kLowest;
+      if (sync_any(!ok)) break;
+      const int rows = s.rows, tiles = s.tiles;
+      // the keys of the first row; further rows' rise with the token
       const int rem0 = s.row0 - s.b * p.TG;
       const bool even = s.b < 0 || !p.causal;
       const int least = even ? s.keys : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0));
-      if (th < N) mr[th] = kLowest;
-      if (!(ok = sync(abort_flag))) break;
+      const uint64_t qdesc = sdesc_sw128(q_smem + qb * C::kQBytes, 16, 1024);
       float l[N];
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.f;
+      int j = 0;
 #pragma unroll 1
-      for (int j = j0; j < tiles; j += 2) {
-        const uint32_t job = q + j, u = job >> 1 & 1u;
-        if (!(ok = warp_wait(s_full + 8 * w, u, abort_flag))) break;
+      for (; j < tiles; ++j, ++it) {
+        const uint32_t ks = it % C::kKSlots, vs = it % C::kVSlots;
+        const int tile_keys = min(s.keys - (s.tile0 + j) * kTileKeys, kTileKeys);
+        const uint32_t v_tile = v_ring + vs * C::kTileBytes;
+        // K; its place is free when P V of the tile before is done
+        ok = warp_wait(k_full + 8 * ks, it / C::kKSlots & 1u, abort_flag) && ok;
+        ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag) && ok;
+        tc_fence_after();
+        {
+          uint32_t from = k_ring + ks * C::kTileBytes + slot_at + slot * 16;
+          uint32_t scale_at = k_ring + ks * C::kTileBytes + slot_at + code_bytes(D) + slot;
+#pragma unroll 1
+          for (int g = 0; g < D / kGroup; ++g, from += 256, scale_at += kBlockSlots) {
+            const uint4 c = lds128(from);
+            const uint32_t s2 = twice_scale(lds8(scale_at)) * 0x10001u, off = scale_offset(s2);
+            uint32_t r[16];
+            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4), s2, off);
+            tmem_st16(a_t + g * 16, r);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_empty + 8 * ks);
+        // twice the scales of V, 0 behind the last key: what stands there must not count
+        ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag) && ok;
+#pragma unroll
+        for (int g = 0; g < D / kGroup; ++g)
+          sts16(vscale + (g * kTileKeys + th) * 2,
+                th < tile_keys ? twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u);
+        tmem_wait_st();
+        tc_fence_before();
+        if (sync_any(!ok)) break;
+        if (warp == 0 && elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
+            if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc);
+            else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc);
+          }
+          mma_commit(s_done);
+        }
+        __syncwarp();
+        ok = warp_wait(s_done, it & 1u, abort_flag);
         tc_fence_after();
         const int key = (s.tile0 + j) * kTileKeys + th;
         const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
         float v[N];
-        // Scores in units of log 2, those of keys that a row does not see -inf.
-        auto load = [&]() {
+        bool grow = j == 0, again = false;
+#pragma unroll 1
+        for (;;) {
+          // Scores in units of log 2, those of keys that a row does not see -inf.
           tmem_ld_n<N>(s_t, v);
           tmem_wait_ld();
 #pragma unroll
@@ -689,92 +553,109 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
                 }
               }
           }
-        };
-        auto minus_max = [&]() {
+          if (grow) {
+            // the maximum moves to the largest score so far
+#pragma unroll
+            for (int r4 = 0; r4 < N; r4 += 4)
+              if (r4 < rows) {
+#pragma unroll
+                for (int r = r4; r < r4 + 4; ++r) {
+                  const float top = warp_max(v[r]);
+                  if (lane == 0) parts[warp * N + r] = top;
+                }
+              }
+            sync_any(false);
+#pragma unroll
+            for (int r4 = 0; r4 < N; r4 += 4)
+              if (r4 < rows) {
+                float o[4] = {};
+                if (j > 0) {
+                  tmem_ld_4(o_t + r4, o);
+                  tmem_wait_ld();
+                }
+#pragma unroll
+                for (int r = r4; r < r4 + 4; ++r) {
+                  const float m = mr[r];
+                  const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[N + r])), fmaxf(parts[2 * N + r], parts[3 * N + r]));
+                  const float alpha = ex2_approx(m - m2);
+                  l[r] *= alpha;
+                  o[r - r4] *= alpha;
+                }
+                if (j > 0) tmem_st_4(o_t + r4, o);
+              }
+            if (j > 0) tmem_wait_st();
+            sync_any(false);                       // all have read the old maxima
+            if (th < ((rows + 3) & ~3)) {
+              const float m = fmaxf(fmaxf(parts[th], parts[N + th]), fmaxf(parts[2 * N + th], parts[3 * N + th]));
+              mr[th] = fmaxf(mr[th], m);
+            }
+            sync_any(false);
+          }
+          float top = -INFINITY;
 #pragma unroll
           for (int r4 = 0; r4 < N; r4 += 4)
             if (r4 < rows) {
               const float4 m = *reinterpret_cast<const float4*>(mr + r4);
-              v[r4] -= m.x; v[r4 + 1] -= m.y; v[r4 + 2] -= m.z; v[r4 + 3] -= m.w;
-            }
-        };
-        load();
-        bool grow = j == j0;
-        if (!grow) {
-          minus_max();
-          float top = -INFINITY;
+              const float e[4] = {v[r4] - m.x, v[r4 + 1] - m.y, v[r4 + 2] - m.z, v[r4 + 3] - m.w};
+              top = max3f(max3f(top, e[0], e[1]), e[2], e[3]);
 #pragma unroll
-          for (int r4 = 0; r4 < N; r4 += 4)
-            if (r4 < rows) top = max3f(max3f(top, v[r4], v[r4 + 1]), v[r4 + 2], v[r4 + 3]);
-          // weights of up to 2^8 are as exact as others; above, the maximum moves
-          if (__any_sync(0xffffffffu, top > 8.f) && lane == 0) grow_mark[w] = (int)job + 1;
-          if (!(ok = sync(abort_flag))) break;
-          grow = grow_mark[w] == (int)job + 1;
-          if (grow) load();
-        }
-        // P V of the group's job before is done: its P may be overwritten, O read
-        if (!(ok = warp_wait(pv_done + 8 * w, u ^ 1u, abort_flag))) break;
-        if (grow) {
-          tc_fence_after();
-#pragma unroll
-          for (int r4 = 0; r4 < N; r4 += 4)
-            if (r4 < rows) {
-#pragma unroll
-              for (int r = r4; r < r4 + 4; ++r) {
-                const float top = warp_max(v[r]);
-                if (lane == 0) parts[wq * N + r] = top;
+              for (int x = 0; x < 4; x += 2) {
+                const int r = r4 + x;
+                v[r] = ex2_approx(e[x]);
+                v[r + 1] = ex2_approx(e[x + 1]);
+                // The weights meet V in bf16; their sum is of the unrounded ones.
+                const uint32_t both = pack_bf16x2(v[r], v[r + 1]);
+                sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
+                sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
               }
             }
-          if (!(ok = sync(abort_flag))) break;
+          if (!again && th < D) {
+            // V over K, whose product is done
+            uint32_t from = v_tile + th * 8, scale_at = vscale + (th / kGroup) * (kTileKeys * 2);
+#pragma unroll 1
+            for (int x = 0; x < kTileBlocks; x += 2) {
+              uint32_t r[16];
 #pragma unroll
-          for (int r4 = 0; r4 < N; r4 += 4)
-            if (r4 < rows) {
-              float o[4] = {};
-              if (j != j0) {
-                tmem_ld_4(o_t + r4, o);
-                tmem_wait_ld();
-              }
+              for (int y = 0; y < 2; ++y, from += block_bytes(D), scale_at += 32) {
+                const uint2 c = lds64(from);
+                const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
+                const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-              for (int r = r4; r < r4 + 4; ++r) {
-                const float m = mr[r];
-                const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[N + r])), fmaxf(parts[2 * N + r], parts[3 * N + r]));
-                const float alpha = ex2_approx(m - m2);
-                l[r] *= alpha;
-                o[r - r4] *= alpha;
+                for (int i = 0; i < 8; ++i)
+                  r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
               }
-              if (j != j0) tmem_st_4(o_t + r4, o);
+              tmem_st16(a_t + x * 8, r);
             }
-          if (j != j0) tmem_wait_st();
-          if (!(ok = sync(abort_flag))) break;     // all have read the old maxima
-          if (th < ((rows + 3) & ~3)) {
-            const float m = fmaxf(fmaxf(parts[th], parts[N + th]), fmaxf(parts[2 * N + th], parts[3 * N + th]));
-            mr[th] = fmaxf(mr[th], m);
+            tmem_wait_st();
           }
-          if (!(ok = sync(abort_flag))) break;
-          minus_max();
+          fence_async_shared();
+          tc_fence_before();
+          // Weights of up to 2^8 are as exact as others; above, the maximum moves and
+          // they are taken again.
+          grow = sync_any(top > 8.f || !ok);
+          if (!grow || again) break;
+          again = true;
+          if (sync_any(!ok)) break;
         }
-        tc_fence_before();
+        if (lane == 0) mbar_arrive(v_empty + 8 * vs);
+        if (grow) break;                           // some wait gave up
+        if (warp == 0 && elect_one()) {
+          tc_fence_after();
+          mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc, j > 0);
+#pragma unroll
+          for (int kk = 1; kk < kTileKeys / 16; ++kk)
+            mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
+          mma_commit(pv_done);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_empty + 8 * w);
 #pragma unroll
         for (int r4 = 0; r4 < N; r4 += 4)
           if (r4 < rows) {
 #pragma unroll
-            for (int r = r4; r < r4 + 4; r += 2) {
-              const float a = ex2_approx(v[r]), b = ex2_approx(v[r + 1]);
-              l[r] += a;
-              l[r + 1] += b;
-              // The weights meet V in bf16; their sum is of the unrounded ones.
-              const uint32_t both = pack_bf16x2(a, b);
-              sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
-              sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
-            }
+            for (int r = r4; r < r4 + 4; ++r) l[r] += v[r];
           }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * w);
       }
-      if (!ok) break;
+      if (j < tiles) break;
       // sums over the keys of a warp, then of the four
 #pragma unroll
       for (int r4 = 0; r4 < N; r4 += 4)
@@ -783,45 +664,70 @@ __global__ void __launch_bounds__(kThreads, 1) quant_attention_kernel(const __gr
           for (int r = r4; r < r4 + 4; ++r) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-            if (lane == 0) parts[wq * N + r] = l[r];
+            if (lane == 0) parts[warp * N + r] = l[r];
           }
         }
-      if (!(ok = sync(abort_flag))) break;
+      ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag);
+      if (sync_any(!ok)) break;
+      tc_fence_after();
+      const bool direct = p.pre_tiles == 0 && s.whole;
       if (th < rows) {
         const float sum = (parts[th] + parts[N + th]) + (parts[2 * N + th] + parts[3 * N + th]);
         // no score above kLowest: nothing is left, or NaN
-        ml[th] = make_float2(mr[th] > kLowest ? mr[th] : sum == 0.f ? -INFINITY : 0.f, sum);
+        const float m = mr[th] > kLowest ? mr[th] : sum == 0.f ? -INFINITY : 0.f;
+        if (!direct) {
+          reinterpret_cast<float2*>(p.part_ml)[(s.b < 0 ? 0 : p.own_first) +
+                                               s.slot * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows) + th] = make_float2(m, sum);
+        } else if (p.lse) {
+          const int rem = rem0 + th, i = p.div_G.quot(rem), g = rem - i * p.G;
+          p.lse[((int64_t)s.b * p.Hq + s.hk * p.G + g) * p.T + i] = row_lse(seen_keys(p, s.kv, s.n, i) > 0, m, sum);
+        }
       }
-      const uint32_t last = q + (uint32_t)(tiles - 1 - ((tiles - 1 - j0) & 1));      // this group's last job
-      if (!(ok = warp_wait(pv_done + 8 * w, last >> 1 & 1u, abort_flag))) break;
-      tc_fence_after();
-      float o[N];
-      tmem_ld_n<N>(o_t, o);
-      tmem_wait_ld();
-      if (th < D) {
-        float* dst = p.part_o + (int64_t)at * D + th;
+      {
+        float o[N];
+        tmem_ld_n<N>(o_t, o);
+        tmem_wait_ld();
+        if (th < D) {
+          if (!direct) {
+            float* dst = p.part_o + (int64_t)((s.b < 0 ? 0 : p.own_first) +
+                                              s.slot * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows)) * D + th;
 #pragma unroll
-        for (int r = 0; r < N; ++r)
-          if (r < rows) dst[r * D] = o[r];
+            for (int r = 0; r < N; ++r)
+              if (r < rows) dst[r * D] = o[r];
+          } else {
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+              if (r < rows) {
+                const int rem = rem0 + r, i = p.div_G.quot(rem), g = rem - i * p.G;
+                const float inv = inverse_sum(seen_keys(p, s.kv, s.n, i) > 0,
+                                              (parts[r] + parts[N + r]) + (parts[2 * N + r] + parts[3 * N + r]));
+                p.out[(((int64_t)s.b * p.T + i) * p.Hq + s.hk * p.G + g) * D + th] = __float2bfloat16(inv != 0.f ? o[r] * inv : 0.f);
+              }
+          }
+        }
       }
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty + 8 * w);
-      q += tiles;
       t += tiles;
-      reader.release(seg_empty);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(seg_empty + 8 * qb);
     }
+    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
+    if (warp == 0 && elect_one()) {
+      mma_commit(pv_done);
+      mbar_drain(pv_done, it & 1u);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kColumns);
   }
 }
 
 // Output row (b, i, h): joins the partial results of its prefix segment and of its
-// own segment, two from each CTA.
+// own segment, one from each CTA.
 template <int D, int N, int kLanes, int kWarps>
 __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_kernel(const __grid_constant__ QAttnParams p) {
   constexpr int kRows = kWarps > 1 ? 1 : 128 / kLanes;   // rows per block
@@ -835,6 +741,12 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Parts pre{0, 0, 0}, own{0, 0, 0};
+  bool direct = false;
+  // CTAs first .. last have a part each; a pair that no schedule makes (a wait gave up) none
+  auto partial = [&](const int2& c, int seg, int slot_rows, int r) {
+    if (c.x < 0 || c.y < c.x || c.y >= p.ctas) return Parts{0, 0, 0};
+    return Parts{c.y - c.x + 1, (seg + c.x) * slot_rows + r, slot_rows};
+  };
   const bool keyed = real && i < n && (p.prefix_len > 0 || seen_keys(p, kv, n, i) > 0);
   if (real && i < n) {
     const int row = i * p.G + g, flat = b * p.TG + row;
@@ -842,15 +754,16 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
     const int rt = row / N, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
     if (p.pre_tiles > 0) {
       const int2 c = p.seg_ctas[pre_seg];
-      pre = segment_parts(c.x, c.y, p.ctas, pre_seg, true, 0, p.pre_slot_rows, flat % N);
+      pre = partial(c, pre_seg, p.pre_slot_rows, flat % N);
     }
     if (own_tiles<N>(p, kv, n, rt) > 0) {
       const int2 c = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
-      own = segment_parts(c.x, c.y, p.ctas, own_seg, true, 0, p.own_slot_rows, row % N);
+      own = partial(c, own_seg, p.own_slot_rows, row % N);
       own.at += p.own_first;
+      direct = p.pre_tiles == 0 && own.n == 1;       // written by the first kernel
     }
   }
-  join_row<D, kLanes, kWarps>(p.part_ml, p.part_o, pre, own, real, keyed, p.out + R * D,
+  join_row<D, kLanes, kWarps>(p.part_ml, p.part_o, pre, own, real && !direct, keyed, p.out + R * D,
                               p.lse ? p.lse + ((int64_t)b * p.Hq + h) * p.T + i : nullptr);
 }
 
@@ -872,9 +785,9 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   w.own_slot_rows = w.TG < w.N ? w.TG : w.N;
   w.pre_slot_rows = (int)(B * w.TG < w.N ? B * w.TG : w.N);
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  // a slot of two partial results for every number segment + CTA
-  const size_t own = (size_t)(B * Hkv * w.own_rt + sms) * 2 * w.own_slot_rows;
-  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + sms) * 2 * w.pre_slot_rows : 0;
+  // a partial result for every number segment + CTA
+  const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
+  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + kCtasPerSm * sms) * w.pre_slot_rows : 0;
   w.own_first = pre;
   w.part_ml = al((size_t)Hkv * (w.pre_rt + B * w.own_rt) * 8);      // behind the segments' CTAs
   w.part_o = w.part_ml + al((pre + own) * 8);
@@ -1021,7 +934,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
   p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
-  p.ctas = sms;
+  p.ctas = kCtasPerSm * sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
