@@ -54,6 +54,10 @@ __device__ __forceinline__ uint32_t code_values(uint32_t raised, uint32_t scales
 __device__ __forceinline__ uint32_t scale_offset(uint32_t scales2) {
   return as_u32(__hmul2(as_bf16x2(scales2), as_bf16x2(0xC140C140u)));        // times -12
 }
+// Two codes, halved.
+__device__ __forceinline__ uint32_t half_codes(uint32_t raised) {
+  return as_u32(__hadd2(as_bf16x2(raised), as_bf16x2(0xC140C140u)));         // minus 12
+}
 #endif
 
 }  // namespace bsa

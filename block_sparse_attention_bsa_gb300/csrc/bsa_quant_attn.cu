@@ -47,18 +47,25 @@ constexpr int kCtasPerSm = 4;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
 constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
 
-template <int D, int N>
+// R: rows of a segment.  kScaled: the scales of V stand in the weights, of which
+// there is a set for each group of 32 channels, and V is made of the codes alone;
+// else they are multiplied into V.
+template <int D, int R, bool kScaled>
 struct Cfg {
-  static constexpr int kQBytes = N * D * 2;
-  static constexpr int kPBytes = N * kTileKeys * 2;
+  static constexpr int kGroups = D / kGroup;
+  static constexpr int kSCols = R < 16 ? 16 : R;                       // columns of S (16 at least)
+  static constexpr int kSets = kScaled ? kGroups : 1;
+  static constexpr int kOCols = kSets * R < 16 ? 16 : kSets * R;       // columns of O, rows of P
+  static constexpr int kQBytes = kSCols * D * 2;
+  static constexpr int kPBytes = kOCols * kTileKeys * 2;
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
-  static constexpr int kKSlots = 2, kVSlots = N == 16 ? 2 : 1;
-  static constexpr int kScaleBytes = (D / kGroup) * kTileKeys * 2;
+  static constexpr int kKSlots = 2, kVSlots = R <= 16 ? 2 : 1;
+  static constexpr int kScaleBytes = kScaled ? 0 : kGroups * kTileKeys * 2;
   static constexpr int kBarBytes = 2048;
   static constexpr int kSmemBytes = 1024 + 2 * kQBytes + kPBytes + (kKSlots + kVSlots) * kTileBytes + kScaleBytes + kBarBytes;
   // TMEM columns: K, then V; S; O
-  static constexpr int kA = 0, kS = 64, kO = 64 + N, kColumns = 128;
-  static_assert(kO + N <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
+  static constexpr int kA = 0, kS = 64, kO = kS + kSCols, kColumns = 128;
+  static_assert(kO + kOCols <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
 };
 
 struct QAttnParams {
@@ -68,6 +75,7 @@ struct QAttnParams {
   int64_t q_sb, q_ss, q_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
   FastDiv div_G, div_TG;
+  int R;                          // rows of a segment
   int TG;                         // rows of a request under one KV head
   int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
@@ -99,19 +107,17 @@ __device__ __forceinline__ int seen_keys(const QAttnParams& p, int kv, int n, in
   return p.causal ? min(max(kv - n + i + 1, 0), kv) : kv;
 }
 // Key tiles of row tile rt of such a request.
-template <int N>
 __device__ __forceinline__ int own_tiles(const QAttnParams& p, int kv, int n, int rt) {
-  const int first = p.div_G.quot(rt * N);
+  const int first = p.div_G.quot(rt * p.R);
   if (first >= n) return 0;
-  const int last = min(n - 1, p.div_G.quot(rt * N + N - 1));
+  const int last = min(n - 1, p.div_G.quot(rt * p.R + p.R - 1));
   return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
 }
 // Key tiles of a request under one KV head.
-template <int N>
 __device__ __forceinline__ int request_tiles(const QAttnParams& p, int kv, int n) {
   int sum = 0;
 #pragma unroll 1
-  for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles<N>(p, kv, n, rt);
+  for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles(p, kv, n, rt);
   return sum;
 }
 
@@ -156,11 +162,24 @@ __device__ __forceinline__ bool sync_any(bool mine) {
   return r != 0;
 }
 
-// N consecutive 32-bit columns of this thread's lane.
+// 4, 8, 16 or 32 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld_4(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float* r) {
   if constexpr (N == 32) {
     tmem_ld32f(taddr, r);
+  } else if constexpr (N == 4) {
+    tmem_ld_4(taddr, r);
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
   } else {
     static_assert(N == 16, "");
     asm volatile(
@@ -171,12 +190,6 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, float* r) {
         : "r"(taddr)
         : "memory");
   }
-}
-__device__ __forceinline__ void tmem_ld_4(uint32_t taddr, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-               : "r"(taddr)
-               : "memory");
 }
 __device__ __forceinline__ void tmem_st_4(uint32_t taddr, const float* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "f"(r[0]), "f"(r[1]), "f"(r[2]),
@@ -210,9 +223,9 @@ __device__ __forceinline__ float warp_max(float z) {
   return __int_as_float(u ^ (u >> 31 & 0x7FFFFFFF));
 }
 
-template <int D, int N>
+template <int D, int R, bool kScaled>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
-  using C = Cfg<D, N>;
+  using C = Cfg<D, R, kScaled>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -222,9 +235,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t v_ring = k_ring + C::kKSlots * C::kTileBytes;         // [kVSlots] blocks of V
   const uint32_t vscale = v_ring + C::kVSlots * C::kTileBytes;         // [D / 32][128] twice the scales of V, bf16
   uint8_t* rest = smem + (vscale - q_smem) + C::kScaleBytes;
-  float* mr = reinterpret_cast<float*>(rest);                          // [N] running maxima
-  float* parts = mr + N;                                               // [4][N] of each warp
-  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * N);           // [2]
+  float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
+  float* parts = mr + R;                                               // [4][R] of each warp
+  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [2]
   int* block_sum = reinterpret_cast<int*>(segs + 2);                   // [kMaxBlocks] tiles of own keys before request 32 i
   int* total_slot = block_sum + kMaxBlocks;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
@@ -238,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t v_empty = seg_full + 80;              // [2] 4 warps
   const uint32_t s_done = seg_full + 96;               // commit
   const uint32_t pv_done = seg_full + 104;             // commit
-  static_assert((5 * N + kMaxBlocks + 4) * 4 + 2 * sizeof(Segment) + 112 <= C::kBarBytes, "barrier block");
+  static_assert((5 * R + kMaxBlocks + 4) * 4 + 2 * sizeof(Segment) + 112 <= C::kBarBytes, "barrier block");
   const uint32_t abort_flag = smem_u32(abort_slot);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;      // known to be uniform
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -269,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll 1
   for (int blk = warp; blk < nblk; blk += kThreads / 32) {
     const int b = blk * 32 + lane;
-    const int mine = b < p.B ? request_tiles<N>(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
+    const int mine = b < p.B ? request_tiles(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
     const int incl = warp_inclusive_sum(mine);
     if (lane == 31) block_sum[blk] = incl;
     if (cta == 0 && b < p.B && p.max_pages > 0) {
@@ -327,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         t1 = t0 + p.pre_tiles;
         s.b = -1;
         s.hk = seg / p.pre_rt;
-        s.row0 = (seg - s.hk * p.pre_rt) * N;
-        s.rows = min(N, p.B * p.TG - s.row0);
+        s.row0 = (seg - s.hk * p.pre_rt) * R;
+        s.rows = min(R, p.B * p.TG - s.row0);
         s.slot = seg + cta;
         s.keys = p.prefix_len;
         s.kv = s.n = 0;
@@ -340,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           const int b = blk * 32 + lane;
           kv = b < p.B ? own_keys(p, b) : 0;
           n = b < p.B ? new_tokens(p, b) : 0;
-          mine = b < p.B ? request_tiles<N>(p, kv, n) : 0;
+          mine = b < p.B ? request_tiles(p, kv, n) : 0;
           upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
           blk_end = __shfl_sync(0xffffffffu, upto, 31);
         }
@@ -352,15 +365,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         s.n = __shfl_sync(0xffffffffu, n, src);
         s.hk = (u - first) / per_head;
         t0 = pre + first + s.hk * per_head;
-        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles<N>(p, s.kv, s.n, 0);
+        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles(p, s.kv, s.n, 0);
 #pragma unroll 1
         while (t >= t0 + m) {
           t0 += m;
-          m = own_tiles<N>(p, s.kv, s.n, ++rt);
+          m = own_tiles(p, s.kv, s.n, ++rt);
         }
         t1 = t0 + m;
-        s.row0 = s.b * p.TG + rt * N;
-        s.rows = min(N, s.n * p.G - rt * N);
+        s.row0 = s.b * p.TG + rt * R;
+        s.rows = min(R, s.n * p.G - rt * R);
         seg = (s.b * p.Hkv + s.hk) * p.own_rt + rt;
         s.slot = seg + cta;
         s.keys = s.kv;
@@ -382,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       // Q rows, and rows of zeros up to a multiple of four
       {
         const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
-        const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (N * 128) + (lane / kVec) * 128;
+        const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (C::kSCols * 128) + (lane / kVec) * 128;
         const int row = s.row0 + min(lane, s.rows - 1);
         const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
         const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
@@ -454,12 +467,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // ------------------------------------------- codes, products, weights, results ---
     const int th = threadIdx.x;                    // key of a tile, and channel of V and O
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t a_t = tmem + lanes + C::kA, s_t = tmem + lanes + C::kS, o_t = tmem + lanes + C::kO;
+    const uint32_t a_t = tmem + lanes + C::kA, s_t = tmem + lanes + C::kS;
+    // of a set of weights for each group, the columns of this channel's
+    const uint32_t o_t = tmem + lanes + C::kO + (kScaled ? warp % C::kGroups * R : 0);
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
     // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
-    const uint32_t p_at = p_smem + (th / 64) * (N * 128) + th % 64 * 2;
-    constexpr uint32_t idesc = idesc_bf16_f32(128, N, false);
-    constexpr int kChunk = (N * 128) >> 4;
+    const uint32_t p_at = p_smem + (th / 64) * (C::kOCols * 128) + th % 64 * 2;
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kSCols, false), idesc_o = idesc_bf16_f32(128, C::kOCols, false);
+    constexpr int kQChunk = (C::kSCols * 128) >> 4, kPChunk = (C::kOCols * 128) >> 4;
     const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       ok = warp_wait(seg_full + 8 * qb, seg_no >> 1 & 1u, abort_flag);
       fence_async_shared();                        // Q rows come by ordinary copies
       const Segment& s = segs[qb];                 // stays there until all are through with it
-      if (th < N) mr[th] = kLowest;
+      if (th < R) mr[th] = kLowest;
       if (sync_any(!ok)) break;
       const int rows = s.rows, tiles = s.tiles;
       // the keys of the first row; further rows' rise with the token
@@ -476,9 +491,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       const bool even = s.b < 0 || !p.causal;
       const int least = even ? s.keys : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0));
       const uint64_t qdesc = sdesc_sw128(q_smem + qb * C::kQBytes, 16, 1024);
-      float l[N];
+      float l[R];
 #pragma unroll
-      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      for (int r = 0; r < R; ++r) l[r] = 0.f;
       int j = 0;
 #pragma unroll 1
       for (; j < tiles; ++j, ++it) {
@@ -506,45 +521,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         __syncwarp();
         if (lane == 0) mbar_arrive(k_empty + 8 * ks);
         // twice the scales of V, 0 behind the last key: what stands there must not count
-        ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag) && ok;
+        if constexpr (!kScaled) {
+          ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag) && ok;
 #pragma unroll
-        for (int g = 0; g < D / kGroup; ++g)
-          sts16(vscale + (g * kTileKeys + th) * 2,
-                th < tile_keys ? twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u);
+          for (int g = 0; g < C::kGroups; ++g)
+            sts16(vscale + (g * kTileKeys + th) * 2,
+                  th < tile_keys ? twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u);
+        }
         tmem_wait_st();
         tc_fence_before();
         if (sync_any(!ok)) break;
-        if (warp == 0 && elect_one()) {
+        if (warp == 0) {                           // all of it, so that the descriptors stay in uniform registers
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
-            if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc);
-            else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)((kk / 4) * kQChunk + (kk % 4) * 2);
+              if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc_s);
+              else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc_s);
+            }
+            mma_commit(s_done);
           }
-          mma_commit(s_done);
+          __syncwarp();
         }
-        __syncwarp();
-        ok = warp_wait(s_done, it & 1u, abort_flag);
+        float vs2[C::kSets];                       // of this key
+        if constexpr (kScaled) {
+          ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag);
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g)
+            vs2[g] = th < tile_keys
+                         ? __uint_as_float(twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) << 16)
+                         : 0.f;
+        }
+        ok = warp_wait(s_done, it & 1u, abort_flag) && ok;
         tc_fence_after();
         const int key = (s.tile0 + j) * kTileKeys + th;
         const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
-        float v[N];
+        float v[R];
         bool grow = j == 0, again = false;
 #pragma unroll 1
         for (;;) {
           // Scores in units of log 2, those of keys that a row does not see -inf.
-          tmem_ld_n<N>(s_t, v);
+          tmem_ld_n<R>(s_t, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int r4 = 0; r4 < N; r4 += 4)
+          for (int r4 = 0; r4 < R; r4 += 4)
             if (r4 < rows) {
 #pragma unroll
               for (int r = r4; r < r4 + 4; ++r) v[r] *= p.scale_log2;
             }
           if (cut) {
 #pragma unroll
-            for (int r4 = 0; r4 < N; r4 += 4)
+            for (int r4 = 0; r4 < R; r4 += 4)
               if (r4 < rows) {
 #pragma unroll
                 for (int r = r4; r < r4 + 4; ++r) {
@@ -556,17 +584,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           if (grow) {
             // the maximum moves to the largest score so far
 #pragma unroll
-            for (int r4 = 0; r4 < N; r4 += 4)
+            for (int r4 = 0; r4 < R; r4 += 4)
               if (r4 < rows) {
 #pragma unroll
                 for (int r = r4; r < r4 + 4; ++r) {
                   const float top = warp_max(v[r]);
-                  if (lane == 0) parts[warp * N + r] = top;
+                  if (lane == 0) parts[warp * R + r] = top;
                 }
               }
             sync_any(false);
 #pragma unroll
-            for (int r4 = 0; r4 < N; r4 += 4)
+            for (int r4 = 0; r4 < R; r4 += 4)
               if (r4 < rows) {
                 float o[4] = {};
                 if (j > 0) {
@@ -576,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
                 for (int r = r4; r < r4 + 4; ++r) {
                   const float m = mr[r];
-                  const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[N + r])), fmaxf(parts[2 * N + r], parts[3 * N + r]));
+                  const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[R + r])), fmaxf(parts[2 * R + r], parts[3 * R + r]));
                   const float alpha = ex2_approx(m - m2);
                   l[r] *= alpha;
                   o[r - r4] *= alpha;
@@ -586,28 +614,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             if (j > 0) tmem_wait_st();
             sync_any(false);                       // all have read the old maxima
             if (th < ((rows + 3) & ~3)) {
-              const float m = fmaxf(fmaxf(parts[th], parts[N + th]), fmaxf(parts[2 * N + th], parts[3 * N + th]));
+              const float m = fmaxf(fmaxf(parts[th], parts[R + th]), fmaxf(parts[2 * R + th], parts[3 * R + th]));
               mr[th] = fmaxf(mr[th], m);
             }
             sync_any(false);
           }
           float top = -INFINITY;
 #pragma unroll
-          for (int r4 = 0; r4 < N; r4 += 4)
+          for (int r4 = 0; r4 < R; r4 += 4)
             if (r4 < rows) {
               const float4 m = *reinterpret_cast<const float4*>(mr + r4);
               const float e[4] = {v[r4] - m.x, v[r4 + 1] - m.y, v[r4 + 2] - m.z, v[r4 + 3] - m.w};
               top = max3f(max3f(top, e[0], e[1]), e[2], e[3]);
 #pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                const int r = r4 + x;
-                v[r] = ex2_approx(e[x]);
-                v[r + 1] = ex2_approx(e[x + 1]);
-                // The weights meet V in bf16; their sum is of the unrounded ones.
-                const uint32_t both = pack_bf16x2(v[r], v[r + 1]);
-                sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
-                sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
-              }
+              for (int x = 0; x < 4; ++x) v[r4 + x] = ex2_approx(e[x]);
+              // The weights meet V in bf16; their sum is of the unrounded ones.
+#pragma unroll
+              for (int g = 0; g < C::kSets; ++g)
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                  const int r = g * R + r4 + x;
+                  const uint32_t both = kScaled ? pack_bf16x2(v[r4 + x] * vs2[g], v[r4 + x + 1] * vs2[g])
+                                                : pack_bf16x2(v[r4 + x], v[r4 + x + 1]);
+                  sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
+                  sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
+                }
             }
           if (!again && th < D) {
             // V over K, whose product is done
@@ -618,11 +649,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
               for (int y = 0; y < 2; ++y, from += block_bytes(D), scale_at += 32) {
                 const uint2 c = lds64(from);
-                const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
-                const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+                if constexpr (kScaled) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
+                  for (int i = 0; i < 8; ++i) r[y * 8 + i] = half_codes(raised_codes(i < 4 ? c.x : c.y, i % 4));
+                } else {
+                  const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
+                  const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
+                }
               }
               tmem_st16(a_t + x * 8, r);
             }
@@ -639,17 +675,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
         if (lane == 0) mbar_arrive(v_empty + 8 * vs);
         if (grow) break;                           // some wait gave up
-        if (warp == 0 && elect_one()) {
+        if (warp == 0) {
           tc_fence_after();
-          mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc, j > 0);
+          if (elect_one()) {
+            mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc_o, j > 0);
 #pragma unroll
-          for (int kk = 1; kk < kTileKeys / 16; ++kk)
-            mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
-          mma_commit(pv_done);
+            for (int kk = 1; kk < kTileKeys / 16; ++kk)
+              mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kPChunk + (kk % 4) * 2), idesc_o);
+            mma_commit(pv_done);
+          }
+          __syncwarp();
         }
-        __syncwarp();
 #pragma unroll
-        for (int r4 = 0; r4 < N; r4 += 4)
+        for (int r4 = 0; r4 < R; r4 += 4)
           if (r4 < rows) {
 #pragma unroll
             for (int r = r4; r < r4 + 4; ++r) l[r] += v[r];
@@ -658,13 +696,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       if (j < tiles) break;
       // sums over the keys of a warp, then of the four
 #pragma unroll
-      for (int r4 = 0; r4 < N; r4 += 4)
+      for (int r4 = 0; r4 < R; r4 += 4)
         if (r4 < rows) {
 #pragma unroll
           for (int r = r4; r < r4 + 4; ++r) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-            if (lane == 0) parts[warp * N + r] = l[r];
+            if (lane == 0) parts[warp * R + r] = l[r];
           }
         }
       ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag);
@@ -672,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       tc_fence_after();
       const bool direct = p.pre_tiles == 0 && s.whole;
       if (th < rows) {
-        const float sum = (parts[th] + parts[N + th]) + (parts[2 * N + th] + parts[3 * N + th]);
+        const float sum = (parts[th] + parts[R + th]) + (parts[2 * R + th] + parts[3 * R + th]);
         // no score above kLowest: nothing is left, or NaN
         const float m = mr[th] > kLowest ? mr[th] : sum == 0.f ? -INFINITY : 0.f;
         if (!direct) {
@@ -684,23 +722,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
       }
       {
-        float o[N];
-        tmem_ld_n<N>(o_t, o);
+        float o[R];
+        tmem_ld_n<R>(o_t, o);
         tmem_wait_ld();
         if (th < D) {
           if (!direct) {
             float* dst = p.part_o + (int64_t)((s.b < 0 ? 0 : p.own_first) +
                                               s.slot * (s.b < 0 ? p.pre_slot_rows : p.own_slot_rows)) * D + th;
 #pragma unroll
-            for (int r = 0; r < N; ++r)
+            for (int r = 0; r < R; ++r)
               if (r < rows) dst[r * D] = o[r];
           } else {
 #pragma unroll
-            for (int r = 0; r < N; ++r)
+            for (int r = 0; r < R; ++r)
               if (r < rows) {
                 const int rem = rem0 + r, i = p.div_G.quot(rem), g = rem - i * p.G;
                 const float inv = inverse_sum(seen_keys(p, s.kv, s.n, i) > 0,
-                                              (parts[r] + parts[N + r]) + (parts[2 * N + r] + parts[3 * N + r]));
+                                              (parts[r] + parts[R + r]) + (parts[2 * R + r] + parts[3 * R + r]));
                 p.out[(((int64_t)s.b * p.T + i) * p.Hq + s.hk * p.G + g) * D + th] = __float2bfloat16(inv != 0.f ? o[r] * inv : 0.f);
               }
           }
@@ -728,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 
 // Output row (b, i, h): joins the partial results of its prefix segment and of its
 // own segment, one from each CTA.
-template <int D, int N, int kLanes, int kWarps>
+template <int D, int kLanes, int kWarps>
 __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_kernel(const __grid_constant__ QAttnParams p) {
   constexpr int kRows = kWarps > 1 ? 1 : 128 / kLanes;   // rows per block
   const int64_t R = (int64_t)blockIdx.x * kRows + (kWarps > 1 ? 0 : threadIdx.x / kLanes);
@@ -750,15 +788,15 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
   const bool keyed = real && i < n && (p.prefix_len > 0 || seen_keys(p, kv, n, i) > 0);
   if (real && i < n) {
     const int row = i * p.G + g, flat = b * p.TG + row;
-    const int pre_seg = hk * p.pre_rt + flat / N;
-    const int rt = row / N, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
+    const int pre_seg = hk * p.pre_rt + flat / p.R;
+    const int rt = row / p.R, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
     if (p.pre_tiles > 0) {
       const int2 c = p.seg_ctas[pre_seg];
-      pre = partial(c, pre_seg, p.pre_slot_rows, flat % N);
+      pre = partial(c, pre_seg, p.pre_slot_rows, flat % p.R);
     }
-    if (own_tiles<N>(p, kv, n, rt) > 0) {
+    if (own_tiles(p, kv, n, rt) > 0) {
       const int2 c = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
-      own = partial(c, own_seg, p.own_slot_rows, row % N);
+      own = partial(c, own_seg, p.own_slot_rows, row % p.R);
       own.at += p.own_first;
       direct = p.pre_tiles == 0 && own.n == 1;       // written by the first kernel
     }
@@ -771,7 +809,7 @@ std::string s(int64_t v) { return std::to_string(v); }
 
 // Rows of a segment, and where the partial results lie in the workspace.
 struct QAttnPlan {
-  int N, TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
+  int R, TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
   size_t own_first, part_ml, part_o, bytes;
 };
 
@@ -779,11 +817,11 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   QAttnPlan w{};
   w.TG = (int)(T * (Hq / Hkv));
   const int64_t most = prefix ? B * w.TG : w.TG;
-  w.N = most <= 16 ? 16 : 32;
-  w.own_rt = (int)cdiv64(w.TG, w.N);
-  w.pre_rt = prefix ? (int)cdiv64(B * w.TG, w.N) : 0;
-  w.own_slot_rows = w.TG < w.N ? w.TG : w.N;
-  w.pre_slot_rows = (int)(B * w.TG < w.N ? B * w.TG : w.N);
+  w.R = most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  w.own_rt = (int)cdiv64(w.TG, w.R);
+  w.pre_rt = prefix ? (int)cdiv64(B * w.TG, w.R) : 0;
+  w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
+  w.pre_slot_rows = (int)(B * w.TG < w.R ? B * w.TG : w.R);
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // a partial result for every number segment + CTA
   const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
@@ -795,7 +833,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   return w;
 }
 
-template <int D, int N>
+template <int D, int R, bool kScaled>
 bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
@@ -805,8 +843,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Cfg<D, N>::kSmemBytes),
+      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, R, kScaled>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Cfg<D, R, kScaled>::kSmemBytes),
                       "cudaFuncSetAttribute(quant_attention_kernel)");
       if (st != BSA_OK) return st;
       if (dev < 64) done[dev] = true;
@@ -821,8 +859,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<D, N>::kSmemBytes;
-  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, N>, p), "quant_attention_kernel launch")) != BSA_OK)
+  cfg.dynamicSmemBytes = Cfg<D, R, kScaled>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, R, kScaled>, p), "quant_attention_kernel launch")) != BSA_OK)
     return st;
   // Eight warps, one warp or eight lanes a row, as in the join of bsa_paged.cu.
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
@@ -830,9 +868,9 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   cfg.blockDim = dim3(lanes == 256 ? 256 : 128);
   cfg.gridDim = dim3((unsigned)cdiv64(rows, cfg.blockDim.x / lanes));
   cfg.dynamicSmemBytes = 0;
-  return cuda_check(lanes == 256  ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 32, 8>, p)
-                    : lanes == 32 ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 32, 1>, p)
-                                  : cudaLaunchKernelEx(&cfg, quant_join_kernel<D, N, 8, 1>, p),
+  return cuda_check(lanes == 256  ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, 32, 8>, p)
+                    : lanes == 32 ? cudaLaunchKernelEx(&cfg, quant_join_kernel<D, 32, 1>, p)
+                                  : cudaLaunchKernelEx(&cfg, quant_join_kernel<D, 8, 1>, p),
                     "quant_join_kernel launch");
 }
 
@@ -931,7 +969,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   while ((1 << p.page_shift) < page) ++p.page_shift;
   p.num_pages = (int)a.k.pages; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
   p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
-  p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
+  p.R = plan.R; p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
   p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = kCtasPerSm * sms;
@@ -945,8 +983,10 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
   p.own_first = (int)plan.own_first;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (plan.N == 16) return qv.D == 128 ? launch_quant<128, 16>(p, cs) : launch_quant<64, 16>(p, cs);
-  return qv.D == 128 ? launch_quant<128, 32>(p, cs) : launch_quant<64, 32>(p, cs);
+  if (plan.R == 4) return qv.D == 128 ? launch_quant<128, 4, true>(p, cs) : launch_quant<64, 4, true>(p, cs);
+  if (plan.R == 8) return qv.D == 128 ? launch_quant<128, 8, true>(p, cs) : launch_quant<64, 8, true>(p, cs);
+  if (plan.R == 16) return qv.D == 128 ? launch_quant<128, 16, false>(p, cs) : launch_quant<64, 16, false>(p, cs);
+  return qv.D == 128 ? launch_quant<128, 32, false>(p, cs) : launch_quant<64, 32, false>(p, cs);
 }
 
 }  // extern "C"
