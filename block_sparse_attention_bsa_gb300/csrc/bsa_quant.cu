@@ -37,6 +37,7 @@ struct QuantParams {
   int64_t table_stride;
   const int32_t* kv_lens;
   const int32_t* other;               // append: new_lens; read: first
+  uint32_t eights;                    // kEights
 };
 
 // What one warp works on.
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
     for (int i = 0; i < 16; ++i) {
       const uint32_t word = stage[stage_at(group, i) + l8 / 2] >> (lane & 1 ? 8 : 0);
       const uint32_t s2 = scale[i] * 0x10001u, off = scale_offset(s2);
-      put(i, code_values(raised_codes(word, 0), s2, off), code_values(raised_codes(word, 1), s2, off));
+      put(i, code_values(raised_codes(word, 0, p.eights), s2, off), code_values(raised_codes(word, 1, p.eights), s2, off));
     }
   } else {
     const uint32_t word[4][2] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
       const uint32_t s2 = scale[i] | scale[i + 1] << 16, off = scale_offset(s2);
       uint32_t v[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = code_values(raised_codes(word[c][i / 8], i % 8 / 2), s2, off);
+      for (int c = 0; c < 4; ++c) v[c] = code_values(raised_codes(word[c][i / 8], i % 8 / 2, p.eights), s2, off);
       put(i, __byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410));
       put(i + 1, __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
     }
@@ -297,6 +298,7 @@ bsa_status check_cache(const char* fn, const char* name, const bsaq_cache* c, bs
 bsa_status launch_blocks(QuantParams& p, int64_t B, int64_t D, const QuantArgs& a, void (*k64)(QuantParams),
                          void (*k128)(QuantParams), const char* what, const char* fn, cudaStream_t stream) {
   p.H = (int)a.k.heads;
+  p.eights = kEights;
   p.blocks_shift = 0;
   while ((1 << p.blocks_shift) < a.k.blocks) ++p.blocks_shift;
   p.num_pages = (int)a.k.pages; p.max_pages = a.max_pages;

@@ -59,10 +59,14 @@ struct Cfg {
   static constexpr int kQBytes = kSCols * D * 2;
   static constexpr int kPBytes = kOCols * kTileKeys * 2;
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
-  static constexpr int kKSlots = 2, kVSlots = R <= 16 ? 2 : 1;
+  static constexpr int kSegSlots = R == 4 ? 3 : R <= 16 ? 2 : 1;                     // segments, with their Q rows
+  static constexpr int kSlots = 2;                                     // tiles
   static constexpr int kScaleBytes = kScaled ? 0 : kGroups * kTileKeys * 2;
+  // What is made of K (groups) and of V (16 registers of 32 slots) before its place is free.
+  static constexpr int kAheadK = kScaled ? 2 : 0, kAheadV = kScaled ? 2 : 0;
+  static constexpr int kAhead = 16 * (kAheadK > kAheadV ? kAheadK : kAheadV > 0 ? kAheadV : 1);
   static constexpr int kBarBytes = 2048;
-  static constexpr int kSmemBytes = 1024 + 2 * kQBytes + kPBytes + (kKSlots + kVSlots) * kTileBytes + kScaleBytes + kBarBytes;
+  static constexpr int kSmemBytes = 1024 + kSegSlots * kQBytes + kPBytes + 2 * kSlots * kTileBytes + kScaleBytes + kBarBytes;
   // TMEM columns: K, then V; S; O
   static constexpr int kA = 0, kS = 64, kO = kS + kSCols, kColumns = 128;
   static_assert(kO + kOCols <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
@@ -86,6 +90,7 @@ struct QAttnParams {
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
   float scale_log2;
+  uint32_t eights;                // kEights
   __nv_bfloat16* out;
   float* lse;
   int2* seg_ctas;                 // workspace: first and last CTA of each segment that has tiles
@@ -229,44 +234,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const uint32_t q_smem = smem_u32(smem);                              // [2] Q rows
-  const uint32_t p_smem = q_smem + 2 * C::kQBytes;                     // P rows
-  const uint32_t k_ring = p_smem + C::kPBytes;                         // [kKSlots] blocks of K
-  const uint32_t v_ring = k_ring + C::kKSlots * C::kTileBytes;         // [kVSlots] blocks of V
-  const uint32_t vscale = v_ring + C::kVSlots * C::kTileBytes;         // [D / 32][128] twice the scales of V, bf16
+  const uint32_t q_smem = smem_u32(smem);                              // [kSegSlots] Q rows
+  const uint32_t p_smem = q_smem + C::kSegSlots * C::kQBytes;                     // P rows
+  const uint32_t k_ring = p_smem + C::kPBytes;                         // [kSlots] blocks of K
+  const uint32_t v_ring = k_ring + C::kSlots * C::kTileBytes;         // [kSlots] blocks of V
+  const uint32_t vscale = v_ring + C::kSlots * C::kTileBytes;         // [D / 32][128] twice the scales of V, bf16
   uint8_t* rest = smem + (vscale - q_smem) + C::kScaleBytes;
   float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
   float* parts = mr + R;                                               // [4][R] of each warp
-  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [2]
-  int* block_sum = reinterpret_cast<int*>(segs + 2);                   // [kMaxBlocks] tiles of own keys before request 32 i
+  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [kSegSlots]
+  int* block_sum = reinterpret_cast<int*>(segs + C::kSegSlots);                  // [kMaxBlocks] tiles of own keys before request 32 i
   int* total_slot = block_sum + kMaxBlocks;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
   int* abort_slot = total_slot + 2;
   // barriers, as shared-memory addresses 8 bytes apart
-  const uint32_t seg_full = smem_u32(total_slot + 4);  // [2] the segment, and 32 lanes' copies of Q rows
-  const uint32_t seg_empty = seg_full + 16;            // [2] 4 warps
-  const uint32_t k_full = seg_full + 32;               // [2] transaction bytes
-  const uint32_t k_empty = seg_full + 48;              // [2] 4 warps
-  const uint32_t v_full = seg_full + 64;               // [2] transaction bytes
-  const uint32_t v_empty = seg_full + 80;              // [2] 4 warps
-  const uint32_t s_done = seg_full + 96;               // commit
-  const uint32_t pv_done = seg_full + 104;             // commit
-  static_assert((5 * R + kMaxBlocks + 4) * 4 + 2 * sizeof(Segment) + 112 <= C::kBarBytes, "barrier block");
+  const uint32_t seg_full = smem_u32(total_slot + 4);            // [kSegSlots] the segment, and 32 lanes' copies of Q rows
+  const uint32_t seg_empty = seg_full + 8 * C::kSegSlots;        // [kSegSlots] 4 warps
+  const uint32_t k_full = seg_empty + 8 * C::kSegSlots;          // [kSlots] transaction bytes
+  const uint32_t v_full = k_full + 8 * C::kSlots;               // [kSlots] transaction bytes
+  const uint32_t k_ready = v_full + 8 * C::kSlots;              // 4 warps: K stands in TMEM
+  const uint32_t s_done = k_ready + 8;                           // commit
+  const uint32_t pv_ready = s_done + 8;                          // 4 warps: V stands in TMEM, P in shared memory
+  const uint32_t pv_done = pv_ready + 8;                         // commit
+  const uint32_t mma_end = pv_done + 8;                          // commit
+  static_assert((5 * R + kMaxBlocks + 4) * 4 + C::kSegSlots * sizeof(Segment) + (2 * C::kSegSlots + 2 * C::kSlots + 5) * 8 <=
+                    C::kBarBytes, "barrier block");
   const uint32_t abort_flag = smem_u32(abort_slot);
 
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;      // known to be uniform
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kSegSlots; ++i) {
       mbar_init(seg_full + 8 * i, 33);
       mbar_init(seg_empty + 8 * i, 4);
-      mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, 4);
-      mbar_init(v_full + 8 * i, 1);
-      mbar_init(v_empty + 8 * i, 4);
     }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 1);
+    }
+    mbar_init(k_ready, 4);
     mbar_init(s_done, 1);
+    mbar_init(pv_ready, 4);
     mbar_init(pv_done, 1);
+    mbar_init(mma_end, 1);
     *abort_slot = 0;
     fence_mbar_init();
   }
@@ -317,21 +327,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   bool ok = true;
 
   if (warp == 4) {
-    // ---------------------------------------- segments, Q rows, copies of tiles ---
+    // ------------------------------- segments, Q rows, copies of tiles, MMAs ---
+    // In turn: S of tile i, P V of tile i, the copies of tile i + 2 into the place of
+    // tile i, its segment found where a new one begins.
     // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kSCols, false), idesc_o = idesc_bf16_f32(128, C::kOCols, false);
+    constexpr int kQChunk = (C::kSCols * 128) >> 4, kPChunk = (C::kOCols * 128) >> 4;
+    const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     const int c = lane % kVec;
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
     int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
-    uint32_t seg_no = 0, it = 0, issued[2] = {0, 0};
     // Lane x copies page x of a tile's K, lane 8 + x of its V.
     const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
     const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
     const int x = lane % 8;
     const bool is_v = lane >= 8, copies = lane < 16 && x < per_tile;
-#pragma unroll 1
-    for (int t = begin; t < end && ok; ++seg_no) {
+    const int64_t page_stride = is_v ? p.v_page : p.k_page;
+    const int tiles = end - begin;
+    uint32_t seg_no = 0;                           // segments found
+    int left = 0, tile = 0, keys = 0, page = 0;    // of the last one: tiles to copy, the next, where its keys end, this lane's page
+    const int32_t* table = nullptr;
+    const uint8_t* head = nullptr;
+    uint32_t starts = 0;                           // bit i % 4: tile i is the first of a segment
+    auto page_of = [&](int t) {
+      const int key = t * kTileKeys + x * per_page * kBlockSlots;
+      int pg = 0;
+      if (copies && key < keys) {
+        pg = table[key >> p.page_shift];
+        if (pg < 0 || pg >= p.num_pages) {
+          atomicOr(&g_bsa_error, kErrPage);
+          pg = 0;
+        }
+      }
+      return pg;
+    };
+    // The segment of tile t of the row, as far as it is this CTA's.
+    auto find_segment = [&](int t) {
       Segment s;
       int t0, t1, seg;
       if (t < pre) {
@@ -382,8 +415,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       s.tiles = min(t1, end) - t;
       s.whole = begin <= t0 && t1 <= end;
       s.pad = 0;
-      const uint32_t qb = seg_no & 1u;
-      if (!(ok = warp_wait(seg_empty + 8 * qb, (seg_no >> 1 & 1u) ^ 1u, abort_flag))) break;
+      // its first tile's pages are on their way while its place is waited for
+      left = s.tiles; tile = s.tile0; keys = s.keys;
+      table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+      head = is_v ? p.v + s.hk * p.v_head : p.k + s.hk * p.k_head;
+      page = page_of(tile);
+      const uint32_t qb = seg_no % C::kSegSlots;
+      if (!warp_wait(seg_empty + 8 * qb, (seg_no / C::kSegSlots & 1u) ^ 1u, abort_flag)) return false;
       if (lane == 0) {
         int2* who = p.seg_ctas + (s.b < 0 ? 0 : p.pre_rt * p.Hkv) + seg;     // the join looks here
         if (t == t0) who->x = cta;
@@ -393,73 +431,103 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       }
       __syncwarp();
       // Q rows, and rows of zeros up to a multiple of four
-      {
-        const __nv_bfloat16* head = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
-        const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (C::kSCols * 128) + (lane / kVec) * 128;
-        const int row = s.row0 + min(lane, s.rows - 1);
-        const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
-        const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
+      const __nv_bfloat16* qh = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
+      const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (C::kSCols * 128) + (lane / kVec) * 128;
+      const int row = s.row0 + min(lane, s.rows - 1);
+      const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
+      const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
 #pragma unroll 4
-        for (int y = 0; y * kRowsPer < ((s.rows + 3) & ~3); ++y) {
-          const int r = y * kRowsPer + lane / kVec;
-          const __nv_bfloat16* src = head + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + y * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
-                       "l"(src), "r"(r < s.rows ? 16 : 0)
-                       : "memory");
-        }
-        // arrives when this lane's copies have landed; the warp goes on
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(seg_full + 8 * qb) : "memory");
+      for (int y = 0; y * kRowsPer < ((s.rows + 3) & ~3); ++y) {
+        const int r = y * kRowsPer + lane / kVec;
+        const __nv_bfloat16* src = qh + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + y * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
+                     "l"(src), "r"(r < s.rows ? 16 : 0)
+                     : "memory");
       }
-      // the tiles
-      const int32_t* table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
-      const uint8_t* head = is_v ? p.v + s.hk * p.v_head : p.k + s.hk * p.k_head;
-      const int64_t page_stride = is_v ? p.v_page : p.k_page;
-      auto page_of = [&](int tile) {
-        const int key = tile * kTileKeys + x * per_page * kBlockSlots;
-        int page = 0;
-        if (copies && key < s.keys) {
-          page = table[key >> p.page_shift];
-          if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_bsa_error, kErrPage);
-            page = 0;
-          }
-        }
-        return page;
-      };
-      int page = page_of(s.tile0);
-#pragma unroll 1
-      for (int j = 0; j < s.tiles && ok; ++j, ++it) {
-        const int next = j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
-        const int tile = s.tile0 + j;
-        const int blocks = (min(s.keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
-        const int count = min(blocks - x * per_page, per_page);
-        const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
-        const uint8_t* from = head + page * page_stride + in_page * block_bytes(D);
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-          const uint32_t slots = which ? C::kVSlots : C::kKSlots, slot = it % slots;
-          const uint32_t full = (which ? v_full : k_full) + 8 * slot, empty = (which ? v_empty : k_empty) + 8 * slot;
-          if (!(ok = warp_wait(empty, (it / slots & 1u) ^ 1u, abort_flag))) break;
-          if (lane == 0) mbar_arrive_expect_tx(full, blocks * block_bytes(D));
-          if (which) ++issued[1];
-          else ++issued[0];
-          __syncwarp();
-          if (copies && count > 0 && is_v == (which == 1))
-            bulk_load((which ? v_ring : k_ring) + slot * C::kTileBytes + x * per_page * block_bytes(D), from,
-                      count * block_bytes(D), full);
-        }
-        page = next;
+      // arrives when this lane's copies have landed; the warp goes on
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(seg_full + 8 * qb) : "memory");
+      ++seg_no;
+      return true;
+    };
+    // K and V of tile i of this CTA.  Their places are free: of the tile that stood
+    // there P V has been asked for, by which K and V were in TMEM.
+    auto copy_tile = [&](int i) {
+      starts &= ~(1u << (i & 3));
+      if (left == 0) {
+        if (!find_segment(begin + i)) return false;
+        starts |= 1u << (i & 3);
       }
-      t += s.tiles;
+      const int blocks = (min(keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
+      const int count = min(blocks - x * per_page, per_page);
+      const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
+      const uint32_t at = i % C::kSlots;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(k_full + 8 * at, blocks * block_bytes(D));
+        mbar_arrive_expect_tx(v_full + 8 * at, blocks * block_bytes(D));
+      }
+      __syncwarp();
+      if (copies && count > 0)
+        bulk_load((is_v ? v_ring : k_ring) + at * C::kTileBytes + x * per_page * block_bytes(D),
+                  head + page * page_stride + in_page * block_bytes(D), count * block_bytes(D), (is_v ? v_full : k_full) + 8 * at);
+      ++tile;
+      if (--left > 0) page = page_of(tile);
+      return true;
+    };
+    int copied = 0, pv_issued = 0;
+    // The copies that have a place.  A segment's place is that of the kSegSlots-th before
+    // it, which is given back when all its P V have been asked for, not sooner: with a
+    // place for one only its first tile waits for that.
+    auto copy_tiles = [&]() {
+#pragma unroll 1
+      while (copied < tiles && copied < pv_issued + C::kSlots && (C::kSegSlots > 1 || left > 0 || copied == pv_issued)) {
+        if (!copy_tile(copied)) return false;
+        ++copied;
+      }
+      return true;
+    };
+    ok = copy_tiles();
+    uint32_t qb = C::kSegSlots - 1;                // of the tile's segment
+    bool first = false;
+#pragma unroll 1
+    for (int i = 0; i < tiles && ok; ++i) {
+      first = starts >> (i & 3) & 1u;
+      if (first && ++qb == C::kSegSlots) qb = 0;
+      if (!(ok = warp_wait(k_ready, i & 1, abort_flag))) break;
+      fence_async_shared();                        // Q rows, which who made K has waited for, come by ordinary copies
+      tc_fence_after();
+      const uint64_t qdesc = sdesc_sw128(q_smem + qb * C::kQBytes, 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)((kk / 4) * kQChunk + (kk % 4) * 2);
+          if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc_s);
+          else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc_s);
+        }
+        mma_commit(s_done);
+      }
+      __syncwarp();
+      if (!(ok = warp_wait(pv_ready, i & 1, abort_flag))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc_o, !first);
+#pragma unroll
+        for (int kk = 1; kk < kTileKeys / 16; ++kk)
+          mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kPChunk + (kk % 4) * 2), idesc_o);
+        mma_commit(pv_done);
+      }
+      __syncwarp();
+      ++pv_issued;
+      ok = copy_tiles();
     }
-    // the copies in flight land before the CTA may leave, after an abort, too
-    if (lane == 0) {
+    // Nothing is in flight when the CTA leaves or frees its TMEM, after an abort either.
+    if (elect_one()) {
 #pragma unroll 1
-      for (uint32_t i = issued[0] > C::kKSlots ? issued[0] - C::kKSlots : 0; i < issued[0]; ++i)
-        mbar_drain(k_full + 8 * (i % C::kKSlots), i / C::kKSlots & 1u);
-#pragma unroll 1
-      for (uint32_t i = issued[1] > C::kVSlots ? issued[1] - C::kVSlots : 0; i < issued[1]; ++i)
-        mbar_drain(v_full + 8 * (i % C::kVSlots), i / C::kVSlots & 1u);
+      for (int i = max(copied - C::kSlots, 0); i < copied; ++i) {
+        mbar_drain(k_full + 8 * (i % C::kSlots), i / C::kSlots & 1);
+        mbar_drain(v_full + 8 * (i % C::kSlots), i / C::kSlots & 1);
+      }
+      mma_commit(mma_end);
+      mbar_drain(mma_end, 0);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
@@ -473,15 +541,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
     // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
     const uint32_t p_at = p_smem + (th / 64) * (C::kOCols * 128) + th % 64 * 2;
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kSCols, false), idesc_o = idesc_bf16_f32(128, C::kOCols, false);
-    constexpr int kQChunk = (C::kSCols * 128) >> 4, kPChunk = (C::kOCols * 128) >> 4;
-    const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
     for (int t = begin; t < end; ++seg_no) {
-      const uint32_t qb = seg_no & 1u;
-      ok = warp_wait(seg_full + 8 * qb, seg_no >> 1 & 1u, abort_flag);
-      fence_async_shared();                        // Q rows come by ordinary copies
+      const uint32_t qb = seg_no % C::kSegSlots;
+      ok = warp_wait(seg_full + 8 * qb, seg_no / C::kSegSlots & 1u, abort_flag);
       const Segment& s = segs[qb];                 // stays there until all are through with it
       if (th < R) mr[th] = kLowest;
       if (sync_any(!ok)) break;
@@ -490,39 +554,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       const int rem0 = s.row0 - s.b * p.TG;
       const bool even = s.b < 0 || !p.causal;
       const int least = even ? s.keys : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0));
-      const uint64_t qdesc = sdesc_sw128(q_smem + qb * C::kQBytes, 16, 1024);
       float l[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.f;
       int j = 0;
 #pragma unroll 1
       for (; j < tiles; ++j, ++it) {
-        const uint32_t ks = it % C::kKSlots, vs = it % C::kVSlots;
+        const uint32_t at = it % C::kSlots, use = it / C::kSlots & 1u;
         const int tile_keys = min(s.keys - (s.tile0 + j) * kTileKeys, kTileKeys);
-        const uint32_t v_tile = v_ring + vs * C::kTileBytes;
-        // K; its place is free when P V of the tile before is done
-        ok = warp_wait(k_full + 8 * ks, it / C::kKSlots & 1u, abort_flag) && ok;
-        ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag) && ok;
-        tc_fence_after();
+        const uint32_t v_tile = v_ring + at * C::kTileBytes;
+        // K, made while P V of the tile before, whose V it takes the place of, is on its way
+        ok = warp_wait(k_full + 8 * at, use, abort_flag) && ok;
+        uint32_t ab[C::kAhead];                    // of K, then of V: what waits for a product to be done
         {
-          uint32_t from = k_ring + ks * C::kTileBytes + slot_at + slot * 16;
-          uint32_t scale_at = k_ring + ks * C::kTileBytes + slot_at + code_bytes(D) + slot;
-#pragma unroll 1
-          for (int g = 0; g < D / kGroup; ++g, from += 256, scale_at += kBlockSlots) {
-            const uint4 c = lds128(from);
-            const uint32_t s2 = twice_scale(lds8(scale_at)) * 0x10001u, off = scale_offset(s2);
-            uint32_t r[16];
+          const uint32_t from = k_ring + at * C::kTileBytes + slot_at + slot * 16;
+          const uint32_t scale_at = k_ring + at * C::kTileBytes + slot_at + code_bytes(D) + slot;
+          auto group = [&](int g, uint32_t* r) {
+            const uint4 c = lds128(from + g * 256);
+            const uint32_t s2 = twice_scale(lds8(scale_at + g * kBlockSlots)) * 0x10001u, off = scale_offset(s2);
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4), s2, off);
-            tmem_st16(a_t + g * 16, r);
+            for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4, p.eights), s2, off);
+          };
+#pragma unroll
+          for (int g = 0; g < C::kAheadK; ++g) group(g, ab + 16 * g);
+          ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag) && ok;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < C::kAheadK; ++g) tmem_st16(a_t + g * 16, ab + 16 * g);
+#pragma unroll 1
+          for (int g = C::kAheadK; g < C::kGroups; ++g) {
+            group(g, ab);
+            tmem_st16(a_t + g * 16, ab);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_empty + 8 * ks);
         // twice the scales of V, 0 behind the last key: what stands there must not count
         if constexpr (!kScaled) {
-          ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag) && ok;
+          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g)
             sts16(vscale + (g * kTileKeys + th) * 2,
@@ -530,31 +598,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
         tmem_wait_st();
         tc_fence_before();
-        if (sync_any(!ok)) break;
-        if (warp == 0) {                           // all of it, so that the descriptors stay in uniform registers
-          tc_fence_after();
-          if (elect_one()) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready);
+        // V of slots 32 x .. 32 x + 31 under this thread's channel
+        auto v_codes = [&](int x, uint32_t* r) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk / 4) * kQChunk + (kk % 4) * 2);
-              if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc_s);
-              else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc_s);
+          for (int y = 0; y < 2; ++y) {
+            const uint2 c = lds64(v_tile + (2 * x + y) * block_bytes(D) + th * 8);
+            if constexpr (kScaled) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r[y * 8 + i] = half_codes(raised_codes(i < 4 ? c.x : c.y, i % 4, p.eights));
+            } else {
+              const uint32_t scale_at = vscale + (th / kGroup) * (kTileKeys * 2) + (2 * x + y) * 32;
+              const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
+              const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4, p.eights), s2[i], scale_offset(s2[i]));
             }
-            mma_commit(s_done);
           }
-          __syncwarp();
-        }
+        };
         float vs2[C::kSets];                       // of this key
         if constexpr (kScaled) {
-          ok = warp_wait(v_full + 8 * vs, it / C::kVSlots & 1u, abort_flag);
+          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g)
             vs2[g] = th < tile_keys
                          ? __uint_as_float(twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) << 16)
                          : 0.f;
+          if (th < D) {
+#pragma unroll
+            for (int x = 0; x < C::kAheadV; ++x) v_codes(x, ab + 16 * x);
+          }
         }
         ok = warp_wait(s_done, it & 1u, abort_flag) && ok;
         tc_fence_after();
+        if constexpr (!kScaled) sync_any(false);   // the scales of V are there
         const int key = (s.tile0 + j) * kTileKeys + th;
         const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
         float v[R];
@@ -642,25 +721,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             }
           if (!again && th < D) {
             // V over K, whose product is done
-            uint32_t from = v_tile + th * 8, scale_at = vscale + (th / kGroup) * (kTileKeys * 2);
+#pragma unroll
+            for (int x = 0; x < C::kAheadV; ++x) tmem_st16(a_t + x * 16, ab + 16 * x);
 #pragma unroll 1
-            for (int x = 0; x < kTileBlocks; x += 2) {
-              uint32_t r[16];
-#pragma unroll
-              for (int y = 0; y < 2; ++y, from += block_bytes(D), scale_at += 32) {
-                const uint2 c = lds64(from);
-                if constexpr (kScaled) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) r[y * 8 + i] = half_codes(raised_codes(i < 4 ? c.x : c.y, i % 4));
-                } else {
-                  const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
-                  const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    r[y * 8 + i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4), s2[i], scale_offset(s2[i]));
-                }
-              }
-              tmem_st16(a_t + x * 8, r);
+            for (int x = C::kAheadV; x < 4; ++x) {
+              v_codes(x, ab);
+              tmem_st16(a_t + x * 16, ab);
             }
             tmem_wait_st();
           }
@@ -673,19 +739,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           again = true;
           if (sync_any(!ok)) break;
         }
-        if (lane == 0) mbar_arrive(v_empty + 8 * vs);
         if (grow) break;                           // some wait gave up
-        if (warp == 0) {
-          tc_fence_after();
-          if (elect_one()) {
-            mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc_o, j > 0);
-#pragma unroll
-            for (int kk = 1; kk < kTileKeys / 16; ++kk)
-              mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kPChunk + (kk % 4) * 2), idesc_o);
-            mma_commit(pv_done);
-          }
-          __syncwarp();
-        }
+        if (lane == 0) mbar_arrive(pv_ready);
 #pragma unroll
         for (int r4 = 0; r4 < R; r4 += 4)
           if (r4 < rows) {
@@ -749,12 +804,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + 8 * qb);
     }
-    // nothing of the MMAs is in flight when TMEM is freed, after an abort either
-    if (warp == 0 && elect_one()) {
-      mma_commit(pv_done);
-      mbar_drain(pv_done, it & 1u);
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -976,6 +1025,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
+  p.eights = kEights;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
   char* ws = static_cast<char*>(workspace);
   p.seg_ctas = reinterpret_cast<int2*>(ws);
