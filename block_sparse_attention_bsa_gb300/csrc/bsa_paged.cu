@@ -53,6 +53,7 @@
 
 #include "bsa_paged.h"
 #include "bsa_paged_device.cuh"
+#include "bsa_quant.h"
 
 namespace bsa {
 namespace {
@@ -60,23 +61,32 @@ namespace {
 constexpr int kTileKeys = 128;
 constexpr int kRowTile = 256;        // rows of a segment
 constexpr int kHalf = 128;           // rows of a job
-constexpr int kPagedThreads = 384;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;     // blocks of 32 requests in the schedule
 
-template <int D>
+// kQ4: the pages hold 4 bits (bsa_quant.h).  Warps 12-15 make the K and V tiles of the
+// ring then, from blocks that warp 0 copies into a ring of their own.
+template <int D, bool kQ4>
 struct PagedCfg {
+  static constexpr int kThreads = kQ4 ? 512 : 384;
   static constexpr int kChunks = D / 64;                      // 128-byte chunks per row
   static constexpr int kQBytes = kHalf * 128 * kChunks;      // 128 rows
   static constexpr int kTileBytes = kTileKeys * 128 * kChunks;
   static constexpr int kBarBytes = 2048;
   static constexpr int kSmemMax = 232448;                     // 227 KB per CTA
-  static constexpr int kFit = (kSmemMax - 1024 - kBarBytes - 2 * kQBytes) / kTileBytes;
-  static constexpr int kStages = kFit > 10 ? 10 : kFit;       // 5 of 32 KB, 10 of 16 KB
-  static constexpr int kSmemBytes = 1024 + kBarBytes + 2 * kQBytes + kStages * kTileBytes;
+  static constexpr int kRaw = kQ4 && D == 64 ? 8 : 3;         // places for blocks of 128 keys (of 4 bits)
+  static constexpr int kRawBytes = kQ4 ? kTileKeys / kBlockSlots * block_bytes(D) : 0;
+  static constexpr int kScaleBytes = kQ4 ? (D / kGroup) * kTileKeys * 2 : 0;
+  static constexpr int kRest = kSmemMax - 1024 - kBarBytes - 2 * kQBytes - kRaw * kRawBytes - kScaleBytes;
+  static constexpr int kFit = kRest / kTileBytes;
+  static constexpr int kStages = kFit > 10 ? 10 : kFit;       // 5 of 32 KB, 10 of 16 KB; 4 and 9 beside blocks
+  static constexpr int kSmemBytes = kSmemMax - kRest + kStages * kTileBytes;
 };
 
 struct PagedParams {
   CUtensorMap tk, tv;             // [pages, Hkv, slots, D] of the whole cache
+  const uint8_t* k4; const uint8_t* v4;                       // or, of 4 bits, its bytes
+  int64_t k4_page, k4_head, v4_page, v4_head;
+  uint32_t eights;                // kEights
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
@@ -179,7 +189,7 @@ struct __align__(16) Segment {
   int pad;
 };
 constexpr int kSegRing = 4;
-constexpr int kSegReaders = 11;      // warps that read every segment
+constexpr int kSegReaders = 11;      // warps that read every segment (one producer less of 4-bit pages)
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3) {
@@ -260,16 +270,18 @@ struct SegmentReader {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
-  using C = PagedCfg<D>;
+template <int D, bool kQ4>
+__global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention_kernel(const __grid_constant__ PagedParams p) {
+  using C = PagedCfg<D, kQ4>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* q_smem = smem;                                  // [2] Q buffers of 128 rows
   uint8_t* ring = smem + 2 * C::kQBytes;
-  Segment* segs = reinterpret_cast<Segment*>(ring + kStages * C::kTileBytes);   // [kSegRing]
+  uint8_t* raw = ring + kStages * C::kTileBytes;           // [kRaw] blocks of 128 keys
+  uint8_t* scales = raw + C::kRaw * C::kRawBytes;          // [D / 32][128] twice the scales of a V tile, bf16
+  Segment* segs = reinterpret_cast<Segment*>(scales + C::kScaleBytes);           // [kSegRing]
   // barriers, as shared-memory addresses 8 bytes apart
   const uint32_t q_full = smem_u32(segs + kSegRing);   // [2] 32 loader threads
   const uint32_t q_empty = q_full + 16;                // [2] commit
@@ -283,13 +295,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   const uint32_t mma_end = q_full + 96;                // commit
   const uint32_t seg_full = q_full + 112;              // [kSegRing] the scheduler
   const uint32_t seg_empty = seg_full + 8 * kSegRing;  // [kSegRing] the 11 warps that read it
-  const uint32_t full = seg_empty + 8 * kSegRing;      // [kStages] transaction bytes
+  const uint32_t full = seg_empty + 8 * kSegRing;      // [kStages] transaction bytes, or the 4 warps that make tiles
   const uint32_t empty = full + 8 * kStages;           // [kStages] commit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(segs + kSegRing) + 2 * (14 + 2 * kSegRing + 2 * kStages);
   const uint32_t abort_flag = empty + 8 * kStages + 4; // behind tmem_slot
   int* total_slot = reinterpret_cast<int*>(tmem_slot + 2);
   int* block_sum = total_slot + 1;      // [kMaxBlocks]: tiles of own keys before request 32 i
-  static_assert(kSegRing * sizeof(Segment) + (14 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 <= C::kBarBytes,
+  // of 4-bit pages
+  int* raw_info = block_sum + kMaxBlocks;                // [kRaw] keys, + 256 where they are of V
+  const uint32_t raw_full = (smem_u32(raw_info + C::kRaw) + 7) & ~7u;    // [kRaw] transaction bytes
+  const uint32_t raw_empty = raw_full + 8 * C::kRaw;     // [kRaw] 4 warps
+  const uint32_t scale_bar = raw_empty + 8 * C::kRaw;    // 4 warps
+  static_assert(kSegRing * sizeof(Segment) + (14 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 + C::kRaw * 20 + 16 <=
+                    C::kBarBytes,
                 "barrier block");
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -306,16 +324,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     mbar_init(mma_end, 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(seg_full + 8 * i, 1);
-      mbar_init(seg_empty + 8 * i, kSegReaders);
+      mbar_init(seg_empty + 8 * i, kSegReaders - (kQ4 ? 1 : 0));
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, kQ4 ? 4 : 1);
       mbar_init(empty + 8 * i, 1);
+    }
+    if constexpr (kQ4) {
+      for (int i = 0; i < C::kRaw; ++i) {
+        mbar_init(raw_full + 8 * i, 1);
+        mbar_init(raw_empty + 8 * i, 4);
+      }
+      mbar_init(scale_bar, 4);
     }
     tmem_slot[1] = 0;                   // abort flag
     fence_mbar_init();
-    tma_prefetch_desc(&p.tk);
-    tma_prefetch_desc(&p.tv);
+    if constexpr (!kQ4) {
+      tma_prefetch_desc(&p.tk);
+      tma_prefetch_desc(&p.tv);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -328,7 +355,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
 #pragma unroll 1
-  for (int blk = warp; blk < nblk; blk += kPagedThreads / 32) {
+  for (int blk = warp; blk < nblk; blk += C::kThreads / 32) {
     const int b = blk * 32 + lane;
     const int mine = b < p.B ? request_tiles(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
     const int incl = warp_inclusive_sum(mine);
@@ -366,7 +393,147 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
   }
   bool ok = true;
 
-  if (warp == 0 || warp == 3) {
+  if (kQ4 && warp == 0) {
+    // ------------------------------------------------- copies of 4-bit blocks ---
+    // In the order of the ring's tiles: of rows above 128 K_0, V_0, K_1, V_1 .., else
+    // K_0, K_1, V_0, K_2, V_1 ..  Lane x copies page x of a tile.
+    const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;
+    const int per_page = kTileKeys / kBlockSlots / per_tile;                    // blocks of a page in a tile
+    uint32_t it = 0;
+    const uint8_t* v_from = nullptr;               // this lane's part of the V that is still to come
+    int v_count = 0, v_keys = 0;
+    bool v_left = false;
+    SegmentReader reader;
+    auto put = [&](const uint8_t* from, int count, int keys, bool is_v) {
+      const uint32_t at = it % C::kRaw;
+      if (!warp_wait(raw_empty + 8 * at, (it / C::kRaw & 1u) ^ 1u, abort_flag)) return false;
+      if (lane == 0) {
+        raw_info[at] = keys + (is_v ? 256 : 0);
+        mbar_arrive_expect_tx(raw_full + 8 * at, (keys + kBlockSlots - 1) / kBlockSlots * block_bytes(D));
+      }
+      __syncwarp();
+      if (lane < per_tile && count > 0)
+        bulk_load(smem_u32(raw) + at * C::kRawBytes + lane * per_page * block_bytes(D), from, count * block_bytes(D),
+                  raw_full + 8 * at);
+      ++it;
+      return true;
+    };
+#pragma unroll 1
+    for (int t = begin; t < end && ok;) {
+      Segment s;
+      if (!(ok = reader.take(segs, seg_full, seg_empty, abort_flag, s))) break;
+      const bool wide = s.rows > kHalf;
+      const int32_t* own_table = p.page_table + s.b * p.table_stride;
+      auto page_of = [&](int j) {
+        const bool pre = s.b < 0 || j < p.fold;
+        const int key = (pre ? j : j - p.fold) * kTileKeys + lane * per_page * kBlockSlots;
+        int page = 0;
+        if (lane < per_tile && key < (pre ? p.prefix_len : s.kv)) {
+          page = (pre ? p.prefix_table : own_table)[key >> p.page_shift];
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_bsa_error, kErrPage);
+            page = 0;
+          }
+        }
+        return page;
+      };
+      int page = page_of(s.tile0);
+#pragma unroll 1
+      for (int j = 0; j < s.tiles && ok; ++j) {
+        const int next = j + 1 < s.tiles ? page_of(s.tile0 + j + 1) : 0;
+        const int tile = s.tile0 + j, source = tile - (tile < p.fold ? 0 : p.fold);       // tile of its table
+        const int keys = tile_keys(p, s.keys, tile);
+        const int count = min((keys + kBlockSlots - 1) / kBlockSlots - lane * per_page, per_page);
+        const int64_t in_page =
+            (source * (kTileKeys / kBlockSlots) & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1)) * block_bytes(D);
+        const uint8_t* vf = p.v4 + page * p.v4_page + s.hk * p.v4_head + in_page;
+        ok = put(p.k4 + page * p.k4_page + s.hk * p.k4_head + in_page, count, keys, false);
+        if (ok && v_left) ok = put(v_from, v_count, v_keys, true);
+        if (ok && wide) ok = put(vf, count, keys, true);
+        v_left = !wide;
+        v_from = vf; v_count = count; v_keys = keys;
+        page = next;
+      }
+      t += s.tiles;
+    }
+    if (ok && v_left) put(v_from, v_count, v_keys, true);
+    // the copies in flight land before the CTA may leave
+    if (lane == 0)
+#pragma unroll 1
+      for (uint32_t i = it > C::kRaw ? it - C::kRaw : 0; i < it; ++i) mbar_drain(raw_full + 8 * (i % C::kRaw), i / C::kRaw & 1u);
+    __syncwarp();
+  } else if (kQ4 && warp >= 12) {
+    // ------------------------------------------------------ codes to bf16 ---
+    // K: a thread a key, rows of 64 channels; V: a thread a channel, rows of 64 keys
+    // (the transposed tile, which takes whole pieces of 16 bytes from a thread); 16-byte
+    // pieces exchanged within 8 rows, as the MMAs read them.
+    const int th = threadIdx.x % 128;
+    const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots, swap = (th % 8) * 16;
+    const uint32_t scale_to = smem_u32(scales);
+    uint32_t stage = 0, phase = 0, sync_phase = 0;
+#pragma unroll 1
+    for (uint32_t it = 0; it < 2u * (uint32_t)(end - begin); ++it) {
+      const uint32_t at = it % C::kRaw;
+      if (!(ok = warp_wait(raw_full + 8 * at, it / C::kRaw & 1u, abort_flag))) break;
+      const int info = raw_info[at], keys = info & 255;
+      const uint32_t from = smem_u32(raw) + at * C::kRawBytes, to = smem_u32(ring) + stage * C::kTileBytes;
+      if (info < 256) {
+        if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
+#pragma unroll 1
+        for (int g = 0; g < D / kGroup; ++g) {
+          const uint4 c = lds128(from + slot_at + g * 256 + slot * 16);
+          const uint32_t s2 = twice_scale(lds8(from + slot_at + code_bytes(D) + g * kBlockSlots + slot)) * 0x10001u;
+          const uint32_t off = scale_offset(s2), word[4] = {c.x, c.y, c.z, c.w};
+          const uint32_t row = to + (g / 2) * (kTileKeys * 128) + th * 128;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = code_values(raised_codes(word[x], i, p.eights), s2, off);
+            sts128(row + (((g % 2) * 4 + x) * 16 ^ swap), r);
+          }
+        }
+      } else {
+        // twice the scales, 0 behind the last key: what stands there must not count
+#pragma unroll
+        for (int g = 0; g < D / kGroup; ++g)
+          sts16(scale_to + (g * kTileKeys + th) * 2,
+                th < keys ? twice_scale(lds8(from + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scale_bar);
+        if (!(ok = warp_wait(scale_bar, sync_phase, abort_flag))) break;
+        sync_phase ^= 1u;
+        if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
+        if (th < D) {
+#pragma unroll 1
+          for (int x = 0; x < kTileKeys / kBlockSlots; ++x) {
+            const uint2 c = lds64(from + x * block_bytes(D) + th * 8);
+            const uint32_t scale_at = scale_to + (th / kGroup) * (kTileKeys * 2) + x * 32;
+            const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
+            const uint32_t s2[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+            uint32_t r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              r[i] = code_values(raised_codes(i < 4 ? c.x : c.y, i % 4, p.eights), s2[i], scale_offset(s2[i]));
+            const uint32_t row = to + (x / 4) * (D * 128) + th * 128;
+            sts128(row + ((x % 4) * 32 ^ swap), r);
+            sts128(row + (((x % 4) * 32 + 16) ^ swap), r + 4);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scale_bar);     // the scales are read
+        if (!(ok = warp_wait(scale_bar, sync_phase, abort_flag))) break;
+        sync_phase ^= 1u;
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(raw_empty + 8 * at);
+        mbar_arrive(full + 8 * stage);
+      }
+      advance<kStages>(stage, phase);
+    }
+  } else if (!kQ4 && (warp == 0 || warp == 3)) {
     // ----------------------------------------------------- TMA producers ---
     // K of tile q, then V of tile q - 1, for every tile of the CTA's row: warp 0
     // fetches K and warp 3 V, each at its places in the ring.  (One warp for both
@@ -462,10 +629,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     // goes through the loop and one lane issues: the descriptors then stay in
     // uniform registers (in a branch of one lane each MMA took 26 instructions).
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kTileKeys, false);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, true);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, D, !kQ4);     // of 4-bit pages V is transposed
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_smem), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t vdesc0 = sdesc_sw128(smem_u32(ring), kTileKeys * 128, 1024);
+    const uint64_t vdesc0 = sdesc_sw128(smem_u32(ring), kQ4 ? 16 : kTileKeys * 128, 1024);
     uint32_t stage = 0, phase = 0;      // next item of the ring
     uint32_t q = 0, qi = 0;             // next job, next Q buffer
     uint32_t k_stage = 0, v_stage = 0;
@@ -524,7 +691,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             // up to the end of the MMA step that it lies in are zeroed (0 times
             // infinity or NaN is NaN), the steps behind are left out.
             const int rest = -v_keys & 15;
-            if (v_keys < kTileKeys && rest != 0) {
+            if (!kQ4 && v_keys < kTileKeys && rest != 0) {
               const uint32_t at = smem_u32(ring) + v_stage * C::kTileBytes + v_keys * 128;
 #pragma unroll 1
               for (int x = lane; x < rest * (D / 8); x += 32) {
@@ -546,7 +713,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
             mma_ts(d_t, a_t, bs, idesc_o, !v_first);
 #pragma unroll
             for (int kk = 1; kk < kTileKeys / 16; ++kk)
-              if (kk * 16 < v_keys) mma_ts_acc<1>(d_t, a_t + kk * 8, bs + (uint64_t)(kk * ((16 * 128) >> 4)), idesc_o);
+              if (kk * 16 < v_keys)
+                mma_ts_acc<1>(d_t, a_t + kk * 8,
+                              bs + (uint64_t)(kQ4 ? (kk / 4) * ((D * 128) >> 4) + (kk % 4) * 2 : kk * ((16 * 128) >> 4)), idesc_o);
             mma_commit(pv_done + 8 * w);
             if (v_last) mma_commit(empty + 8 * v_stage);
           }
@@ -672,7 +841,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_attention_kernel(const
     }
     asm volatile("cp.async.wait_all;" ::: "memory");         // after an abort, too
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // --------------------------------------------------- softmax + results ---
     const uint32_t w = (warp - 4) / 4;             // the group: it takes the jobs q with q % 2 == w
     const int wq = warp % 4;
@@ -1016,7 +1185,7 @@ bsa_status encode_cache(CUtensorMap* m, const bsa_tensor& t, const char* fn, con
   return BSA_OK;
 }
 
-template <int D>
+template <int D, bool kQ4>
 bsa_status set_smem() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -1025,8 +1194,8 @@ bsa_status set_smem() {
   if (st != BSA_OK) return st;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 64 || !done[dev]) {
-    st = cuda_check(cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PagedCfg<D>::kSmemBytes),
+    st = cuda_check(cudaFuncSetAttribute(paged_attention_kernel<D, kQ4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PagedCfg<D, kQ4>::kSmemBytes),
                     "cudaFuncSetAttribute(paged_attention_kernel)");
     if (st != BSA_OK) return st;
     if (dev < 64) done[dev] = true;
@@ -1034,9 +1203,9 @@ bsa_status set_smem() {
   return BSA_OK;
 }
 
-template <int D>
+template <int D, bool kQ4>
 bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
-  bsa_status st = set_smem<D>();
+  bsa_status st = set_smem<D, kQ4>();
   if (st != BSA_OK) return st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1046,9 +1215,9 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)p.ctas);
-  cfg.blockDim = dim3(kPagedThreads);
-  cfg.dynamicSmemBytes = PagedCfg<D>::kSmemBytes;
-  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, paged_attention_kernel<D>, p), "paged_attention_kernel launch")) != BSA_OK)
+  cfg.blockDim = dim3(PagedCfg<D, kQ4>::kThreads);
+  cfg.dynamicSmemBytes = PagedCfg<D, kQ4>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kQ4>, p), "paged_attention_kernel launch")) != BSA_OK)
     return st;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   // Eight warps, one warp or eight lanes a row, by the number of rows (us of the
@@ -1065,6 +1234,59 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
                     "paged_join_kernel launch");
 }
 
+// Key tiles at most, with the keys that the tables could hold.
+int64_t most_tiles_of(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t max_pages, int64_t prefix_len) {
+  const int64_t G = qv.H / Hkv;
+  return qv.B * Hkv * cdiv64(qv.S * G, kRowTile) * (cdiv64(max_pages * page, kTileKeys) + cdiv64(prefix_len, kTileKeys)) +
+         Hkv * cdiv64(qv.B * qv.S * G, kRowTile) * cdiv64(prefix_len, kTileKeys);
+}
+
+// What a launch takes but for the cache itself; `a`: its tables and lengths.
+PagedParams make_params(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t pages, const PagedArgs& a,
+                        const int32_t* prefix_table, int32_t prefix_len, int32_t causal, float softmax_scale, void* out,
+                        float* lse, void* workspace, const PagedPlan& plan, int64_t most_tiles, int sms) {
+  PagedParams p{};
+  const int64_t G = qv.H / Hkv, flat_rows = qv.B * qv.S * G;
+  p.q = static_cast<const __nv_bfloat16*>(qv.ptr); p.q_sb = qv.stride_b; p.q_ss = qv.stride_s; p.q_sh = qv.stride_h;
+  p.B = (int)qv.B; p.T = (int)qv.S; p.Hq = (int)qv.H; p.Hkv = (int)Hkv; p.G = (int)G;
+  p.page_shift = 4;
+  while ((1 << p.page_shift) < page) ++p.page_shift;
+  p.num_pages = (int)pages; p.max_pages = a.max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
+  p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
+  p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
+  p.pre_tiles = plan.fold ? 0 : (int)cdiv64(prefix_len, kTileKeys);
+  p.fold = plan.fold ? (int)cdiv64(prefix_len, kTileKeys) : 0;
+  p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
+  p.ctas = sms;
+  // Weights of about an eighth of a microsecond: a wide prefix tile (two jobs of
+  // 0.9 us on the tensor cores, more while others fetch) against a tile of own
+  // keys for a few rows (1.5 us at its share of the memory rate).  us at prefix :
+  // own = 1:1 / 4:3 / 5:3 / 2:1 -- 64 requests, 8k prefix, 512 own keys 57 / 52 /
+  // 49 / 46; 64, 4k, 1,024 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188;
+  // 256, 32k, ragged up to 512 187 / 177 / 180 / 205.  The way in and out of the
+  // prefix's segment (Q rows, results: 7 us where it is wide) is spread over its
+  // tiles: 61 requests with 28 shared and 775 own keys 70 -> 47 us, their prefix
+  // being 8 segments of one tile that one block got; nothing from 8k on.
+  p.pre_w = p.own_w = 1;
+  p.pre_over = 0;
+  if (p.pre_tiles > 0 && most_tiles < INT32_MAX / 80) {
+    const bool wide_pre = flat_rows > kHalf, wide_own = qv.S * G > kHalf;
+    p.pre_w = wide_pre ? 20 : 12;
+    p.pre_over = (wide_pre ? 56 : 24) / p.pre_tiles;
+    p.own_w = wide_own ? 20 : 12;
+  }
+  p.page_table = a.page_table; p.table_stride = a.table_stride; p.kv_lens = a.kv_lens; p.new_lens = a.new_lens;
+  p.prefix_table = prefix_table;
+  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.seg_ctas = reinterpret_cast<int2*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+  p.own_first = (int)plan.own_first;
+  return p;
+}
+
 }  // namespace
 
 unsigned int read_and_clear_paged_error() { return take_error_word(); }
@@ -1072,6 +1294,27 @@ unsigned int read_and_clear_paged_error() { return take_error_word(); }
 bsa_status launch_paged_wait_probe(unsigned long long limit_ns, cudaStream_t stream) {
   wait_probe_kernel<<<1, 32, 0, stream>>>(limit_ns);
   return cuda_check(cudaGetLastError(), "wait_probe_kernel launch (paged attention)");
+}
+
+size_t wide_quant_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
+  return plan_paged(B, T, Hq, Hkv, d, prefix, sms).bytes;
+}
+
+bsa_status launch_wide_quant(const bsa_tensor& qv, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
+                             int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
+                             void* workspace, cudaStream_t stream) {
+  const int64_t page = a.k.blocks * kBlockSlots;
+  const int sms = num_sms();
+  PagedArgs t{};
+  t.page_table = a.page_table; t.table_stride = a.table_stride; t.max_pages = a.max_pages; t.kv_lens = a.kv_lens;
+  t.new_lens = new_lens;
+  PagedParams p = make_params(qv, a.k.heads, page, a.k.pages, t, prefix_table, prefix_len, causal, softmax_scale, out, lse,
+                              workspace, plan_paged(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms),
+                              most_tiles_of(qv, a.k.heads, page, a.max_pages, prefix_len), sms);
+  p.k4 = static_cast<const uint8_t*>(a.k.ptr); p.v4 = static_cast<const uint8_t*>(a.v.ptr);
+  p.k4_page = a.k.stride_page; p.k4_head = a.k.stride_head; p.v4_page = a.v.stride_page; p.v4_head = a.v.stride_head;
+  p.eights = kEights;
+  return qv.D == 128 ? launch_paged<128, true>(p, stream) : launch_paged<64, true>(p, stream);
 }
 
 }  // namespace bsa
@@ -1123,12 +1366,11 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   const int64_t G = qv.H / a.k.H;
   const int sms = num_sms();
   // rows, tiles and slot numbers are 32-bit on the device
-  const int64_t flat_rows = qv.B * qv.S * G, row_tiles = cdiv64(qv.S * G, kRowTile);
+  const int64_t flat_rows = qv.B * qv.S * G;
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   if (q_extent >= (int64_t)1 << 35)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": q reaches over " + s(q_extent) + " elements (2^35 at most)");
-  const int64_t most_tiles = qv.B * a.k.H * row_tiles * (cdiv64(max_pages * a.k.S, kTileKeys) + cdiv64(prefix_len, kTileKeys)) +
-                             a.k.H * cdiv64(flat_rows, kRowTile) * cdiv64(prefix_len, kTileKeys);
+  const int64_t most_tiles = most_tiles_of(qv, a.k.H, a.k.S, max_pages, prefix_len);
   if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.H > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
                                               s(max_pages * a.k.S + prefix_len) + " keys are too many for one call");
@@ -1157,48 +1399,12 @@ bsa_status bsap_forward(const bsa_tensor* q, const bsa_tensor* k_cache, const bs
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < i; ++j)
       if ((st = check_apart(fn, writes[j], writes[i])) != BSA_OK) return st;
-  PagedParams p{};
+  PagedParams p = make_params(qv, a.k.H, a.k.S, a.k.B, a, prefix_table, prefix_len, causal, softmax_scale, out, lse, workspace,
+                              plan, most_tiles, sms);
   if ((st = encode_cache(&p.tk, a.k, fn, "k_cache")) != BSA_OK) return st;
   if ((st = encode_cache(&p.tv, a.v, fn, "v_cache")) != BSA_OK) return st;
-  p.q = static_cast<const __nv_bfloat16*>(qv.ptr); p.q_sb = qv.stride_b; p.q_ss = qv.stride_s; p.q_sh = qv.stride_h;
-  p.B = (int)qv.B; p.T = (int)qv.S; p.Hq = (int)qv.H; p.Hkv = (int)a.k.H; p.G = (int)G;
-  p.page_shift = 4;
-  while ((1 << p.page_shift) < a.k.S) ++p.page_shift;
-  p.num_pages = (int)a.k.B; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
-  p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
-  p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
-  p.pre_tiles = plan.fold ? 0 : (int)cdiv64(prefix_len, kTileKeys);
-  p.fold = plan.fold ? (int)cdiv64(prefix_len, kTileKeys) : 0;
-  p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
-  p.ctas = sms;
-  // Weights of about an eighth of a microsecond: a wide prefix tile (two jobs of
-  // 0.9 us on the tensor cores, more while others fetch) against a tile of own
-  // keys for a few rows (1.5 us at its share of the memory rate).  us at prefix :
-  // own = 1:1 / 4:3 / 5:3 / 2:1 -- 64 requests, 8k prefix, 512 own keys 57 / 52 /
-  // 49 / 46; 64, 4k, 1,024 80 / 68 / 60 / 59; 256, 32k, 256 175 / 164 / 163 / 188;
-  // 256, 32k, ragged up to 512 187 / 177 / 180 / 205.  The way in and out of the
-  // prefix's segment (Q rows, results: 7 us where it is wide) is spread over its
-  // tiles: 61 requests with 28 shared and 775 own keys 70 -> 47 us, their prefix
-  // being 8 segments of one tile that one block got; nothing from 8k on.
-  p.pre_w = p.own_w = 1;
-  p.pre_over = 0;
-  if (p.pre_tiles > 0 && most_tiles < INT32_MAX / 80) {
-    const bool wide_pre = flat_rows > kHalf, wide_own = qv.S * G > kHalf;
-    p.pre_w = wide_pre ? 20 : 12;
-    p.pre_over = (wide_pre ? 56 : 24) / p.pre_tiles;
-    p.own_w = wide_own ? 20 : 12;
-  }
-  p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
-  p.prefix_table = prefix_table;
-  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
-  p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse;
-  char* ws = static_cast<char*>(workspace);
-  p.seg_ctas = reinterpret_cast<int2*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + plan.part_ml);
-  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
-  p.own_first = (int)plan.own_first;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return qv.D == 128 ? launch_paged<128>(p, cs) : launch_paged<64>(p, cs);
+  return qv.D == 128 ? launch_paged<128, false>(p, cs) : launch_paged<64, false>(p, cs);
 }
 
 }  // extern "C"

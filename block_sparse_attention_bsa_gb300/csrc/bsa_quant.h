@@ -23,6 +23,12 @@ struct QuantArgs {
   const int32_t* page_table; int64_t table_stride; int max_pages;
   const int32_t* kv_lens;
 };
+// Attention of many rows over 4-bit pages (bsa_paged.cu): its workspace, and the
+// launch for arguments that bsaq_forward has checked.
+size_t wide_quant_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms);
+bsa_status launch_wide_quant(const bsa_tensor& q, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
+                             int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
+                             void* workspace, cudaStream_t stream);
 bsa_status check_quant(const char* fn, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
                        const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
                        int64_t B, QuantArgs* a);
@@ -62,6 +68,29 @@ __device__ __forceinline__ uint32_t scale_offset(uint32_t scales2) {
 // Two codes, halved.
 __device__ __forceinline__ uint32_t half_codes(uint32_t raised) {
   return as_u32(__hadd2(as_bf16x2(raised), as_bf16x2(0xC140C140u)));         // minus 12
+}
+
+// Shared memory by its address.
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* r) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tst.shared.b16 [%0], lo;\n\t}" ::"r"(addr), "r"(v) : "memory");
 }
 #endif
 

@@ -202,25 +202,6 @@ __device__ __forceinline__ void tmem_st_4(uint32_t taddr, const float* r) {
                : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tst.shared.b16 [%0], lo;\n\t}" ::"r"(addr), "r"(v) : "memory");
-}
-
 // The largest of a warp's numbers; NaN counts as kLowest, and so does all below it.
 __device__ __forceinline__ float warp_max(float z) {
   int u = __float_as_int(z > kLowest ? z : kLowest);
@@ -862,6 +843,9 @@ struct QAttnPlan {
   size_t own_first, part_ml, part_o, bytes;
 };
 
+// Whether so many rows read the same keys that they are the first operand.
+bool many_rows(int64_t B, int64_t T, int64_t G, bool prefix) { return (prefix ? B * T * G : T * G) > 32; }
+
 QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
   QAttnPlan w{};
   w.TG = (int)(T * (Hq / Hkv));
@@ -937,7 +921,9 @@ size_t bsaq_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has
   if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq > kMaxHeads || Hq % Hkv ||
       (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 16)
     return 0;
-  return plan_quant(B, T, Hq, Hkv, d, has_prefix != 0, sms > 0 ? sms : num_sms()).bytes;
+  if (sms == 0) sms = num_sms();
+  return many_rows(B, T, Hq / Hkv, has_prefix != 0) ? wide_quant_bytes(B, T, Hq, Hkv, d, has_prefix != 0, sms)
+                                                    : plan_quant(B, T, Hq, Hkv, d, has_prefix != 0, sms).bytes;
 }
 
 bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
@@ -980,7 +966,8 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms);
   const int64_t most_tiles = a.k.heads * (qv.B * plan.own_rt * cdiv64(max_pages * page, kTileKeys) +
                                           plan.pre_rt * cdiv64(prefix_len, kTileKeys));
-  const size_t need = plan.bytes;
+  const bool wide = many_rows(qv.B, qv.S, G, prefix_len > 0);
+  const size_t need = wide ? wide_quant_bytes(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms) : plan.bytes;
   if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.heads > INT32_MAX ||
       need / (4 * (size_t)qv.D) > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
@@ -1009,6 +996,9 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < i; ++j)
       if ((st = check_apart(fn, writes[j], writes[i])) != BSA_OK) return st;
+  if (wide)
+    return launch_wide_quant(qv, a, new_lens, prefix_table, prefix_len, causal, softmax_scale, out, lse, workspace,
+                             reinterpret_cast<cudaStream_t>(stream));
   QAttnParams p{};
   p.k = static_cast<const uint8_t*>(a.k.ptr); p.v = static_cast<const uint8_t*>(a.v.ptr);
   p.k_page = a.k.stride_page; p.k_head = a.k.stride_head; p.v_page = a.v.stride_page; p.v_head = a.v.stride_head;
