@@ -87,6 +87,7 @@ struct PagedParams {
   const uint8_t* k4; const uint8_t* v4;                       // or, of 4 bits, its bytes
   int64_t k4_page, k4_head, v4_page, v4_head;
   uint32_t eights;                // kEights
+  int early;                      // the kernel behind may start beside this one (it waits for it at its end)
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   // read or written that it uses (and nothing by the read-only path, whose loads
   // may be taken from before this point).  2 us less a call in a row of them.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kQ4 && p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
 #pragma unroll 1
@@ -1204,7 +1206,7 @@ bsa_status set_smem() {
 }
 
 template <int D, bool kQ4>
-bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
+bsa_status launch_paged(const PagedParams& p, cudaStream_t stream, bool join = true) {
   bsa_status st = set_smem<D, kQ4>();
   if (st != BSA_OK) return st;
   cudaLaunchAttribute attr{};
@@ -1219,6 +1221,7 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream) {
   cfg.dynamicSmemBytes = PagedCfg<D, kQ4>::kSmemBytes;
   if ((st = cuda_check(cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kQ4>, p), "paged_attention_kernel launch")) != BSA_OK)
     return st;
+  if (!join) return BSA_OK;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   // Eight warps, one warp or eight lanes a row, by the number of rows (us of the
   // join: 32 rows of 40 partial results 6.4, with one warp 9; 2,048 rows of 2 to
@@ -1300,9 +1303,10 @@ size_t wide_quant_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d
   return plan_paged(B, T, Hq, Hkv, d, prefix, sms).bytes;
 }
 
-bsa_status launch_wide_quant(const bsa_tensor& qv, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
-                             int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
-                             void* workspace, cudaStream_t stream) {
+// The arguments of a launch over 4-bit pages.
+static PagedParams quant_params(const bsa_tensor& qv, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
+                                int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
+                                void* workspace) {
   const int64_t page = a.k.blocks * kBlockSlots;
   const int sms = num_sms();
   PagedArgs t{};
@@ -1314,7 +1318,32 @@ bsa_status launch_wide_quant(const bsa_tensor& qv, const QuantArgs& a, const int
   p.k4 = static_cast<const uint8_t*>(a.k.ptr); p.v4 = static_cast<const uint8_t*>(a.v.ptr);
   p.k4_page = a.k.stride_page; p.k4_head = a.k.stride_head; p.v4_page = a.v.stride_page; p.v4_head = a.v.stride_head;
   p.eights = kEights;
+  return p;
+}
+
+bsa_status launch_wide_quant(const bsa_tensor& qv, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
+                             int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
+                             void* workspace, cudaStream_t stream) {
+  const PagedParams p = quant_params(qv, a, new_lens, prefix_table, prefix_len, causal, softmax_scale, out, lse, workspace);
   return qv.D == 128 ? launch_paged<128, true>(p, stream) : launch_paged<64, true>(p, stream);
+}
+
+PrefixPart prefix_part(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, int sms) {
+  const PagedPlan w = plan_paged(B, T, Hq, Hkv, d, true, sms);
+  return PrefixPart{w.pre_rt, w.pre_slot_rows, w.own_first};
+}
+
+bsa_status launch_prefix_quant(const bsa_tensor& qv, const QuantArgs& a, const int32_t* new_lens,
+                               const int32_t* prefix_table, int32_t prefix_len, float softmax_scale, void* seg_ctas,
+                               float* part_ml, float* part_o, cudaStream_t stream) {
+  QuantArgs alone = a;
+  alone.max_pages = 0;
+  PagedParams p = quant_params(qv, alone, new_lens, prefix_table, prefix_len, 1, softmax_scale, nullptr, nullptr, nullptr);
+  p.seg_ctas = static_cast<int2*>(seg_ctas);
+  p.part_ml = part_ml;
+  p.part_o = part_o;
+  p.early = 1;
+  return qv.D == 128 ? launch_paged<128, true>(p, stream, false) : launch_paged<64, true>(p, stream, false);
 }
 
 }  // namespace bsa

@@ -29,6 +29,19 @@ size_t wide_quant_bytes(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d
 bsa_status launch_wide_quant(const bsa_tensor& q, const QuantArgs& a, const int32_t* new_lens, const int32_t* prefix_table,
                              int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
                              void* workspace, cudaStream_t stream);
+// The same kernel for the prefix alone, whose partial results the narrow kernel's
+// join reads: row tiles of the batch under a KV head (256 rows each; 0 where the
+// prefix goes with the requests' own keys), rows of a partial result, and of all.
+struct PrefixPart {
+  int rt, slot_rows;
+  size_t rows;
+};
+constexpr int kWideRows = 256, kWideHalf = 128;
+PrefixPart prefix_part(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, int sms);
+// The kernel launched behind it may start beside it, and waits for it at its end.
+bsa_status launch_prefix_quant(const bsa_tensor& q, const QuantArgs& a, const int32_t* new_lens,
+                               const int32_t* prefix_table, int32_t prefix_len, float softmax_scale, void* seg_ctas,
+                               float* part_ml, float* part_o, cudaStream_t stream);
 bsa_status check_quant(const char* fn, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
                        const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
                        int64_t B, QuantArgs* a);

@@ -86,6 +86,7 @@ struct QAttnParams {
   int pre_tiles;                  // key tiles of the prefix
   int pre_slot_rows, own_slot_rows;   // rows of a partial result
   int ctas;
+  int wide_ctas;                  // CTAs of the launch before, which has the prefix (pre_tiles is 0 here), or 0
   const int32_t* page_table; int64_t table_stride;
   const int32_t* kv_lens; const int32_t* new_lens;
   const int32_t* prefix_table;
@@ -266,8 +267,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     tmem_relinquish();
   }
   // Launched when the blocks of the kernel before leave: up to here nothing is
-  // read or written that it uses.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // read or written that it uses.  Beside the prefix's kernel, which has waited for
+  // what came before it and shares nothing with this one, the wait is at the end: the
+  // join behind waits for this kernel only.
+  if (p.wide_ctas == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
 #pragma unroll 1
@@ -744,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag);
       if (sync_any(!ok)) break;
       tc_fence_after();
-      const bool direct = p.pre_tiles == 0 && s.whole;
+      const bool direct = p.pre_rt == 0 && s.whole;
       if (th < rows) {
         const float sum = (parts[th] + parts[R + th]) + (parts[2 * R + th] + parts[3 * R + th]);
         // no score above kLowest: nothing is left, or NaN
@@ -792,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     tc_fence_after();
     tmem_dealloc(tmem, C::kColumns);
   }
+  if (p.wide_ctas != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Output row (b, i, h): joins the partial results of its prefix segment and of its
@@ -818,17 +822,21 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
   const bool keyed = real && i < n && (p.prefix_len > 0 || seen_keys(p, kv, n, i) > 0);
   if (real && i < n) {
     const int row = i * p.G + g, flat = b * p.TG + row;
-    const int pre_seg = hk * p.pre_rt + flat / p.R;
     const int rt = row / p.R, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
-    if (p.pre_tiles > 0) {
-      const int2 c = p.seg_ctas[pre_seg];
-      pre = partial(c, pre_seg, p.pre_slot_rows, flat % p.R);
+    if (p.wide_ctas > 0) {
+      const int seg = hk * p.pre_rt + flat / kWideRows;
+      const int2 c = p.seg_ctas[seg];
+      const bool two = p.B * p.TG - (flat - flat % kWideRows) <= kWideHalf;
+      pre = segment_parts(c.x, c.y, p.wide_ctas, seg, two, flat % kWideRows / kWideHalf, p.pre_slot_rows, flat % kWideHalf);
+    } else if (p.pre_rt > 0) {
+      const int seg = hk * p.pre_rt + flat / p.R;
+      pre = partial(p.seg_ctas[seg], seg, p.pre_slot_rows, flat % p.R);
     }
     if (own_tiles(p, kv, n, rt) > 0) {
       const int2 c = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
       own = partial(c, own_seg, p.own_slot_rows, row % p.R);
       own.at += p.own_first;
-      direct = p.pre_tiles == 0 && own.n == 1;       // written by the first kernel
+      direct = p.pre_rt == 0 && own.n == 1;       // written by the first kernel
     }
   }
   join_row<D, kLanes, kWarps>(p.part_ml, p.part_o, pre, own, real && !direct, keyed, p.out + R * D,
@@ -837,28 +845,42 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
 
 std::string s(int64_t v) { return std::to_string(v); }
 
-// Rows of a segment, and where the partial results lie in the workspace.
+// How a call is split, the rows of a segment, and where the partial results lie.
 struct QAttnPlan {
+  // kNarrow: this file's kernel alone; kWide: that of the bf16 pages alone; kBoth: that
+  // one for the prefix, this one for the requests' own keys
+  enum { kNarrow, kWide, kBoth } way;
   int R, TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
   size_t own_first, part_ml, part_o, bytes;
 };
-
-// Whether so many rows read the same keys that they are the first operand.
-bool many_rows(int64_t B, int64_t T, int64_t G, bool prefix) { return (prefix ? B * T * G : T * G) > 32; }
 
 QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
   QAttnPlan w{};
   w.TG = (int)(T * (Hq / Hkv));
   const int64_t most = prefix ? B * w.TG : w.TG;
-  w.R = most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  const PrefixPart wide = prefix ? prefix_part(B, T, Hq, Hkv, d, sms) : PrefixPart{};
+  w.way = most <= 32 ? QAttnPlan::kNarrow : w.TG <= 32 && wide.rt > 0 ? QAttnPlan::kBoth : QAttnPlan::kWide;
+  if (w.way == QAttnPlan::kWide) {
+    w.bytes = wide_quant_bytes(B, T, Hq, Hkv, d, prefix, sms);
+    return w;
+  }
+  const int64_t rows = w.way == QAttnPlan::kBoth ? w.TG : most;
+  w.R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   w.own_rt = (int)cdiv64(w.TG, w.R);
-  w.pre_rt = prefix ? (int)cdiv64(B * w.TG, w.R) : 0;
   w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
-  w.pre_slot_rows = (int)(B * w.TG < w.R ? B * w.TG : w.R);
-  auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   // a partial result for every number segment + CTA
   const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
-  const size_t pre = prefix ? (size_t)(Hkv * w.pre_rt + kCtasPerSm * sms) * w.pre_slot_rows : 0;
+  size_t pre = 0;
+  if (w.way == QAttnPlan::kBoth) {
+    w.pre_rt = wide.rt;
+    w.pre_slot_rows = wide.slot_rows;
+    pre = wide.rows;
+  } else if (prefix) {
+    w.pre_rt = (int)cdiv64(B * w.TG, w.R);
+    w.pre_slot_rows = (int)(B * w.TG < w.R ? B * w.TG : w.R);
+    pre = (size_t)(Hkv * w.pre_rt + kCtasPerSm * sms) * w.pre_slot_rows;
+  }
+  auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w.own_first = pre;
   w.part_ml = al((size_t)Hkv * (w.pre_rt + B * w.own_rt) * 8);      // behind the segments' CTAs
   w.part_o = w.part_ml + al((pre + own) * 8);
@@ -921,9 +943,7 @@ size_t bsaq_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has
   if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq > kMaxHeads || Hq % Hkv ||
       (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 16)
     return 0;
-  if (sms == 0) sms = num_sms();
-  return many_rows(B, T, Hq / Hkv, has_prefix != 0) ? wide_quant_bytes(B, T, Hq, Hkv, d, has_prefix != 0, sms)
-                                                    : plan_quant(B, T, Hq, Hkv, d, has_prefix != 0, sms).bytes;
+  return plan_quant(B, T, Hq, Hkv, d, has_prefix != 0, sms > 0 ? sms : num_sms()).bytes;
 }
 
 bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
@@ -964,10 +984,11 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   const int64_t flat_rows = qv.B * qv.S * G, page = a.k.blocks * kBlockSlots;
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms);
-  const int64_t most_tiles = a.k.heads * (qv.B * plan.own_rt * cdiv64(max_pages * page, kTileKeys) +
-                                          plan.pre_rt * cdiv64(prefix_len, kTileKeys));
-  const bool wide = many_rows(qv.B, qv.S, G, prefix_len > 0);
-  const size_t need = wide ? wide_quant_bytes(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms) : plan.bytes;
+  const int64_t own_rt = plan.way == QAttnPlan::kWide ? cdiv64(plan.TG, kWideHalf) : plan.own_rt;
+  const int64_t pre_rt = plan.way == QAttnPlan::kWide ? cdiv64(flat_rows, kWideHalf) : plan.pre_rt;
+  const int64_t most_tiles =
+      a.k.heads * (qv.B * own_rt * cdiv64(max_pages * page, kTileKeys) + (pre_rt + qv.B) * cdiv64(prefix_len, kTileKeys));
+  const size_t need = plan.bytes;
   if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.heads > INT32_MAX ||
       need / (4 * (size_t)qv.D) > INT32_MAX)
     return set_error(BSA_ERR_UNSUPPORTED, std::string(fn) + ": " + s(flat_rows) + " rows of up to " +
@@ -996,7 +1017,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   for (int i = 0; i < 3; ++i)
     for (int j = 0; j < i; ++j)
       if ((st = check_apart(fn, writes[j], writes[i])) != BSA_OK) return st;
-  if (wide)
+  if (plan.way == QAttnPlan::kWide)
     return launch_wide_quant(qv, a, new_lens, prefix_table, prefix_len, causal, softmax_scale, out, lse, workspace,
                              reinterpret_cast<cudaStream_t>(stream));
   QAttnParams p{};
@@ -1009,7 +1030,8 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.num_pages = (int)a.k.pages; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
   p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
   p.R = plan.R; p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
-  p.pre_tiles = (int)cdiv64(prefix_len, kTileKeys);
+  p.pre_tiles = plan.way == QAttnPlan::kBoth ? 0 : (int)cdiv64(prefix_len, kTileKeys);
+  p.wide_ctas = plan.way == QAttnPlan::kBoth ? sms : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
   p.ctas = kCtasPerSm * sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
@@ -1023,6 +1045,10 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
   p.own_first = (int)plan.own_first;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (plan.way == QAttnPlan::kBoth &&
+      (st = launch_prefix_quant(qv, a, new_lens, prefix_table, prefix_len, softmax_scale, p.seg_ctas, p.part_ml, p.part_o,
+                                cs)) != BSA_OK)
+    return st;
   if (plan.R == 4) return qv.D == 128 ? launch_quant<128, 4, true>(p, cs) : launch_quant<64, 4, true>(p, cs);
   if (plan.R == 8) return qv.D == 128 ? launch_quant<128, 8, true>(p, cs) : launch_quant<64, 8, true>(p, cs);
   if (plan.R == 16) return qv.D == 128 ? launch_quant<128, 16, false>(p, cs) : launch_quant<64, 16, false>(p, cs);
