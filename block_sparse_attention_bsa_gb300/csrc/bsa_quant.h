@@ -78,9 +78,22 @@ __device__ __forceinline__ uint32_t code_values(uint32_t raised, uint32_t scales
 __device__ __forceinline__ uint32_t scale_offset(uint32_t scales2) {
   return as_u32(__hmul2(as_bf16x2(scales2), as_bf16x2(0xC140C140u)));        // times -12
 }
-// Two codes, halved.
-__device__ __forceinline__ uint32_t half_codes(uint32_t raised) {
-  return as_u32(__hadd2(as_bf16x2(raised), as_bf16x2(0xC140C140u)));         // minus 12
+// A scale times 2^n, as bf16 bits.
+__device__ __forceinline__ uint32_t scale_times(uint32_t b, int n) { return b == 255u ? 0x7FFFu : (b << 4) + 0x3800u + (n << 7); }
+
+// The codes of eight neighbours in a word, without their scale: r[i] are those of
+// numbers 2 i and 2 i + 1, divided by 64 where i is even and by 8 where it is odd.
+// Four bits at the foot of a bf16, or four bits higher with the lowest one of its
+// exponent among them, are (c + 8) 2^-133 and (c + 8) 2^-129: numbers below and just
+// above the border of the subnormal ones are equally spaced.  One mask each, where
+// numbers that carry their exponent take a shift, too.
+__device__ __forceinline__ void bare_codes(uint32_t word, uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? word : word >> 8;
+    r[i] = i % 2 == 0 ? as_u32(__hfma2(as_bf16x2(w & 0x000F000Fu), as_bf16x2(0x7F007F00u), as_bf16x2(0xBE00BE00u)))    // 2^127, -1/8
+                      : as_u32(__hfma2(as_bf16x2(w & 0x00F000F0u), as_bf16x2(0x7E807E80u), as_bf16x2(0xBF80BF80u)));   // 2^126, -1
+  }
 }
 
 // Shared memory by its address.
@@ -98,6 +111,9 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t* r) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");

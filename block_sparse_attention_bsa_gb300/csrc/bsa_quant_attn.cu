@@ -47,29 +47,32 @@ constexpr int kCtasPerSm = 4;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
 constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
 
-// R: rows of a segment.  kScaled: the scales of V stand in the weights, of which
-// there is a set for each group of 32 channels, and V is made of the codes alone;
-// else they are multiplied into V.
-template <int D, int R, bool kScaled>
+// R: rows of a segment.  kBare: K and V are made of the codes alone, and the scales
+// stand beside the products: S has a set of columns for each group of 32 channels,
+// whose rows of Q are 0 in the others, and so has P, each set times its group's
+// scales of V.  Else the scales are multiplied into K and V.
+template <int D, int R, bool kBare>
 struct Cfg {
   static constexpr int kGroups = D / kGroup;
-  static constexpr int kSCols = R < 16 ? 16 : R;                       // columns of S (16 at least)
-  static constexpr int kSets = kScaled ? kGroups : 1;
-  static constexpr int kOCols = kSets * R < 16 ? 16 : kSets * R;       // columns of O, rows of P
-  static constexpr int kQBytes = kSCols * D * 2;
-  static constexpr int kPBytes = kOCols * kTileKeys * 2;
+  static constexpr int kSets = kBare ? kGroups : 1;
+  static constexpr int kCols = kSets * R < 16 ? 16 : kSets * R;        // columns of S and of O, rows of Q and of P
+  static constexpr int kSegSlots = R == 4 ? 3 : R <= 16 ? 2 : 1;       // segments, with their Q rows
+  static constexpr int kQBytes = kCols * D * 2;                        // as the MMAs read them
+  static constexpr int kQSlotBytes = kBare ? R * D * 2 : kQBytes;      // of a segment; bare: as they come
+  static constexpr int kQTotal = kSegSlots * kQSlotBytes + (kBare ? kQBytes : 0);
+  static constexpr int kPBytes = kCols * kTileKeys * 2;
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
-  static constexpr int kSegSlots = R == 4 ? 3 : R <= 16 ? 2 : 1;                     // segments, with their Q rows
   static constexpr int kSlots = 2;                                     // tiles
-  static constexpr int kScaleBytes = kScaled ? 0 : kGroups * kTileKeys * 2;
+  static constexpr int kScaleBytes = kBare ? 0 : kGroups * kTileKeys * 2;
   // What is made of K (groups) and of V (16 registers of 32 slots) before its place is free.
-  static constexpr int kAheadK = kScaled ? 2 : 0, kAheadV = kScaled ? 2 : 0;
+  static constexpr int kAheadK = kBare ? 2 : 0, kAheadV = kBare ? 2 : 0;
   static constexpr int kAhead = 16 * (kAheadK > kAheadV ? kAheadK : kAheadV > 0 ? kAheadV : 1);
-  static constexpr int kBarBytes = 2048;
-  static constexpr int kSmemBytes = 1024 + kSegSlots * kQBytes + kPBytes + 2 * kSlots * kTileBytes + kScaleBytes + kBarBytes;
+  static constexpr int kBarBytes = kBare ? 1024 : 2048;
+  static constexpr int kSmemBytes = 1024 + kQTotal + kPBytes + 2 * kSlots * kTileBytes + kScaleBytes + kBarBytes;
   // TMEM columns: K, then V; S; O
-  static constexpr int kA = 0, kS = 64, kO = kS + kSCols, kColumns = 128;
-  static_assert(kO + kOCols <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
+  static constexpr int kA = 0, kS = 64, kO = kS + kCols, kColumns = 128;
+  static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "the MMAs' rows are exchanged within 1024 bytes");
+  static_assert(kO + kCols <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
 };
 
 struct QAttnParams {
@@ -210,18 +213,19 @@ __device__ __forceinline__ float warp_max(float z) {
   return __int_as_float(u ^ (u >> 31 & 0x7FFFFFFF));
 }
 
-template <int D, int R, bool kScaled>
+template <int D, int R, bool kBare>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
-  using C = Cfg<D, R, kScaled>;
+  using C = Cfg<D, R, kBare>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const uint32_t q_smem = smem_u32(smem);                              // [kSegSlots] Q rows
-  const uint32_t p_smem = q_smem + C::kSegSlots * C::kQBytes;                     // P rows
-  const uint32_t k_ring = p_smem + C::kPBytes;                         // [kSlots] blocks of K
-  const uint32_t v_ring = k_ring + C::kSlots * C::kTileBytes;         // [kSlots] blocks of V
-  const uint32_t vscale = v_ring + C::kSlots * C::kTileBytes;         // [D / 32][128] twice the scales of V, bf16
-  uint8_t* rest = smem + (vscale - q_smem) + C::kScaleBytes;
+  const uint32_t p_smem = smem_u32(smem);                              // P rows
+  const uint32_t q_smem = p_smem + C::kPBytes;                         // bare: Q as the MMAs read it; [kSegSlots] Q rows
+  const uint32_t q_rows = q_smem + (kBare ? C::kQBytes : 0);
+  const uint32_t k_ring = q_smem + C::kQTotal;                         // [kSlots] blocks of K
+  const uint32_t v_ring = k_ring + C::kSlots * C::kTileBytes;          // [kSlots] blocks of V
+  const uint32_t vscale = v_ring + C::kSlots * C::kTileBytes;          // [D / 32][128] twice the scales of V, bf16
+  uint8_t* rest = smem + (vscale - p_smem) + C::kScaleBytes;
   float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
   float* parts = mr + R;                                               // [4][R] of each warp
   Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [kSegSlots]
@@ -261,6 +265,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     mbar_init(mma_end, 1);
     *abort_slot = 0;
     fence_mbar_init();
+  }
+  if constexpr (kBare) {                           // what is not of a row's group stays 0
+    for (int i = threadIdx.x; i < C::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(smem + C::kPBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), C::kColumns);
@@ -317,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, C::kSCols, false), idesc_o = idesc_bf16_f32(128, C::kOCols, false);
-    constexpr int kQChunk = (C::kSCols * 128) >> 4, kPChunk = (C::kOCols * 128) >> 4;
+    constexpr uint32_t idesc = idesc_bf16_f32(128, C::kCols, false);
+    constexpr int kChunk = (C::kCols * 128) >> 4;
     const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     const int c = lane % kVec;
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
@@ -416,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       __syncwarp();
       // Q rows, and rows of zeros up to a multiple of four
       const __nv_bfloat16* qh = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
-      const uint32_t base = q_smem + qb * C::kQBytes + (c / 8) * (C::kSCols * 128) + (lane / kVec) * 128;
+      const uint32_t to = q_rows + qb * C::kQSlotBytes;
       const int row = s.row0 + min(lane, s.rows - 1);
       const int b = p.div_TG.quot(row), rem = row - b * p.TG, i = p.div_G.quot(rem), g = rem - i * p.G;
       const uint32_t off = (uint32_t)((b * p.q_sb + i * p.q_ss + g * p.q_sh) / 8);    // below 2^32: host check
@@ -424,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       for (int y = 0; y * kRowsPer < ((s.rows + 3) & ~3); ++y) {
         const int r = y * kRowsPer + lane / kVec;
         const __nv_bfloat16* src = qh + (uint64_t)__shfl_sync(0xffffffffu, off, r) * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + y * kRowsPer * 128 + ((c % 8) ^ (r % 8)) * 16),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         to + (kBare ? r * (D * 2) + c * 16 : (c / 8) * (C::kCols * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16)),
                      "l"(src), "r"(r < s.rows ? 16 : 0)
                      : "memory");
       }
@@ -479,13 +487,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       if (!(ok = warp_wait(k_ready, i & 1, abort_flag))) break;
       fence_async_shared();                        // Q rows, which who made K has waited for, come by ordinary copies
       tc_fence_after();
-      const uint64_t qdesc = sdesc_sw128(q_smem + qb * C::kQBytes, 16, 1024);
+      const uint64_t qdesc = sdesc_sw128(q_smem + (kBare ? 0 : qb * C::kQBytes), 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = (uint64_t)((kk / 4) * kQChunk + (kk % 4) * 2);
-          if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc_s);
-          else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc_s);
+          const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
+          if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc);
+          else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc);
         }
         mma_commit(s_done);
       }
@@ -493,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       if (!(ok = warp_wait(pv_ready, i & 1, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc_o, !first);
+        mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc, !first);
 #pragma unroll
         for (int kk = 1; kk < kTileKeys / 16; ++kk)
-          mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kPChunk + (kk % 4) * 2), idesc_o);
+          mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
         mma_commit(pv_done);
       }
       __syncwarp();
@@ -521,10 +529,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t a_t = tmem + lanes + C::kA, s_t = tmem + lanes + C::kS;
     // of a set of weights for each group, the columns of this channel's
-    const uint32_t o_t = tmem + lanes + C::kO + (kScaled ? warp % C::kGroups * R : 0);
+    const uint32_t o_t = tmem + lanes + C::kO + (kBare ? warp % C::kGroups * R : 0);
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
     // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
-    const uint32_t p_at = p_smem + (th / 64) * (C::kOCols * 128) + th % 64 * 2;
+    const uint32_t p_at = p_smem + (th / 64) * (C::kCols * 128) + th % 64 * 2;
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
     for (int t = begin; t < end; ++seg_no) {
@@ -532,6 +540,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       ok = warp_wait(seg_full + 8 * qb, seg_no / C::kSegSlots & 1u, abort_flag);
       const Segment& s = segs[qb];                 // stays there until all are through with it
       if (th < R) mr[th] = kLowest;
+      if constexpr (kBare) {
+        // Q rows of each group, 0 elsewhere; every second pair of channels by 8, as K's
+        // codes there come out 8 times as large (all S so far are done)
+#pragma unroll
+        for (int x = th; x < R * D / 4; x += 128) {
+          const int r = x / (D / 4), ch = x % (D / 4) * 4, n = ch / kGroup * R + r;
+          uint2 q4 = lds64(q_rows + qb * C::kQSlotBytes + x * 8);
+          q4.y = as_u32(__hmul2(as_bf16x2(q4.y), as_bf16x2(0x3E003E00u)));
+          sts64(q_smem + (ch / 64) * (C::kCols * 128) + n * 128 + ((ch % 64 / 8) ^ (n % 8)) * 16 + ch % 8 * 2, q4);
+        }
+        fence_async_shared();
+      }
       if (sync_any(!ok)) break;
       const int rows = s.rows, tiles = s.tiles;
       // the keys of the first row; further rows' rise with the token
@@ -555,10 +575,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           const uint32_t scale_at = k_ring + at * C::kTileBytes + slot_at + code_bytes(D) + slot;
           auto group = [&](int g, uint32_t* r) {
             const uint4 c = lds128(from + g * 256);
-            const uint32_t s2 = twice_scale(lds8(scale_at + g * kBlockSlots)) * 0x10001u, off = scale_offset(s2);
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+            if constexpr (kBare) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4, p.eights), s2, off);
+              for (int i = 0; i < 4; ++i) bare_codes(word[i], r + 4 * i);
+            } else {
+              const uint32_t s2 = twice_scale(lds8(scale_at + g * kBlockSlots)) * 0x10001u, off = scale_offset(s2);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = code_values(raised_codes(word[i / 4], i % 4, p.eights), s2, off);
+            }
           };
 #pragma unroll
           for (int g = 0; g < C::kAheadK; ++g) group(g, ab + 16 * g);
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           }
         }
         // twice the scales of V, 0 behind the last key: what stands there must not count
-        if constexpr (!kScaled) {
+        if constexpr (!kBare) {
           ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g)
@@ -589,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint2 c = lds64(v_tile + (2 * x + y) * block_bytes(D) + th * 8);
-            if constexpr (kScaled) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) r[y * 8 + i] = half_codes(raised_codes(i < 4 ? c.x : c.y, i % 4, p.eights));
+            if constexpr (kBare) {
+              bare_codes(c.x, r + y * 8);
+              bare_codes(c.y, r + y * 8 + 4);
             } else {
               const uint32_t scale_at = vscale + (th / kGroup) * (kTileKeys * 2) + (2 * x + y) * 32;
               const uint4 sa = lds128(scale_at), sb = lds128(scale_at + 16);
@@ -602,14 +627,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             }
           }
         };
-        float vs2[C::kSets];                       // of this key
-        if constexpr (kScaled) {
-          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
+        float ks[C::kSets], vs[C::kSets];          // this key's scales of K and of V, times what the codes lack
+        if constexpr (kBare) {
+          const uint32_t scale_at = at * C::kTileBytes + slot_at + code_bytes(D) + slot;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g)
-            vs2[g] = th < tile_keys
-                         ? __uint_as_float(twice_scale(lds8(v_tile + slot_at + code_bytes(D) + g * kBlockSlots + slot)) << 16)
-                         : 0.f;
+            ks[g] = __uint_as_float(scale_times(lds8(k_ring + scale_at + g * kBlockSlots), 6) << 16);
+          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
+          // 0 behind the last key: what stands there must not count
+#pragma unroll
+          for (int g = 0; g < C::kGroups; ++g)
+            vs[g] = th < tile_keys ? __uint_as_float(scale_times(lds8(v_ring + scale_at + g * kBlockSlots), th & 2 ? 3 : 6) << 16) : 0.f;
           if (th < D) {
 #pragma unroll
             for (int x = 0; x < C::kAheadV; ++x) v_codes(x, ab + 16 * x);
@@ -617,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
         ok = warp_wait(s_done, it & 1u, abort_flag) && ok;
         tc_fence_after();
-        if constexpr (!kScaled) sync_any(false);   // the scales of V are there
+        if constexpr (!kBare) sync_any(false);   // the scales of V are there
         const int key = (s.tile0 + j) * kTileKeys + th;
         const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
         float v[R];
@@ -625,14 +653,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll 1
         for (;;) {
           // Scores in units of log 2, those of keys that a row does not see -inf.
-          tmem_ld_n<R>(s_t, v);
-          tmem_wait_ld();
+          {
+            float d[C::kSets * R];
+            tmem_ld_n<C::kSets * R>(s_t, d);
+            tmem_wait_ld();
 #pragma unroll
-          for (int r4 = 0; r4 < R; r4 += 4)
-            if (r4 < rows) {
+            for (int r = 0; r < R; ++r) {
+              v[r] = d[r];
+              if constexpr (kBare) {
+                v[r] *= ks[0];
 #pragma unroll
-              for (int r = r4; r < r4 + 4; ++r) v[r] *= p.scale_log2;
+                for (int g = 1; g < C::kGroups; ++g) v[r] = fmaf(d[g * R + r], ks[g], v[r]);
+              }
+              v[r] *= p.scale_log2;
             }
+          }
           if (cut) {
 #pragma unroll
             for (int r4 = 0; r4 < R; r4 += 4)
@@ -697,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
                 for (int x = 0; x < 4; x += 2) {
                   const int r = g * R + r4 + x;
-                  const uint32_t both = kScaled ? pack_bf16x2(v[r4 + x] * vs2[g], v[r4 + x + 1] * vs2[g])
+                  const uint32_t both = kBare ? pack_bf16x2(v[r4 + x] * vs[g], v[r4 + x + 1] * vs[g])
                                                 : pack_bf16x2(v[r4 + x], v[r4 + x + 1]);
                   sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
                   sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
@@ -888,7 +923,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   return w;
 }
 
-template <int D, int R, bool kScaled>
+template <int D, int R, bool kBare>
 bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
@@ -898,8 +933,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, R, kScaled>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Cfg<D, R, kScaled>::kSmemBytes),
+      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, R, kBare>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Cfg<D, R, kBare>::kSmemBytes),
                       "cudaFuncSetAttribute(quant_attention_kernel)");
       if (st != BSA_OK) return st;
       if (dev < 64) done[dev] = true;
@@ -914,8 +949,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<D, R, kScaled>::kSmemBytes;
-  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, R, kScaled>, p), "quant_attention_kernel launch")) != BSA_OK)
+  cfg.dynamicSmemBytes = Cfg<D, R, kBare>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, R, kBare>, p), "quant_attention_kernel launch")) != BSA_OK)
     return st;
   // Eight warps, one warp or eight lanes a row, as in the join of bsa_paged.cu.
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
