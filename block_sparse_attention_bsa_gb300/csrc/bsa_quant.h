@@ -78,8 +78,8 @@ __device__ __forceinline__ uint32_t code_values(uint32_t raised, uint32_t scales
 __device__ __forceinline__ uint32_t scale_offset(uint32_t scales2) {
   return as_u32(__hmul2(as_bf16x2(scales2), as_bf16x2(0xC140C140u)));        // times -12
 }
-// A scale times 2^n, as bf16 bits.
-__device__ __forceinline__ uint32_t scale_times(uint32_t b, int n) { return b == 255u ? 0x7FFFu : (b << 4) + 0x3800u + (n << 7); }
+// A scale times 2^n (255 is not told apart).
+__device__ __forceinline__ float scale_float(uint32_t b, int n) { return __uint_as_float((b << 20) + ((112u + n) << 23)); }
 
 // The codes of eight neighbours in a word, without their scale: r[i] are those of
 // numbers 2 i and 2 i + 1, divided by 64 where i is even and by 8 where it is odd.

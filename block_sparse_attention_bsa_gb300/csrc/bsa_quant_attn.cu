@@ -27,6 +27,7 @@
 //    lanes issues S; they turn scores into weights, then V into bf16, a channel per
 //    thread, over K's place in TMEM; one lane issues P V.
 #include <cuda_bf16.h>
+#include <math_constants.h>
 
 #include <cfloat>
 #include <cmath>
@@ -532,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     const uint32_t o_t = tmem + lanes + C::kO + (kBare ? warp % C::kGroups * R : 0);
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
     // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
-    const uint32_t p_at = p_smem + (th / 64) * (C::kCols * 128) + th % 64 * 2;
+    uint32_t p_at[8];                              // of rows r, r % 8 = 0 .. 7, but for 128 r
+#pragma unroll
+    for (int r = 0; r < 8; ++r) p_at[r] = (p_smem + (th / 64) * (C::kCols * 128) + th % 64 * 2) ^ (r << 4);
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
     for (int t = begin; t < end; ++seg_no) {
@@ -553,11 +556,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         fence_async_shared();
       }
       if (sync_any(!ok)) break;
-      const int rows = s.rows, tiles = s.tiles;
+      const int rows = s.rows, tiles = s.tiles, keys = s.keys, tile0 = s.tile0;
+      const int sb = s.b, skv = s.kv, sn = s.n;
       // the keys of the first row; further rows' rise with the token
-      const int rem0 = s.row0 - s.b * p.TG;
-      const bool even = s.b < 0 || !p.causal;
-      const int least = even ? s.keys : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0));
+      const int rem0 = s.row0 - sb * p.TG;
+      const bool even = sb < 0 || !p.causal;
+      const int least = even ? keys : seen_keys(p, skv, sn, p.div_G.quot(rem0));
       float l[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.f;
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll 1
       for (; j < tiles; ++j, ++it) {
         const uint32_t at = it % C::kSlots, use = it / C::kSlots & 1u;
-        const int tile_keys = min(s.keys - (s.tile0 + j) * kTileKeys, kTileKeys);
+        const int tile_keys = min(keys - (tile0 + j) * kTileKeys, kTileKeys);
         const uint32_t v_tile = v_ring + at * C::kTileBytes;
         // K, made while P V of the tile before, whose V it takes the place of, is on its way
         ok = warp_wait(k_full + 8 * at, use, abort_flag) && ok;
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           tc_fence_after();
 #pragma unroll
           for (int g = 0; g < C::kAheadK; ++g) tmem_st16(a_t + g * 16, ab + 16 * g);
-#pragma unroll 1
+#pragma unroll kBare ? 4 : 1
           for (int g = C::kAheadK; g < C::kGroups; ++g) {
             group(g, ab);
             tmem_st16(a_t + g * 16, ab);
@@ -630,14 +634,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         float ks[C::kSets], vs[C::kSets];          // this key's scales of K and of V, times what the codes lack
         if constexpr (kBare) {
           const uint32_t scale_at = at * C::kTileBytes + slot_at + code_bytes(D) + slot;
+          uint32_t most = 0;
 #pragma unroll
-          for (int g = 0; g < C::kGroups; ++g)
-            ks[g] = __uint_as_float(scale_times(lds8(k_ring + scale_at + g * kBlockSlots), 6) << 16);
+          for (int g = 0; g < C::kGroups; ++g) {
+            const uint32_t b = lds8(k_ring + scale_at + g * kBlockSlots);
+            ks[g] = scale_float(b, 6);
+            most = max(most, b);
+          }
           ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
-          // 0 behind the last key: what stands there must not count
 #pragma unroll
-          for (int g = 0; g < C::kGroups; ++g)
-            vs[g] = th < tile_keys ? __uint_as_float(scale_times(lds8(v_ring + scale_at + g * kBlockSlots), th & 2 ? 3 : 6) << 16) : 0.f;
+          for (int g = 0; g < C::kGroups; ++g) {
+            const uint32_t b = lds8(v_ring + scale_at + g * kBlockSlots);
+            vs[g] = scale_float(b, th & 2 ? 3 : 6);
+            most = max(most, b);
+          }
+          if (most == 255u) {                      // some group is not finite, or nothing was written here
+#pragma unroll
+            for (int g = 0; g < C::kGroups; ++g) {
+              if (lds8(k_ring + scale_at + g * kBlockSlots) == 255u) ks[g] = CUDART_NAN_F;
+              if (lds8(v_ring + scale_at + g * kBlockSlots) == 255u) vs[g] = th < tile_keys ? CUDART_NAN_F : 0.f;
+            }
+          }
           if (th < D) {
 #pragma unroll
             for (int x = 0; x < C::kAheadV; ++x) v_codes(x, ab + 16 * x);
@@ -646,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         ok = warp_wait(s_done, it & 1u, abort_flag) && ok;
         tc_fence_after();
         if constexpr (!kBare) sync_any(false);   // the scales of V are there
-        const int key = (s.tile0 + j) * kTileKeys + th;
-        const bool cut = (s.tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
+        const int key = (tile0 + j) * kTileKeys + th;
+        const bool cut = (tile0 + j + 1) * kTileKeys > least;       // some row does not see all of the tile
         float v[R];
         bool grow = j == 0, again = false;
 #pragma unroll 1
@@ -674,8 +691,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
               if (r4 < rows) {
 #pragma unroll
                 for (int r = r4; r < r4 + 4; ++r) {
-                  const int seen = even ? least : seen_keys(p, s.kv, s.n, p.div_G.quot(rem0 + r));
-                  if (key >= min(seen, s.keys)) v[r] = -INFINITY;
+                  const int seen = even ? least : seen_keys(p, skv, sn, p.div_G.quot(rem0 + r));
+                  if (key >= min(seen, keys)) v[r] = -INFINITY;
                 }
               }
           }
@@ -734,15 +751,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
                   const int r = g * R + r4 + x;
                   const uint32_t both = kBare ? pack_bf16x2(v[r4 + x] * vs[g], v[r4 + x + 1] * vs[g])
                                                 : pack_bf16x2(v[r4 + x], v[r4 + x + 1]);
-                  sts16((p_at ^ ((r & 7) << 4)) + r * 128, both);
-                  sts16((p_at ^ (((r + 1) & 7) << 4)) + (r + 1) * 128, both >> 16);
+                  sts16(p_at[r & 7] + r * 128, both);
+                  sts16(p_at[(r + 1) & 7] + (r + 1) * 128, both >> 16);
                 }
             }
           if (!again && th < D) {
             // V over K, whose product is done
 #pragma unroll
             for (int x = 0; x < C::kAheadV; ++x) tmem_st16(a_t + x * 16, ab + 16 * x);
-#pragma unroll 1
+#pragma unroll kBare ? 4 : 1
             for (int x = C::kAheadV; x < 4; ++x) {
               v_codes(x, ab);
               tmem_st16(a_t + x * 16, ab);
