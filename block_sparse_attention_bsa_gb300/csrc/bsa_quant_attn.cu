@@ -44,7 +44,6 @@ namespace {
 constexpr int kTileKeys = 128;
 constexpr int kTileBlocks = kTileKeys / kBlockSlots;
 constexpr int kThreads = 160;
-constexpr int kCtasPerSm = 4;
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
 constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
 
@@ -63,17 +62,17 @@ struct Cfg {
   static constexpr int kQTotal = kSegSlots * kQSlotBytes + (kBare ? kQBytes : 0);
   static constexpr int kPBytes = kCols * kTileKeys * 2;
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
-  static constexpr int kSlots = 2;                                     // tiles
+  static constexpr int kSlots = 3;                                     // places for the blocks of a tile of K or of V
   static constexpr int kScaleBytes = kBare ? 0 : kGroups * kTileKeys * 2;
   // What is made of K (groups) and of V (16 registers of 32 slots) before its place is free.
-  static constexpr int kAheadK = kBare ? 2 : 0, kAheadV = kBare ? 2 : 0;
+  static constexpr int kAheadK = kBare ? 1 : 0, kAheadV = kBare ? 1 : 0;
   static constexpr int kAhead = 16 * (kAheadK > kAheadV ? kAheadK : kAheadV > 0 ? kAheadV : 1);
   static constexpr int kBarBytes = kBare ? 1024 : 2048;
-  static constexpr int kSmemBytes = 1024 + kQTotal + kPBytes + 2 * kSlots * kTileBytes + kScaleBytes + kBarBytes;
-  // TMEM columns: K, then V; S; O
-  static constexpr int kA = 0, kS = 64, kO = kS + kCols, kColumns = 128;
+  static constexpr int kSmemBytes = 1024 + kQTotal + kPBytes + kSlots * kTileBytes + kScaleBytes + kBarBytes;
+  static constexpr int kA = 64, kSO = 2 * kCols;                       // columns of the two allocations: K, then V; S and O
+  static constexpr int kCtas = 4;                         // per SM, which has 512
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "the MMAs' rows are exchanged within 1024 bytes");
-  static_assert(kO + kCols <= kColumns && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "");
+  static_assert(kCtas * (kA + kSO) <= 512 && kCtas * (kSmemBytes + 1024) <= 233472, "");
 };
 
 struct QAttnParams {
@@ -215,7 +214,7 @@ __device__ __forceinline__ float warp_max(float z) {
 }
 
 template <int D, int R, bool kBare>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
   using C = Cfg<D, R, kBare>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -223,28 +222,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t p_smem = smem_u32(smem);                              // P rows
   const uint32_t q_smem = p_smem + C::kPBytes;                         // bare: Q as the MMAs read it; [kSegSlots] Q rows
   const uint32_t q_rows = q_smem + (kBare ? C::kQBytes : 0);
-  const uint32_t k_ring = q_smem + C::kQTotal;                         // [kSlots] blocks of K
-  const uint32_t v_ring = k_ring + C::kSlots * C::kTileBytes;          // [kSlots] blocks of V
-  const uint32_t vscale = v_ring + C::kSlots * C::kTileBytes;          // [D / 32][128] twice the scales of V, bf16
+  const uint32_t ring = q_smem + C::kQTotal;                           // [kSlots] blocks of K_0, V_0, K_1, V_1 ..
+  const uint32_t vscale = ring + C::kSlots * C::kTileBytes;          // [D / 32][128] twice the scales of V, bf16
   uint8_t* rest = smem + (vscale - p_smem) + C::kScaleBytes;
   float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
   float* parts = mr + R;                                               // [4][R] of each warp
   Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [kSegSlots]
   int* block_sum = reinterpret_cast<int*>(segs + C::kSegSlots);                  // [kMaxBlocks] tiles of own keys before request 32 i
   int* total_slot = block_sum + kMaxBlocks;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
-  int* abort_slot = total_slot + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);   // [2]
+  int* abort_slot = total_slot + 3;
   // barriers, as shared-memory addresses 8 bytes apart
   const uint32_t seg_full = smem_u32(total_slot + 4);            // [kSegSlots] the segment, and 32 lanes' copies of Q rows
   const uint32_t seg_empty = seg_full + 8 * C::kSegSlots;        // [kSegSlots] 4 warps
-  const uint32_t k_full = seg_empty + 8 * C::kSegSlots;          // [kSlots] transaction bytes
-  const uint32_t v_full = k_full + 8 * C::kSlots;               // [kSlots] transaction bytes
-  const uint32_t k_ready = v_full + 8 * C::kSlots;              // 4 warps: K stands in TMEM
+  const uint32_t full = seg_empty + 8 * C::kSegSlots;            // [kSlots] transaction bytes
+  const uint32_t k_ready = full + 8 * C::kSlots;                 // 4 warps: K stands in TMEM
   const uint32_t s_done = k_ready + 8;                           // commit
   const uint32_t pv_ready = s_done + 8;                          // 4 warps: V stands in TMEM, P in shared memory
   const uint32_t pv_done = pv_ready + 8;                         // commit
   const uint32_t mma_end = pv_done + 8;                          // commit
-  static_assert((5 * R + kMaxBlocks + 4) * 4 + C::kSegSlots * sizeof(Segment) + (2 * C::kSegSlots + 2 * C::kSlots + 5) * 8 <=
+  static_assert((5 * R + kMaxBlocks + 4) * 4 + C::kSegSlots * sizeof(Segment) + (2 * C::kSegSlots + C::kSlots + 5) * 8 <=
                     C::kBarBytes, "barrier block");
   const uint32_t abort_flag = smem_u32(abort_slot);
 
@@ -255,10 +252,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       mbar_init(seg_full + 8 * i, 33);
       mbar_init(seg_empty + 8 * i, 4);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(k_full + 8 * i, 1);
-      mbar_init(v_full + 8 * i, 1);
-    }
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(full + 8 * i, 1);
     mbar_init(k_ready, 4);
     mbar_init(s_done, 1);
     mbar_init(pv_ready, 4);
@@ -271,7 +265,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     for (int i = threadIdx.x; i < C::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(smem + C::kPBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), C::kColumns);
+    // Two pieces, since a piece is a power of two.  No SM holds so many CTAs that each
+    // could have its first one and wait for its second.
+    tmem_alloc(smem_u32(tmem_slot), C::kA);
+    tmem_alloc(smem_u32(tmem_slot + 1), C::kSO);
     tmem_relinquish();
   }
   // Launched when the blocks of the kernel before leave: up to here nothing is
@@ -307,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     if (lane == 0) *total_slot = before;
   }
   __syncthreads();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_a = tmem_slot[0], tmem_s = tmem_slot[1], tmem_o = tmem_s + C::kCols;
   int begin = 0, end = 0;
   {
     const Cut cut(p, *total_slot);
@@ -320,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 
   if (warp == 4) {
     // ------------------------------- segments, Q rows, copies of tiles, MMAs ---
-    // In turn: S of tile i, P V of tile i, the copies of tile i + 2 into the place of
-    // tile i, its segment found where a new one begins.
+    // In turn: S of tile i, V of tile i + 1, P V of tile i, K of tile i + 2, whose segment
+    // is found where a new one begins.
     // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
@@ -331,20 +328,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     const int c = lane % kVec;
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
     int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
-    // Lane x copies page x of a tile's K, lane 8 + x of its V.
+    // Lane x copies page x of a tile.
     const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
     const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
-    const int x = lane % 8;
-    const bool is_v = lane >= 8, copies = lane < 16 && x < per_tile;
-    const int64_t page_stride = is_v ? p.v_page : p.k_page;
+    const bool copies = lane < per_tile;
     const int tiles = end - begin;
     uint32_t seg_no = 0;                           // segments found
     int left = 0, tile = 0, keys = 0, page = 0;    // of the last one: tiles to copy, the next, where its keys end, this lane's page
     const int32_t* table = nullptr;
-    const uint8_t* head = nullptr;
+    const uint8_t* k_head = nullptr;
+    const uint8_t* v_head = nullptr;
     uint32_t starts = 0;                           // bit i % 4: tile i is the first of a segment
     auto page_of = [&](int t) {
-      const int key = t * kTileKeys + x * per_page * kBlockSlots;
+      const int key = t * kTileKeys + lane * per_page * kBlockSlots;
       int pg = 0;
       if (copies && key < keys) {
         pg = table[key >> p.page_shift];
@@ -410,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       // its first tile's pages are on their way while its place is waited for
       left = s.tiles; tile = s.tile0; keys = s.keys;
       table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
-      head = is_v ? p.v + s.hk * p.v_head : p.k + s.hk * p.k_head;
+      k_head = p.k + s.hk * p.k_head;
+      v_head = p.v + s.hk * p.v_head;
       page = page_of(tile);
       const uint32_t qb = seg_no % C::kSegSlots;
       if (!warp_wait(seg_empty + 8 * qb, (seg_no / C::kSegSlots & 1u) ^ 1u, abort_flag)) return false;
@@ -442,41 +439,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       ++seg_no;
       return true;
     };
-    // K and V of tile i of this CTA.  Their places are free: of the tile that stood
-    // there P V has been asked for, by which K and V were in TMEM.
-    auto copy_tile = [&](int i) {
-      starts &= ~(1u << (i & 3));
-      if (left == 0) {
-        if (!find_segment(begin + i)) return false;
-        starts |= 1u << (i & 3);
-      }
-      const int blocks = (min(keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
-      const int count = min(blocks - x * per_page, per_page);
-      const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
-      const uint32_t at = i % C::kSlots;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(k_full + 8 * at, blocks * block_bytes(D));
-        mbar_arrive_expect_tx(v_full + 8 * at, blocks * block_bytes(D));
-      }
-      __syncwarp();
-      if (copies && count > 0)
-        bulk_load((is_v ? v_ring : k_ring) + at * C::kTileBytes + x * per_page * block_bytes(D),
-                  head + page * page_stride + in_page * block_bytes(D), count * block_bytes(D), (is_v ? v_full : k_full) + 8 * at);
-      ++tile;
-      if (--left > 0) page = page_of(tile);
-      return true;
-    };
-    int copied = 0, pv_issued = 0;
-    // The copies that have a place.  A segment's place is that of the kSegSlots-th before
-    // it, which is given back when all its P V have been asked for, not sooner: with a
-    // place for one only its first tile waits for that.
+    // The copies that have a place: K of tile i where V of tile i - 2 stood, once P V of
+    // that has been asked for; V of tile i where K of tile i - 1 stood, once that is in
+    // TMEM.  A segment's place is that of the kSegSlots-th before it, which is given back
+    // when all its P V have been asked for, not sooner: with a place for one only its
+    // first tile waits for that.
+    int copied = 0, s_issued = 0, pv_issued = 0;   // tiles of K and of V, S, P V
     auto copy_tiles = [&]() {
 #pragma unroll 1
-      while (copied < tiles && copied < pv_issued + C::kSlots && (C::kSegSlots > 1 || left > 0 || copied == pv_issued)) {
-        if (!copy_tile(copied)) return false;
-        ++copied;
+      for (;; ++copied) {
+        const int i = copied >> 1;
+        const bool v = copied & 1;
+        if (i >= tiles || (v ? i > s_issued : i > pv_issued + 1)) return true;
+        if (!v) {
+          starts &= ~(1u << (i & 3));
+          if (left == 0) {
+            if (C::kSegSlots == 1 && i > pv_issued) return true;
+            if (!find_segment(begin + i)) return false;
+            starts |= 1u << (i & 3);
+          }
+        }
+        const int blocks = (min(keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
+        const int count = min(blocks - lane * per_page, per_page);
+        const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
+        const uint32_t at = copied % C::kSlots;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * at, blocks * block_bytes(D));
+        __syncwarp();
+        if (copies && count > 0)
+          bulk_load(ring + at * C::kTileBytes + lane * per_page * block_bytes(D),
+                    (v ? v_head + page * p.v_page : k_head + page * p.k_page) + in_page * block_bytes(D), count * block_bytes(D),
+                    full + 8 * at);
+        if (v) {
+          ++tile;
+          if (--left > 0) page = page_of(tile);
+        }
       }
-      return true;
     };
     ok = copy_tiles();
     uint32_t qb = C::kSegSlots - 1;                // of the tile's segment
@@ -493,19 +490,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2);
-          if (kk == 0) mma_ts_acc<0>(tmem + C::kS, tmem + C::kA, qdesc, idesc);
-          else mma_ts_acc<1>(tmem + C::kS, tmem + C::kA + kk * 8, qdesc + off, idesc);
+          if (kk == 0) mma_ts_acc<0>(tmem_s, tmem_a, qdesc, idesc);
+          else mma_ts_acc<1>(tmem_s, tmem_a + kk * 8, qdesc + off, idesc);
         }
         mma_commit(s_done);
       }
       __syncwarp();
+      ++s_issued;
+      if (!(ok = copy_tiles())) break;
       if (!(ok = warp_wait(pv_ready, i & 1, abort_flag))) break;
       tc_fence_after();
       if (elect_one()) {
-        mma_ts(tmem + C::kO, tmem + C::kA, pdesc, idesc, !first);
+        mma_ts(tmem_o, tmem_a, pdesc, idesc, !first);
 #pragma unroll
         for (int kk = 1; kk < kTileKeys / 16; ++kk)
-          mma_ts_acc<1>(tmem + C::kO, tmem + C::kA + kk * 8, pdesc + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
+          mma_ts_acc<1>(tmem_o, tmem_a + kk * 8, pdesc + (uint64_t)((kk / 4) * kChunk + (kk % 4) * 2), idesc);
         mma_commit(pv_done);
       }
       __syncwarp();
@@ -515,10 +514,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // Nothing is in flight when the CTA leaves or frees its TMEM, after an abort either.
     if (elect_one()) {
 #pragma unroll 1
-      for (int i = max(copied - C::kSlots, 0); i < copied; ++i) {
-        mbar_drain(k_full + 8 * (i % C::kSlots), i / C::kSlots & 1);
-        mbar_drain(v_full + 8 * (i % C::kSlots), i / C::kSlots & 1);
-      }
+      for (int i = max(copied - C::kSlots, 0); i < copied; ++i) mbar_drain(full + 8 * (i % C::kSlots), i / C::kSlots & 1);
       mma_commit(mma_end);
       mbar_drain(mma_end, 0);
     }
@@ -528,9 +524,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // ------------------------------------------- codes, products, weights, results ---
     const int th = threadIdx.x;                    // key of a tile, and channel of V and O
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t a_t = tmem + lanes + C::kA, s_t = tmem + lanes + C::kS;
+    const uint32_t a_t = tmem_a + lanes, s_t = tmem_s + lanes;
     // of a set of weights for each group, the columns of this channel's
-    const uint32_t o_t = tmem + lanes + C::kO + (kBare ? warp % C::kGroups * R : 0);
+    const uint32_t o_t = tmem_o + lanes + (kBare ? warp % C::kGroups * R : 0);
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots;
     // where this key's weights stand in P: rows of 64 keys, 16-byte pieces exchanged within 8 rows
     uint32_t p_at[8];                              // of rows r, r % 8 = 0 .. 7, but for 128 r
@@ -568,15 +564,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       int j = 0;
 #pragma unroll 1
       for (; j < tiles; ++j, ++it) {
-        const uint32_t at = it % C::kSlots, use = it / C::kSlots & 1u;
+        const uint32_t nk = 2 * it, nv = nk + 1, k_at = nk % C::kSlots, v_at = nv % C::kSlots;
         const int tile_keys = min(keys - (tile0 + j) * kTileKeys, kTileKeys);
-        const uint32_t v_tile = v_ring + at * C::kTileBytes;
+        const uint32_t k_tile = ring + k_at * C::kTileBytes, v_tile = ring + v_at * C::kTileBytes;
         // K, made while P V of the tile before, whose V it takes the place of, is on its way
-        ok = warp_wait(k_full + 8 * at, use, abort_flag) && ok;
+        ok = warp_wait(full + 8 * k_at, nk / C::kSlots & 1u, abort_flag) && ok;
         uint32_t ab[C::kAhead];                    // of K, then of V: what waits for a product to be done
         {
-          const uint32_t from = k_ring + at * C::kTileBytes + slot_at + slot * 16;
-          const uint32_t scale_at = k_ring + at * C::kTileBytes + slot_at + code_bytes(D) + slot;
+          const uint32_t from = k_tile + slot_at + slot * 16;
+          const uint32_t scale_at = k_tile + slot_at + code_bytes(D) + slot;
           auto group = [&](int g, uint32_t* r) {
             const uint4 c = lds128(from + g * 256);
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
@@ -601,9 +597,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             tmem_st16(a_t + g * 16, ab);
           }
         }
+        // This key's scales, times what the codes lack; not finite: NaN, but 0 behind the
+        // last key, whatever stands there.
+        auto read_scales = [&](uint32_t tile, int n, float* s) {
+          uint32_t most = 0;
+#pragma unroll
+          for (int g = 0; g < C::kSets; ++g) {
+            const uint32_t b = lds8(tile + slot_at + code_bytes(D) + g * kBlockSlots + slot);
+            s[g] = scale_float(b, n);
+            most = max(most, b);
+          }
+          if (most == 255u) {
+#pragma unroll
+            for (int g = 0; g < C::kSets; ++g)
+              if (lds8(tile + slot_at + code_bytes(D) + g * kBlockSlots + slot) == 255u) s[g] = th < tile_keys ? CUDART_NAN_F : 0.f;
+          }
+        };
+        float ks[C::kSets];
+        if constexpr (kBare) read_scales(k_tile, 6, ks);
         // twice the scales of V, 0 behind the last key: what stands there must not count
         if constexpr (!kBare) {
-          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
+          ok = warp_wait(full + 8 * v_at, nv / C::kSlots & 1u, abort_flag) && ok;
 #pragma unroll
           for (int g = 0; g < C::kGroups; ++g)
             sts16(vscale + (g * kTileKeys + th) * 2,
@@ -631,30 +645,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             }
           }
         };
-        float ks[C::kSets], vs[C::kSets];          // this key's scales of K and of V, times what the codes lack
+        float vs[C::kSets];
         if constexpr (kBare) {
-          const uint32_t scale_at = at * C::kTileBytes + slot_at + code_bytes(D) + slot;
-          uint32_t most = 0;
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const uint32_t b = lds8(k_ring + scale_at + g * kBlockSlots);
-            ks[g] = scale_float(b, 6);
-            most = max(most, b);
-          }
-          ok = warp_wait(v_full + 8 * at, use, abort_flag) && ok;
-#pragma unroll
-          for (int g = 0; g < C::kGroups; ++g) {
-            const uint32_t b = lds8(v_ring + scale_at + g * kBlockSlots);
-            vs[g] = scale_float(b, th & 2 ? 3 : 6);
-            most = max(most, b);
-          }
-          if (most == 255u) {                      // some group is not finite, or nothing was written here
-#pragma unroll
-            for (int g = 0; g < C::kGroups; ++g) {
-              if (lds8(k_ring + scale_at + g * kBlockSlots) == 255u) ks[g] = CUDART_NAN_F;
-              if (lds8(v_ring + scale_at + g * kBlockSlots) == 255u) vs[g] = th < tile_keys ? CUDART_NAN_F : 0.f;
-            }
-          }
+          ok = warp_wait(full + 8 * v_at, nv / C::kSlots & 1u, abort_flag) && ok;
+          read_scales(v_tile, th & 2 ? 3 : 6, vs);
           if (th < D) {
 #pragma unroll
             for (int x = 0; x < C::kAheadV; ++x) v_codes(x, ab + 16 * x);
@@ -675,26 +669,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             tmem_ld_n<C::kSets * R>(s_t, d);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              v[r] = d[r];
+            for (int r = 0; r < R; r += 2) {
+              float2 z = make_float2(d[r], d[r + 1]);
               if constexpr (kBare) {
-                v[r] *= ks[0];
+                z = __fmul2_rn(z, make_float2(ks[0], ks[0]));
 #pragma unroll
-                for (int g = 1; g < C::kGroups; ++g) v[r] = fmaf(d[g * R + r], ks[g], v[r]);
+                for (int g = 1; g < C::kGroups; ++g)
+                  z = __ffma2_rn(make_float2(d[g * R + r], d[g * R + r + 1]), make_float2(ks[g], ks[g]), z);
               }
-              v[r] *= p.scale_log2;
+              z = __fmul2_rn(z, make_float2(p.scale_log2, p.scale_log2));
+              v[r] = z.x;
+              v[r + 1] = z.y;
             }
           }
           if (cut) {
+            if (even) {
 #pragma unroll
-            for (int r4 = 0; r4 < R; r4 += 4)
-              if (r4 < rows) {
+              for (int r = 0; r < R; ++r)
+                if (key >= least) v[r] = -INFINITY;
+            } else {
 #pragma unroll
-                for (int r = r4; r < r4 + 4; ++r) {
-                  const int seen = even ? least : seen_keys(p, skv, sn, p.div_G.quot(rem0 + r));
-                  if (key >= min(seen, keys)) v[r] = -INFINITY;
-                }
-              }
+              for (int r = 0; r < R; ++r)
+                if (key >= min(seen_keys(p, skv, sn, p.div_G.quot(rem0 + r)), keys)) v[r] = -INFINITY;
+            }
           }
           if (grow) {
             // the maximum moves to the largest score so far
@@ -739,7 +736,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           for (int r4 = 0; r4 < R; r4 += 4)
             if (r4 < rows) {
               const float4 m = *reinterpret_cast<const float4*>(mr + r4);
-              const float e[4] = {v[r4] - m.x, v[r4 + 1] - m.y, v[r4 + 2] - m.z, v[r4 + 3] - m.w};
+              const float2 e01 = __fadd2_rn(make_float2(v[r4], v[r4 + 1]), make_float2(-m.x, -m.y));
+              const float2 e23 = __fadd2_rn(make_float2(v[r4 + 2], v[r4 + 3]), make_float2(-m.z, -m.w));
+              const float e[4] = {e01.x, e01.y, e23.x, e23.y};
               top = max3f(max3f(top, e[0], e[1]), e[2], e[3]);
 #pragma unroll
               for (int x = 0; x < 4; ++x) v[r4 + x] = ex2_approx(e[x]);
@@ -749,8 +748,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
 #pragma unroll
                 for (int x = 0; x < 4; x += 2) {
                   const int r = g * R + r4 + x;
-                  const uint32_t both = kBare ? pack_bf16x2(v[r4 + x] * vs[g], v[r4 + x + 1] * vs[g])
-                                                : pack_bf16x2(v[r4 + x], v[r4 + x + 1]);
+                  float2 w = make_float2(v[r4 + x], v[r4 + x + 1]);
+                  if constexpr (kBare) w = __fmul2_rn(w, make_float2(vs[g], vs[g]));
+                  const uint32_t both = pack_bf16x2(w.x, w.y);
                   sts16(p_at[r & 7] + r * 128, both);
                   sts16(p_at[(r + 1) & 7] + (r + 1) * 128, both >> 16);
                 }
@@ -781,7 +781,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         for (int r4 = 0; r4 < R; r4 += 4)
           if (r4 < rows) {
 #pragma unroll
-            for (int r = r4; r < r4 + 4; ++r) l[r] += v[r];
+            for (int r = r4; r < r4 + 4; r += 2) {
+              const float2 sum = __fadd2_rn(make_float2(l[r], l[r + 1]), make_float2(v[r], v[r + 1]));
+              l[r] = sum.x;
+              l[r + 1] = sum.y;
+            }
           }
       }
       if (j < tiles) break;
@@ -845,7 +849,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kColumns);
+    tmem_dealloc(tmem_a, C::kA);
+    tmem_dealloc(tmem_s, C::kSO);
   }
   if (p.wide_ctas != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -906,6 +911,11 @@ struct QAttnPlan {
   size_t own_first, part_ml, part_o, bytes;
 };
 
+int ctas_per_sm(int64_t D, int R) {
+  if (D == 128) return R == 4 ? Cfg<128, 4, true>::kCtas : R == 8 ? Cfg<128, 8, true>::kCtas : R == 16 ? Cfg<128, 16, false>::kCtas : Cfg<128, 32, false>::kCtas;
+  return R == 4 ? Cfg<64, 4, true>::kCtas : R == 8 ? Cfg<64, 8, true>::kCtas : R == 16 ? Cfg<64, 16, false>::kCtas : Cfg<64, 32, false>::kCtas;
+}
+
 QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
   QAttnPlan w{};
   w.TG = (int)(T * (Hq / Hkv));
@@ -921,7 +931,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   w.own_rt = (int)cdiv64(w.TG, w.R);
   w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
   // a partial result for every number segment + CTA
-  const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
+  const size_t own = (size_t)(B * Hkv * w.own_rt + ctas_per_sm(d, w.R) * sms) * w.own_slot_rows;
   size_t pre = 0;
   if (w.way == QAttnPlan::kBoth) {
     w.pre_rt = wide.rt;
@@ -930,7 +940,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   } else if (prefix) {
     w.pre_rt = (int)cdiv64(B * w.TG, w.R);
     w.pre_slot_rows = (int)(B * w.TG < w.R ? B * w.TG : w.R);
-    pre = (size_t)(Hkv * w.pre_rt + kCtasPerSm * sms) * w.pre_slot_rows;
+    pre = (size_t)(Hkv * w.pre_rt + ctas_per_sm(d, w.R) * sms) * w.pre_slot_rows;
   }
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w.own_first = pre;
@@ -1085,7 +1095,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.pre_tiles = plan.way == QAttnPlan::kBoth ? 0 : (int)cdiv64(prefix_len, kTileKeys);
   p.wide_ctas = plan.way == QAttnPlan::kBoth ? sms : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
-  p.ctas = kCtasPerSm * sms;
+  p.ctas = ctas_per_sm(qv.D, plan.R) * sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
