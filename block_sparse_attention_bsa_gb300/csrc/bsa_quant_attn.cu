@@ -44,19 +44,22 @@ namespace {
 constexpr int kTileKeys = 128;
 constexpr int kTileBlocks = kTileKeys / kBlockSlots;
 constexpr int kThreads = 160;
+constexpr int kCtasPerSm = 4;        // 16 x 8,192 keys in 44 us; three 47, five (72 registers a thread) 45
 constexpr int kMaxBlocks = kMaxPagedBatch / 32;      // blocks of 32 requests in the schedule
 constexpr float kLowest = -3e38f;                    // stands for a maximum of no score yet
 
 // R: rows of a segment.  kBare: K and V are made of the codes alone, and the scales
 // stand beside the products: S has a set of columns for each group of 32 channels,
 // whose rows of Q are 0 in the others, and so has P, each set times its group's
-// scales of V.  Else the scales are multiplied into K and V.
-template <int D, int R, bool kBare>
+// scales of V.  Else (16 rows of heads of 128, whose sets TMEM has no room for) the
+// scales are multiplied into K and V.
+template <int D, int R>
 struct Cfg {
+  static constexpr bool kBare = D / kGroup * R <= 32;
   static constexpr int kGroups = D / kGroup;
   static constexpr int kSets = kBare ? kGroups : 1;
   static constexpr int kCols = kSets * R < 16 ? 16 : kSets * R;        // columns of S and of O, rows of Q and of P
-  static constexpr int kSegSlots = R == 4 ? 3 : R <= 16 ? 2 : 1;       // segments, with their Q rows
+  static constexpr int kSegSlots = R == 4 ? 3 : 2;                     // segments, with their Q rows
   static constexpr int kQBytes = kCols * D * 2;                        // as the MMAs read them
   static constexpr int kQSlotBytes = kBare ? R * D * 2 : kQBytes;      // of a segment; bare: as they come
   static constexpr int kQTotal = kSegSlots * kQSlotBytes + (kBare ? kQBytes : 0);
@@ -67,12 +70,11 @@ struct Cfg {
   // What is made of K (groups) and of V (16 registers of 32 slots) before its place is free.
   static constexpr int kAheadK = kBare ? 1 : 0, kAheadV = kBare ? 1 : 0;
   static constexpr int kAhead = 16 * (kAheadK > kAheadV ? kAheadK : kAheadV > 0 ? kAheadV : 1);
-  static constexpr int kBarBytes = kBare ? 1024 : 2048;
+  static constexpr int kBarBytes = 2048;
   static constexpr int kSmemBytes = 1024 + kQTotal + kPBytes + kSlots * kTileBytes + kScaleBytes + kBarBytes;
-  static constexpr int kA = 64, kSO = 2 * kCols;                       // columns of the two allocations: K, then V; S and O
-  static constexpr int kCtas = 4;                         // per SM, which has 512
+  static constexpr int kA = 0, kS = 64, kO = kS + kCols, kColumns = 128;       // TMEM columns: K, then V; S; O
   static_assert(kPBytes % 1024 == 0 && kQBytes % 1024 == 0, "the MMAs' rows are exchanged within 1024 bytes");
-  static_assert(kCtas * (kA + kSO) <= 512 && kCtas * (kSmemBytes + 1024) <= 233472, "");
+  static_assert(kO + kCols <= kColumns && kCtasPerSm * kColumns <= 512 && kCtasPerSm * (kSmemBytes + 1024) <= 233472, "an SM's columns and shared memory");
 };
 
 struct QAttnParams {
@@ -213,9 +215,10 @@ __device__ __forceinline__ float warp_max(float z) {
   return __int_as_float(u ^ (u >> 31 & 0x7FFFFFFF));
 }
 
-template <int D, int R, bool kBare>
-__global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
-  using C = Cfg<D, R, kBare>;
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
+  using C = Cfg<D, R>;
+  constexpr bool kBare = C::kBare;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -230,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
   Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [kSegSlots]
   int* block_sum = reinterpret_cast<int*>(segs + C::kSegSlots);                  // [kMaxBlocks] tiles of own keys before request 32 i
   int* total_slot = block_sum + kMaxBlocks;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);   // [2]
-  int* abort_slot = total_slot + 3;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
+  int* abort_slot = total_slot + 2;
   // barriers, as shared-memory addresses 8 bytes apart
   const uint32_t seg_full = smem_u32(total_slot + 4);            // [kSegSlots] the segment, and 32 lanes' copies of Q rows
   const uint32_t seg_empty = seg_full + 8 * C::kSegSlots;        // [kSegSlots] 4 warps
@@ -265,10 +268,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
     for (int i = threadIdx.x; i < C::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(smem + C::kPBytes)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (warp == 0) {
-    // Two pieces, since a piece is a power of two.  No SM holds so many CTAs that each
-    // could have its first one and wait for its second.
-    tmem_alloc(smem_u32(tmem_slot), C::kA);
-    tmem_alloc(smem_u32(tmem_slot + 1), C::kSO);
+    tmem_alloc(smem_u32(tmem_slot), C::kColumns);
     tmem_relinquish();
   }
   // Launched when the blocks of the kernel before leave: up to here nothing is
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
     if (lane == 0) *total_slot = before;
   }
   __syncthreads();
-  const uint32_t tmem_a = tmem_slot[0], tmem_s = tmem_slot[1], tmem_o = tmem_s + C::kCols;
+  const uint32_t tmem_a = *tmem_slot + C::kA, tmem_s = *tmem_slot + C::kS, tmem_o = *tmem_slot + C::kO;
   int begin = 0, end = 0;
   {
     const Cut cut(p, *total_slot);
@@ -441,9 +441,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
     };
     // The copies that have a place: K of tile i where V of tile i - 2 stood, once P V of
     // that has been asked for; V of tile i where K of tile i - 1 stood, once that is in
-    // TMEM.  A segment's place is that of the kSegSlots-th before it, which is given back
-    // when all its P V have been asked for, not sooner: with a place for one only its
-    // first tile waits for that.
+    // TMEM.  (A segment's place is that of the kSegSlots-th before it, all P V of which
+    // have been asked for by then: its results are on their way out.)
     int copied = 0, s_issued = 0, pv_issued = 0;   // tiles of K and of V, S, P V
     auto copy_tiles = [&]() {
 #pragma unroll 1
@@ -454,7 +453,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
         if (!v) {
           starts &= ~(1u << (i & 3));
           if (left == 0) {
-            if (C::kSegSlots == 1 && i > pv_issued) return true;
             if (!find_segment(begin + i)) return false;
             starts |= 1u << (i & 3);
           }
@@ -849,8 +847,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, R, kBare>::kCtas) quant_atten
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_a, C::kA);
-    tmem_dealloc(tmem_s, C::kSO);
+    tmem_dealloc(*tmem_slot, C::kColumns);
   }
   if (p.wide_ctas != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -911,27 +908,28 @@ struct QAttnPlan {
   size_t own_first, part_ml, part_o, bytes;
 };
 
-int ctas_per_sm(int64_t D, int R) {
-  if (D == 128) return R == 4 ? Cfg<128, 4, true>::kCtas : R == 8 ? Cfg<128, 8, true>::kCtas : R == 16 ? Cfg<128, 16, false>::kCtas : Cfg<128, 32, false>::kCtas;
-  return R == 4 ? Cfg<64, 4, true>::kCtas : R == 8 ? Cfg<64, 8, true>::kCtas : R == 16 ? Cfg<64, 16, false>::kCtas : Cfg<64, 32, false>::kCtas;
-}
+// Up to so many rows of a segment the keys are the first operand.  16 requests of
+// 8,192 keys, heads of 128 (us here / with the rows as the first operand): 8 rows 51 /
+// 104, 16 rows 65 / 104; with a form for 32 rows 96 / 104 for 24 and 102 / 102 for 32,
+// and 41 / 34 where the keys were 300.
+constexpr int kNarrowRows = 16;
 
 QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
   QAttnPlan w{};
   w.TG = (int)(T * (Hq / Hkv));
   const int64_t most = prefix ? B * w.TG : w.TG;
   const PrefixPart wide = prefix ? prefix_part(B, T, Hq, Hkv, d, sms) : PrefixPart{};
-  w.way = most <= 32 ? QAttnPlan::kNarrow : w.TG <= 32 && wide.rt > 0 ? QAttnPlan::kBoth : QAttnPlan::kWide;
+  w.way = most <= kNarrowRows ? QAttnPlan::kNarrow : w.TG <= kNarrowRows && wide.rt > 0 ? QAttnPlan::kBoth : QAttnPlan::kWide;
   if (w.way == QAttnPlan::kWide) {
     w.bytes = wide_quant_bytes(B, T, Hq, Hkv, d, prefix, sms);
     return w;
   }
   const int64_t rows = w.way == QAttnPlan::kBoth ? w.TG : most;
-  w.R = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  w.R = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   w.own_rt = (int)cdiv64(w.TG, w.R);
   w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
   // a partial result for every number segment + CTA
-  const size_t own = (size_t)(B * Hkv * w.own_rt + ctas_per_sm(d, w.R) * sms) * w.own_slot_rows;
+  const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
   size_t pre = 0;
   if (w.way == QAttnPlan::kBoth) {
     w.pre_rt = wide.rt;
@@ -940,7 +938,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   } else if (prefix) {
     w.pre_rt = (int)cdiv64(B * w.TG, w.R);
     w.pre_slot_rows = (int)(B * w.TG < w.R ? B * w.TG : w.R);
-    pre = (size_t)(Hkv * w.pre_rt + ctas_per_sm(d, w.R) * sms) * w.pre_slot_rows;
+    pre = (size_t)(Hkv * w.pre_rt + kCtasPerSm * sms) * w.pre_slot_rows;
   }
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w.own_first = pre;
@@ -950,7 +948,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, b
   return w;
 }
 
-template <int D, int R, bool kBare>
+template <int D, int R>
 bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   static std::mutex mu;
   static bool done[64] = {};
@@ -960,8 +958,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev >= 64 || !done[dev]) {
-      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, R, kBare>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Cfg<D, R, kBare>::kSmemBytes),
+      st = cuda_check(cudaFuncSetAttribute(quant_attention_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           Cfg<D, R>::kSmemBytes),
                       "cudaFuncSetAttribute(quant_attention_kernel)");
       if (st != BSA_OK) return st;
       if (dev < 64) done[dev] = true;
@@ -976,8 +974,8 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<D, R, kBare>::kSmemBytes;
-  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, R, kBare>, p), "quant_attention_kernel launch")) != BSA_OK)
+  cfg.dynamicSmemBytes = Cfg<D, R>::kSmemBytes;
+  if ((st = cuda_check(cudaLaunchKernelEx(&cfg, quant_attention_kernel<D, R>, p), "quant_attention_kernel launch")) != BSA_OK)
     return st;
   // Eight warps, one warp or eight lanes a row, as in the join of bsa_paged.cu.
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
@@ -1095,7 +1093,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   p.pre_tiles = plan.way == QAttnPlan::kBoth ? 0 : (int)cdiv64(prefix_len, kTileKeys);
   p.wide_ctas = plan.way == QAttnPlan::kBoth ? sms : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
-  p.ctas = ctas_per_sm(qv.D, plan.R) * sms;
+  p.ctas = kCtasPerSm * sms;
   p.page_table = page_table; p.table_stride = table_stride; p.kv_lens = kv_lens; p.new_lens = new_lens;
   p.prefix_table = prefix_table;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)qv.D)) * 1.4426950408889634f;
@@ -1111,10 +1109,9 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
       (st = launch_prefix_quant(qv, a, new_lens, prefix_table, prefix_len, softmax_scale, p.seg_ctas, p.part_ml, p.part_o,
                                 cs)) != BSA_OK)
     return st;
-  if (plan.R == 4) return qv.D == 128 ? launch_quant<128, 4, true>(p, cs) : launch_quant<64, 4, true>(p, cs);
-  if (plan.R == 8) return qv.D == 128 ? launch_quant<128, 8, true>(p, cs) : launch_quant<64, 8, true>(p, cs);
-  if (plan.R == 16) return qv.D == 128 ? launch_quant<128, 16, false>(p, cs) : launch_quant<64, 16, false>(p, cs);
-  return qv.D == 128 ? launch_quant<128, 32, false>(p, cs) : launch_quant<64, 32, false>(p, cs);
+  if (plan.R == 4) return qv.D == 128 ? launch_quant<128, 4>(p, cs) : launch_quant<64, 4>(p, cs);
+  if (plan.R == 8) return qv.D == 128 ? launch_quant<128, 8>(p, cs) : launch_quant<64, 8>(p, cs);
+  return qv.D == 128 ? launch_quant<128, 16>(p, cs) : launch_quant<64, 16>(p, cs);
 }
 
 }  // extern "C"
