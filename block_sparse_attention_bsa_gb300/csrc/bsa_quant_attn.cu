@@ -208,13 +208,6 @@ __device__ __forceinline__ void tmem_st_4(uint32_t taddr, const float* r) {
                : "memory");
 }
 
-// The largest of a warp's numbers; NaN counts as kLowest, and so does all below it.
-__device__ __forceinline__ float warp_max(float z) {
-  int u = __float_as_int(z > kLowest ? z : kLowest);
-  u = __reduce_max_sync(0xffffffffu, u ^ (u >> 31 & 0x7FFFFFFF));
-  return __int_as_float(u ^ (u >> 31 & 0x7FFFFFFF));
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(const __grid_constant__ QAttnParams p) {
   using C = Cfg<D, R>;
@@ -229,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t vscale = ring + C::kSlots * C::kTileBytes;          // [D / 32][128] twice the scales of V, bf16
   uint8_t* rest = smem + (vscale - p_smem) + C::kScaleBytes;
   float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
-  float* parts = mr + R;                                               // [4][R] of each warp
-  Segment* segs = reinterpret_cast<Segment*>(parts + 4 * R);           // [kSegSlots]
-  int* block_sum = reinterpret_cast<int*>(segs + C::kSegSlots);                  // [kMaxBlocks] tiles of own keys before request 32 i
-  int* total_slot = block_sum + kMaxBlocks;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(total_slot + 1);
-  int* abort_slot = total_slot + 2;
+  float* of_row = mr + R;                                              // [R] factors, then sums
+  Segment* segs = reinterpret_cast<Segment*>(of_row + R);           // [kSegSlots]
+  int* block_tiles = reinterpret_cast<int*>(segs + C::kSegSlots);      // [kMaxBlocks] tiles of own keys of requests 32 i ..
+  int* block_sum = block_tiles + kMaxBlocks;                           // [kMaxBlocks] and of those before
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(block_sum + kMaxBlocks);
+  int* abort_slot = block_sum + kMaxBlocks + 1;
   // barriers, as shared-memory addresses 8 bytes apart
-  const uint32_t seg_full = smem_u32(total_slot + 4);            // [kSegSlots] the segment, and 32 lanes' copies of Q rows
+  const uint32_t seg_full = smem_u32(block_sum + kMaxBlocks + 2);           // [kSegSlots] the segment, and 32 lanes' copies of Q rows
   const uint32_t seg_empty = seg_full + 8 * C::kSegSlots;        // [kSegSlots] 4 warps
   const uint32_t full = seg_empty + 8 * C::kSegSlots;            // [kSlots] transaction bytes
   const uint32_t k_ready = full + 8 * C::kSlots;                 // 4 warps: K stands in TMEM
@@ -244,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t pv_ready = s_done + 8;                          // 4 warps: V stands in TMEM, P in shared memory
   const uint32_t pv_done = pv_ready + 8;                         // commit
   const uint32_t mma_end = pv_done + 8;                          // commit
-  static_assert((5 * R + kMaxBlocks + 4) * 4 + C::kSegSlots * sizeof(Segment) + (2 * C::kSegSlots + C::kSlots + 5) * 8 <=
+  static_assert((2 * R + 2 * kMaxBlocks + 2) * 4 + C::kSegSlots * sizeof(Segment) + (2 * C::kSegSlots + C::kSlots + 5) * 8 <=
                     C::kBarBytes, "barrier block");
   const uint32_t abort_flag = smem_u32(abort_slot);
 
@@ -276,38 +269,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   // what came before it and shares nothing with this one, the wait is at the end: the
   // join behind waits for this kernel only.
   if (p.wide_ctas == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the schedule: tiles of own keys per block of 32 requests, then their sums
+  // the schedule: tiles of own keys per block of 32 requests; warp 4, which looks for
+  // segments, keeps the first block's
   const int nblk = (p.B + 31) / 32;
+  int kv = 0, n = 0, mine = 0, upto = 0;           // of this lane's request: keys, new tokens, tiles, tiles up to its end
 #pragma unroll 1
-  for (int blk = warp; blk < nblk; blk += kThreads / 32) {
+  for (int blk = 4 - warp; blk < nblk; blk += kThreads / 32) {
     const int b = blk * 32 + lane;
-    const int mine = b < p.B ? request_tiles(p, own_keys(p, b), new_tokens(p, b)) * p.Hkv : 0;
-    const int incl = warp_inclusive_sum(mine);
-    if (lane == 31) block_sum[blk] = incl;
+    const int kv_b = b < p.B ? own_keys(p, b) : 0, n_b = b < p.B ? new_tokens(p, b) : 0;
+    const int mine_b = request_tiles(p, kv_b, n_b);
+    const int incl = warp_inclusive_sum(mine_b * p.Hkv);
+    if (lane == 31) block_tiles[blk] = incl;
+    if (blk == 0) { kv = kv_b; n = n_b; mine = mine_b; upto = incl; }
     if (cta == 0 && b < p.B && p.max_pages > 0) {
-      const int kv = p.kv_lens[b];
-      if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+      const int given = p.kv_lens[b];
+      if (given < 0 || given > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) {
-    int before = 0;
+  int total = 0;
 #pragma unroll 1
-    for (int i = 0; i < nblk; i += 32) {
-      const int v = i + lane < nblk ? block_sum[i + lane] : 0;
-      const int incl = warp_inclusive_sum(v) + before;
-      if (i + lane < nblk) block_sum[i + lane] = incl - v;
-      before = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) *total_slot = before;
+  for (int i = 0; i < nblk; i += 32) {
+    const int v = i + lane < nblk ? block_tiles[i + lane] : 0;
+    const int incl = warp_inclusive_sum(v) + total;
+    if (warp == 4 && i + lane < nblk) block_sum[i + lane] = incl - v;
+    total = __shfl_sync(0xffffffffu, incl, 31);
   }
-  __syncthreads();
+  __syncwarp();
   const uint32_t tmem_a = *tmem_slot + C::kA, tmem_s = *tmem_slot + C::kS, tmem_o = *tmem_slot + C::kO;
   int begin = 0, end = 0;
   {
-    const Cut cut(p, *total_slot);
+    const Cut cut(p, total);
     if (cta < cut.n) {
       begin = cut.begin(cta);
       end = cut.begin(cta + 1);
@@ -327,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     const int c = lane % kVec;
     const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
-    int blk = -1, blk_end = 0, kv = 0, n = 0, mine = 0, upto = 0;
+    int blk = 0, blk_end = __shfl_sync(0xffffffffu, upto, 31);
     // Lane x copies page x of a tile.
     const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
     const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
@@ -341,15 +335,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     uint32_t starts = 0;                           // bit i % 4: tile i is the first of a segment
     auto page_of = [&](int t) {
       const int key = t * kTileKeys + lane * per_page * kBlockSlots;
-      int pg = 0;
-      if (copies && key < keys) {
-        pg = table[key >> p.page_shift];
-        if (pg < 0 || pg >= p.num_pages) {
-          atomicOr(&g_bsa_error, kErrPage);
-          pg = 0;
-        }
-      }
-      return pg;
+      return copies && key < keys ? table[key >> p.page_shift] : 0;          // looked at when it is used
     };
     // The segment of tile t of the row, as far as it is this CTA's.
     auto find_segment = [&](int t) {
@@ -457,6 +443,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             starts |= 1u << (i & 3);
           }
         }
+        if (page < 0 || page >= p.num_pages) {
+          atomicOr(&g_bsa_error, kErrPage);
+          page = 0;
+        }
         const int blocks = (min(keys - tile * kTileKeys, kTileKeys) + kBlockSlots - 1) / kBlockSlots;
         const int count = min(blocks - lane * per_page, per_page);
         const int in_page = tile * kTileBlocks & ((1 << (p.page_shift - 4)) - 1) & ~(per_page - 1);
@@ -530,6 +520,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     uint32_t p_at[8];                              // of rows r, r % 8 = 0 .. 7, but for 128 r
 #pragma unroll
     for (int r = 0; r < 8; ++r) p_at[r] = (p_smem + (th / 64) * (C::kCols * 128) + th % 64 * 2) ^ (r << 4);
+    // Joins a value of each thread for every row over the 128 threads, by way of P's
+    // memory (128 / kPass threads a row), and gives it to one of them.
+    constexpr int kPass = C::kPBytes / 512 < R ? C::kPBytes / 512 : R, kShare = 128 / kPass;
+    float* const scratch = reinterpret_cast<float*>(smem);
+    auto rows_of_threads = [&](const float* x, auto first, auto join, auto put) {
+#pragma unroll
+      for (int r0 = 0; r0 < R; r0 += kPass) {
+        if (r0 > 0) sync_any(false);
+#pragma unroll
+        for (int r = 0; r < kPass; ++r) scratch[r * 128 + th] = first(x[r0 + r]);
+        sync_any(false);
+        float y;
+#pragma unroll
+        for (int i = 0; i < kPass / 4; ++i) {
+          const float4 f = reinterpret_cast<const float4*>(scratch + th / kShare * 128)[th % kShare + i * kShare];
+          const float z = join(join(f.x, f.y), join(f.z, f.w));
+          y = i == 0 ? z : join(y, z);
+        }
+#pragma unroll
+        for (int o = kShare / 2; o > 0; o >>= 1) y = join(y, __shfl_xor_sync(0xffffffffu, y, o));
+        if (th % kShare == 0) put(r0 + th / kShare, y);
+      }
+    };
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
     for (int t = begin; t < end; ++seg_no) {
@@ -692,42 +705,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             }
           }
           if (grow) {
-            // the maximum moves to the largest score so far
-#pragma unroll
-            for (int r4 = 0; r4 < R; r4 += 4)
-              if (r4 < rows) {
-#pragma unroll
-                for (int r = r4; r < r4 + 4; ++r) {
-                  const float top = warp_max(v[r]);
-                  if (lane == 0) parts[warp * R + r] = top;
-                }
-              }
+            // The maximum moves to the largest score so far: of rows that some threads
+            // share, written where P will stand (NaN, and what is below kLowest, as that).
+            rows_of_threads(
+                v, [](float z) { return z > kLowest ? z : kLowest; }, [](float a, float b) { return fmaxf(a, b); },
+                [&](int r, float top) {
+                  const float m = mr[r];
+                  mr[r] = fmaxf(m, top);
+                  of_row[r] = ex2_approx(m - fmaxf(m, top));
+                });
             sync_any(false);
 #pragma unroll
             for (int r4 = 0; r4 < R; r4 += 4)
               if (r4 < rows) {
-                float o[4] = {};
+                const float4 a = *reinterpret_cast<const float4*>(of_row + r4);
+                l[r4] *= a.x; l[r4 + 1] *= a.y; l[r4 + 2] *= a.z; l[r4 + 3] *= a.w;
                 if (j > 0) {
+                  float o[4];
                   tmem_ld_4(o_t + r4, o);
                   tmem_wait_ld();
+                  o[0] *= a.x; o[1] *= a.y; o[2] *= a.z; o[3] *= a.w;
+                  tmem_st_4(o_t + r4, o);
                 }
-#pragma unroll
-                for (int r = r4; r < r4 + 4; ++r) {
-                  const float m = mr[r];
-                  const float m2 = fmaxf(fmaxf(m, fmaxf(parts[r], parts[R + r])), fmaxf(parts[2 * R + r], parts[3 * R + r]));
-                  const float alpha = ex2_approx(m - m2);
-                  l[r] *= alpha;
-                  o[r - r4] *= alpha;
-                }
-                if (j > 0) tmem_st_4(o_t + r4, o);
               }
             if (j > 0) tmem_wait_st();
-            sync_any(false);                       // all have read the old maxima
-            if (th < ((rows + 3) & ~3)) {
-              const float m = fmaxf(fmaxf(parts[th], parts[R + th]), fmaxf(parts[2 * R + th], parts[3 * R + th]));
-              mr[th] = fmaxf(mr[th], m);
-            }
-            sync_any(false);
           }
           float top = -INFINITY;
 #pragma unroll
@@ -787,23 +788,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           }
       }
       if (j < tiles) break;
-      // sums over the keys of a warp, then of the four
-#pragma unroll
-      for (int r4 = 0; r4 < R; r4 += 4)
-        if (r4 < rows) {
-#pragma unroll
-          for (int r = r4; r < r4 + 4; ++r) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-            if (lane == 0) parts[warp * R + r] = l[r];
-          }
-        }
       ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag);
+      rows_of_threads(
+          l, [](float z) { return z; }, [](float a, float b) { return a + b; }, [&](int r, float sum) { of_row[r] = sum; });
       if (sync_any(!ok)) break;
       tc_fence_after();
       const bool direct = p.pre_rt == 0 && s.whole;
       if (th < rows) {
-        const float sum = (parts[th] + parts[R + th]) + (parts[2 * R + th] + parts[3 * R + th]);
+        const float sum = of_row[th];
         // no score above kLowest: nothing is left, or NaN
         const float m = mr[th] > kLowest ? mr[th] : sum == 0.f ? -INFINITY : 0.f;
         if (!direct) {
@@ -830,8 +822,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             for (int r = 0; r < R; ++r)
               if (r < rows) {
                 const int rem = rem0 + r, i = p.div_G.quot(rem), g = rem - i * p.G;
-                const float inv = inverse_sum(seen_keys(p, s.kv, s.n, i) > 0,
-                                              (parts[r] + parts[R + r]) + (parts[2 * R + r] + parts[3 * R + r]));
+                const float inv = inverse_sum(seen_keys(p, s.kv, s.n, i) > 0, of_row[r]);
                 p.out[(((int64_t)s.b * p.T + i) * p.Hq + s.hk * p.G + g) * D + th] = __float2bfloat16(inv != 0.f ? o[r] * inv : 0.f);
               }
           }
