@@ -75,7 +75,7 @@ struct PagedCfg {
   static constexpr int kSmemMax = 232448;                     // 227 KB per CTA
   static constexpr int kRaw = kQ4 && D == 64 ? 8 : 3;         // places for blocks of 128 keys (of 4 bits)
   static constexpr int kRawBytes = kQ4 ? kTileKeys / kBlockSlots * block_bytes(D) : 0;
-  static constexpr int kScaleBytes = kQ4 ? (D / kGroup) * kTileKeys * 2 : 0;
+  static constexpr int kScaleBytes = kQ4 ? 2 * (D / kGroup) * kTileKeys * 2 : 0;
   static constexpr int kRest = kSmemMax - 1024 - kBarBytes - 2 * kQBytes - kRaw * kRawBytes - kScaleBytes;
   static constexpr int kFit = kRest / kTileBytes;
   static constexpr int kStages = kFit > 10 ? 10 : kFit;       // 5 of 32 KB, 10 of 16 KB; 4 and 9 beside blocks
@@ -87,7 +87,8 @@ struct PagedParams {
   const uint8_t* k4; const uint8_t* v4;                       // or, of 4 bits, its bytes
   int64_t k4_page, k4_head, v4_page, v4_head;
   uint32_t eights;                // kEights
-  int early;                      // the kernel behind may start beside this one (it waits for it at its end)
+  int early;                      // the kernel behind starts beside this one, on the SMs that it leaves (and waits for it at its end)
+  int beside_keys;                // own keys at most of a request, which are that kernel's
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
   int B, T, Hq, Hkv, G, page_shift, num_pages, max_pages, prefix_len, causal;
@@ -145,19 +146,19 @@ struct Cut {
   int pre, pre_w, own_w;          // prefix tiles, weights
   int n, q, r;                    // CTAs, units of all tiles = q n + r
   float inv_n;                    // 1 / n
-  __device__ __forceinline__ Cut(const PagedParams& p, int own) {
+  __device__ __forceinline__ Cut(const PagedParams& p, int own, int ctas) {
     pre = p.pre_tiles * p.pre_rt * p.Hkv;
     pre_w = p.pre_w;
     own_w = p.own_w;
     // the way in and out of the prefix's segments, as far as a block's share is
     // more than a tile (a tile that weighs more would leave blocks without one)
-    pre_w += min(p.pre_over, max((pre * pre_w + own * own_w) / p.ctas - pre_w, 0));
+    pre_w += min(p.pre_over, max((pre * pre_w + own * own_w) / ctas - pre_w, 0));
     const int units = pre * pre_w + own * own_w;
-    n = min(p.ctas, units / max(pre > 0 ? pre_w : 0, own > 0 ? own_w : 1));
+    n = min(ctas, units / max(pre > 0 ? pre_w : 0, own > 0 ? own_w : 1));
     // Two tiles each where some CTA has two anyway, or where a tile leaves 128 KB
     // of partial results (33 tiles of 8 heads 13.0 -> 12.3 us, 16 prefix tiles of
     // 8 heads for 256 rows 21.4 -> 19.1 us).
-    if (pre + own > p.ctas || (pre > 0 && p.B * p.TG > kHalf)) n = min(n, max((pre + own) / 2, min(n, 1)));
+    if (pre + own > ctas || (pre > 0 && p.B * p.TG > kHalf)) n = min(n, max((pre + own) / 2, min(n, 1)));
     q = n > 0 ? units / n : 0;
     r = units - q * n;
     inv_n = 1.f / (float)max(n, 1);
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   uint8_t* q_smem = smem;                                  // [2] Q buffers of 128 rows
   uint8_t* ring = smem + 2 * C::kQBytes;
   uint8_t* raw = ring + kStages * C::kTileBytes;           // [kRaw] blocks of 128 keys
-  uint8_t* scales = raw + C::kRaw * C::kRawBytes;          // [D / 32][128] twice the scales of a V tile, bf16
+  uint8_t* scales = raw + C::kRaw * C::kRawBytes;          // [2][D / 32][128] twice the scales of a V tile, bf16
   Segment* segs = reinterpret_cast<Segment*>(scales + C::kScaleBytes);           // [kSegRing]
   // barriers, as shared-memory addresses 8 bytes apart
   const uint32_t q_full = smem_u32(segs + kSegRing);   // [2] 32 loader threads
@@ -304,10 +305,11 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   int* block_sum = total_slot + 1;      // [kMaxBlocks]: tiles of own keys before request 32 i
   // of 4-bit pages
   int* raw_info = block_sum + kMaxBlocks;                // [kRaw] keys, + 256 where they are of V
-  const uint32_t raw_full = (smem_u32(raw_info + C::kRaw) + 7) & ~7u;    // [kRaw] transaction bytes
+  int* beside = raw_info + C::kRaw;                      // [warps] tiles of the kernel beside
+  const uint32_t raw_full = (smem_u32(beside + C::kThreads / 32) + 7) & ~7u;    // [kRaw] transaction bytes
   const uint32_t raw_empty = raw_full + 8 * C::kRaw;     // [kRaw] 4 warps
   const uint32_t scale_bar = raw_empty + 8 * C::kRaw;    // 4 warps
-  static_assert(kSegRing * sizeof(Segment) + (14 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 + C::kRaw * 20 + 16 <=
+  static_assert(kSegRing * sizeof(Segment) + (14 + 2 * kSegRing + 2 * kStages) * 8 + 12 + kMaxBlocks * 4 + C::kRaw * 20 + 16 + 64 <=
                     C::kBarBytes,
                 "barrier block");
 
@@ -369,6 +371,14 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
       }
     }
   }
+  if (kQ4 && p.early) {
+    int tiles = 0;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += C::kThreads)
+      if (new_tokens(p, b) > 0) tiles += (min(max(p.kv_lens[b], 0), p.beside_keys) + kTileKeys - 1) / kTileKeys;
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0) beside[warp] = tiles;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -387,7 +397,14 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   const uint32_t tmem = *tmem_slot;
   int begin = 0, end = 0;
   {
-    const Cut cut(p, *total_slot);
+    int ctas = p.ctas;
+    if (kQ4 && p.early) {
+      int tiles = 0;
+#pragma unroll 1
+      for (int i = 0; i < C::kThreads / 32; ++i) tiles += beside[i];
+      ctas = prefix_sms(p.ctas, p.pre_tiles * p.pre_rt * p.Hkv, p.B * p.TG > kHalf, tiles * p.Hkv);
+    }
+    const Cut cut(p, *total_slot, ctas);
     if (cta < cut.n) {
       begin = cut.begin(cta);
       end = cut.begin(cta + 1);
@@ -471,8 +488,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
     // pieces exchanged within 8 rows, as the MMAs read them.
     const int th = threadIdx.x % 128;
     const uint32_t slot_at = (th / kBlockSlots) * block_bytes(D), slot = th % kBlockSlots, swap = (th % 8) * 16;
-    const uint32_t scale_to = smem_u32(scales);
-    uint32_t stage = 0, phase = 0, sync_phase = 0;
+    uint32_t stage = 0, phase = 0, v_no = 0;
 #pragma unroll 1
     for (uint32_t it = 0; it < 2u * (uint32_t)(end - begin); ++it) {
       const uint32_t at = it % C::kRaw;
@@ -481,7 +497,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
       const uint32_t from = smem_u32(raw) + at * C::kRawBytes, to = smem_u32(ring) + stage * C::kTileBytes;
       if (info < 256) {
         if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
-#pragma unroll 1
+#pragma unroll
         for (int g = 0; g < D / kGroup; ++g) {
           const uint4 c = lds128(from + slot_at + g * 256 + slot * 16);
           const uint32_t s2 = twice_scale(lds8(from + slot_at + code_bytes(D) + g * kBlockSlots + slot)) * 0x10001u;
@@ -496,18 +512,20 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
           }
         }
       } else {
-        // twice the scales, 0 behind the last key: what stands there must not count
+        // twice the scales, 0 behind the last key: what stands there must not count (who
+        // still reads the ones before has not come to this barrier)
+        const uint32_t scale_to = smem_u32(scales) + (v_no & 1u) * (C::kScaleBytes / 2);
 #pragma unroll
         for (int g = 0; g < D / kGroup; ++g)
           sts16(scale_to + (g * kTileKeys + th) * 2,
                 th < keys ? twice_scale(lds8(from + slot_at + code_bytes(D) + g * kBlockSlots + slot)) : 0u);
         __syncwarp();
         if (lane == 0) mbar_arrive(scale_bar);
-        if (!(ok = warp_wait(scale_bar, sync_phase, abort_flag))) break;
-        sync_phase ^= 1u;
+        if (!(ok = warp_wait(scale_bar, v_no & 1u, abort_flag))) break;
+        ++v_no;
         if (!(ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag))) break;
         if (th < D) {
-#pragma unroll 1
+#pragma unroll
           for (int x = 0; x < kTileKeys / kBlockSlots; ++x) {
             const uint2 c = lds64(from + x * block_bytes(D) + th * 8);
             const uint32_t scale_at = scale_to + (th / kGroup) * (kTileKeys * 2) + x * 32;
@@ -522,10 +540,6 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
             sts128(row + (((x % 4) * 32 + 16) ^ swap), r + 4);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(scale_bar);     // the scales are read
-        if (!(ok = warp_wait(scale_bar, sync_phase, abort_flag))) break;
-        sync_phase ^= 1u;
       }
       fence_async_shared();
       __syncwarp();
@@ -1343,6 +1357,7 @@ bsa_status launch_prefix_quant(const bsa_tensor& qv, const QuantArgs& a, const i
   p.part_ml = part_ml;
   p.part_o = part_o;
   p.early = 1;
+  p.beside_keys = (int)(a.max_pages * a.k.blocks * kBlockSlots);
   return qv.D == 128 ? launch_paged<128, true>(p, stream, false) : launch_paged<64, true>(p, stream, false);
 }
 

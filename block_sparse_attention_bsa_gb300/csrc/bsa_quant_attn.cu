@@ -135,9 +135,9 @@ __device__ __forceinline__ int request_tiles(const QAttnParams& p, int kv, int n
 // The row of tiles, cut into equal pieces.
 struct Cut {
   int n, q, r;                    // CTAs that get some; tiles = q n + r
-  __device__ __forceinline__ Cut(const QAttnParams& p, int own) {
+  __device__ __forceinline__ Cut(const QAttnParams& p, int own, int ctas) {
     const int tiles = p.pre_tiles * p.pre_rt * p.Hkv + own;
-    n = min(p.ctas, tiles);
+    n = min(ctas, tiles);
     q = n > 0 ? tiles / n : 0;
     r = tiles - q * n;
   }
@@ -301,7 +301,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   const uint32_t tmem_a = *tmem_slot + C::kA, tmem_s = *tmem_slot + C::kS, tmem_o = *tmem_slot + C::kO;
   int begin = 0, end = 0;
   {
-    const Cut cut(p, total);
+    // beside the prefix's kernel: the SMs that it leaves (the first CTAs are placed there,
+    // those behind have no tiles)
+    int ctas = p.ctas;
+    if (p.wide_ctas > 0)
+      ctas = kCtasPerSm * (p.wide_ctas - prefix_sms(p.wide_ctas, (p.prefix_len + kTileKeys - 1) / kTileKeys * p.pre_rt * p.Hkv,
+                                                    p.B * p.TG > kWideHalf, total));
+    const Cut cut(p, total, ctas);
     if (cta < cut.n) {
       begin = cut.begin(cta);
       end = cut.begin(cta + 1);
