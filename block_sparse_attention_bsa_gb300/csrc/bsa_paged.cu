@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   if (kQ4 && p.early) {
     int tiles = 0;
 #pragma unroll 1
-    for (int b = threadIdx.x; b < p.B; b += C::kThreads)
+    for (int b = threadIdx.x; b < p.B && p.beside_keys > 0; b += C::kThreads)      // without own keys: no lengths either
       if (new_tokens(p, b) > 0) tiles += (min(max(p.kv_lens[b], 0), p.beside_keys) + kTileKeys - 1) / kTileKeys;
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     if (lane == 0) beside[warp] = tiles;

@@ -22,10 +22,29 @@
 //    products or its data the others work, with no hand-over between them.  (One CTA
 //    of 20 warps, each role's warps handing tiles to the next role's, took 1,790
 //    cycles a tile, most of it in one warp's way through its part of a tile.)  A CTA's
-//    warp 4 goes through its segments, loads their Q rows and copies each tile's
-//    blocks page by page; warps 0-3 turn K into bf16, a key per thread; one of their
-//    lanes issues S; they turn scores into weights, then V into bf16, a channel per
-//    thread, over K's place in TMEM; one lane issues P V.
+//    warp 4 goes through its segments, loads their Q rows, copies each tile's blocks
+//    page by page into three places (K_0, V_0, K_1, V_1 ..) and issues the products;
+//    warps 0-3 turn K into bf16, a key per thread, scores into weights, and V into
+//    bf16, a channel per thread, over K's place in TMEM.
+//  * A code without its scale takes half an instruction (bare_codes).  So the scales
+//    stand beside the products where TMEM has columns for a set per group of 32
+//    channels, up to 8 rows of heads of 128 and 16 of 64: with the scales in K and V,
+//    24 heads of one row took 89 us instead of 74.
+//  * The maximum of a row moves only when a score passes it by more than 2^8, so that
+//    most tiles need one barrier of the four warps.
+//  * A prefix that more rows than a segment's share is the work of bsa_paged.cu's
+//    kernel (its rows are the products' rows), which runs beside this one on SMs shared
+//    out by their tiles; the join reads the partial results of both.  64 requests on one
+//    prompt of 8,209 keys, up to 1,024 own ones each: 40 us; this kernel alone 83, that
+//    one alone 50.
+//
+// Bound by instructions: a tile of 128 keys takes an SM about 1,150 cycles, in which its
+// schedulers issue 65 to 70 % of the time (2.2 to 2.4 instructions a value of K and V,
+// of which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
+// Device times, of the measured copy rate: 16 requests of 1,024 to 65,536 keys, 32
+// heads over 8 of 128: 142 us (65 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
+// 77 us (54 %); one request of 4,097 keys 9.9 us, of which 4 are the way in, the join
+// and the launches; 24 requests with five drafts, heads of 64: 18.5 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -67,9 +86,7 @@ struct Cfg {
   static constexpr int kTileBytes = kTileBlocks * block_bytes(D);      // of K or of V
   static constexpr int kSlots = 3;                                     // places for the blocks of a tile of K or of V
   static constexpr int kScaleBytes = kBare ? 0 : kGroups * kTileKeys * 2;
-  // What is made of K (groups) and of V (16 registers of 32 slots) before its place is free.
-  static constexpr int kAheadK = kBare ? 1 : 0, kAheadV = kBare ? 1 : 0;
-  static constexpr int kAhead = 16 * (kAheadK > kAheadV ? kAheadK : kAheadV > 0 ? kAheadV : 1);
+  static constexpr int kAhead = kBare ? 1 : 0;         // quarters of a tile made before their place is free
   static constexpr int kBarBytes = 2048;
   static constexpr int kSmemBytes = 1024 + kQTotal + kPBytes + kSlots * kTileBytes + kScaleBytes + kBarBytes;
   static constexpr int kA = 0, kS = 64, kO = kS + kCols, kColumns = 128;       // TMEM columns: K, then V; S; O
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         const uint32_t k_tile = ring + k_at * C::kTileBytes, v_tile = ring + v_at * C::kTileBytes;
         // K, made while P V of the tile before, whose V it takes the place of, is on its way
         ok = warp_wait(full + 8 * k_at, nk / C::kSlots & 1u, abort_flag) && ok;
-        uint32_t ab[C::kAhead];                    // of K, then of V: what waits for a product to be done
+        uint32_t ab[16];                           // of K, then of V: 32 of this thread's values
         {
           const uint32_t from = k_tile + slot_at + slot * 16;
           const uint32_t scale_at = k_tile + slot_at + code_bytes(D) + slot;
@@ -603,13 +620,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
             }
           };
 #pragma unroll
-          for (int g = 0; g < C::kAheadK; ++g) group(g, ab + 16 * g);
+          for (int g = 0; g < C::kAhead; ++g) group(g, ab);
           ok = warp_wait(pv_done, (it & 1u) ^ 1u, abort_flag) && ok;
           tc_fence_after();
 #pragma unroll
-          for (int g = 0; g < C::kAheadK; ++g) tmem_st16(a_t + g * 16, ab + 16 * g);
+          for (int g = 0; g < C::kAhead; ++g) tmem_st16(a_t + g * 16, ab);
 #pragma unroll kBare ? 4 : 1
-          for (int g = C::kAheadK; g < C::kGroups; ++g) {
+          for (int g = C::kAhead; g < C::kGroups; ++g) {
             group(g, ab);
             tmem_st16(a_t + g * 16, ab);
           }
@@ -668,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           read_scales(v_tile, th & 2 ? 3 : 6, vs);
           if (th < D) {
 #pragma unroll
-            for (int x = 0; x < C::kAheadV; ++x) v_codes(x, ab + 16 * x);
+            for (int x = 0; x < C::kAhead; ++x) v_codes(x, ab);
           }
         }
         ok = warp_wait(s_done, it & 1u, abort_flag) && ok;
@@ -763,9 +780,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
           if (!again && th < D) {
             // V over K, whose product is done
 #pragma unroll
-            for (int x = 0; x < C::kAheadV; ++x) tmem_st16(a_t + x * 16, ab + 16 * x);
+            for (int x = 0; x < C::kAhead; ++x) tmem_st16(a_t + x * 16, ab);
 #pragma unroll kBare ? 4 : 1
-            for (int x = C::kAheadV; x < 4; ++x) {
+            for (int x = C::kAhead; x < 4; ++x) {
               v_codes(x, ab);
               tmem_st16(a_t + x * 16, ab);
             }

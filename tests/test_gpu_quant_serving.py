@@ -398,3 +398,44 @@ def test_binding_refusals_on_the_gpu():
         bsa.bsa_forward_paged_q4(q[:, :, :3], *args)
     bsa.bsa_device_status()
     assert math.isfinite(float(bsa.bsa_forward_paged_q4(q, *args)[0].float().sum()))
+
+
+@pytest.mark.parametrize("B,T,prefix,Hq,Hkv,d", [(200, 2, 0, 4, 2, 64), (1100, 1, 0, 4, 1, 128), (1100, 1, 300, 4, 1, 64),
+                                                 (170, 3, 150, 8, 2, 128)])
+def test_more_requests_than_one_pass_over_the_lengths_takes(B, T, prefix, Hq, Hkv, d):
+    """Batches whose lengths five warps, or one warp's 32 sums of 32, do not take at
+    once: runs of requests without a key, and the last one with the most."""
+    g = torch.Generator().manual_seed(330)
+    lens = torch.randint(0, 40, (B,), generator=g)
+    lens[40:110] = 0
+    lens[-1] = 500
+    pool = QPool(lens.tolist(), prefix, Hkv, d, 16, DEV, 331)
+    q = randn((B, T, Hq, d), 332)
+    out, lse = bsa.bsa_forward_paged_q4(q.to(DEV), pool.gk, pool.gv, pool.gtable, pool.kv_lens, prefix_table=pool.gprefix,
+                                        prefix_len=prefix)
+    bsa.bsa_device_status()
+    check_attention(out, lse, attend64(q, pool))
+
+
+def test_a_prefix_alone_needs_no_table_and_no_lengths():
+    """max_pages 0 with null pointers for the table and the lengths, for few rows, for
+    rows of the prefix's kernel, and for chunks."""
+    from block_sparse_attention_bsa_gb300._lib import load
+    from block_sparse_attention_bsa_gb300.paged import _tensor
+    from block_sparse_attention_bsa_gb300.quant import _caches
+    lib = load()
+    pool = QPool([1, 1], 333, 2, 64, 64, DEV, 340)
+    for B, T in ((1, 1), (70, 1), (2, 40)):
+        x = randn((B, T, 8, 64), 341)
+        q = x.to(DEV)
+        out, lse = torch.empty_like(q), torch.empty(B, 8, T, device=DEV)
+        n = bsa.bsa_forward_paged_q4_workspace_size(B, T, 8, 2, 64, True)
+        ws = torch.empty(n, dtype=U8, device=DEV)
+        kc, vc, _ = _caches(pool.gk, pool.gv, 0)
+        assert lib.bsaq_forward(_tensor(q, "q", 0), kc, vc, None, 0, 0, None, None, pool.gprefix.data_ptr(), 333, 1, 0.0,
+                                out.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+        bsa.bsa_device_status()
+        ref = QPool.__new__(QPool)
+        ref.prefix_len, ref.pre_k, ref.pre_v, ref.lens = 333, pool.pre_k, pool.pre_v, [0] * B
+        ref.own_k, ref.own_v = [pool.pre_k[:0]] * B, [pool.pre_v[:0]] * B
+        check_attention(out, lse, attend64(x, ref))
