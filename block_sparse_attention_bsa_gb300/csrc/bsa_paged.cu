@@ -1223,19 +1223,26 @@ template <int D, bool kQ4>
 bsa_status launch_paged(const PagedParams& p, cudaStream_t stream, bool join = true) {
   bsa_status st = set_smem<D, kQ4>();
   if (st != BSA_OK) return st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  // Beside another kernel: pairs of CTAs, so that those without tiles leave pairs of SMs
+  // to it.  (An SM of this kernel whose neighbour had four CTAs of the other took up to
+  // 203 us where it takes 135; which SMs are neighbours was up to chance.)
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = 2;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = p.early && p.ctas % 2 == 0 ? 2 : 1;
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(PagedCfg<D, kQ4>::kThreads);
   cfg.dynamicSmemBytes = PagedCfg<D, kQ4>::kSmemBytes;
   if ((st = cuda_check(cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, kQ4>, p), "paged_attention_kernel launch")) != BSA_OK)
     return st;
   if (!join) return BSA_OK;
+  cfg.numAttrs = 1;
   const int64_t rows = (int64_t)p.B * p.T * p.Hq;
   // Eight warps, one warp or eight lanes a row, by the number of rows (us of the
   // join: 32 rows of 40 partial results 6.4, with one warp 9; 2,048 rows of 2 to

@@ -98,11 +98,12 @@ __device__ __forceinline__ void bare_codes(uint32_t word, uint32_t* r) {
 
 // SMs of `sms` that the prefix gets where its tiles (of rows above 128 or not) and own
 // tiles of few rows are two kernels side by side: by their times, 1.75 and 1.0 us
-// against 0.62 for a tile.
+// against 0.62 for a tile; SMs come in pairs.
 __device__ __forceinline__ int prefix_sms(int sms, int prefix_tiles, bool two_jobs, int own_tiles) {
   if (own_tiles == 0) return sms;
   const float w = (float)prefix_tiles * (two_jobs ? 1.75f : 1.0f), o = (float)own_tiles * 0.62f;
-  return min(max((int)((float)sms * w / (w + o) + 0.5f), 1), sms - 1);
+  const int pair = sms % 2 == 0 ? 2 : 1;
+  return max(min((int)((float)(sms / pair) * w / (w + o) + 0.5f) * pair, sms - pair), pair);
 }
 
 // Shared memory by its address.

@@ -35,7 +35,7 @@
 //  * A prefix that more rows than a segment's share is the work of bsa_paged.cu's
 //    kernel (its rows are the products' rows), which runs beside this one on SMs shared
 //    out by their tiles; the join reads the partial results of both.  64 requests on one
-//    prompt of 8,209 keys, up to 1,024 own ones each: 40 us; this kernel alone 83, that
+//    prompt of 8,209 keys, up to 1,024 own ones each: 37.5 us; this kernel alone 83, that
 //    one alone 50.
 //
 // Bound by instructions: a tile of 128 keys takes an SM about 1,150 cycles, in which its
@@ -43,8 +43,8 @@
 // of which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
 // Device times, of the measured copy rate: 16 requests of 1,024 to 65,536 keys, 32
 // heads over 8 of 128: 142 us (65 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
-// 77 us (54 %); one request of 4,097 keys 9.9 us, of which 4 are the way in, the join
-// and the launches; 24 requests with five drafts, heads of 64: 18.5 us.
+// 75 us (55 %); one request of 4,097 keys 9.2 us, of which 4 are the way in, the join
+// and the launches; 24 requests with five drafts, heads of 64: 17.6 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -282,10 +282,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     tmem_relinquish();
   }
   // Launched when the blocks of the kernel before leave: up to here nothing is
-  // read or written that it uses.  Beside the prefix's kernel, which has waited for
-  // what came before it and shares nothing with this one, the wait is at the end: the
-  // join behind waits for this kernel only.
-  if (p.wide_ctas == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // read or written that it uses.  The join may then come in as room is left (its
+  // launch shows less: one token 9.9 -> 9.2 us).  Beside the prefix's kernel, which has
+  // waited for what came before it and shares nothing with this one, one CTA waits at
+  // the end, as the join behind waits for this kernel only; the join is not let in
+  // before, when the SMs with room are few.
+  if (p.wide_ctas == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   // the schedule: tiles of own keys per block of 32 requests; warp 4, which looks for
   // segments, keeps the first block's
   const int nblk = (p.B + 31) / 32;
@@ -322,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // those behind have no tiles)
     int ctas = p.ctas;
     if (p.wide_ctas > 0)
-      ctas = kCtasPerSm * (p.wide_ctas - prefix_sms(p.wide_ctas, (p.prefix_len + kTileKeys - 1) / kTileKeys * p.pre_rt * p.Hkv,
-                                                    p.B * p.TG > kWideHalf, total));
+      ctas = kCtasPerSm * max(p.wide_ctas - prefix_sms(p.wide_ctas, (p.prefix_len + kTileKeys - 1) / kTileKeys * p.pre_rt * p.Hkv,
+                                                       p.B * p.TG > kWideHalf, total), 1);
     const Cut cut(p, total, ctas);
     if (cta < cut.n) {
       begin = cut.begin(cta);
@@ -863,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     tc_fence_after();
     tmem_dealloc(*tmem_slot, C::kColumns);
   }
-  if (p.wide_ctas != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.wide_ctas != 0 && cta == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Output row (b, i, h): joins the partial results of its prefix segment and of its
@@ -877,9 +882,10 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
   const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
   const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
   // Read before the wait: this grid starts when the main kernel's blocks have all
-  // left, each of which has waited for whatever wrote the lengths.
+  // waited for whatever wrote the lengths.
   const int kv = own_keys(p, b), n = new_tokens(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // what follows waits in its turn
   Parts pre{0, 0, 0}, own{0, 0, 0};
   bool direct = false;
   // CTAs first .. last have a part each; a pair that no schedule makes (a wait gave up) none
