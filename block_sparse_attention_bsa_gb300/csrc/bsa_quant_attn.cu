@@ -48,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -934,18 +935,29 @@ struct QAttnPlan {
 // and 41 / 34 where the keys were 300.
 constexpr int kNarrowRows = 16;
 
-QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, bool prefix, int sms) {
+// A prefix of few tiles stays with this kernel though its rows are many, up to one tile
+// a CTA.  us alone / with the prefix in the other kernel: 64 requests of 8 heads of 4
+// rows, 128 shared keys (0.8 tiles a CTA) 25.8 / 31.2, 300 (2.5) 32.5 / 29.8; 16
+// requests, 500 keys (0.8) 16.5 / 23.6; 24 of 2 heads of 10 rows, 1,000 keys (0.4) 15.7 /
+// 17.7, 4,000 (1.6) 20.0 / 20.8; 64 of 8 heads of 12 rows, 300 keys (1.9) 41.5 / 35.1.
+
+QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, int64_t prefix_len, int sms) {
   QAttnPlan w{};
+  const bool prefix = prefix_len > 0;
   w.TG = (int)(T * (Hq / Hkv));
   const int64_t most = prefix ? B * w.TG : w.TG;
   const PrefixPart wide = prefix ? prefix_part(B, T, Hq, Hkv, d, sms) : PrefixPart{};
-  w.way = most <= kNarrowRows ? QAttnPlan::kNarrow : w.TG <= kNarrowRows && wide.rt > 0 ? QAttnPlan::kBoth : QAttnPlan::kWide;
+  const int64_t rows = most <= kNarrowRows ? most : w.TG;
+  w.R = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+  const bool few = w.TG <= kNarrowRows && wide.rt > 0 &&
+                   Hkv * cdiv64(B * w.TG, w.R) * cdiv64(prefix_len, kTileKeys) <= kCtasPerSm * sms;
+  w.way = most <= kNarrowRows || few ? QAttnPlan::kNarrow
+          : w.TG <= kNarrowRows && wide.rt > 0 ? QAttnPlan::kBoth
+                                               : QAttnPlan::kWide;
   if (w.way == QAttnPlan::kWide) {
     w.bytes = wide_quant_bytes(B, T, Hq, Hkv, d, prefix, sms);
     return w;
   }
-  const int64_t rows = w.way == QAttnPlan::kBoth ? w.TG : most;
-  w.R = rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
   w.own_rt = (int)cdiv64(w.TG, w.R);
   w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
   // a partial result for every number segment + CTA
@@ -1023,7 +1035,10 @@ size_t bsaq_forward_workspace_size(int B, int T, int Hq, int Hkv, int d, int has
   if (B <= 0 || B > kMaxPagedBatch || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq > kMaxHeads || Hq % Hkv ||
       (d != 64 && d != 128) || sms < 0 || (int64_t)B * T * (Hq / Hkv) > INT32_MAX / 16)
     return 0;
-  return plan_quant(B, T, Hq, Hkv, d, has_prefix != 0, sms > 0 ? sms : num_sms()).bytes;
+  if (sms == 0) sms = num_sms();
+  if (!has_prefix) return plan_quant(B, T, Hq, Hkv, d, 0, sms).bytes;
+  // of a short prefix and of a long one
+  return std::max(plan_quant(B, T, Hq, Hkv, d, 1, sms).bytes, plan_quant(B, T, Hq, Hkv, d, INT32_MAX / 2, sms).bytes);
 }
 
 bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bsaq_cache* v_cache,
@@ -1063,7 +1078,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   // rows, tiles and slot numbers are 32-bit on the device
   const int64_t flat_rows = qv.B * qv.S * G, page = a.k.blocks * kBlockSlots;
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
-  const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len > 0, sms);
+  const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len, sms);
   const int64_t own_rt = plan.way == QAttnPlan::kWide ? cdiv64(plan.TG, kWideHalf) : plan.own_rt;
   const int64_t pre_rt = plan.way == QAttnPlan::kWide ? cdiv64(flat_rows, kWideHalf) : plan.pre_rt;
   const int64_t most_tiles =
