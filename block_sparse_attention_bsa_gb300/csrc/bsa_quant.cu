@@ -110,9 +110,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
   w.b = blockIdx.y;
   w.which = blockIdx.z;
   // Launched when the blocks of the kernel before leave: nothing it may have
-  // written is read before this point.  The next kernel may come in as room is left.
+  // written is read before this point.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n = p.other ? min(max(p.other[w.b], 0), p.S) : p.S;
   if (!find_place<D>(p, (int64_t)p.kv_lens[w.b] - n, n, &w)) return;
 
@@ -265,7 +264,6 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
   w.b = blockIdx.y;
   w.which = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t from = p.other ? max(p.other[w.b], 0) : 0;
   const int64_t keys = (int64_t)p.kv_lens[w.b] - from;
   if (!find_place<D>(p, from, keys < p.S ? keys : p.S, &w)) return;
