@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
     int tiles = 0;
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B && p.beside_keys > 0; b += C::kThreads)      // without own keys: no lengths either
-      if (new_tokens(p, b) > 0) tiles += (min(max(p.kv_lens[b], 0), p.beside_keys) + kTileKeys - 1) / kTileKeys;
+      if (const int own = new_tokens(p, b) > 0 ? min(max(p.kv_lens[b], 0), p.beside_keys) : 0)
+        tiles += (own + kTileKeys - 1) / kTileKeys + kSegmentWay;
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     if (lane == 0) beside[warp] = tiles;
   }

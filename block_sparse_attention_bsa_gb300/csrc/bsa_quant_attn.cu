@@ -16,7 +16,8 @@
 //    rows (b, i, g) of the whole batch under one KV head, for a request's own keys
 //    the rows (i, g) of that request.  All segments' tiles of 128 keys are put in
 //    one row and cut into equal pieces, one for each CTA, whatever the lengths are
-//    (they are read from the device).  A cut segment, or one beside a prefix, leaves
+//    (they are read from the device); a segment's way in and out counts as a tile (24
+//    heads of one row 75 -> 70 us, five drafts 15.6 -> 14.2).  A cut segment, or one beside a prefix, leaves
 //    partial results that quant_join_kernel puts together; segment + CTA numbers them.
 //  * Four CTAs per SM, each through its piece by itself: while one waits for its
 //    products or its data the others work, with no hand-over between them.  (One CTA
@@ -35,16 +36,16 @@
 //  * A prefix that more rows than a segment's share is the work of bsa_paged.cu's
 //    kernel (its rows are the products' rows), which runs beside this one on SMs shared
 //    out by their tiles; the join reads the partial results of both.  64 requests on one
-//    prompt of 8,209 keys, up to 1,024 own ones each: 37.5 us; this kernel alone 83, that
+//    prompt of 8,209 keys, up to 1,024 own ones each: 35 us; this kernel alone 83, that
 //    one alone 50.
 //
 // Bound by instructions: a tile of 128 keys takes an SM about 1,150 cycles, in which its
 // schedulers issue 65 to 70 % of the time (2.2 to 2.4 instructions a value of K and V,
 // of which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
 // Device times, of the measured copy rate: 16 requests of 1,024 to 65,536 keys, 32
-// heads over 8 of 128: 142 us (65 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
-// 75 us (55 %); one request of 4,097 keys 9.2 us, of which 4 are the way in, the join
-// and the launches; 24 requests with five drafts, heads of 64: 17.6 us.
+// heads over 8 of 128: 135 us (69 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
+// 70 us (59 %); one request of 4,097 keys 9.4 us, of which 4 are the way in, the join
+// and the launches; 24 requests with five drafts on 1,000 shared keys, heads of 64: 14 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -104,7 +105,6 @@ struct QAttnParams {
   FastDiv div_G, div_TG;
   int R;                          // rows of a segment
   int TG;                         // rows of a request under one KV head
-  int own_rt;                     // row tiles of a request
   int pre_rt;                     // row tiles of the whole batch (prefix)
   int pre_tiles;                  // key tiles of the prefix
   int pre_slot_rows, own_slot_rows;   // rows of a partial result
@@ -135,29 +135,21 @@ __device__ __forceinline__ int new_tokens(const QAttnParams& p, int b) {
 __device__ __forceinline__ int seen_keys(const QAttnParams& p, int kv, int n, int i) {
   return p.causal ? min(max(kv - n + i + 1, 0), kv) : kv;
 }
-// Key tiles of row tile rt of such a request.
-__device__ __forceinline__ int own_tiles(const QAttnParams& p, int kv, int n, int rt) {
-  const int first = p.div_G.quot(rt * p.R);
-  if (first >= n) return 0;
-  const int last = min(n - 1, p.div_G.quot(rt * p.R + p.R - 1));
-  return (seen_keys(p, kv, n, last) + kTileKeys - 1) / kTileKeys;
+// Key tiles of such a request under one KV head (whose rows are one segment's).
+__device__ __forceinline__ int own_tiles(const QAttnParams& p, int kv, int n) {
+  return n > 0 ? (seen_keys(p, kv, n, n - 1) + kTileKeys - 1) / kTileKeys : 0;
 }
-// Key tiles of a request under one KV head.
-__device__ __forceinline__ int request_tiles(const QAttnParams& p, int kv, int n) {
-  int sum = 0;
-#pragma unroll 1
-  for (int rt = 0; rt < p.own_rt; ++rt) sum += own_tiles(p, kv, n, rt);
-  return sum;
-}
+// Places in the row that a segment of so many tiles takes: its way in and out, then its tiles.
+__device__ __forceinline__ int segment_units(int tiles) { return tiles > 0 ? kSegmentWay + tiles : 0; }
 
-// The row of tiles, cut into equal pieces.
+// The row of all segments, cut into equal pieces.
 struct Cut {
-  int n, q, r;                    // CTAs that get some; tiles = q n + r
+  int n, q, r;                    // CTAs that get some; units = q n + r
   __device__ __forceinline__ Cut(const QAttnParams& p, int own, int ctas) {
-    const int tiles = p.pre_tiles * p.pre_rt * p.Hkv + own;
-    n = min(ctas, tiles);
-    q = n > 0 ? tiles / n : 0;
-    r = tiles - q * n;
+    const int units = segment_units(p.pre_tiles) * p.pre_rt * p.Hkv + own;
+    n = min(ctas, units);
+    q = n > 0 ? units / n : 0;
+    r = units - q * n;
   }
   __device__ __forceinline__ int begin(int c) const { return c * q + min(c, r); }
 };
@@ -167,7 +159,7 @@ struct __align__(16) Segment {
   int b;               // request, -1: prefix
   int hk;
   int row0, rows;      // first flat row (b * T + i) * G + g, and how many
-  int tile0, tiles;    // first key tile and how many
+  int tile0, tiles;    // first key tile and how many; 0: no further segment
   int slot;            // number of the partial result (segment + CTA)
   int keys;            // where its keys end
   int kv, n;           // of the request
@@ -242,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   float* mr = reinterpret_cast<float*>(rest);                          // [R] running maxima
   float* of_row = mr + R;                                              // [R] factors, then sums
   Segment* segs = reinterpret_cast<Segment*>(of_row + R);           // [kSegSlots]
-  int* block_tiles = reinterpret_cast<int*>(segs + C::kSegSlots);      // [kMaxBlocks] tiles of own keys of requests 32 i ..
-  int* block_sum = block_tiles + kMaxBlocks;                           // [kMaxBlocks] and of those before
+  int* block_units = reinterpret_cast<int*>(segs + C::kSegSlots);      // [kMaxBlocks] units of own keys of requests 32 i ..
+  int* block_sum = block_units + kMaxBlocks;                           // [kMaxBlocks] and of those before
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(block_sum + kMaxBlocks);
   int* abort_slot = block_sum + kMaxBlocks + 1;
   // barriers, as shared-memory addresses 8 bytes apart
@@ -292,17 +284,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
-  // the schedule: tiles of own keys per block of 32 requests; warp 4, which looks for
+  // the schedule: units of own keys per block of 32 requests; warp 4, which looks for
   // segments, keeps the first block's
   const int nblk = (p.B + 31) / 32;
-  int kv = 0, n = 0, mine = 0, upto = 0;           // of this lane's request: keys, new tokens, tiles, tiles up to its end
+  int kv = 0, n = 0, mine = 0, upto = 0;           // of this lane's request: keys, new tokens, units under a head, units up to its end
 #pragma unroll 1
   for (int blk = 4 - warp; blk < nblk; blk += kThreads / 32) {
     const int b = blk * 32 + lane;
     const int kv_b = b < p.B ? own_keys(p, b) : 0, n_b = b < p.B ? new_tokens(p, b) : 0;
-    const int mine_b = request_tiles(p, kv_b, n_b);
+    const int mine_b = segment_units(own_tiles(p, kv_b, n_b));
     const int incl = warp_inclusive_sum(mine_b * p.Hkv);
-    if (lane == 31) block_tiles[blk] = incl;
+    if (lane == 31) block_units[blk] = incl;
     if (blk == 0) { kv = kv_b; n = n_b; mine = mine_b; upto = incl; }
     if (cta == 0 && b < p.B && p.max_pages > 0) {
       const int given = p.kv_lens[b];
@@ -315,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
   int total = 0;
 #pragma unroll 1
   for (int i = 0; i < nblk; i += 32) {
-    const int v = i + lane < nblk ? block_tiles[i + lane] : 0;
+    const int v = i + lane < nblk ? block_units[i + lane] : 0;
     const int incl = warp_inclusive_sum(v) + total;
     if (warp == 4 && i + lane < nblk) block_sum[i + lane] = incl - v;
     total = __shfl_sync(0xffffffffu, incl, 31);
@@ -342,20 +334,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     // ------------------------------- segments, Q rows, copies of tiles, MMAs ---
     // In turn: S of tile i, V of tile i + 1, P V of tile i, K of tile i + 2, whose segment
     // is found where a new one begins.
-    // Lane l holds request 32 blk + l: its lengths, tiles, and the tiles up to its end.
+    // Lane l holds request 32 blk + l: its lengths, units, and the units up to its end.
     constexpr int kVec = D / 8;                    // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kVec;            // rows per warp-wide copy
     constexpr uint32_t idesc = idesc_bf16_f32(128, C::kCols, false);
     constexpr int kChunk = (C::kCols * 128) >> 4;
     const uint64_t pdesc = sdesc_sw128(p_smem, 16, 1024);
     const int c = lane % kVec;
-    const int pre = p.pre_tiles * p.pre_rt * p.Hkv;
+    const int pre_units = segment_units(p.pre_tiles), pre = pre_units * p.pre_rt * p.Hkv;
     int blk = 0, blk_end = __shfl_sync(0xffffffffu, upto, 31);
     // Lane x copies page x of a tile.
     const int per_tile = p.page_shift >= 7 ? 1 : kTileKeys >> p.page_shift;      // pages of a tile
     const int per_page = kTileBlocks / per_tile;                                 // blocks of a page in it
     const bool copies = lane < per_tile;
-    const int tiles = end - begin;
+    int at_unit = begin;                           // up to where segments have been found
+    int tiles = INT32_MAX;                         // of this CTA, once the last segment is known
     uint32_t seg_no = 0;                           // segments found
     int left = 0, tile = 0, keys = 0, page = 0;    // of the last one: tiles to copy, the next, where its keys end, this lane's page
     const int32_t* table = nullptr;
@@ -366,74 +359,76 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       const int key = t * kTileKeys + lane * per_page * kBlockSlots;
       return copies && key < keys ? table[key >> p.page_shift] : 0;          // looked at when it is used
     };
-    // The segment of tile t of the row, as far as it is this CTA's.
-    auto find_segment = [&](int t) {
-      Segment s;
-      int t0, t1, seg;
-      if (t < pre) {
-        seg = t / p.pre_tiles;
-        t0 = seg * p.pre_tiles;
-        t1 = t0 + p.pre_tiles;
-        s.b = -1;
-        s.hk = seg / p.pre_rt;
-        s.row0 = (seg - s.hk * p.pre_rt) * R;
-        s.rows = min(R, p.B * p.TG - s.row0);
-        s.slot = seg + cta;
-        s.keys = p.prefix_len;
-        s.kv = s.n = 0;
-      } else {
-        const int u = t - pre;
-        if (u >= blk_end) {                          // the last block that begins at or before u
-          ++blk;
-          while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
-          const int b = blk * 32 + lane;
-          kv = b < p.B ? own_keys(p, b) : 0;
-          n = b < p.B ? new_tokens(p, b) : 0;
-          mine = b < p.B ? request_tiles(p, kv, n) : 0;
-          upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
-          blk_end = __shfl_sync(0xffffffffu, upto, 31);
+    // The segment at the row's unit at_unit, as far as it is this CTA's; one of no tiles
+    // when there is none.
+    auto find_segment = [&]() {
+      Segment s{};
+      int seg = 0, start = 0, m = 0;               // its number, first unit, tiles
+      left = 0;
+      if (at_unit < end) {
+        if (at_unit < pre) {
+          seg = at_unit / pre_units;
+          start = seg * pre_units;
+          m = p.pre_tiles;
+          s.b = -1;
+          s.hk = seg / p.pre_rt;
+          s.row0 = (seg - s.hk * p.pre_rt) * R;
+          s.rows = min(R, p.B * p.TG - s.row0);
+          s.keys = p.prefix_len;
+        } else {
+          const int u = at_unit - pre;
+          if (u >= blk_end) {                          // the last block that begins at or before u
+            ++blk;
+            while (blk + 1 < nblk && block_sum[blk + 1] <= u) ++blk;
+            const int b = blk * 32 + lane;
+            kv = b < p.B ? own_keys(p, b) : 0;
+            n = b < p.B ? new_tokens(p, b) : 0;
+            mine = b < p.B ? segment_units(own_tiles(p, kv, n)) : 0;
+            upto = warp_inclusive_sum(mine * p.Hkv) + block_sum[blk];
+            blk_end = __shfl_sync(0xffffffffu, upto, 31);
+          }
+          const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
+          const int per_head = __shfl_sync(0xffffffffu, mine, src);
+          const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
+          s.b = blk * 32 + src;
+          s.kv = __shfl_sync(0xffffffffu, kv, src);
+          s.n = __shfl_sync(0xffffffffu, n, src);
+          s.hk = (u - first) / per_head;
+          s.row0 = s.b * p.TG;
+          s.rows = s.n * p.G;
+          s.keys = s.kv;
+          seg = s.b * p.Hkv + s.hk;
+          start = pre + first + s.hk * per_head;
+          m = per_head - kSegmentWay;
         }
-        const int src = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;   // there is one: u < blk_end
-        const int per_head = __shfl_sync(0xffffffffu, mine, src);
-        const int first = __shfl_sync(0xffffffffu, upto, src) - per_head * p.Hkv;
-        s.b = blk * 32 + src;
-        s.kv = __shfl_sync(0xffffffffu, kv, src);
-        s.n = __shfl_sync(0xffffffffu, n, src);
-        s.hk = (u - first) / per_head;
-        t0 = pre + first + s.hk * per_head;
-        int rt = 0, m = p.own_rt == 1 ? per_head : own_tiles(p, s.kv, s.n, 0);
-#pragma unroll 1
-        while (t >= t0 + m) {
-          t0 += m;
-          m = own_tiles(p, s.kv, s.n, ++rt);
-        }
-        t1 = t0 + m;
-        s.row0 = s.b * p.TG + rt * R;
-        s.rows = min(R, s.n * p.G - rt * R);
-        seg = (s.b * p.Hkv + s.hk) * p.own_rt + rt;
+        s.tile0 = max(at_unit - start - kSegmentWay, 0);
+        left = max(min(m, end - start - kSegmentWay) - s.tile0, 0);
+        s.tiles = left;
+        s.whole = left == m;
         s.slot = seg + cta;
-        s.keys = s.kv;
+        at_unit = start + kSegmentWay + m;
+        // its first tile's pages are on their way while its place is waited for
+        tile = s.tile0; keys = s.keys;
+        table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
+        k_head = p.k + s.hk * p.k_head;
+        v_head = p.v + s.hk * p.v_head;
+        page = left > 0 ? page_of(tile) : 0;
       }
-      s.tile0 = t - t0;
-      s.tiles = min(t1, end) - t;
-      s.whole = begin <= t0 && t1 <= end;
-      s.pad = 0;
-      // its first tile's pages are on their way while its place is waited for
-      left = s.tiles; tile = s.tile0; keys = s.keys;
-      table = s.b < 0 ? p.prefix_table : p.page_table + s.b * p.table_stride;
-      k_head = p.k + s.hk * p.k_head;
-      v_head = p.v + s.hk * p.v_head;
-      page = page_of(tile);
       const uint32_t qb = seg_no % C::kSegSlots;
       if (!warp_wait(seg_empty + 8 * qb, (seg_no / C::kSegSlots & 1u) ^ 1u, abort_flag)) return false;
       if (lane == 0) {
         int2* who = p.seg_ctas + (s.b < 0 ? 0 : p.pre_rt * p.Hkv) + seg;     // the join looks here
-        if (t == t0) who->x = cta;
-        if (t1 <= end) who->y = cta;
+        if (left > 0 && s.tile0 == 0) who->x = cta;
+        if (left > 0 && s.tile0 + left == m) who->y = cta;
         segs[qb] = s;
         mbar_arrive(seg_full + 8 * qb);
       }
       __syncwarp();
+      ++seg_no;
+      if (left == 0) {
+        mbar_arrive(seg_full + 8 * qb);
+        return true;
+      }
       // Q rows, and rows of zeros up to a multiple of four
       const __nv_bfloat16* qh = p.q + (int64_t)s.hk * p.G * p.q_sh + c * 8;
       const uint32_t to = q_rows + qb * C::kQSlotBytes;
@@ -451,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
       }
       // arrives when this lane's copies have landed; the warp goes on
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(seg_full + 8 * qb) : "memory");
-      ++seg_no;
       return true;
     };
     // The copies that have a place: K of tile i where V of tile i - 2 stood, once P V of
@@ -468,7 +462,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         if (!v) {
           starts &= ~(1u << (i & 3));
           if (left == 0) {
-            if (!find_segment(begin + i)) return false;
+            if (!find_segment()) return false;
+            if (left == 0) {
+              tiles = i;
+              return true;
+            }
             starts |= 1u << (i & 3);
           }
         }
@@ -574,12 +572,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
     };
     uint32_t it = 0, seg_no = 0;
 #pragma unroll 1
-    for (int t = begin; t < end; ++seg_no) {
+    for (;; ++seg_no) {
       const uint32_t qb = seg_no % C::kSegSlots;
       ok = warp_wait(seg_full + 8 * qb, seg_no / C::kSegSlots & 1u, abort_flag);
       const Segment& s = segs[qb];                 // stays there until all are through with it
       if (th < R) mr[th] = kLowest;
-      if constexpr (kBare) {
+      const bool none = s.tiles == 0;
+      if (kBare && !none) {
         // Q rows of each group, 0 elsewhere; every second pair of channels by 8, as K's
         // codes there come out 8 times as large (all S so far are done)
 #pragma unroll
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
         fence_async_shared();
       }
-      if (sync_any(!ok)) break;
+      if (sync_any(!ok || none)) break;
       const int rows = s.rows, tiles = s.tiles, keys = s.keys, tile0 = s.tile0;
       const int sb = s.b, skv = s.kv, sn = s.n;
       // the keys of the first row; further rows' rise with the token
@@ -858,7 +857,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) quant_attention_kernel(c
         }
       }
       tc_fence_before();
-      t += tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(seg_empty + 8 * qb);
     }
@@ -897,7 +895,7 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
   const bool keyed = real && i < n && (p.prefix_len > 0 || seen_keys(p, kv, n, i) > 0);
   if (real && i < n) {
     const int row = i * p.G + g, flat = b * p.TG + row;
-    const int rt = row / p.R, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
+    const int own_seg = b * p.Hkv + hk;
     if (p.wide_ctas > 0) {
       const int seg = hk * p.pre_rt + flat / kWideRows;
       const int2 c = p.seg_ctas[seg];
@@ -907,9 +905,9 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) quant_join_ker
       const int seg = hk * p.pre_rt + flat / p.R;
       pre = partial(p.seg_ctas[seg], seg, p.pre_slot_rows, flat % p.R);
     }
-    if (own_tiles(p, kv, n, rt) > 0) {
+    if (own_tiles(p, kv, n) > 0) {
       const int2 c = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
-      own = partial(c, own_seg, p.own_slot_rows, row % p.R);
+      own = partial(c, own_seg, p.own_slot_rows, row);
       own.at += p.own_first;
       direct = p.pre_rt == 0 && own.n == 1;       // written by the first kernel
     }
@@ -925,7 +923,7 @@ struct QAttnPlan {
   // kNarrow: this file's kernel alone; kWide: that of the bf16 pages alone; kBoth: that
   // one for the prefix, this one for the requests' own keys
   enum { kNarrow, kWide, kBoth } way;
-  int R, TG, own_rt, pre_rt, pre_slot_rows, own_slot_rows;
+  int R, TG, pre_rt, pre_slot_rows, own_slot_rows;
   size_t own_first, part_ml, part_o, bytes;
 };
 
@@ -958,10 +956,9 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, i
     w.bytes = wide_quant_bytes(B, T, Hq, Hkv, d, prefix, sms);
     return w;
   }
-  w.own_rt = (int)cdiv64(w.TG, w.R);
-  w.own_slot_rows = w.TG < w.R ? w.TG : w.R;
+  w.own_slot_rows = w.TG;              // at most R
   // a partial result for every number segment + CTA
-  const size_t own = (size_t)(B * Hkv * w.own_rt + kCtasPerSm * sms) * w.own_slot_rows;
+  const size_t own = (size_t)(B * Hkv + kCtasPerSm * sms) * w.own_slot_rows;
   size_t pre = 0;
   if (w.way == QAttnPlan::kBoth) {
     w.pre_rt = wide.rt;
@@ -974,7 +971,7 @@ QAttnPlan plan_quant(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t d, i
   }
   auto al = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w.own_first = pre;
-  w.part_ml = al((size_t)Hkv * (w.pre_rt + B * w.own_rt) * 8);      // behind the segments' CTAs
+  w.part_ml = al((size_t)Hkv * (w.pre_rt + B) * 8);      // behind the segments' CTAs
   w.part_o = w.part_ml + al((pre + own) * 8);
   w.bytes = w.part_o + al((pre + own) * d * 4);
   return w;
@@ -1079,7 +1076,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   const int64_t flat_rows = qv.B * qv.S * G, page = a.k.blocks * kBlockSlots;
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len, sms);
-  const int64_t own_rt = plan.way == QAttnPlan::kWide ? cdiv64(plan.TG, kWideHalf) : plan.own_rt;
+  const int64_t own_rt = plan.way == QAttnPlan::kWide ? cdiv64(plan.TG, kWideHalf) : 1;
   const int64_t pre_rt = plan.way == QAttnPlan::kWide ? cdiv64(flat_rows, kWideHalf) : plan.pre_rt;
   const int64_t most_tiles =
       a.k.heads * (qv.B * own_rt * cdiv64(max_pages * page, kTileKeys) + (pre_rt + qv.B) * cdiv64(prefix_len, kTileKeys));
@@ -1124,7 +1121,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   while ((1 << p.page_shift) < page) ++p.page_shift;
   p.num_pages = (int)a.k.pages; p.max_pages = max_pages; p.prefix_len = prefix_len; p.causal = causal ? 1 : 0;
   p.div_G = fast_div((uint32_t)G); p.div_TG = fast_div((uint32_t)plan.TG);
-  p.R = plan.R; p.TG = plan.TG; p.own_rt = plan.own_rt; p.pre_rt = plan.pre_rt;
+  p.R = plan.R; p.TG = plan.TG; p.pre_rt = plan.pre_rt;
   p.pre_tiles = plan.way == QAttnPlan::kBoth ? 0 : (int)cdiv64(prefix_len, kTileKeys);
   p.wide_ctas = plan.way == QAttnPlan::kBoth ? sms : 0;
   p.pre_slot_rows = plan.pre_slot_rows; p.own_slot_rows = plan.own_slot_rows;
