@@ -98,7 +98,11 @@ __device__ __forceinline__ uint8_t* find_block(const QuantParams& p, const Place
 // one slot (of either half), and a lane's 16-byte pieces, fall on different banks.
 __device__ __forceinline__ int stage_at(int group, int slot) { return group * 72 + (slot >> 3) * 36 + (slot & 7) * 4; }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+// The larger magnitudes of two pairs of bf16.
+__device__ __forceinline__ uint32_t largest2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<__nv_bfloat162*>(&a)), __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
 
 // Grid: x = (block, heads), y = request, z = K or V.
 template <int D>
@@ -118,28 +122,26 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
   // 4 channels of 16 slots (zeros where a slot is not written)
   const uint32_t fresh = w.active ? (1u << w.end) - (1u << w.first) : 0u;
   uint2 x[16];
-  const __nv_bfloat16* src = p.x[w.which] + w.b * p.sb[w.which] + w.h * p.sh[w.which] + w.l * 4;
+  const __nv_bfloat16* src = p.x[w.which] + w.b * p.sb[w.which] + w.h * p.sh[w.which] + w.t0 * p.ss[w.which] + w.l * 4;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 16; ++i, src += p.ss[w.which]) {
     x[i] = make_uint2(0u, 0u);
-    if (fresh >> i & 1u) x[i] = *reinterpret_cast<const uint2*>(src + (w.t0 + i) * p.ss[w.which]);
+    if (fresh >> i & 1u) x[i] = *reinterpret_cast<const uint2*>(src);
   }
   // the page has come while those are on their way
   uint8_t* block = find_block<D>(p, w);
   if (!block) return;
-  // Largest magnitudes, two slots in a word: bits without the sign are ordered as
-  // the numbers are, with infinity and NaN on top.
+  // Largest magnitudes, two slots in a word; NaN stays NaN.
   uint32_t most[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t a = max_u16x2(x[2 * i].x & 0x7FFF7FFFu, x[2 * i].y & 0x7FFF7FFFu);
-    const uint32_t b = max_u16x2(x[2 * i + 1].x & 0x7FFF7FFFu, x[2 * i + 1].y & 0x7FFF7FFFu);
-    most[i] = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    const uint32_t a = largest2(x[2 * i].x, x[2 * i].y), b = largest2(x[2 * i + 1].x, x[2 * i + 1].y);
+    most[i] = largest2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
   }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most[i] = max_u16x2(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+    for (int i = 0; i < 8; ++i) most[i] = largest2(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
   // Lane l8 of a group's eight works out the scales of slots 2 l8 and 2 l8 + 1.
   uint32_t mine = 0, byte[2];
   float inv[2];
@@ -279,10 +281,11 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
     const uint32_t four = i < 4 ? sc.x : i < 8 ? sc.y : i < 12 ? sc.z : sc.w;
     scale[i] = twice_scale((four >> (8 * (i % 4))) & 255u);
   }
-  __nv_bfloat16* dst = p.y[w.which] + w.b * p.sb[w.which] + w.h * p.sh[w.which] + w.l * 4;
-  auto put = [&](int i, uint32_t lo, uint32_t hi) {
-    if (w.active && i >= w.first && i < w.end)
-      *reinterpret_cast<uint2*>(dst + (w.t0 + i) * p.ss[w.which]) = make_uint2(lo, hi);
+  const uint32_t wanted = w.active ? (1u << w.end) - (1u << w.first) : 0u;
+  __nv_bfloat16* dst = p.y[w.which] + w.b * p.sb[w.which] + w.h * p.sh[w.which] + w.t0 * p.ss[w.which] + w.l * 4;
+  auto put = [&](int i, uint32_t lo, uint32_t hi) {    // i = 0 .. 15 in turn
+    if (wanted >> i & 1u) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+    dst += p.ss[w.which];
   };
   if (w.which == 0) {
     *reinterpret_cast<uint4*>(stage + stage_at(group, 2 * l8)) = c0;
