@@ -15,12 +15,14 @@
 // slot, are exchanged in shared memory.  Both kernels move whole rows and whole
 // blocks, in whole sectors of 32 bytes.
 //
-// Bound by DRAM: 16 requests' 4,096 tokens of 8 heads of 128 are written in 60.4 us
-// (340 MB, 83 % of the measured copy rate) and read back in 53.4 us (94 %); 5 of
-// 4,099 tokens in 21.7 and 19.1 us, where the way in and out counts 3 us; one token
-// each of 64 requests takes 3.0 us.  What it took: the rows are asked for before the
-// page is known (a warp waits once instead of twice), and stores of half sectors were
-// joined; together 66.8 -> 60.4 us.
+// Bound by DRAM: 16 requests' 4,096 tokens of 8 heads of 128 are written in 55.8 us
+// (340 MB, 90 % of the measured copy rate) and read back in 52.5 us (95 %); 5 of
+// 4,099 tokens in 20.1 and 18.3 us, where the way in and out counts 3 us; one token
+// each of 64 requests takes 2.7 us.  What it took: the rows are asked for before the
+// page is known (a warp waits once instead of twice) and stores of half sectors were
+// joined, 66.8 -> 60.4 us; 820 -> 690 instructions a warp (rows stepped through,
+// largest magnitudes of half the words at each step of the exchange), 60.4 -> 55.8, and
+// 680 -> 420 in reading, 53.4 -> 52.5.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -138,15 +140,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
     const uint32_t a = largest2(x[2 * i].x, x[2 * i].y), b = largest2(x[2 * i + 1].x, x[2 * i + 1].y);
     most[i] = largest2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
   }
+  // Of eight words a lane gives half away at each step, so that lane l8 of a group's
+  // eight ends with word l8: it works out the scales of slots 2 l8 and 2 l8 + 1.
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1)
+  for (int o = 4; o > 0; o >>= 1) {
+    const bool upper = l8 & o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most[i] = largest2(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-  // Lane l8 of a group's eight works out the scales of slots 2 l8 and 2 l8 + 1.
-  uint32_t mine = 0, byte[2];
+    for (int i = 0; i < o; ++i) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? most[i] : most[i + o], o);
+      most[i] = largest2(upper ? most[i + o] : most[i], got);
+    }
+  }
+  const uint32_t mine = most[0];
+  uint32_t byte[2];
   float inv[2];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) mine = l8 == i ? most[i] : mine;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const uint32_t bits = e ? mine >> 16 : mine & 0xFFFFu;
@@ -184,6 +191,14 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
       if (fresh >> (2 * l8 + e) & 1u) scales[2 * l8 + e] = (uint8_t)byte[e];
   }
 
+  // the group's 16 factors, by way of the stage
+  float rs[16];
+  reinterpret_cast<float2*>(stage)[lane] = make_float2(inv[0], inv[1]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(rs + 4 * i) = reinterpret_cast<const float4*>(stage)[group * 4 + i];
+  __syncwarp();
+
   // 1.5 2^23 + 8 + c, whose bits are kRaised + c + 8: words of codes are sums of these.
   // The product is not rounded on its own.
   constexpr uint32_t kRaised = 0x4B400000u;
@@ -197,7 +212,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
     uint32_t part[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float r = __shfl_sync(0xffffffffu, inv[i % 2], (lane & ~7) + i / 2);
+      const float r = rs[i];
       const uint32_t u = low(x[i].x, r) + (low(x[i].y, r) << 4) + (high(x[i].x, r) << 16) + (high(x[i].y, r) << 20) -
                          kRaised * (1u + (1u << 4) + (1u << 16) + (1u << 20));
       part[i] = odd ? u << 8 : u;
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantise_kernel(const __grid_co
     uint32_t v[4][2] = {{0u - kSum, 0u - kSum}, {0u - kSum, 0u - kSum}, {0u - kSum, 0u - kSum}, {0u - kSum, 0u - kSum}};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float r = __shfl_sync(0xffffffffu, inv[i % 2], (lane & ~7) + i / 2);
+      const float r = rs[i];
       const int at = 4 * (i % 8 / 2) + 16 * (i % 2);
       v[0][i / 8] += low(x[i].x, r) << at;
       v[1][i / 8] += high(x[i].x, r) << at;
@@ -275,11 +290,20 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
   const uint4* codes = reinterpret_cast<const uint4*>(block + w.l * 32);
   const uint4 c0 = codes[0], c1 = codes[1];
   const uint4 sc = *reinterpret_cast<const uint4*>(block + code_bytes(D) + (group % (D / kGroup)) * kBlockSlots);
-  uint32_t scale[16];                                  // twice each slot's
+  // twice the scales of slots 2 i and 2 i + 1; 255 stands for NaN
+  uint32_t scale[8];
+  const uint32_t four[4] = {sc.x, sc.y, sc.z, sc.w};
+  uint32_t full = 0u;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t four = i < 4 ? sc.x : i < 8 ? sc.y : i < 12 ? sc.z : sc.w;
-    scale[i] = twice_scale((four >> (8 * (i % 4))) & 255u);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t word = four[i / 2];
+    scale[i] = (__byte_perm(word, 0u, i % 2 ? 0x4342 : 0x4140) << 4) + 0x38803880u;
+    full |= ((word & 0x7F7F7F7Fu) + 0x01010101u) & word;      // bit 7 of a byte of 255
+  }
+  if (full & 0x80808080u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      scale[i] = twice_scale((four[i / 2] >> (16 * (i % 2))) & 255u) | twice_scale((four[i / 2] >> (16 * (i % 2) + 8)) & 255u) << 16;
   }
   const uint32_t wanted = w.active ? (1u << w.end) - (1u << w.first) : 0u;
   __nv_bfloat16* dst = p.y[w.which] + w.b * p.sb[w.which] + w.h * p.sh[w.which] + w.t0 * p.ss[w.which] + w.l * 4;
@@ -294,14 +318,14 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint32_t word = stage[stage_at(group, i) + l8 / 2] >> (lane & 1 ? 8 : 0);
-      const uint32_t s2 = scale[i] * 0x10001u, off = scale_offset(s2);
+      const uint32_t s2 = __byte_perm(scale[i / 2], 0u, i % 2 ? 0x3232 : 0x1010), off = scale_offset(s2);
       put(i, code_values(raised_codes(word, 0, p.eights), s2, off), code_values(raised_codes(word, 1, p.eights), s2, off));
     }
   } else {
     const uint32_t word[4][2] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {                  // two slots at a time, then two channels
-      const uint32_t s2 = scale[i] | scale[i + 1] << 16, off = scale_offset(s2);
+      const uint32_t s2 = scale[i / 2], off = scale_offset(s2);
       uint32_t v[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) v[c] = code_values(raised_codes(word[c][i / 8], i % 8 / 2, p.eights), s2, off);
