@@ -33,15 +33,15 @@
 //    24 heads of one row took 89 us instead of 74.
 //  * The maximum of a row moves only when a score passes it by more than 2^8, so that
 //    most tiles need one barrier of the four warps.
-//  * A prefix that more rows than a segment's share is the work of bsa_paged.cu's
+//  * A prefix of more rows than a segment's, unless it is short, is the work of bsa_paged.cu's
 //    kernel (its rows are the products' rows), which runs beside this one on SMs shared
 //    out by their tiles; the join reads the partial results of both.  64 requests on one
 //    prompt of 8,209 keys, up to 1,024 own ones each: 35 us; this kernel alone 83, that
 //    one alone 50.
 //
 // Bound by instructions: a tile of 128 keys takes an SM about 1,150 cycles, in which its
-// schedulers issue 65 to 70 % of the time (2.2 to 2.4 instructions a value of K and V,
-// of which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
+// schedulers issue 65 to 70 % of the time (2.9 instructions a value of K and V, of
+// which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
 // Device times, of the measured copy rate: 16 requests of 1,024 to 65,536 keys, 32
 // heads over 8 of 128: 135 us (69 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
 // 70 us (59 %); one request of 4,097 keys 9.4 us, of which 4 are the way in, the join
