@@ -102,7 +102,7 @@ constexpr int kSegmentWay = 1;
 // SMs of `sms` that the prefix gets where its tiles (of rows above 128 or not) and own
 // tiles (and ways) of few rows are two kernels side by side: by their times, 1.75 and 1.0 us
 // against 0.42 for a tile; SMs come in pairs.  (0.62 took 3 us more for 64 requests on
-// one prompt of 8,209 keys, 4 for 256 samples of one of 32,768.)
+// one prompt of 8,209 keys and for 256 samples of one of 32,768.)
 __device__ __forceinline__ int prefix_sms(int sms, int prefix_tiles, bool two_jobs, int own_tiles) {
   if (own_tiles == 0) return sms;
   const float w = (float)prefix_tiles * (two_jobs ? 1.75f : 1.0f), o = (float)own_tiles * 0.42f;

@@ -418,14 +418,14 @@ def test_more_requests_than_one_pass_over_the_lengths_takes(B, T, prefix, Hq, Hk
 
 
 def test_a_prefix_alone_needs_no_table_and_no_lengths():
-    """max_pages 0 with null pointers for the table and the lengths, for few rows, for
-    rows of the prefix's kernel, and for chunks."""
+    """max_pages 0 with null pointers for the table and the lengths: few rows, many rows
+    in either kernel or beside one another, and chunks."""
     from block_sparse_attention_bsa_gb300._lib import load
     from block_sparse_attention_bsa_gb300.paged import _tensor
     from block_sparse_attention_bsa_gb300.quant import _caches
     lib = load()
     pool = QPool([1, 1], 333, 2, 64, 64, DEV, 340)
-    for B, T in ((1, 1), (70, 1), (2, 40)):
+    for B, T in ((1, 1), (70, 1), (200, 1), (2, 40)):
         x = randn((B, T, 8, 64), 341)
         q = x.to(DEV)
         out, lse = torch.empty_like(q), torch.empty(B, 8, T, device=DEV)
@@ -439,3 +439,88 @@ def test_a_prefix_alone_needs_no_table_and_no_lengths():
         ref.prefix_len, ref.pre_k, ref.pre_v, ref.lens = 333, pool.pre_k, pool.pre_v, [0] * B
         ref.own_k, ref.own_v = [pool.pre_k[:0]] * B, [pool.pre_v[:0]] * B
         check_attention(out, lse, attend64(x, ref))
+
+
+# B, T, new, prefix, Hq, Hkv, d, page, causal: prefixes whose tiles, of segments of few
+# rows, are more than the GPU's 608 blocks, beside own keys of few rows
+BESIDE = {
+    "4 rows": (160, 1, False, 700, 8, 2, 128, 64, True),
+    "4 rows, 120 in all": (30, 1, False, 2000, 8, 2, 128, 16, True),
+    "8 rows": (64, 2, True, 613, 8, 2, 64, 32, True),
+    "12 rows": (80, 3, True, 700, 8, 2, 128, 128, False),
+    "10 rows of 64": (70, 5, True, 1300, 4, 2, 64, 16, True),
+}
+
+
+def beside(name, seed):
+    B, T, ragged, prefix, Hq, Hkv, d, page, causal = BESIDE[name]
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, 300, (B,), generator=g)
+    lens[3:7] = 0
+    new = torch.minimum(torch.randint(0, T + 1, (B,), generator=g), lens).tolist() if ragged else None
+    pool = QPool(lens.tolist(), prefix, Hkv, d, page, DEV, seed + 1)
+    q, counts = randn((B, T, Hq, d), seed + 2), ints(new) if ragged else None
+
+    def attend(x, **kw):
+        return bsa.bsa_forward_paged_q4(x, pool.gk, pool.gv, pool.gtable, pool.kv_lens, new_lens=counts,
+                                        prefix_table=pool.gprefix, prefix_len=prefix, causal=causal, **kw)
+
+    return pool, q, new, causal, attend
+
+
+@pytest.mark.parametrize("name", BESIDE)
+def test_a_long_prefix_beside_own_keys_of_few_rows(name):
+    pool, q, new, causal, attend = beside(name, 350)
+    out, lse = attend(q.to(DEV))
+    bsa.bsa_device_status()
+    check_attention(out, lse, attend64(q, pool, new, causal))
+    # a row that is not finite is felt by no other
+    i = next(b for b in range(len(pool.lens) - 1, 0, -1) if pool.lens[b] > 0 and (new is None or new[b] > 0))
+    bad = q.clone()
+    bad[i, 0, 1, 5] = float("nan")
+    out2, lse2 = attend(bad.to(DEV))
+    bsa.bsa_device_status()
+    assert torch.isnan(out2[i, 0, 1]).all() and torch.isnan(lse2[i, 1, 0])
+    out2[i, 0, 1], lse2[i, 1, 0] = out[i, 0, 1], lse[i, 1, 0]
+    assert torch.equal(out2, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("name", ["4 rows", "8 rows"])
+def test_long_prefixes_captured_on_two_streams_and_behind_one_another(name):
+    """Kernels that start before the ones in front of them have left: twenty calls in a
+    row with one workspace, in two graphs on two streams at once, and eager ones beside
+    them, each with inputs that are written right before; the same bits every time."""
+    pool, q, _, _, attend = beside(name, 360)
+    xs = [q.to(DEV), q.flip(0).contiguous().to(DEV)]
+    want = [attend(x) for x in xs]
+    B, T, Hq, d = q.shape
+    n = bsa.bsa_forward_paged_q4_workspace_size(B, T, Hq, pool.gk.shape[1], d, True)
+    streams, graphs, outs = [torch.cuda.Stream() for _ in range(2)], [], []
+    for s, x in zip(streams, xs):
+        room, ws = torch.empty_like(x), torch.empty(n, dtype=U8, device=DEV)
+        out = [torch.empty_like(x) for _ in range(20)]
+        lse = [torch.empty(B, Hq, T, device=DEV) for _ in range(20)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for i in range(20):
+                room.fill_(float("nan"))
+                room.copy_(x)
+                attend(room, out=out[i], lse=lse[i], workspace=ws)
+        graphs.append(g)
+        outs.append((out, lse, room, ws))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for o, l, *_ in outs:
+            for t in (*o, *l):
+                t.fill_(7.0)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [attend(x) for x in xs]
+        torch.cuda.synchronize()
+        for (o, l, *_), (wo, wl), (eo, el) in zip(outs, want, eager):
+            assert torch.equal(eo, wo) and torch.equal(el, wl)
+            assert all(torch.equal(t, wo) for t in o) and all(torch.equal(t, wl) for t in l)
+    bsa.bsa_device_status()
