@@ -34,11 +34,13 @@ def bsa_cache_q4_shape(pages: int, page_size: int, Hkv: int, d: int):
 def _cache(t, name: str, index: int):
     """Packed bsaq_cache and the head dim."""
     if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is _U8:
-        shape, stride = t.shape, t.stride()
-        if (len(shape) == 4 and shape[3] % 17 == 0 and stride[3] == 1
-                and (shape[2] <= 1 or stride[2] == shape[3])):
-            d = shape[3] // 17 * 2
-            return _pack_cache(t.data_ptr(), *shape[:3], d, *stride[:2]), d
+        shape = t.shape
+        if len(shape) == 4:
+            pages, heads, blocks, row = shape
+            page, head, block, one = t.stride()
+            if row % 17 == 0 and one == 1 and (blocks <= 1 or block == row):
+                d = row // 17 * 2
+                return _pack_cache(t.data_ptr(), pages, heads, blocks, d, page, head), d
     raise _wrong(t, name, index, "[pages, Hkv, page_size / 16, 17 d / 2] with contiguous blocks", _U8)
 
 
@@ -92,19 +94,27 @@ def bsa_cache_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: 
     shape = (B, int(length), k_cache.shape[1], d)
     if not 0 < shape[1] < 1 << 31:
         raise ValueError(f"length {shape[1]} is out of range")
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and _tensor(t, name, dev) and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
-    return _on(dev, stream, _read_launch, (kc, vc, table, stride, n, lens, begin), shape, k_cache.device, k_out, v_out)
+    kd, vd = _rows_out(k_out, "k_out", shape, dev), _rows_out(v_out, "v_out", shape, dev)
+    return _on(dev, stream, _read_launch, (kc, vc, table, stride, n, lens, begin), shape, k_cache.device, k_out, v_out, kd, vd)
 
 
-def _read_launch(args, shape, device, k_out, v_out, handle):
-    if k_out is None:
+def _rows_out(t, name: str, shape, index: int):
+    if t is None:
+        return None
+    packed = _tensor(t, name, index)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    return packed
+
+
+def _read_launch(args, shape, device, k_out, v_out, kd, vd, handle):
+    if kd is None:
         k_out = torch.zeros(shape, dtype=_BF, device=device)
-    if v_out is None:
+        kd = _tensor(k_out, "k_out", device.index)
+    if vd is None:
         v_out = torch.zeros(shape, dtype=_BF, device=device)
-    index = device.index
-    st = _load().bsaq_cache_read(*args, _tensor(k_out, "k_out", index), _tensor(v_out, "v_out", index), handle)
+        vd = _tensor(v_out, "v_out", device.index)
+    st = _load().bsaq_cache_read(*args, kd, vd, handle)
     if st:
         _check(st)
     return k_out, v_out
