@@ -75,9 +75,9 @@ __device__ __forceinline__ bool find_place(const QuantParams& p, int64_t from, i
   const int64_t pos0 = ((from >> 4) + blk) * 16;       // rounds down where negative, too
   w->t0 = pos0 - from;
   w->first = (int)(w->t0 < 0 ? -w->t0 : 0);
-  const int64_t left = n - w->t0;
+  const int64_t left = n - w->t0;                      // may be below what 32 bits hold
+  if (left <= w->first) return false;
   w->end = (int)(left < 16 ? left : 16);
-  if (w->end <= w->first) return false;
   const int64_t at = pos0 >> (4 + p.blocks_shift);
   w->page = -1;
   if (pos0 >= 0 && at < p.max_pages) w->page = p.page_table[w->b * p.table_stride + at];
