@@ -282,7 +282,12 @@ __global__ void __launch_bounds__(kQuantThreads) read_kernel(const __grid_consta
   w.which = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t from = p.other ? max(p.other[w.b], 0) : 0;
-  const int64_t keys = (int64_t)p.kv_lens[w.b] - from;
+  const int kv = p.kv_lens[w.b];
+  if (kv < 0) {                                        // no block of such a request is looked up: said here
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_quant_error, kErrPage);
+    return;
+  }
+  const int64_t keys = kv - from;
   if (!find_place<D>(p, from, keys < p.S ? keys : p.S, &w)) return;
   const uint8_t* block = find_block<D>(p, w);
   if (!block) return;

@@ -40,3 +40,17 @@ def test_read_from_far_behind_the_last_key_reads_nothing(lens, first, length):
             n = max(0, min(lens[b] - first[b], length))
             assert torch.equal(got[b, :n].cpu(), rows[b][first[b]:first[b] + n])
             assert (got[b, n:] == 7).all()
+
+
+def test_read_reports_a_negative_length():
+    """As the append and the attention do; other requests are read."""
+    pool = QPool([40, 20], 0, 2, 64, 16, DEV, 406)
+    for first in (None, ints([0, 3])):
+        bsa.bsa_device_status()
+        k, v = bsa.bsa_cache_read_q4(pool.gk, pool.gv, pool.gtable, ints([-1, 20]), 30, first=first)
+        with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES.*bsaq_cache_read"):
+            bsa.bsa_device_status()
+        f = 0 if first is None else 3
+        assert torch.equal(k[1, :20 - f].cpu(), pool.own_k[1][f:]) and torch.equal(v[1, :20 - f].cpu(), pool.own_v[1][f:])
+        assert (k[0] == 0).all()
+    bsa.bsa_device_status()
