@@ -513,10 +513,11 @@ bsa_status bsa_device_status(bsa_stream_t stream) {
   const unsigned int ep = read_and_clear_paged_error();
   // and those of the 4-bit cache's calls
   const unsigned int eq = read_and_clear_quant_error();
-  const unsigned int ea = read_and_clear_quant_attn_error();
+  unsigned int ea = read_and_clear_quant_attn_error();
   if (ef == 0xFFFFFFFFu || eb == 0xFFFFFFFFu || er == 0xFFFFFFFFu || ep == 0xFFFFFFFFu || eq == 0xFFFFFFFFu ||
       ea == 0xFFFFFFFFu)
     return set_error(BSA_ERR_CUDA, "bsa_device_status: cannot read the device error word");
+  if (ep & kErrQuantPage) ea |= kErrPage;      // met by the paged attention's kernel at work for bsaq_forward
   int bad = 0;
   const int zero = 0;
   if ((st = cuda_check(cudaMemcpyFromSymbol(&bad, g_debug_bad_rows, sizeof(bad)), "read BSA_DEBUG counter")) !=

@@ -67,6 +67,7 @@ constexpr int kMaxBlocks = kMaxPagedBatch / 32;     // blocks of 32 requests in 
 // ring then, from blocks that warp 0 copies into a ring of their own.
 template <int D, bool kQ4>
 struct PagedCfg {
+  static constexpr unsigned int kErr = kQ4 ? kErrQuantPage : kErrPage;      // a bad page or length, told by the call's name
   static constexpr int kThreads = kQ4 ? 512 : 384;
   static constexpr int kChunks = D / 64;                      // 128-byte chunks per row
   static constexpr int kQBytes = kHalf * 128 * kChunks;      // 128 rows
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
     if (cta == 0 && b < p.B) {
       if (p.max_pages > 0) {
         const int kv = p.kv_lens[b];
-        if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, kErrPage);
+        if (kv < 0 || kv > p.max_pages << p.page_shift) atomicOr(&g_bsa_error, C::kErr);
       }
     }
   }
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
         if (lane < per_tile && key < (pre ? p.prefix_len : s.kv)) {
           page = (pre ? p.prefix_table : own_table)[key >> p.page_shift];
           if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_bsa_error, kErrPage);
+            atomicOr(&g_bsa_error, C::kErr);
             page = 0;
           }
         }
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
         if (lane < per_tile && key < (pre ? p.prefix_len : s.kv)) {
           page = (pre ? p.prefix_table : own_table)[key >> p.page_shift];
           if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_bsa_error, kErrPage);
+            atomicOr(&g_bsa_error, C::kErr);
             page = p.num_pages;
           }
         }

@@ -8,10 +8,12 @@
 
 namespace bsa {
 
-// Bit of the device error words of bsa_rope.cu and bsa_paged.cu: a page table
-// entry that names no page, or a length without pages (bit 0: a bounded wait
-// gave up).
+// Bit of the device error words of bsa_rope.cu, bsa_paged.cu and the 4-bit cache's
+// files: a page table entry that names no page, or a length without pages (bit 0:
+// a bounded wait gave up).
 constexpr unsigned int kErrPage = 2u;
+// The same in the word of bsa_paged.cu where its kernel works for bsaq_forward.
+constexpr unsigned int kErrQuantPage = 4u;
 unsigned int read_and_clear_rope_error();
 unsigned int read_and_clear_paged_error();
 bsa_status launch_paged_wait_probe(unsigned long long limit_ns, cudaStream_t stream);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_bsa_gb300 as bsa
-from paged_utils import BF
+from paged_utils import BF, Pool
 from quant_utils import QPool
 
 pytestmark = pytest.mark.gpu
@@ -16,6 +16,10 @@ FAR = 2 ** 31 - 1
 @pytest.fixture(scope="module", autouse=True)
 def built():
     bsa.build()
+
+
+def randn(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(BF)
 
 
 def ints(x):
@@ -53,4 +57,50 @@ def test_read_reports_a_negative_length():
         f = 0 if first is None else 3
         assert torch.equal(k[1, :20 - f].cpu(), pool.own_k[1][f:]) and torch.equal(v[1, :20 - f].cpu(), pool.own_v[1][f:])
         assert (k[0] == 0).all()
+    bsa.bsa_device_status()
+
+
+# lens, T, prefix, Hq, Hkv, d, page: a kernel of few rows, the one of many rows, both beside one another
+WAYS = {
+    "few rows": ([70, 40], 1, 40, 8, 2, 128, 32),
+    "a chunk": ([70, 40], 17, 40, 8, 2, 64, 32),
+    "a chunk and its prefix": ([200] * 3, 100, 300, 16, 2, 128, 64),
+    "a long prefix beside own keys": ([70, 3] * 80, 1, 700, 8, 2, 128, 64),
+}
+
+
+@pytest.mark.parametrize("bad", ["table", "prefix", "length"])
+@pytest.mark.parametrize("way", WAYS)
+def test_bad_pages_are_reported_under_the_call_that_met_them(way, bad):
+    lens, T, prefix, Hq, Hkv, d, page = WAYS[way]
+    pool = QPool(lens, prefix, Hkv, d, page, DEV, 400)
+    q = randn((len(lens), T, Hq, d), 401).to(DEV)
+    table, shared, kv = pool.gtable.clone(), pool.gprefix.clone(), pool.kv_lens.clone()
+    if bad == "table":
+        table[0, 0] = pool.total
+    elif bad == "prefix":
+        shared[-(-prefix // page) - 1] = -1
+    else:
+        kv[0] = table.shape[1] * page + 1
+    bsa.bsa_device_status()
+    bsa.bsa_forward_paged_q4(q, pool.gk, pool.gv, table, kv, prefix_table=shared, prefix_len=prefix)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES.*reached bsaq_forward") as e:
+        bsa.bsa_device_status()
+    assert "bsap_forward" not in str(e.value)
+    bsa.bsa_device_status()
+
+
+def test_bad_pages_of_both_caches_attentions_are_told_apart():
+    x = randn((1, 40, 4, 64), 402).to(DEV)
+    plain, packed = Pool([60], 0, 2, 64, 16, DEV, 403, fill=1.0), QPool([60], 0, 2, 64, 16, DEV, 404)
+    plain.gtable[0, 1] = packed.gtable[0, 1] = -1
+    bsa.bsa_device_status()
+    bsa.bsa_forward_paged(x, plain.gk, plain.gv, plain.gtable, plain.kv_lens)
+    with pytest.raises(bsa.BsaError, match="reached bsap_forward") as e:
+        bsa.bsa_device_status()
+    assert "bsaq" not in str(e.value)
+    bsa.bsa_forward_paged(x, plain.gk, plain.gv, plain.gtable, plain.kv_lens)
+    bsa.bsa_forward_paged_q4(x, packed.gk, packed.gv, packed.gtable, packed.kv_lens)
+    with pytest.raises(bsa.BsaError, match="reached bsap_forward and bsaq_forward"):
+        bsa.bsa_device_status()
     bsa.bsa_device_status()
