@@ -356,7 +356,10 @@ __global__ void __launch_bounds__(PagedCfg<D, kQ4>::kThreads, 1) paged_attention
   // read or written that it uses (and nothing by the read-only path, whose loads
   // may be taken from before this point).  2 us less a call in a row of them.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (kQ4 && p.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (kQ4 && p.early && threadIdx.x == C::kThreads - 32) {            // the last warp has the least to do here
+    fence_waited();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   // the schedule: tiles of own keys per block of 32 requests, then their sums
   const int nblk = (p.B + 31) / 32;
 #pragma unroll 1
@@ -1093,23 +1096,20 @@ __global__ void __launch_bounds__(kWarps > 1 ? 32 * kWarps : 128) paged_join_ker
   const int r0 = real ? (int)R : 0;
   const int bt = r0 / p.Hq, h = r0 - bt * p.Hq;
   const int b = bt / p.T, i = bt - b * p.T, hk = p.div_G.quot(h), g = h - hk * p.G;
-  // Read before the wait: this grid starts when the main kernel's blocks have all
-  // left, each of which has waited for whatever wrote the lengths.
-  const int kv = own_keys(p, b), n = new_tokens(p, b);
+  const int row = i * p.G + g, flat = b * p.TG + row, rt = row / kRowTile;
+  const int pre_seg = hk * p.pre_rt + flat / kRowTile, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // One wait on memory for all of it: a segment's CTAs are read before the lengths tell
+  // whether it has any (if not, they are any bytes and not looked at).
+  const int2 pc = p.pre_tiles > 0 ? p.seg_ctas[pre_seg] : make_int2(0, 0), oc = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
+  const int kv = own_keys(p, b), n = new_tokens(p, b);
   // Partial results: from each CTA of a segment one, or two of a segment of up
   // to 128 rows (one of each group).
   Parts pre{0, 0, 0}, own{0, 0, 0};
   bool direct = false;
   const bool keyed = real && i < n && (p.prefix_len > 0 || min(seen_keys(p, kv, n, i), kv) > 0);
   if (real && i < n) {
-    const int row = i * p.G + g, flat = b * p.TG + row;
-    const int pre_seg = hk * p.pre_rt + flat / kRowTile;
-    const int rt = row / kRowTile, own_seg = (b * p.Hkv + hk) * p.own_rt + rt;
     const int mine = own_tiles(p, kv, n, rt);
-    int2 pc = make_int2(0, 0), oc = make_int2(0, 0);
-    if (p.pre_tiles > 0) pc = p.seg_ctas[pre_seg];
-    if (mine > 0) oc = p.seg_ctas[p.pre_rt * p.Hkv + own_seg];
     if (p.pre_tiles > 0) {
       const bool two = p.B * p.TG - (flat - flat % kRowTile) <= kHalf;
       pre = segment_parts(pc.x, pc.y, p.ctas, pre_seg, two, flat % kRowTile / kHalf, p.pre_slot_rows, flat % kHalf);

@@ -40,6 +40,14 @@ __device__ __forceinline__ int warp_inclusive_sum(int v) {
 // proxy (the MMAs read Q and V through it).
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// For a kernel that reads what earlier ones have written with no griddepcontrol.wait of
+// its own before it, but behind a kernel that has waited for them.  PTX gives a launch
+// that is let in early no more than leave to run, so the order is made on both sides:
+// in front the thread that lets the next kernel in passes this between its wait and
+// that instruction (no path may come to it without the wait), and behind it whoever
+// reads passes it before, or stands behind a barrier with a thread that has.
+__device__ __forceinline__ void fence_waited() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 // 32 bytes, a whole sector, to a 32-byte aligned address.
 __device__ __forceinline__ void store_32(void* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
