@@ -1260,13 +1260,6 @@ bsa_status launch_paged(const PagedParams& p, cudaStream_t stream, bool join = t
                     "paged_join_kernel launch");
 }
 
-// Key tiles at most, with the keys that the tables could hold.
-int64_t most_tiles_of(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t max_pages, int64_t prefix_len) {
-  const int64_t G = qv.H / Hkv;
-  return qv.B * Hkv * cdiv64(qv.S * G, kRowTile) * (cdiv64(max_pages * page, kTileKeys) + cdiv64(prefix_len, kTileKeys)) +
-         Hkv * cdiv64(qv.B * qv.S * G, kRowTile) * cdiv64(prefix_len, kTileKeys);
-}
-
 // What a launch takes but for the cache itself; `a`: its tables and lengths.
 PagedParams make_params(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t pages, const PagedArgs& a,
                         const int32_t* prefix_table, int32_t prefix_len, int32_t causal, float softmax_scale, void* out,
@@ -1314,6 +1307,12 @@ PagedParams make_params(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t
 }
 
 }  // namespace
+
+int64_t most_tiles_of(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t max_pages, int64_t prefix_len) {
+  const int64_t G = qv.H / Hkv;
+  return qv.B * Hkv * cdiv64(qv.S * G, kRowTile) * (cdiv64(max_pages * page, kTileKeys) + cdiv64(prefix_len, kTileKeys)) +
+         Hkv * cdiv64(qv.B * qv.S * G, kRowTile) * cdiv64(prefix_len, kTileKeys);
+}
 
 unsigned int read_and_clear_paged_error() { return take_error_word(); }
 

@@ -50,6 +50,9 @@ struct PagedArgs {
   const int32_t* page_table; int64_t table_stride; int max_pages;
   const int32_t* kv_lens; const int32_t* new_lens;
 };
+// Key tiles at most of an attention over pages, with the keys that the tables could
+// hold: what bsap_forward and bsaq_forward limit (32 bits count them on the device).
+int64_t most_tiles_of(const bsa_tensor& qv, int64_t Hkv, int64_t page, int64_t max_pages, int64_t prefix_len);
 bsa_status check_paged(const char* fn, const bsa_tensor* k_cache, const bsa_tensor* v_cache,
                        const int32_t* page_table, int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
                        const int32_t* new_lens, int64_t B, PagedArgs* a);

@@ -1084,10 +1084,7 @@ bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, const bs
   const int64_t flat_rows = qv.B * qv.S * G, page = a.k.blocks * kBlockSlots;
   const int64_t q_extent = (qv.B - 1) * qv.stride_b + (qv.S - 1) * qv.stride_s + qv.H * qv.stride_h + qv.D;
   const QAttnPlan plan = plan_quant(qv.B, qv.S, qv.H, a.k.heads, qv.D, prefix_len, sms);
-  const int64_t own_rt = plan.way == QAttnPlan::kWide ? cdiv64(plan.TG, kWideHalf) : 1;
-  const int64_t pre_rt = plan.way == QAttnPlan::kWide ? cdiv64(flat_rows, kWideHalf) : plan.pre_rt;
-  const int64_t most_tiles =
-      a.k.heads * (qv.B * own_rt * cdiv64(max_pages * page, kTileKeys) + (pre_rt + qv.B) * cdiv64(prefix_len, kTileKeys));
+  const int64_t most_tiles = most_tiles_of(qv, a.k.heads, page, max_pages, prefix_len);
   const size_t need = plan.bytes;
   if (flat_rows > INT32_MAX / 16 || most_tiles > INT32_MAX / 8 || flat_rows * a.k.heads > INT32_MAX ||
       need / (4 * (size_t)qv.D) > INT32_MAX)
