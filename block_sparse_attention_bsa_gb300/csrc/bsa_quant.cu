@@ -473,6 +473,18 @@ static bsa_status check_rows_caches(const char* fn, const bsa_tensor view[2], co
   return BSA_OK;
 }
 
+// What a call writes against the tables and lengths that its other blocks still read.
+static bsa_status check_tables_apart(const char* fn, const Bytes written[2], const QuantArgs& a, int64_t B,
+                                     const char* other_name, const int32_t* other) {
+  const Bytes reads[] = {bytes_at("page_table", a.page_table, 4 * ((B - 1) * a.table_stride + a.max_pages)),
+                         bytes_at("kv_lens", a.kv_lens, 4 * B), bytes_at(other_name, other, 4 * B)};
+  bsa_status st;
+  for (int i = 0; i < 2; ++i)
+    for (const Bytes& r : reads)
+      if ((st = check_apart(fn, r, written[i])) != BSA_OK) return st;
+  return BSA_OK;
+}
+
 }  // namespace bsa
 
 using namespace bsa;
@@ -495,6 +507,8 @@ bsa_status bsaq_cache_append(const bsa_tensor* k, const bsa_tensor* v, const bsa
   if ((st = check_aligned(fn, "new_lens", new_lens, 4)) != BSA_OK) return st;
   if ((st = check_rows_caches(fn, x, names, a)) != BSA_OK) return st;
   if (a.k.ptr == a.v.ptr) return set_error(BSA_ERR_INVALID_ARG, std::string(fn) + ": v_cache shares memory with k_cache");
+  const Bytes written[2] = {bytes_of("k_cache", a.k), bytes_of("v_cache", a.v)};
+  if ((st = check_tables_apart(fn, written, a, x[0].B, "new_lens", new_lens)) != BSA_OK) return st;
   QuantParams p{};
   for (int i = 0; i < 2; ++i) {
     p.x[i] = static_cast<const __nv_bfloat16*>(x[i].ptr);
@@ -521,6 +535,8 @@ bsa_status bsaq_cache_read(const bsaq_cache* k_cache, const bsaq_cache* v_cache,
   if ((st = check_aligned(fn, "first", first, 4)) != BSA_OK) return st;
   if ((st = check_rows_caches(fn, y, names, a)) != BSA_OK) return st;
   if ((st = check_apart(fn, "k_out", y[0], "v_out", y[1])) != BSA_OK) return st;
+  const Bytes written[2] = {bytes_of("k_out", y[0]), bytes_of("v_out", y[1])};
+  if ((st = check_tables_apart(fn, written, a, y[0].B, "first", first)) != BSA_OK) return st;
   QuantParams p{};
   for (int i = 0; i < 2; ++i) {
     p.y[i] = static_cast<__nv_bfloat16*>(const_cast<void*>(y[i].ptr));

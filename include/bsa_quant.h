@@ -79,8 +79,8 @@ BSA_API bsa_status bsaq_cache_append(const bsa_tensor* k, const bsa_tensor* v, c
  *   first[b] + t, for keys below kv_lens[b]; rows behind, and rows from S on, are
  *   not written.  first: device int32 [B], or NULL = 0; taken as 0 where negative.
  *   A negative length is reported, as a missing page of a row that is asked for is.
- *   The outputs share no memory with the caches or one another (refused from the
- *   first to behind the last byte of each). */
+ *   The outputs share no memory with the caches, the table, the lengths, first or one
+ *   another (refused from the first to behind the last byte of each). */
 BSA_API bsa_status bsaq_cache_read(const bsaq_cache* k_cache, const bsaq_cache* v_cache, const int32_t* page_table,
                                    int64_t table_stride, int32_t max_pages, const int32_t* kv_lens,
                                    const int32_t* first, const bsa_tensor* k_out, const bsa_tensor* v_out,

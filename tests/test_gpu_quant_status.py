@@ -5,7 +5,7 @@ import torch
 
 import block_sparse_attention_bsa_gb300 as bsa
 from paged_utils import BF, Pool
-from quant_utils import QPool
+from quant_utils import QPool, U8
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -103,4 +103,32 @@ def test_bad_pages_of_both_caches_attentions_are_told_apart():
     bsa.bsa_forward_paged_q4(x, packed.gk, packed.gv, packed.gtable, packed.kv_lens)
     with pytest.raises(bsa.BsaError, match="reached bsap_forward and bsaq_forward"):
         bsa.bsa_device_status()
+    bsa.bsa_device_status()
+
+
+def test_tables_and_lengths_right_beside_what_is_written():
+    """In one allocation with the outputs of a read, and with the caches of an append,
+    one element before the first byte and one behind the last."""
+    pool = QPool([40, 20], 0, 2, 64, 16, DEV, 407)
+    want = bsa.bsa_cache_read_q4(pool.gk, pool.gv, pool.gtable, pool.kv_lens, 40)
+    n = want[0].numel() * 2
+    for at in (16, 16 + n):
+        room = torch.zeros(n + 64, dtype=U8, device=DEV)
+        out = room[16:16 + n].view(BF).view(want[0].shape)
+        lens = room[at - 8 if at == 16 else at:][:8].view(I32)
+        lens.copy_(pool.kv_lens)
+        k, v = bsa.bsa_cache_read_q4(pool.gk, pool.gv, pool.gtable, lens, 40, k_out=out)
+        assert k is out and torch.equal(k, want[0]) and torch.equal(v, want[1])
+        with pytest.raises(bsa.BsaError, match="k_out shares memory with kv_lens"):
+            bsa.bsa_cache_read_q4(pool.gk, pool.gv, pool.gtable, room[12:20].view(I32), 40, k_out=out)
+    m = pool.gk.numel()
+    room = torch.zeros(m + 64, dtype=U8, device=DEV)
+    kc, vc = room[16:16 + m].view(pool.gk.shape), torch.zeros_like(pool.gv)
+    lens = room[16 + m:16 + m + 8].view(I32)
+    lens.copy_(pool.kv_lens)
+    bsa.bsa_cache_append_q4(*want, kc, vc, pool.gtable, lens, new_lens=pool.kv_lens)
+    k, v = bsa.bsa_cache_read_q4(kc, vc, pool.gtable, lens, 40)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    with pytest.raises(bsa.BsaError, match="k_cache shares memory with kv_lens"):
+        bsa.bsa_cache_append_q4(*want, kc, vc, pool.gtable, room[16:24].view(I32))
     bsa.bsa_device_status()
