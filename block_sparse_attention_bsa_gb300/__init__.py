@@ -38,6 +38,7 @@ from .quant import (  # noqa: F401
     bsa_cache_append_q4,
     bsa_cache_q4_shape,
     bsa_cache_read_q4,
+    bsa_debug_paged_q4_wait_probe,
     bsa_forward_paged_q4,
     bsa_forward_paged_q4_workspace_size,
 )

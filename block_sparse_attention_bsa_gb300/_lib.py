@@ -110,6 +110,7 @@ QUANT_SIGNATURES = {
     "bsaq_cache_read": (_I, [_P, _P, _P, _I64, _I32, _P, _P, _P, _P, _P]),
     "bsaq_forward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "bsaq_forward": (_I, [_P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "bsaq_debug_wait_probe": (_I, [ctypes.c_uint64, _P]),
 }
 
 

@@ -566,6 +566,12 @@ bsa_status bsap_debug_wait_probe(uint64_t limit_ns, bsa_stream_t stream) {
   return st != BSA_OK ? st : launch_paged_wait_probe(limit_ns, reinterpret_cast<cudaStream_t>(stream));
 }
 
+bsa_status bsaq_debug_wait_probe(uint64_t limit_ns, bsa_stream_t stream) {
+  clear_error();
+  const bsa_status st = check_probe_limit("bsaq_debug_wait_probe", limit_ns);
+  return st != BSA_OK ? st : launch_quant_wait_probe(limit_ns, reinterpret_cast<cudaStream_t>(stream));
+}
+
 bsa_status bsa_debug_wait_probe(int32_t family, uint64_t limit_ns, bsa_stream_t stream) {
   clear_error();
   if (family != 0 && family != 1)

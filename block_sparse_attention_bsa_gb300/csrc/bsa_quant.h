@@ -10,6 +10,7 @@ namespace bsa {
 
 unsigned int read_and_clear_quant_error();        // append and read
 unsigned int read_and_clear_quant_attn_error();
+bsa_status launch_quant_wait_probe(unsigned long long limit_ns, cudaStream_t stream);
 
 constexpr int kGroup = 32;                        // channels that share a scale
 constexpr int kBlockSlots = 16;

@@ -1030,6 +1030,11 @@ bsa_status launch_quant(const QAttnParams& p, cudaStream_t stream) {
 
 unsigned int read_and_clear_quant_attn_error() { return take_error_word(); }
 
+bsa_status launch_quant_wait_probe(unsigned long long limit_ns, cudaStream_t stream) {
+  wait_probe_kernel<<<1, 32, 0, stream>>>(limit_ns);
+  return cuda_check(cudaGetLastError(), "wait_probe_kernel launch (4-bit paged attention)");
+}
+
 }  // namespace bsa
 
 using namespace bsa;

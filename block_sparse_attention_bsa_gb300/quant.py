@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from ._lib import load as _load
-from .api import _check, _check_buffer
+from .api import _check, _check_buffer, _stream_ptr
 from .paged import _BF, _F32, _U8, PAGE_SIZES_SUPPORTED, _check_overlap, _gpu, _ints, _on, _table, _tensor, _wrong
 
 _pack_cache = Struct("7q").pack             # bsaq_cache
@@ -193,3 +193,8 @@ def _forward_launch(q, k_cache, v_cache, args, out, lse, return_lse, workspace, 
     if st:
         _check(st)
     return out, lse
+
+
+def bsa_debug_paged_q4_wait_probe(limit_ns: int, stream=None) -> None:
+    """``bsa_debug_wait_probe`` for the kernels of the attention over 4-bit pages."""
+    _check(_load().bsaq_debug_wait_probe(int(limit_ns), _stream_ptr(stream)))

@@ -103,6 +103,9 @@ BSA_API bsa_status bsaq_forward(const bsa_tensor* q, const bsaq_cache* k_cache, 
                                 int32_t prefix_len, int32_t causal, float softmax_scale, void* out, float* lse,
                                 void* workspace, size_t ws_bytes, bsa_stream_t stream);
 
+/* bsap_debug_wait_probe for the attention over 4-bit pages (1 ms to 10 s). */
+BSA_API bsa_status bsaq_debug_wait_probe(uint64_t limit_ns, bsa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

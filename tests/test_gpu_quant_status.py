@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import block_sparse_attention_bsa_gb300 as bsa
-from paged_utils import BF, Pool
+from paged_utils import BF, Pool, attend64, check_attention
 from quant_utils import QPool, U8
 
 pytestmark = pytest.mark.gpu
@@ -132,3 +132,30 @@ def test_tables_and_lengths_right_beside_what_is_written():
     with pytest.raises(bsa.BsaError, match="k_cache shares memory with kv_lens"):
         bsa.bsa_cache_append_q4(*want, kc, vc, pool.gtable, room[16:24].view(I32))
     bsa.bsa_device_status()
+
+
+def test_a_wait_that_gave_up_is_reported_once_and_the_next_call_is_right():
+    """One thread waits, with the kernels' bounded wait and a limit of 20 ms, for a phase
+    that nothing completes, and leaves: the word of the kernel of few rows."""
+    pool = QPool([300, 5], 130, 2, 64, 16, DEV, 408)
+    q = randn((2, 1, 4, 64), 409)
+    args = (q.to(DEV), pool.gk, pool.gv, pool.gtable, pool.kv_lens)
+    bsa.bsa_device_status()
+    bsa.bsa_debug_paged_q4_wait_probe(20_000_000)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_TIMEOUT.*in the paged attention kernels"):
+        bsa.bsa_device_status()
+    bsa.bsa_device_status()
+    bsa.bsa_debug_paged_q4_wait_probe(20_000_000)
+    bsa.bsa_debug_wait_probe(1, 20_000_000)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_TIMEOUT.*in the paged attention and other kernels"):
+        bsa.bsa_device_status()
+    table = pool.gtable.clone()
+    table[0, 1] = -1
+    bsa.bsa_forward_paged_q4(*args[:3], table, pool.kv_lens)
+    bsa.bsa_debug_paged_q4_wait_probe(20_000_000)
+    with pytest.raises(bsa.BsaError, match="BSA_ERR_INVALID_INDICES.*bsaq_forward; a bounded device wait also gave up"):
+        bsa.bsa_device_status()
+    bsa.bsa_device_status()
+    out, lse = bsa.bsa_forward_paged_q4(*args, prefix_table=pool.gprefix, prefix_len=130)
+    bsa.bsa_device_status()
+    check_attention(out, lse, attend64(q, pool))

@@ -1,4 +1,4 @@
-"""Limits of the attention over 4-bit pages: those of the one over bf16 pages (CPU only:
+"""Limits of the attention over 4-bit pages, those of the one over bf16 pages (CPU only:
 every call below fails host-side validation, so fake device pointers are never
 dereferenced)."""
 
@@ -43,3 +43,9 @@ def test_both_attentions_over_pages_take_the_same_sizes(lib, B, T, Hq, Hkv, page
         st = fn(ctypes.byref(q), *map(ctypes.byref, caches), FAKE, pages, pages, FAKE, None, FAKE if prefix else None, prefix, 1,
                 0.0, 1 << 45, None, 1 << 47, 16, None)
         assert st == (2 if refused else 3), lib.bsa_get_last_error().decode()
+
+
+@pytest.mark.parametrize("limit", [0, 999_999, 10_000_000_001])
+def test_wait_probe_refuses_limits_out_of_range(lib, limit):
+    assert lib.bsaq_debug_wait_probe(limit, None) == 1
+    assert lib.bsa_get_last_error().decode().startswith("bsaq_debug_wait_probe: limit_ns")
