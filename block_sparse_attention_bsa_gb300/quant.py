@@ -58,10 +58,12 @@ def bsa_cache_append_q4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     Positions, lengths and tables are those of ``bsa_cache_append``: token t of
     request b goes to key ``kv_lens[b] - n + t``, n = ``new_lens[b]`` (default T)
     new tokens being counted in ``kv_lens[b]``.  32 neighbouring channels share a
-    scale; a value is off by at most half of it, 1/13 of the largest of the 32.
-    A group with a value that is not finite reads as NaN.  Keys with rotary
-    positions are rotated before (``bsa_rope_axes``).  A block of 16 slots that
-    one request's new tokens touch may not be touched by another's.
+    scale, from 2^-15 to 1.75 2^16; a value is off by at most half of it, which is
+    at most 1/13 of the largest of the 32, or 2^-16 where that is more: values below
+    2^-16 read as 0 in a group of such.  Above 7 times the largest scale, 802,816,
+    they saturate.  A group with a value that is not finite reads as NaN.  Keys
+    with rotary positions are rotated before (``bsa_rope_axes``).  A block of 16
+    slots that one request's new tokens touch may not be touched by another's.
     """
     dev = _gpu(k, "k")
     kd, vd = _tensor(k, "k", dev), _tensor(v, "v", dev)
