@@ -101,9 +101,14 @@ __device__ __forceinline__ void bare_codes(uint32_t word, uint32_t* r) {
 constexpr int kSegmentWay = 1;
 
 // SMs of `sms` that the prefix gets where its tiles (of rows above 128 or not) and own
-// tiles (and ways) of few rows are two kernels side by side: by their times, 1.75 and 1.0 us
-// against 0.42 for a tile; SMs come in pairs.  (0.62 took 3 us more for 64 requests on
-// one prompt of 8,209 keys and for 256 samples of one of 32,768.)
+// tiles (and ways) of few rows are two kernels side by side, in pairs of SMs.  1.75 and
+// 1.0 are the times of a prefix's tile in us.  0.42 is not that of an own tile, which is
+// 0.56 for 4 rows of heads of 128 (and others for other rows and heads, not told apart
+// here): it was chosen by the times of whole calls, 0.62 taking 3 us more for 64 requests
+// on one prompt of 8,209 keys and for 256 samples of one of 32,768.  It has to stand in
+// for what is not counted, the way in and out of the prefix's segments; shapes in between
+// are up to a sixth slower than at their best split (64 requests on 1,200 keys 25.8 to 30
+// us by where the cut falls).  Results do not depend on it.
 __device__ __forceinline__ int prefix_sms(int sms, int prefix_tiles, bool two_jobs, int own_tiles) {
   if (own_tiles == 0) return sms;
   const float w = (float)prefix_tiles * (two_jobs ? 1.75f : 1.0f), o = (float)own_tiles * 0.42f;

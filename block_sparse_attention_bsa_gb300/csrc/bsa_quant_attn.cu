@@ -44,7 +44,7 @@
 // which 1.3 make bf16 of the codes); DRAM could bring a tile of heads of 128 in 748.
 // Device times, of the measured copy rate: 16 requests of 1,024 to 65,536 keys, 32
 // heads over 8 of 128: 135 us (69 %); 20 of 500 to 9,000 keys, 24 heads of one row each:
-// 70 us (59 %); one request of 4,097 keys 9.4 us, of which 4 are the way in, the join
+// 70 us (59 %); one request of 4,097 keys 9.1 us, of which 4 are the way in, the join
 // and the launches; 24 requests with five drafts on 1,000 shared keys, heads of 64: 14 us.
 #include <cuda_bf16.h>
 #include <math_constants.h>
